@@ -29,6 +29,7 @@ BLK_ERR_POSITION = -8
 BLK_ERR_DEVICE = -9
 BLK_ERR_SCRATCH_LIMIT = -10
 BLK_ERR_TOKEN = -11
+BLK_ERR_PAGE = -12
 BLK_STATIC_SCRATCH_BYTES = 1 << 20
 BLK_FLAG_CHAIN = 1
 BLK_WFMT_F16, BLK_WFMT_I8, BLK_WFMT_U4 = 0, 1, 2
@@ -41,8 +42,10 @@ EXPORTED = ("blk_create", "blk_destroy", "blk_set_flags", "blk_workspace_bytes",
             "blk_decode_batch_stack_workspace_bytes", "blk_decode_batch_stack",
             "blk_wait_probe", "blk_qworkspace_bytes", "blk_prefill_q", "blk_prefill_kv_q",
             "blk_decode_q", "blk_decode_stack_q", "blk_set_window", "blk_set_rope_yarn",
-            "blk_prefill_stack_workspace_bytes", "blk_prefill_stack")
-BLK_N_KERNELS = 16
+            "blk_prefill_stack_workspace_bytes", "blk_prefill_stack", "blk_page_plan",
+            "blk_page_append", "blk_attn_paged_workspace_bytes", "blk_attn_paged",
+            "blk_step_paged_workspace_bytes", "blk_step_paged", "blk_step_paged_stack")
+BLK_N_KERNELS = 24
 
 WEIGHT_FIELDS = ("ln1_g", "wq", "wk", "wv", "bq", "bk", "bv", "wo", "ln2_g", "w_gate", "w_up",
                  "w_down")
@@ -80,6 +83,15 @@ class BlkYarn(ctypes.Structure):
     _fields_ = [("freq_scale", ctypes.c_double), ("ext_factor", ctypes.c_double),
                 ("attn_factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
                 ("beta_slow", ctypes.c_double), ("n_ctx_orig", ctypes.c_int64)]
+
+
+class BlkPagedBatch(ctypes.Structure):
+    """A batch over paged caches (blk_paged_batch); ``keep`` holds its tensors."""
+    _fields_ = ([(n, ctypes.c_int64) for n in ("n_seqs", "n_rows", "max_new", "max_len")] +
+                [(n, ctypes.c_void_p) for n in ("row_start", "cache_lens", "block_table")] +
+                [("max_blocks", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                 ("prefix_pages", ctypes.c_void_p), ("prefix_len", ctypes.c_int64),
+                 ("page_size", ctypes.c_int32)])
 
 
 class BlkError(RuntimeError):
@@ -183,6 +195,25 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                        i64, vp, ctypes.POINTER(vp), ctypes.POINTER(vp), vp,
                                        ctypes.c_size_t, vp]
     lib.blk_decode_stack_q.restype = i32
+    bt = ctypes.POINTER(BlkPagedBatch)
+    lib.blk_page_plan.argtypes = [vp, ctypes.c_int32, i64, vp, vp, vp, i64, vp, i64, i64, vp, vp, vp,
+                                  vp, vp]
+    lib.blk_page_plan.restype = i32
+    lib.blk_page_append.argtypes = [vp, vp, vp, i64, i64, vp, i64, ctypes.c_int32, i64, vp, vp, vp]
+    lib.blk_page_append.restype = i32
+    lib.blk_attn_paged_workspace_bytes.argtypes = [vp, i64, i64, i32]
+    lib.blk_attn_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.blk_attn_paged.argtypes = [vp, bt, vp, i64, vp, vp, vp, i64, vp, ctypes.c_size_t, vp]
+    lib.blk_attn_paged.restype = i32
+    lib.blk_step_paged_workspace_bytes.argtypes = [vp, i64, i64, i32]
+    lib.blk_step_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.blk_step_paged.argtypes = [vp, ctypes.POINTER(BlkWeights), bt, vp, vp, vp, vp, vp, vp, vp,
+                                   ctypes.c_size_t, vp]
+    lib.blk_step_paged.restype = i32
+    lib.blk_step_paged_stack.argtypes = [vp, ctypes.POINTER(BlkWeights), i32, bt,
+                                         ctypes.POINTER(vp), ctypes.POINTER(vp), vp, vp, vp, vp, vp,
+                                         ctypes.c_size_t, vp]
+    lib.blk_step_paged_stack.restype = i32
     _lib = lib
     return lib
 
@@ -337,6 +368,46 @@ def blk_lm_head(handle, x, T, norm_g, w_lm, vocab, logits, tokens, ws, ws_bytes,
                               stream)
 
 
+def blk_page_plan(handle, page_size, n_seqs, cache_lens, new_lens, free_pages, n_free, block_table,
+                  max_blocks, n_rows, row_start, slot_map, pos, used, stream) -> int:
+    return load().blk_page_plan(handle, page_size, n_seqs, cache_lens, new_lens, free_pages, n_free,
+                                block_table, max_blocks, n_rows, row_start, slot_map, pos, used,
+                                stream)
+
+
+def blk_page_append(handle, k, v, row_stride, head_stride, slot_map, n_rows, page_size, n_pages,
+                    k_pages, v_pages, stream) -> int:
+    return load().blk_page_append(handle, k, v, row_stride, head_stride, slot_map, n_rows,
+                                  page_size, n_pages, k_pages, v_pages, stream)
+
+
+def blk_attn_paged_workspace_bytes(handle, max_rows: int, max_seqs: int, with_prefix) -> int:
+    return load().blk_attn_paged_workspace_bytes(handle, max_rows, max_seqs, 1 if with_prefix else 0)
+
+
+def blk_attn_paged(handle, batch: BlkPagedBatch, q, q_stride, k_pages, v_pages, out, out_stride, ws,
+                   ws_bytes, stream) -> int:
+    return load().blk_attn_paged(handle, batch, q, q_stride, k_pages, v_pages, out, out_stride, ws,
+                                 ws_bytes, stream)
+
+
+def blk_step_paged_workspace_bytes(handle, max_rows: int, max_seqs: int, with_prefix) -> int:
+    return load().blk_step_paged_workspace_bytes(handle, max_rows, max_seqs, 1 if with_prefix else 0)
+
+
+def blk_step_paged(handle, w: BlkWeights, batch: BlkPagedBatch, x, pos, slot_map, k_pages, v_pages,
+                   out, ws, ws_bytes, stream) -> int:
+    return load().blk_step_paged(handle, w, batch, x, pos, slot_map, k_pages, v_pages, out, ws,
+                                 ws_bytes, stream)
+
+
+def blk_step_paged_stack(handle, w_array, n_layers, batch: BlkPagedBatch, k_pages, v_pages, x, pos,
+                         slot_map, out, ws, ws_bytes, stream) -> int:
+    """w_array: (BlkWeights * n); k_pages/v_pages: (c_void_p * n)."""
+    return load().blk_step_paged_stack(handle, w_array, n_layers, batch, k_pages, v_pages, x, pos,
+                                       slot_map, out, ws, ws_bytes, stream)
+
+
 def blk_check(handle, stream) -> int:
     return load().blk_check(handle, stream)
 
@@ -362,6 +433,14 @@ def blk_timing_read(handle, kernel: int):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _check_tensor(t, dtype, what, shape=None, contiguous=True):
+    """A tensor that the library reads or writes by its raw pointer: on the GPU, of
+    this type, (contiguous) and of this shape where one is given."""
+    if (t.dtype != dtype or not t.is_cuda or (shape is not None and tuple(t.shape) != shape) or
+            (contiguous and not t.is_contiguous())):
+        raise BlkError(BLK_ERR_SHAPE, f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
 class Block:
@@ -497,6 +576,134 @@ class Block:
                               self._stream(stream))
         if rc != BLK_OK:
             raise BlkError(rc, "blk_decode_batch")
+
+    # ---- paged cache: pools [n_pages, n_kv_heads, page_size, head_dim] fp16
+
+    def page_plan(self, page_size: int, cache_lens, new_lens, free_pages, block_table, row_start,
+                  slot_map, pos, used, stream=None):
+        """Block tables, slot map and positions of a step from the requests' lengths.
+
+        cache_lens, new_lens (or None: one new token each): int64 [B]; free_pages:
+        int32, taken from the front (used[0] of them); block_table: int32 [B,
+        max_blocks], the new pages' entries written; row_start int64 [B + 1],
+        slot_map and pos int64 [n_rows], used int64 [1]: written."""
+        import torch
+        B, n = cache_lens.numel(), slot_map.numel()
+        for t, shape, what in ((cache_lens, (B,), "cache_lens"), (row_start, (B + 1,), "row_start"),
+                               (slot_map, (n,), "slot_map"), (pos, (n,), "pos"), (used, (1,), "used")):
+            _check_tensor(t, torch.int64, what, shape)
+        if new_lens is not None:
+            _check_tensor(new_lens, torch.int64, "new_lens", (B,))
+        _check_tensor(free_pages, torch.int32, "free_pages", (free_pages.numel(),))
+        if block_table.dim() != 2:
+            raise BlkError(BLK_ERR_SHAPE, "block_table")
+        _check_tensor(block_table, torch.int32, "block_table", (B, block_table.shape[1]))
+        rc = blk_page_plan(self.handle, page_size, B, cache_lens.data_ptr(), _ptr(new_lens),
+                           free_pages.data_ptr(), free_pages.numel(), block_table.data_ptr(),
+                           block_table.shape[1], n, row_start.data_ptr(), slot_map.data_ptr(),
+                           pos.data_ptr(), used.data_ptr(), self._stream(stream))
+        if rc != BLK_OK:
+            raise BlkError(rc, "blk_page_plan")
+
+    def _pools(self, k_pages, v_pages):
+        import torch
+        s = self.cfg
+        if k_pages.dim() != 4:
+            raise BlkError(BLK_ERR_SHAPE, "k_pages")
+        shape = (k_pages.shape[0], s.n_kv_heads, k_pages.shape[2], s.head_dim)
+        _check_tensor(k_pages, torch.float16, "k_pages", shape)
+        _check_tensor(v_pages, torch.float16, "v_pages", shape)
+
+    def page_append(self, k, v, slot_map, k_pages, v_pages, stream=None):
+        """Rows of k and v (fp16 [n, n_kv_heads, head_dim], the last dimension
+        contiguous, both with the same strides) into the slots of slot_map (int64
+        [n]; -1 leaves a row out)."""
+        import torch
+        s = self.cfg
+        self._pools(k_pages, v_pages)
+        n = slot_map.numel()
+        _check_tensor(slot_map, torch.int64, "slot_map", (n,))
+        for t, what in ((k, "k"), (v, "v")):
+            _check_tensor(t, torch.float16, what, (n, s.n_kv_heads, s.head_dim), contiguous=False)
+        st = k.stride()
+        if st != v.stride() or st[2] != 1:
+            raise BlkError(BLK_ERR_SHAPE, "page_append: strides")
+        rc = blk_page_append(self.handle, k.data_ptr(), v.data_ptr(), st[0], st[1],
+                             slot_map.data_ptr(), n, k_pages.shape[2], k_pages.shape[0],
+                             k_pages.data_ptr(), v_pages.data_ptr(), self._stream(stream))
+        if rc != BLK_OK:
+            raise BlkError(rc, "blk_page_append")
+
+    def paged_batch(self, row_start, cache_lens, block_table, n_rows: int, page_size: int,
+                    n_pages: int, max_new: int, max_len: int, prefix_pages=None) -> BlkPagedBatch:
+        """The batch of a paged step, for every layer: row_start int64 [B + 1], cache_lens
+        int64 [B], block_table int32 [B, max_blocks] (device); max_new and max_len bound
+        a sequence's new tokens and its slots with them; prefix_pages: int32 pages
+        whose slots begin every sequence (a shared prefix), or None."""
+        import torch
+        B = cache_lens.numel()
+        _check_tensor(cache_lens, torch.int64, "cache_lens", (B,))
+        _check_tensor(row_start, torch.int64, "row_start", (B + 1,))
+        if block_table.dim() != 2:
+            raise BlkError(BLK_ERR_SHAPE, "block_table")
+        _check_tensor(block_table, torch.int32, "block_table", (B, block_table.shape[1]))
+        pre = 0
+        if prefix_pages is not None:
+            _check_tensor(prefix_pages, torch.int32, "prefix_pages", (prefix_pages.numel(),))
+            pre = prefix_pages.numel() * page_size
+        b = BlkPagedBatch(B, n_rows, max_new, max_len, row_start.data_ptr(), cache_lens.data_ptr(),
+                          block_table.data_ptr(), block_table.shape[1], n_pages,
+                          _ptr(prefix_pages) if pre else None, pre, page_size)
+        b.keep = (row_start, cache_lens, block_table, prefix_pages)
+        return b
+
+    def attn_paged_workspace_bytes(self, max_rows: int, max_seqs: int, prefix: bool = True) -> int:
+        return blk_attn_paged_workspace_bytes(self.handle, max_rows, max_seqs, prefix)
+
+    def _paged_pools(self, batch, k_pages, v_pages):
+        self._pools(k_pages, v_pages)
+        if (k_pages.shape[0], k_pages.shape[2]) != (batch.n_pages, batch.page_size):
+            raise BlkError(BLK_ERR_SHAPE, "the pools are not those of the batch")
+
+    def attn_paged(self, batch: BlkPagedBatch, q, k_pages, v_pages, out, ws, stream=None):
+        """Attention of the batch's rows: q, out fp16 [n_rows, n_heads, head_dim], heads
+        contiguous, rows at any stride."""
+        import torch
+        s = self.cfg
+        self._paged_pools(batch, k_pages, v_pages)
+        for t, what in ((q, "q"), (out, "out")):
+            _check_tensor(t, torch.float16, what, (batch.n_rows, s.n_heads, s.head_dim),
+                          contiguous=False)
+            if t.stride()[1:] != (s.head_dim, 1):
+                raise BlkError(BLK_ERR_SHAPE, what)
+        rc = blk_attn_paged(self.handle, batch, q.data_ptr(), q.stride(0), k_pages.data_ptr(),
+                            v_pages.data_ptr(), out.data_ptr(), out.stride(0), ws.data_ptr(),
+                            ws.numel() * ws.element_size(), self._stream(stream))
+        if rc != BLK_OK:
+            raise BlkError(rc, "blk_attn_paged")
+
+    def step_paged_workspace_bytes(self, max_rows: int, max_seqs: int, prefix: bool = True) -> int:
+        return blk_step_paged_workspace_bytes(self.handle, max_rows, max_seqs, prefix)
+
+    def step_paged(self, w: BlkWeights, batch: BlkPagedBatch, x, pos, slot_map, k_pages, v_pages,
+                   out, ws, stream=None):
+        """One block step of the batch: x, out fp16 [n_rows, hidden]; pos, slot_map as
+        page_plan writes them."""
+        self._paged_pools(batch, k_pages, v_pages)
+        self._paged_rows(batch, x, pos, slot_map, out)
+        rc = blk_step_paged(self.handle, w, batch, x.data_ptr(), pos.data_ptr(),
+                            slot_map.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                            out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                            self._stream(stream))
+        if rc != BLK_OK:
+            raise BlkError(rc, "blk_step_paged")
+
+    def _paged_rows(self, batch, x, pos, slot_map, out):
+        import torch
+        for t, what in ((x, "x"), (out, "out")):
+            _check_tensor(t, torch.float16, what, (batch.n_rows, self.cfg.hidden))
+        for t, what in ((pos, "pos"), (slot_map, "slot_map")):
+            _check_tensor(t, torch.int64, what, (batch.n_rows,))
 
     def embed(self, table, ids, x, stream=None):
         """x[t] = table[ids[t]] (fp16 [vocab, hidden] table, int64 ids)."""

@@ -14,6 +14,7 @@
 #include "gemm_fr.h"
 #include "gemm_tc.h"
 #include "kernels.h"
+#include "paged.h"
 
 using namespace blk;
 
@@ -23,13 +24,16 @@ constexpr int kMaxPending = 1024;
 enum KernelId {
   kKRmsNorm = 0, kKGemmQKV, kKSplitReduce, kKAttnPrefill, kKGemmO, kKGemmGateUp,
   kKGemmDown, kKDecodeStep, kKAttnMerge, kKLmHead, kKArgmax, kKEmbed, kKDecodeAttnBatch,
-  kKQkvFinish, kKDequant, kKReduceNorm, kKCount
+  kKQkvFinish, kKDequant, kKReduceNorm, kKPagePlan, kKPageAppend, kKPagedFew, kKPagedMany,
+  kKPagedPrefix, kKPagedMerge, kKPagedSched, kKCount
 };
 static_assert(kKCount <= BLK_N_KERNELS, "kernel id table");
 const char* const kKernelNames[BLK_N_KERNELS] = {
     "rmsnorm_rows", "gemm_qkv", "splitk_reduce", "attn_prefill", "gemm_o",
     "gemm_gateup", "gemm_down", "decode_persistent", "attn_merge", "lm_head", "argmax_reduce",
-    "embed", "decode_attn_batch", "qkv_finish", "dequant_weights", "splitk_reduce_norm"};
+    "embed", "decode_attn_batch", "qkv_finish", "dequant_weights", "splitk_reduce_norm",
+    "page_plan", "page_append", "attn_paged_few", "attn_paged_many", "attn_paged_prefix",
+    "attn_paged_merge", "attn_paged_sched"};
 }  // namespace
 
 struct blk_handle_s {
@@ -1100,6 +1104,7 @@ int blk_check(blk_handle h, void* stream) {
   if (v == kDevTimeout) return BLK_ERR_DEVICE_TIMEOUT;
   if (v == kDevPosition) return BLK_ERR_POSITION;
   if (v == kDevToken) return BLK_ERR_TOKEN;
+  if (v == kDevPage) return BLK_ERR_PAGE;
   return BLK_OK;
 }
 
@@ -1227,6 +1232,438 @@ int blk_decode_batch_stack(blk_handle h, const blk_weights* w, int n_layers,
 
 }  // extern "C"
 
+// ------------------------------------------------------------- paged cache
+namespace {
+
+constexpr int64_t kMaxPagedRows = (int64_t)1 << 20;
+
+// log2 of a supported page size, else -1.
+int page_log2(int64_t page) {
+  return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1;
+}
+
+bool on_device(blk_handle h) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+int check_pool(blk_handle h, int64_t page_size, int64_t n_pages) {
+  if (page_log2(page_size) < 0) return BLK_ERR_SHAPE;
+  // (page, kv head) pairs are the tensor maps' last coordinate
+  if (n_pages < 1 || n_pages > 0x7ffffffe / h->cfg.n_kv_heads) return BLK_ERR_SHAPE;
+  return BLK_OK;
+}
+
+int check_paged(blk_handle h, const blk_paged_batch* b) {
+  if (!h || !b) return BLK_ERR_NULL;
+  if (!b->row_start || !b->cache_lens || !b->block_table) return BLK_ERR_NULL;
+  if (!aligned(b->row_start, 8) || !aligned(b->cache_lens, 8) || !aligned(b->block_table, 4))
+    return BLK_ERR_ALIGN;
+  const int rc = check_pool(h, b->page_size, b->n_pages);
+  if (rc) return rc;
+  if (b->n_seqs < 1 || b->n_seqs > kMaxSeqs || b->n_rows < 1 || b->n_rows > kMaxPagedRows ||
+      b->max_new < 1 || b->max_new > b->n_rows || b->max_blocks < 1 ||
+      b->max_blocks > (int64_t)1 << 31 || b->max_len < 1 || b->max_len > 0x7fffff00)
+    return BLK_ERR_SHAPE;
+  if (b->max_len > b->max_blocks * b->page_size) return BLK_ERR_CACHE_OVERFLOW;
+  if (b->prefix_len < 0 || b->prefix_len % b->page_size || b->prefix_len >= b->max_len)
+    return BLK_ERR_SHAPE;
+  if (b->prefix_len > 0) {
+    if (!b->prefix_pages) return BLK_ERR_NULL;
+    if (!aligned(b->prefix_pages, 4)) return BLK_ERR_ALIGN;
+    if (h->window > 0) return BLK_ERR_SHAPE;
+  }
+  return BLK_OK;
+}
+
+// Attention workspace: partials and (m, l) of the own parts, the cut units,
+// the many-row kernel's schedule; with a prefix also its partials and the
+// whole units' parts by row and head.
+struct PagedWs {
+  size_t part, ml, cut, pref, unit, own, own_ml, info, ppart, pml, pown, pown_ml, total;
+};
+PagedWs paged_ws(const blk_config& c, int64_t N, int64_t B, bool prefix, int num_sms) {
+  const size_t D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads;
+  const size_t few = (size_t)2 * num_sms * 2 * kPagedFewRows;
+  const size_t many = (size_t)num_sms * 2 * kPagedManyRows;
+  const size_t rows = few > many ? few : many;
+  const size_t units = (size_t)(N / (2 * paged_btok((int)(Hq / Hkv))) + B);
+  PagedWs w;
+  size_t o = 0;
+  w.part = o; o = align_up(o + rows * D * 4);
+  w.ml = o; o = align_up(o + rows * 8);
+  w.cut = o; o = align_up(o + (size_t)2 * num_sms * sizeof(PagedPiece));
+  w.pref = o; o = align_up(o + (units + 2) * 8);
+  w.unit = o; o = align_up(o + units * sizeof(PagedUnit));
+  w.own = w.own_ml = w.info = w.ppart = w.pml = w.pown = w.pown_ml = o;
+  if (prefix) {
+    w.own = o; o = align_up(o + (size_t)N * Hq * D * 4);
+    w.own_ml = o; o = align_up(o + (size_t)N * Hq * 8);
+    w.info = o; o = align_up(o + (size_t)N * Hkv * sizeof(int4));
+    w.ppart = o; o = align_up(o + many * D * 4);
+    w.pml = o; o = align_up(o + many * 8);
+    w.pown = o; o = align_up(o + (size_t)N * Hq * D * 4);
+    w.pown_ml = o; o = align_up(o + (size_t)N * Hq * 8);
+  }
+  w.total = o;
+  return w;
+}
+
+int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_t q_stride,
+                   const void* k_pages, const void* v_pages, void* out, int64_t out_stride,
+                   unsigned char* base, cudaStream_t s, Timer& tm) {
+  const blk_config& c = h->cfg;
+  const int D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads, G = Hq / Hkv;
+  const bool prefix = b->prefix_len > 0;
+  const PagedWs lay = paged_ws(c, b->n_rows, b->n_seqs, prefix, h->num_sms);
+  const int64_t page = b->page_size, heads = b->n_pages * Hkv;
+  PagedManyParams m = {};
+  PagedAttnParams& a = m.a;
+  a.q = static_cast<const __half*>(q); a.q_stride = q_stride;
+  a.out = static_cast<__half*>(out); a.out_stride = out_stride;
+  a.row_start = b->row_start; a.cache_lens = b->cache_lens;
+  a.table = b->block_table; a.prefix_pages = b->prefix_pages;
+  a.max_blocks = b->max_blocks; a.n_pages = b->n_pages; a.window = h->window;
+  a.max_len = b->max_len; a.prefix_len = b->prefix_len;
+  a.B = (int)b->n_seqs; a.N = (int)b->n_rows; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.G = G;
+  a.page_lg = page_log2(page); a.max_new = (int)b->max_new;
+  a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+  a.part = reinterpret_cast<float*>(base + lay.part);
+  a.ml = reinterpret_cast<float2*>(base + lay.ml);
+  a.cut = reinterpret_cast<PagedPiece*>(base + lay.cut);
+  a.err = h->status;
+  const bool few = paged_few_rows(G, b->max_new);
+  CUtensorMap few_k, few_v;
+  if (few) {
+    // a page's slots (at most 64 of them) and all of D in one box
+    const int64_t kd[4] = {64, page, D / 64, heads}, ks[3] = {(int64_t)D * 2, 128, page * D * 2};
+    const int kb[4] = {64, (int)(page < 64 ? page : 64), D / 64, 1};
+    if (make_tmap_4d(&few_k, k_pages, kd, ks, kb) || make_tmap_4d(&few_v, v_pages, kd, ks, kb))
+      return BLK_ERR_CUDA;
+  }
+  if (!few || prefix) {
+    const int64_t kd[3] = {D, page, heads}, ks[2] = {(int64_t)D * 2, page * D * 2};
+    const int kb[3] = {64, (int)page, 1};
+    const int64_t qd[3] = {D, Hq, b->n_rows}, qs[2] = {(int64_t)D * 2, q_stride * 2};
+    const int qb[3] = {64, G, paged_btok(G)};
+    if (make_tmap_3d(&a.tm_k, k_pages, kd, ks, kb) || make_tmap_3d(&a.tm_v, v_pages, kd, ks, kb) ||
+        make_tmap_3d(&a.tm_q, q, qd, qs, qb))
+      return BLK_ERR_CUDA;
+  }
+  m.btok = paged_btok(G);
+  PagedMergeParams mg = {};
+  if (prefix) {
+    a.own = reinterpret_cast<float*>(base + lay.own);
+    a.own_ml = reinterpret_cast<float2*>(base + lay.own_ml);
+    a.row_info = reinterpret_cast<int4*>(base + lay.info);
+    PagedManyParams pm = m;
+    pm.prefix = 1;
+    pm.units = (int)((b->n_rows + 2 * m.btok - 1) / (2 * m.btok));
+    pm.a.part = reinterpret_cast<float*>(base + lay.ppart);
+    pm.a.ml = reinterpret_cast<float2*>(base + lay.pml);
+    pm.a.own = reinterpret_cast<float*>(base + lay.pown);
+    pm.a.own_ml = reinterpret_cast<float2*>(base + lay.pown_ml);
+    pm.a.slot_rows = kPagedManyRows;
+    const int64_t tiles = (b->prefix_len + kPagedManyTile - 1) / kPagedManyTile;
+    const int64_t T = (int64_t)Hkv * pm.units * tiles;
+    pm.a.nc = (int)(T < h->num_sms ? T : h->num_sms);
+    BLK_LAUNCH(tm, kKPagedPrefix, launch_paged_many(pm, s, true));
+    mg.prefix = 1;
+    mg.pre_part = pm.a.part; mg.pre_ml = pm.a.ml;
+    mg.pre_own = pm.a.own; mg.pre_own_ml = pm.a.own_ml;
+    mg.pre_nc = pm.a.nc; mg.pre_rows = kPagedManyRows;
+    mg.pre_units = pm.units; mg.pre_tiles = (int)tiles;
+    mg.pre_tok = 2 * m.btok; mg.pre_btok = m.btok;
+  }
+  if (few) {
+    a.tm_k = few_k;
+    a.tm_v = few_v;
+    paged_few_part_rows(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
+    BLK_LAUNCH(tm, kKPagedFew, launch_paged_few(a, s, true));
+  } else {
+    int64_t* pref = reinterpret_cast<int64_t*>(base + lay.pref) + 1;
+    PagedUnit* unit = reinterpret_cast<PagedUnit*>(base + lay.unit);
+    m.units = (int)(b->n_rows / (2 * m.btok) + b->n_seqs);
+    m.pref = pref;
+    m.unit = unit;
+    a.nc = h->num_sms;
+    a.slot_rows = kPagedManyRows;
+    BLK_LAUNCH(tm, kKPagedSched, launch_paged_sched(m, pref, unit, s, true));
+    BLK_LAUNCH(tm, kKPagedMany, launch_paged_many(m, s, true));
+  }
+  mg.a = a;
+  mg.own_btok = few ? kPagedFewRows : m.btok;
+  BLK_LAUNCH(tm, kKPagedMerge, launch_paged_merge(mg, h->num_sms, s));
+  return BLK_OK;
+}
+
+int check_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_t q_stride,
+                     const void* k_pages, const void* v_pages, const void* out,
+                     int64_t out_stride, const void* ws, size_t ws_bytes) {
+  const int rc = check_paged(h, b);
+  if (rc) return rc;
+  if (!q || !k_pages || !v_pages || !out || !ws) return BLK_ERR_NULL;
+  for (const void* ptr : {q, k_pages, v_pages, out, ws})
+    if (!aligned(ptr, 16)) return BLK_ERR_ALIGN;
+  const int64_t width = (int64_t)h->cfg.n_heads * h->cfg.head_dim;
+  for (int64_t st : {q_stride, out_stride}) {
+    if (st % 8) return BLK_ERR_ALIGN;
+    if (st < width || st > (int64_t)1 << 32) return BLK_ERR_SHAPE;
+  }
+  if (ws_bytes < paged_ws(h->cfg, b->n_rows, b->n_seqs, b->prefix_len > 0, h->num_sms).total)
+    return BLK_ERR_WORKSPACE;
+  return BLK_OK;
+}
+
+// A step's workspace: the batched-decode buffers for N rows, the new K/V
+// [Hkv][N][D] on their way to the pages, the attention's workspace, and the
+// two activation buffers of a stack.
+struct StepPagedWs {
+  size_t xn16, q16, attn16, h32, hn16, act16, part32, k16, v16, attn, act[2], total;
+};
+int step_splits(int64_t N) { return N <= kFrMaxRows ? kMaxSplitsBatch : kMaxSplits; }
+StepPagedWs step_paged_ws(const blk_config& c, int64_t N, int64_t B, bool prefix, int num_sms) {
+  const size_t H = c.hidden, D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads,
+               I = c.intermediate;
+  StepPagedWs w;
+  size_t o = 0;
+  w.xn16 = o; o = align_up(o + N * H * 2);
+  w.q16 = o; o = align_up(o + N * Hq * D * 2);
+  w.attn16 = o; o = align_up(o + N * Hq * D * 2);
+  w.h32 = o; o = align_up(o + N * H * 4);
+  w.hn16 = o; o = align_up(o + N * H * 2);
+  w.act16 = o; o = align_up(o + N * I * 2);
+  // split-K partials of QKV (few rows only), o_proj and down
+  const size_t qkv = N <= kFrMaxRows ? (Hq + 2 * Hkv) * D : 0, nmax = qkv > H ? qkv : H;
+  w.part32 = o; o = align_up(o + (size_t)step_splits(N) * N * nmax * 4);
+  w.k16 = o; o = align_up(o + N * Hkv * D * 2);
+  w.v16 = o; o = align_up(o + N * Hkv * D * 2);
+  w.attn = o; o = align_up(o + paged_ws(c, N, B, prefix, num_sms).total);
+  for (int i = 0; i < 2; ++i) { w.act[i] = o; o = align_up(o + N * H * 2); }
+  w.total = o;
+  return w;
+}
+
+int check_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b, const void* x,
+                     const int64_t* pos, const int64_t* slot_map, const void* k_pages,
+                     const void* v_pages, const void* out, const void* ws, size_t ws_bytes) {
+  int rc = check_paged(h, b);
+  if (rc) return rc;
+  rc = check_weights(h->cfg, w);
+  if (rc) return rc;
+  if (!x || !pos || !slot_map || !k_pages || !v_pages || !out || !ws) return BLK_ERR_NULL;
+  for (const void* ptr : {x, k_pages, v_pages, out, ws})
+    if (!aligned(ptr, 16)) return BLK_ERR_ALIGN;
+  if (!aligned(pos, 8) || !aligned(slot_map, 8)) return BLK_ERR_ALIGN;
+  if (ws_bytes < step_paged_ws(h->cfg, b->n_rows, b->n_seqs, b->prefix_len > 0, h->num_sms).total)
+    return BLK_ERR_WORKSPACE;
+  return BLK_OK;
+}
+
+// One layer of a paged step (arguments checked).  x_normed and next_ln1 as in
+// run_decode_batch.
+int run_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b, const void* x,
+                   const int64_t* pos, const int64_t* slot_map, void* k_pages, void* v_pages,
+                   void* out, unsigned char* base, cudaStream_t s, bool x_normed,
+                   const __half* next_ln1) {
+  const blk_config& c = h->cfg;
+  const StepPagedWs lay = step_paged_ws(c, b->n_rows, b->n_seqs, b->prefix_len > 0, h->num_sms);
+  __half* xn16 = reinterpret_cast<__half*>(base + lay.xn16);
+  __half* q16 = reinterpret_cast<__half*>(base + lay.q16);
+  __half* attn16 = reinterpret_cast<__half*>(base + lay.attn16);
+  const int H = c.hidden, D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads, M = (int)b->n_rows;
+  const bool first_pdl = (h->flags & BLK_FLAG_CHAIN) != 0;
+  Timer tm{h, s};
+  if (!x_normed)
+    BLK_LAUNCH(tm, kKRmsNorm,
+               launch_rmsnorm_rows(x, false, static_cast<const __half*>(w->ln1_g), M, H,
+                                   c.rms_eps, xn16, s, first_pdl));
+  // QKV + bias + RoPE; the new K/V go to a buffer [Hkv][M][D] (a cache of M
+  // slots as the projection's epilogue sees it) and from there to their pages
+  TcGemmParams g = {};
+  if (make_tmap_2d(&g.tmA, xn16, M, H, tc_a_box_rows(M)) ||
+      make_tmap_2d(&g.tmB[0], w->wq, (int64_t)Hq * D, H, 64) ||
+      make_tmap_2d(&g.tmB[1], w->wk, (int64_t)Hkv * D, H, 64) ||
+      make_tmap_2d(&g.tmB[2], w->wv, (int64_t)Hkv * D, H, 64))
+    return BLK_ERR_CUDA;
+  g.M = M; g.N = (Hq + 2 * Hkv) * D; g.K = H; g.a_rows = tc_a_box_rows(M);
+  g.seg_rows[0] = Hq * D; g.seg_rows[1] = Hkv * D; g.seg_rows[2] = Hkv * D;
+  if (c.has_qkv_bias) {
+    g.bias[0] = static_cast<const __half*>(w->bq);
+    g.bias[1] = static_cast<const __half*>(w->bk);
+    g.bias[2] = static_cast<const __half*>(w->bv);
+  }
+  g.pos = pos; g.rope = h->rope; g.rope_len = c.max_ctx;
+  g.Hq = Hq; g.Hkv = Hkv; g.D = D;
+  g.q16 = q16;
+  g.kc = reinterpret_cast<__half*>(base + lay.k16);
+  g.vc = reinterpret_cast<__half*>(base + lay.v16);
+  g.max_ctx = M; g.cache_len = 0;
+  g.err = h->status;
+  float* part = reinterpret_cast<float*>(base + lay.part32);
+  if (M <= kFrMaxRows) {
+    FrGemmParams fq = {};
+    fq.x = xn16; fq.w[0] = w->wq; fq.w[1] = w->wk; fq.w[2] = w->wv;
+    for (int i = 0; i < 3; ++i) fq.seg_rows[i] = g.seg_rows[i];
+    fq.M = M; fq.N = g.N; fq.K = H;
+    fq.max_splits = 4;
+    fq.part = part; fq.err = h->status;
+    BLK_LAUNCH(tm, kKGemmQKV, launch_fr_gemm(fq, kFrPart, h->num_sms, s, true));
+    g.part = part;
+    g.splits = fq.splits;
+    BLK_LAUNCH(tm, kKQkvFinish, launch_qkv_finish(g, s));
+  } else {
+    BLK_LAUNCH(tm, kKGemmQKV, launch_tc_gemm(g, kTcQKV, h->num_sms, s, true));
+  }
+  PageAppendParams pa = {};
+  pa.k = g.kc; pa.v = g.vc;
+  pa.row_stride = D; pa.head_stride = (int64_t)M * D;
+  pa.slot_map = slot_map;
+  pa.k_pages = static_cast<__half*>(k_pages); pa.v_pages = static_cast<__half*>(v_pages);
+  pa.n_slots = b->n_pages * b->page_size;
+  pa.N = M; pa.Hkv = Hkv; pa.D = D; pa.page_lg = page_log2(b->page_size);
+  pa.err = h->status;
+  BLK_LAUNCH(tm, kKPageAppend, launch_page_append(pa, h->num_sms, s, true));
+  const int rc = run_attn_paged(h, b, q16, (int64_t)Hq * D, k_pages, v_pages, attn16,
+                                (int64_t)Hq * D, base + lay.attn, s, tm);
+  if (rc) return rc;
+  return run_block_tail(h, w, x, attn16, reinterpret_cast<float*>(base + lay.h32),
+                        reinterpret_cast<__half*>(base + lay.hn16),
+                        reinterpret_cast<__half*>(base + lay.act16), part, step_splits(M), true,
+                        true, out, M, s, tm, next_ln1, xn16);
+}
+
+}  // namespace
+
+extern "C" {
+
+int blk_page_plan(blk_handle h, int32_t page_size, int64_t n_seqs, const int64_t* cache_lens,
+                  const int64_t* new_lens, const int32_t* free_pages, int64_t n_free,
+                  int32_t* block_table, int64_t max_blocks, int64_t n_rows, int64_t* row_start,
+                  int64_t* slot_map, int64_t* pos, int64_t* used, void* stream) {
+  if (!h || !cache_lens || !block_table || !row_start || !slot_map || !pos || !used ||
+      (n_free > 0 && !free_pages))
+    return BLK_ERR_NULL;
+  for (const void* p : {(const void*)cache_lens, (const void*)new_lens, (const void*)row_start,
+                        (const void*)slot_map, (const void*)pos, (const void*)used})
+    if (!aligned(p, 8)) return BLK_ERR_ALIGN;
+  if (!aligned(free_pages, 4) || !aligned(block_table, 4)) return BLK_ERR_ALIGN;
+  if (page_log2(page_size) < 0 || n_seqs < 1 || n_seqs > kMaxSeqs || n_rows < 1 ||
+      n_rows > kMaxPagedRows || max_blocks < 1 || max_blocks > (int64_t)1 << 31 || n_free < 0 ||
+      n_free > 0x7fffffff)
+    return BLK_ERR_SHAPE;
+  if (!on_device(h)) return BLK_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  PagePlanParams p = {};
+  p.cache_lens = cache_lens; p.new_lens = new_lens; p.free_pages = free_pages;
+  p.table = block_table; p.row_start = row_start; p.slot_map = slot_map; p.pos = pos;
+  p.used = used; p.max_blocks = max_blocks; p.n_free = n_free; p.N = n_rows;
+  p.B = (int)n_seqs; p.page_lg = page_log2(page_size); p.err = h->status;
+  Timer tm{h, s};
+  BLK_LAUNCH(tm, kKPagePlan, launch_page_plan(p, h->num_sms, s, true));
+  return BLK_OK;
+}
+
+int blk_page_append(blk_handle h, const void* k, const void* v, int64_t row_stride,
+                    int64_t head_stride, const int64_t* slot_map, int64_t n_rows,
+                    int32_t page_size, int64_t n_pages, void* k_pages, void* v_pages,
+                    void* stream) {
+  if (!h || !k || !v || !slot_map || !k_pages || !v_pages) return BLK_ERR_NULL;
+  for (const void* p : {k, v, (const void*)k_pages, (const void*)v_pages})
+    if (!aligned(p, 16)) return BLK_ERR_ALIGN;
+  if (!aligned(slot_map, 8) || row_stride % 8 || head_stride % 8) return BLK_ERR_ALIGN;
+  const int rc = check_pool(h, page_size, n_pages);
+  if (rc) return rc;
+  if (n_rows < 1 || n_rows > kMaxPagedRows || row_stride < 0 || head_stride < 0)
+    return BLK_ERR_SHAPE;
+  if (!on_device(h)) return BLK_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  PageAppendParams p = {};
+  p.k = static_cast<const __half*>(k); p.v = static_cast<const __half*>(v);
+  p.row_stride = row_stride; p.head_stride = head_stride; p.slot_map = slot_map;
+  p.k_pages = static_cast<__half*>(k_pages); p.v_pages = static_cast<__half*>(v_pages);
+  p.n_slots = n_pages * page_size;
+  p.N = (int)n_rows; p.Hkv = h->cfg.n_kv_heads; p.D = h->cfg.head_dim;
+  p.page_lg = page_log2(page_size); p.err = h->status;
+  Timer tm{h, s};
+  BLK_LAUNCH(tm, kKPageAppend, launch_page_append(p, h->num_sms, s, true));
+  return BLK_OK;
+}
+
+size_t blk_attn_paged_workspace_bytes(blk_handle h, int64_t max_rows, int64_t max_seqs,
+                                      int with_prefix) {
+  if (!h || max_rows < 1 || max_rows > kMaxPagedRows || max_seqs < 1 || max_seqs > kMaxSeqs)
+    return 0;
+  return paged_ws(h->cfg, max_rows, max_seqs, with_prefix != 0, h->num_sms).total;
+}
+
+int blk_attn_paged(blk_handle h, const blk_paged_batch* batch, const void* q, int64_t q_stride,
+                   const void* k_pages, const void* v_pages, void* out, int64_t out_stride,
+                   void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_attn_paged(h, batch, q, q_stride, k_pages, v_pages, out, out_stride, ws,
+                                  ws_bytes);
+  if (rc) return rc;
+  if (!on_device(h)) return BLK_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timer tm{h, s};
+  return run_attn_paged(h, batch, q, q_stride, k_pages, v_pages, out, out_stride,
+                        static_cast<unsigned char*>(ws), s, tm);
+}
+
+size_t blk_step_paged_workspace_bytes(blk_handle h, int64_t max_rows, int64_t max_seqs,
+                                      int with_prefix) {
+  if (!h || max_rows < 1 || max_rows > kMaxPagedRows || max_seqs < 1 || max_seqs > kMaxSeqs)
+    return 0;
+  // few rows keep more split-K partials: enough for either side of that bound
+  const size_t a = step_paged_ws(h->cfg, max_rows, max_seqs, with_prefix != 0, h->num_sms).total;
+  if (max_rows <= kFrMaxRows) return a;
+  const size_t b = step_paged_ws(h->cfg, kFrMaxRows, max_seqs, with_prefix != 0, h->num_sms).total;
+  return a > b ? a : b;
+}
+
+int blk_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* batch,
+                   const void* x, const int64_t* pos, const int64_t* slot_map, void* k_pages,
+                   void* v_pages, void* out, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_step_paged(h, w, batch, x, pos, slot_map, k_pages, v_pages, out, ws,
+                                  ws_bytes);
+  if (rc) return rc;
+  if (!on_device(h)) return BLK_ERR_CUDA;
+  return run_step_paged(h, w, batch, x, pos, slot_map, k_pages, v_pages, out,
+                        static_cast<unsigned char*>(ws), static_cast<cudaStream_t>(stream), false,
+                        nullptr);
+}
+
+int blk_step_paged_stack(blk_handle h, const blk_weights* w, int n_layers,
+                         const blk_paged_batch* batch, void* const* k_pages,
+                         void* const* v_pages, const void* x, const int64_t* pos,
+                         const int64_t* slot_map, void* out, void* ws, size_t ws_bytes,
+                         void* stream) {
+  if (!h || !w || !batch || !k_pages || !v_pages || !ws) return BLK_ERR_NULL;
+  if (n_layers < 1) return BLK_ERR_SHAPE;
+  // every layer's arguments are checked before anything is enqueued
+  for (int l = 0; l < n_layers; ++l) {
+    const int rc = check_step_paged(h, &w[l], batch, x, pos, slot_map, k_pages[l], v_pages[l],
+                                    out, ws, ws_bytes);
+    if (rc) return rc;
+  }
+  if (!on_device(h)) return BLK_ERR_CUDA;
+  const StepPagedWs lay = step_paged_ws(h->cfg, batch->n_rows, batch->n_seqs,
+                                        batch->prefix_len > 0, h->num_sms);
+  unsigned char* base = static_cast<unsigned char*>(ws);
+  for (int l = 0; l < n_layers; ++l) {
+    const void* in = l == 0 ? x : base + lay.act[(l - 1) % 2];
+    void* to = l == n_layers - 1 ? out : base + lay.act[l % 2];
+    const __half* next_ln1 =
+        l + 1 < n_layers ? static_cast<const __half*>(w[l + 1].ln1_g) : nullptr;
+    const int rc = run_step_paged(h, &w[l], batch, in, pos, slot_map, k_pages[l], v_pages[l], to,
+                                  base, static_cast<cudaStream_t>(stream), l > 0, next_ln1);
+    if (rc) return rc;
+  }
+  return BLK_OK;
+}
+
+}  // extern "C"
+
 size_t blk_internal_decode_ws_bytes(blk_handle h) {
   const blk_config& c = h->cfg;
   return decode_ws_bytes(c.hidden, c.n_heads, c.n_kv_heads, c.head_dim, c.intermediate,
@@ -1295,6 +1732,8 @@ const char* blk_status_str(int status) {
     case BLK_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait timed out";
     case BLK_ERR_POSITION: return "a position id was outside [0, max_ctx) and was clamped";
     case BLK_ERR_TOKEN: return "a token id was outside [0, vocab) (embedding row zeroed)";
+    case BLK_ERR_PAGE:
+      return "a sequence of a paged batch was refused (rows, length or pages do not fit)";
     case BLK_ERR_DEVICE: return "the current GPU is not sm_103 (GB300)";
     case BLK_ERR_SCRATCH_LIMIT:
       return "the shape needs more decode scratch than blk_decode_static's fixed 1 MiB array";
@@ -1312,6 +1751,8 @@ cudaError_t configure_kernels() {
   if (e == cudaSuccess) e = configure_prefill_attn();
   if (e == cudaSuccess) e = configure_lm_head();
   if (e == cudaSuccess) e = configure_decode_attn_batch();
+  if (e == cudaSuccess) e = configure_paged_few();
+  if (e == cudaSuccess) e = configure_paged_many();
   return e;
 }
 }  // namespace blk

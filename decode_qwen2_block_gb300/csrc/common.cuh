@@ -12,6 +12,7 @@ namespace blk {
 constexpr int kDevTimeout = 1;
 constexpr int kDevPosition = 2;
 constexpr int kDevToken = 3;     // a token id outside [0, vocab)
+constexpr int kDevPage = 4;      // a paged batch: pages, lengths or row ranges do not fit
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;

@@ -847,7 +847,7 @@ cudaError_t launch_splitk_reduce(const TcGemmParams& p, int num_sms, cudaStream_
 }
 
 cudaError_t launch_qkv_finish(const TcGemmParams& p, cudaStream_t s) {
-  if (p.splits < 2 || p.splits > 16 || !p.part || p.D / 2 > 64) return cudaErrorInvalidValue;
+  if (p.splits < 1 || p.splits > 16 || !p.part || p.D / 2 > 64) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.Hq + 2 * p.Hkv, p.M);
   cfg.blockDim = dim3(p.D / 2);

@@ -1,0 +1,137 @@
+// Serving over a paged K/V cache: parameter blocks and launchers of the plan
+// (block tables, slot map), append and attention kernels.
+//
+// Pools: K and V each [n_pages][Hkv][page][D] fp16, page 16, 32, 64 or 128
+// slots.  Slot s of a sequence is slot s % page of page block_table[s / page].
+// Row t of sequence b (rows row_start[b] .. row_start[b + 1] - 1 of the batch)
+// sits in slot cache_lens[b] + t.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace blk {
+
+constexpr int kMaxSeqs = 4096;      // sequences of one batch
+
+// ------------------------------------------------------- plan and append
+struct PagePlanParams {
+  const int64_t* cache_lens;   // [B]
+  const int64_t* new_lens;     // [B], null: one each
+  const int32_t* free_pages;   // [n_free]
+  int32_t* table;              // [B][max_blocks]
+  int64_t* row_start;          // [B + 1]
+  int64_t* slot_map;           // [N]
+  int64_t* pos;                // [N]
+  int64_t* used;               // [1]
+  int64_t max_blocks, n_free, N;
+  int B, page_lg;
+  int* err;
+};
+cudaError_t launch_page_plan(const PagePlanParams& p, int num_sms, cudaStream_t s, bool pdl);
+
+struct PageAppendParams {
+  const __half* k;             // row r, head h at r * row_stride + h * head_stride
+  const __half* v;
+  int64_t row_stride, head_stride;
+  const int64_t* slot_map;     // [N]
+  __half* k_pages;
+  __half* v_pages;
+  int64_t n_slots;             // n_pages * page
+  int N, Hkv, D, page_lg;
+  int* err;
+};
+cudaError_t launch_page_append(const PageAppendParams& p, int num_sms, cudaStream_t s, bool pdl);
+
+// -------------------------------------------------------------- attention
+// A kernel's CTAs share the batch's K/V tiles evenly: the tiles of every unit
+// (a group of rows of one sequence and one kv head) are numbered in one line
+// and CTA i takes tiles [i T / n, (i + 1) T / n).  A unit inside one CTA is
+// finished there; of a cut unit every CTA leaves a partial (its unnormalised
+// O, maximum m in log2 units and sum l, fp32) in one of its two slots: slot 0
+// when the piece opens the CTA's range, else slot 1.
+struct PagedPiece {            // what merging needs of one cut unit
+  int c0, c1;                  // CTAs that hold its pieces, in order (c0 = -1: none)
+  int s0;                      // slot of the piece in c0 (0 in the others)
+  int rows;                    // partial rows of the unit
+  int r0;                      // batch row of its first token
+  int g;                       // kv head
+};
+
+struct PagedAttnParams {
+  CUtensorMap tm_k, tm_v;      // pools (few rows: boxes of one page or 64 slots, all of D;
+                               //   many rows: 64 columns of one page or 128 slots)
+  CUtensorMap tm_q;            // many rows: q as (D, Hq, N), box (64, G, tokens)
+  const __half* q;             // row r at r * q_stride: [Hq][D]
+  int64_t q_stride;
+  __half* out;                 // row r at r * out_stride
+  int64_t out_stride;
+  const int64_t* row_start;    // [B + 1]
+  const int64_t* cache_lens;   // [B]
+  const int32_t* table;        // [B][max_blocks]
+  const int32_t* prefix_pages; // [prefix_len / page] or null
+  int64_t max_blocks, n_pages, window;
+  int64_t max_len;             // slots of the longest sequence, new ones with it; it fits the
+                               //   table's rows and 31 bits
+  int64_t prefix_len;          // slots below it are the shared prefix's
+  int B, N, Hq, Hkv, D, G, page_lg, max_new;
+  float scale_log2;
+  int nc;                      // CTAs of the kernel
+  int slot_rows;               // partial rows of one slot
+  float* part;                 // [nc][2][slot_rows][D]
+  float2* ml;                  // [nc][2][slot_rows] (m, l)
+  PagedPiece* cut;             // [nc]: the unit that begins in CTA i and goes on behind it
+  // shared prefix: own parts are merged with the prefix's, so whole units
+  // leave their (O, m, l) by row and head, and every row says where its own
+  // part is
+  float* own;                  // [N][Hq][D]
+  float2* own_ml;              // [N][Hq]
+  int4* row_info;              // [N][Hkv]: c0 (-1 whole, -2 no part), c1, s0, partial row of head 0
+  int* err;
+};
+
+// Rows of one unit that the few-row kernel takes (16 per MMA row tile).
+constexpr int kPagedFewRows = 64;
+bool paged_few_rows(int G, int64_t max_new);
+size_t paged_few_part_rows(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows);
+cudaError_t launch_paged_few(const PagedAttnParams& p, cudaStream_t s, bool pdl);
+cudaError_t configure_paged_few();
+
+// Many rows: prompts and long runs of new tokens, and the shared prefix (its
+// rows are the whole batch's).  Units are 2 blocks of 128 / G tokens.
+struct PagedUnit {             // own parts: written by the schedule kernel
+  int b, tok, ntok, r0;        // sequence, first token, tokens, batch row of that token
+  int L, n, lo, hi;            // the sequence's; slots that some row sees: [lo, hi)
+};
+struct PagedManyParams {
+  PagedAttnParams a;
+  int prefix;                  // 1: the shared prefix's parts, of all N rows
+  int btok;                    // tokens of a block
+  int units;                   // prefix: units of one kv head; own: at most this many
+  const int64_t* pref;         // own: [units + 1] tiles before each unit; pref[-1]: how many
+  const PagedUnit* unit;       // own: [units]
+};
+inline int paged_btok(int G) { return 128 / G; }
+constexpr int kPagedManyRows = 256;     // partial rows of a slot
+constexpr int kPagedManyTile = 128;     // slots of a tile
+cudaError_t launch_paged_sched(const PagedManyParams& p, int64_t* pref, PagedUnit* unit,
+                               cudaStream_t s, bool pdl);
+cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl);
+cudaError_t configure_paged_many();
+
+// Merges cut units (and, with a prefix, every row's own and prefix parts).
+struct PagedMergeParams {
+  PagedAttnParams a;           // the own parts
+  int prefix;                  // 1: merge by rows with the prefix's partials
+  int own_btok;                // tokens of a block of 128 partial rows (few rows: all of them)
+  const float* pre_part;       // prefix partials [pre_nc][2][pre_rows][D]
+  const float2* pre_ml;
+  const float* pre_own;        // prefix parts of units inside one CTA, by row and head
+  const float2* pre_own_ml;
+  int pre_nc, pre_rows, pre_units, pre_tiles, pre_tok, pre_btok;
+};
+cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStream_t s);
+
+}  // namespace blk

@@ -1,0 +1,764 @@
+// Attention over a paged K/V cache for few new rows per sequence (decode, or a
+// few drafted tokens): at most 64 rows (token, query head of the kv head's
+// group) of one sequence share a pass over its K/V.
+//
+//   out[r, h] = softmax(q[r, h] . K / sqrt(D)) V  over the slots row r sees,
+//   [max(0, p - W + 1), p] for a row in slot p (W the window, 0 = all).
+//
+// Bound by memory: every K/V byte is read once for all rows of the unit.  The
+// batch is ragged and its lengths live on the device, so the CTAs cut the
+// line of all units' 64-slot tiles into equal ranges (see paged.h) instead of
+// splitting every sequence alike: each sums the sequences' tile counts itself
+// (B <= 4096 lengths), finds its range and walks it.
+//   warp 4     producer: walks (kv head, sequence, tile), looks up the pages and
+//              copies K and V boxes of one page (at most 64 slots, all of D) by
+//              TMA with the 128-byte swizzle; the unit's q rows come with its
+//              first tile as bulk copies into rows padded by 16 bytes.
+//   warps 0-3  16 slots each: S = Q K^T by mma.sync m16n8k16 (the rows are the M
+//              side: at most 64, a tcgen05 MMA's 128 rows would be padding),
+//              the row maxima meet in shared memory, P (fp16, in [0, 1]: the
+//              rounding is at most 2^-11 of a weight) goes there too, and each
+//              warp forms O for its quarter of the columns over all 64 slots.
+//              So a unit's end needs no merge of O between warps, which with
+//              short sequences would cost more than their tiles.
+// Slots of a tile that no row of the unit sees (behind the last, before the
+// first window, pages that were not loaded) have their V rows zeroed in shared
+// memory: 0 * NaN would reach O.  Every wait is bounded.
+#include <math.h>
+
+#include "common.cuh"
+#include "paged.h"
+#include "paged_dev.cuh"
+
+namespace blk {
+namespace {
+
+constexpr int kTile = 64;            // slots of a tile
+constexpr int kConsumers = 128, kThreads = 160;
+constexpr int kMinTiles = 2;         // tiles that a CTA takes at least, where there are any
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Box (0, 0, 0, z) at slot y of a page: all D / 64 halves of the page's slots.
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int y, int z,
+                                         uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(0), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void st_zero16(uint32_t addr) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+
+struct TileInfo {      // what the consumers need of a tile
+  int slot0;           // its first slot
+  int lo, hi;          // slots that some row of the unit sees: [lo, hi)
+  int L, n;            // the unit's history and new tokens
+  int r0, g;           // its first batch row, its kv head
+  int flags;           // 1 first tile of the piece, 2 last, 4 end of the CTA's range
+  int dst;             // -1 the whole unit, else the partial slot
+};
+
+template <int D, int MT>
+struct FSmem {
+  static constexpr int kKV = kTile * D * 2;                     // K or V of a tile
+  static constexpr int kStages = (MT == 4 ? 65536 : 98304) / (2 * kKV);
+  static constexpr int kQBufs = MT == 1 ? 2 : 1;
+  static constexpr int kQStride = D * 2 + 16;                   // bytes (conflict-free ldmatrix)
+  static constexpr int kQBytes = 16 * MT * kQStride;
+  static constexpr int kPStride = kTile * 2 + 16;
+  static constexpr int kQOff = kStages * 2 * kKV;
+  static constexpr int kPOff = kQOff + kQBufs * kQBytes;
+  static constexpr int kStatOff = kPOff + 16 * MT * kPStride;   // [4 warps][16 MT] floats
+  static constexpr int kInfoOff = kStatOff + 4 * 16 * MT * 4;
+  static constexpr int kBarOff = (kInfoOff + kStages * (int)sizeof(TileInfo) + 15) / 16 * 16;
+  static constexpr int kEnd = kBarOff + (2 * kStages + 2 * kQBufs) * 8 + 64;
+  static constexpr size_t kBytes = (size_t)kEnd + 1024;         // the ring is 1024-aligned
+};
+
+__device__ __forceinline__ int seq_tiles(const PagedAttnParams& p, const PagedSeq& s) {
+  if (s.n == 0) return 0;
+  return (s.L + s.n + kTile - 1) / kTile - paged_lo(p, s.L) / kTile;
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_few_kernel(const __grid_constant__ PagedAttnParams p) {
+  using Sm = FSmem<D, MT>;
+  constexpr int S = Sm::kStages, QB = Sm::kQBufs;
+  constexpr int kCPR = D / 8;           // 16-byte pieces of a row
+  constexpr int kNT = D / 32;           // 8-column tiles of O per warp
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring = smem_u32(smem), qbase = smem_u32(smem + Sm::kQOff),
+                 pbase = smem_u32(smem + Sm::kPOff);
+  float* stat = reinterpret_cast<float*>(smem + Sm::kStatOff);
+  volatile TileInfo* infos = reinterpret_cast<volatile TileInfo*>(smem + Sm::kInfoOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Sm::kBarOff);
+  uint64_t* empty = full + S;
+  uint64_t* q_empty = empty + S;
+  __shared__ int64_t wsum[kThreads / 32];
+  __shared__ int start_b;
+  __shared__ int64_t start_cum;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  griddep_wait();
+  griddep_launch();
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);
+    }
+    for (int s = 0; s < QB; ++s) mbar_init(&q_empty[s], 4);
+    fence_mbar_init();
+    start_b = 0;
+    start_cum = 0;
+  }
+  // tiles of all sequences (one kv head), and those before this thread's
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int64_t mine = 0;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const PagedSeq s = load_seq(p, b);
+    mine += seq_tiles(p, s);
+    bad |= s.bad;
+  }
+  if (bad && blockIdx.x == 0) set_error(p.err, kDevPage);
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, T1 = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += wsum[w];
+    T1 += wsum[w];
+  }
+  before += inc - mine;
+  const int64_t T = T1 * p.Hkv;
+  const int64_t enough = (T + kMinTiles - 1) / kMinTiles;
+  const int nc = (int)(enough < p.nc ? (enough < 1 ? 1 : enough) : p.nc);
+  const int cta = blockIdx.x;
+  const int64_t t0 = cta < nc ? T * cta / nc : T, t1 = cta < nc ? T * (cta + 1) / nc : T;
+  if (t0 >= t1) {   // (uniform over the CTA)
+    if (tid == 0) p.cut[cta].c0 = -1;
+    return;
+  }
+  const int64_t x0 = t0 % T1;
+  if (mine > 0 && before <= x0 && x0 < before + mine) {
+    int64_t cum = before;
+    int b = b0;
+    for (;; ++b) {
+      const int nt = seq_tiles(p, load_seq(p, b));
+      if (x0 < cum + nt) break;
+      cum += nt;
+    }
+    start_b = b;
+    start_cum = cum;
+  }
+  __syncthreads();
+
+  if (warp == 4) {
+    // -------------------------------------------------------------- producer
+    const int bs_lg = p.page_lg < 6 ? p.page_lg : 6, bs = 1 << bs_lg;   // slots of a box
+    const int boxes = kTile >> bs_lg;
+    const uint32_t box_bytes = (uint32_t)bs * D * 2;
+    int b = start_b, g = (int)(t0 / T1);
+    int64_t cum = start_cum, lin = t0;
+    int it = 0, seg = 0, base32 = -1;
+    PagedSeq mys = {};
+    bool ok = true;
+    PagedPiece cut;
+    cut.c0 = -1;
+    while (lin < t1 && ok) {
+      if (b >= p.B) {        // the next kv head begins again with the first sequence
+        b = 0;
+        cum = 0;
+        ++g;
+      }
+      if ((b & ~31) != base32) {
+        base32 = b & ~31;
+        if (base32 + lane < p.B) mys = load_seq(p, base32 + lane);
+        else mys = PagedSeq{};
+      }
+      PagedSeq s;
+      s.r0 = __shfl_sync(0xffffffffu, mys.r0, b & 31);
+      s.n = __shfl_sync(0xffffffffu, mys.n, b & 31);
+      s.L = __shfl_sync(0xffffffffu, mys.L, b & 31);
+      const int nt = seq_tiles(p, s);
+      if (nt == 0) {
+        ++b;
+        continue;
+      }
+      const int64_t us = (int64_t)g * T1 + cum;      // the unit's first tile in the line
+      const int xa = (int)(lin - us), xb = (int)min((int64_t)nt, t1 - us);
+      const bool whole = xa == 0 && xb == nt;
+      const int dst = whole ? -1 : (lin == t0 ? 0 : 1);
+      if (xa == 0) {
+        const int c1 = whole ? cta : (int)(((us + nt) * nc - 1) / T);
+        if (!whole) {
+          cut.c0 = cta;
+          cut.c1 = c1;
+          cut.s0 = dst;
+          cut.rows = s.n * p.G;
+          cut.r0 = s.r0;
+          cut.g = g;
+        }
+        if (p.row_info)
+          for (int t = lane; t < s.n; t += 32)
+            p.row_info[(int64_t)(s.r0 + t) * p.Hkv + g] =
+                make_int4(whole ? -1 : cta, c1, whole ? 0 : dst, t * p.G);
+      }
+      const int lo = paged_lo(p, s.L), hi = s.L + s.n, j0 = lo / kTile;
+      const int32_t* row = p.table + (int64_t)b * p.max_blocks;
+      const int qb = seg % QB;
+      for (int x = xa; x < xb; ++x, ++it) {
+        const int st = it % S;
+        const int slot0 = (j0 + x) * kTile;
+        // box i of the tile: slots slot0 + i * bs ..; lanes 0-15 take K, 16-31 V
+        const int i = lane & 15, first = slot0 + (i << bs_lg);
+        const bool take = i < boxes && first < hi && first + bs > lo;
+        int64_t page = -1;
+        if (take) page = row[first >> p.page_lg];
+        const bool in = page >= 0 && page < p.n_pages;
+        if (take && !in) set_error(p.err, kDevPage);
+        if (it >= S && !mbar_wait(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
+        if (x == xa && seg >= QB &&
+            !mbar_wait(&q_empty[qb], (uint32_t)(seg / QB - 1) & 1u, p.err))
+          ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const unsigned m = __ballot_sync(0xffffffffu, take);
+        const int qrows = x == xa ? s.n * p.G : 0;
+        if (lane == 0) {
+          volatile TileInfo& f = infos[st];
+          f.slot0 = slot0;
+          f.lo = lo;
+          f.hi = hi;
+          f.L = s.L;
+          f.n = s.n;
+          f.r0 = s.r0;
+          f.g = g;
+          f.flags = (x == xa ? 1 : 0) | (x == xb - 1 ? 2 : 0);
+          f.dst = dst;
+          mbar_arrive_expect_tx(&full[st], __popc(m) * box_bytes + qrows * D * 2);
+        }
+        __syncwarp();
+        if (take) {
+          const uint32_t to = ring + st * 2 * Sm::kKV + (lane < 16 ? 0 : Sm::kKV) + i * box_bytes;
+          // a bad page reads as zeros: the coordinate lies behind the pool
+          const int z = in ? (int)(page * p.Hkv + g) : (int)(p.n_pages * p.Hkv);
+          tma_page(to, lane < 16 ? &p.tm_k : &p.tm_v, first & ((1 << p.page_lg) - 1), z,
+                   &full[st]);
+        }
+        for (int r = lane; r < qrows; r += 32) {
+          const int t = r / p.G, hh = r - t * p.G;
+          bulk_g2s(smem + Sm::kQOff + qb * Sm::kQBytes + r * Sm::kQStride,
+                   p.q + (int64_t)(s.r0 + t) * p.q_stride + (int64_t)(g * p.G + hh) * D, D * 2,
+                   &full[st]);
+        }
+      }
+      lin = us + xb;
+      cum += nt;
+      ++b;
+      ++seg;
+    }
+    if (lane == 0) {
+      volatile PagedPiece& c = p.cut[cta];
+      c.c1 = cut.c1;
+      c.s0 = cut.s0;
+      c.rows = cut.rows;
+      c.r0 = cut.r0;
+      c.g = cut.g;
+      c.c0 = ok ? cut.c0 : -1;
+    }
+    const int st = it % S;
+    if (ok && it >= S && !mbar_wait(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      if (lane == 0) {
+        infos[st].flags = 4;
+        mbar_arrive(&full[st]);
+      }
+    } else {
+      // copies in flight land before shared memory goes away
+      for (int k = max(0, it - S); k < it; ++k)
+        mbar_wait(&full[k % S], (uint32_t)(k / S) & 1u, nullptr);
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- consumers
+  const int grp = lane >> 2, tig = lane & 3;
+  const int bs_lg = p.page_lg < 6 ? p.page_lg : 6;
+  const int slab = warp * 16;
+  const float sl2 = p.scale_log2;
+  float m_r[MT][2], l_r[MT][2], O[MT][kNT][4];
+  int last[MT][2], low[MT][2];
+  int seg = 0;
+  // byte offset of (slot row r of the tile, 16-byte piece c) in a K or V tile of
+  // boxes [D / 64][bs slots][128 B] with the 128-byte swizzle
+  auto tile_off = [&](int r, int c) -> uint32_t {
+    const int box = r >> bs_lg, rr = r & ((1 << bs_lg) - 1);
+    return (uint32_t)(((box * (D / 64) + (c >> 3)) << (bs_lg + 7)) + rr * 128 +
+                      (((c & 7) ^ (rr & 7)) << 4));
+  };
+  for (int it = 0;; ++it) {
+    const int st = it % S;
+    bool ok = mbar_wait(&full[st], (uint32_t)(it / S) & 1u, p.err);
+    ok = __all_sync(0xffffffffu, ok);
+    // the four warps agree on giving up: none stays behind at a barrier
+    int give_up;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\t"
+        "bar.red.popc.u32 %0, 1, %2, a;\n\t}"
+        : "=r"(give_up)
+        : "r"(ok ? 0 : 1), "r"(kConsumers)
+        : "memory");
+    if (give_up) return;
+    const int flags = infos[st].flags;
+    if (flags & 4) return;
+    const int slot0 = infos[st].slot0, n = infos[st].n;
+    const int vlo = max(0, infos[st].lo - slot0), vhi = min(kTile, infos[st].hi - slot0);
+    const uint32_t kb = ring + st * 2 * Sm::kKV, vb = kb + Sm::kKV;
+    if (flags & 1) {
+      const int L = infos[st].L;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const int row = mt * 16 + grp + 8 * h2;
+          last[mt][h2] = L + min(row / p.G, n - 1);
+          low[mt][h2] = (int)window_lo(p.window, last[mt][h2]);
+          m_r[mt][h2] = -INFINITY;
+          l_r[mt][h2] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kNT; ++i) O[mt][i][2 * h2] = O[mt][i][2 * h2 + 1] = 0.f;
+        }
+    }
+    const uint32_t qs = qbase + (seg % QB) * Sm::kQBytes;
+    const bool active = slab < vhi && slab + 16 > vlo;
+    float sc[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) sc[mt][k][0] = sc[mt][k][1] = sc[mt][k][2] = sc[mt][k][3] = 0.f;
+    const int mm = lane >> 3;
+    if (active) {
+      // S = Q K^T of this warp's 16 slots
+      const int kr = slab + (mm >> 1) * 8 + (lane & 7);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t bk[4];
+        ldsm_x4(kb + tile_off(kr, ks * 2 + (mm & 1)), bk);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t a[4];
+          ldsm_x4(qs + (mt * 16 + (mm & 1) * 8 + (lane & 7)) * Sm::kQStride +
+                      (ks * 16 + (mm >> 1) * 8) * 2, a);
+          mma16816(sc[mt][0], a, bk[0], bk[1]);
+          mma16816(sc[mt][1], a, bk[2], bk[3]);
+        }
+      }
+    }
+    // scores in log2 units, -inf where the row does not see the slot
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = slab + k * 8 + 2 * tig + (e & 1), slot = slot0 + c, h2 = e >> 1;
+          const bool seen = c >= vlo && slot <= last[mt][h2] && slot >= low[mt][h2];
+          sc[mt][k][e] = active && seen ? sc[mt][k][e] * sl2 : -INFINITY;
+          mx[h2] = fmaxf(mx[h2], sc[mt][k][e]);
+        }
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        mx[h2] = fmaxf(mx[h2], __shfl_xor_sync(0xffffffffu, mx[h2], 1));
+        mx[h2] = fmaxf(mx[h2], __shfl_xor_sync(0xffffffffu, mx[h2], 2));
+        if (tig == 0) stat[warp * 16 * MT + mt * 16 + grp + 8 * h2] = mx[h2];
+      }
+    }
+    named_sync(1, kConsumers);
+    if ((flags & 2) && lane == 0) mbar_arrive(&q_empty[seg % QB]);   // q has been used
+    float corr[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        const int row = mt * 16 + grp + 8 * h2;
+        float mx = m_r[mt][h2];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mx = fmaxf(mx, stat[w * 16 * MT + row]);
+        corr[mt][h2] = mx == -INFINITY ? 1.f : exp2f(m_r[mt][h2] - mx);
+        m_r[mt][h2] = mx;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float pv[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float s = sc[mt][k][2 * h2 + e];
+            pv[e] = s == -INFINITY ? 0.f : exp2f(s - mx);
+            sum += pv[e];
+          }
+          const __half2 ph = __floats2half2_rn(pv[0], pv[1]);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(pbase + row * Sm::kPStride +
+                                                      (slab + k * 8 + 2 * tig) * 2),
+                       "r"(*reinterpret_cast<const uint32_t*>(&ph))
+                       : "memory");
+        }
+        l_r[mt][h2] = l_r[mt][h2] * corr[mt][h2] + sum;
+      }
+    if (active && (slab < vlo || slab + 16 > vhi)) {
+      for (int i = lane; i < 16 * kCPR; i += 32) {
+        const int r = slab + i / kCPR;
+        if (r < vlo || r >= vhi) st_zero16(vb + tile_off(r, i % kCPR));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before a later copy there
+    }
+    named_sync(1, kConsumers);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < kNT; ++i) {
+        O[mt][i][0] *= corr[mt][0];
+        O[mt][i][1] *= corr[mt][0];
+        O[mt][i][2] *= corr[mt][1];
+        O[mt][i][3] *= corr[mt][1];
+      }
+    // O += P V for this warp's D / 4 columns
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      if (ks * 16 >= vhi || ks * 16 + 16 <= vlo) continue;
+      uint32_t bv[kNT / 2][4];
+      const int vr = ks * 16 + (mm & 1) * 8 + (lane & 7);
+#pragma unroll
+      for (int i = 0; i < kNT / 2; ++i)
+        ldsm_x4_t(vb + tile_off(vr, warp * kNT + 2 * i + (mm >> 1)), bv[i]);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t a[4];
+        ldsm_x4(pbase + (mt * 16 + (mm & 1) * 8 + (lane & 7)) * Sm::kPStride +
+                    (ks * 16 + (mm >> 1) * 8) * 2, a);
+#pragma unroll
+        for (int i = 0; i < kNT / 2; ++i) {
+          mma16816(O[mt][2 * i], a, bv[i][0], bv[i][1]);
+          mma16816(O[mt][2 * i + 1], a, bv[i][2], bv[i][3]);
+        }
+      }
+    }
+    if (flags & 2) {
+      // the piece's end: the warps' sums of l meet, then rows go out
+      const int rows = n * p.G, r0 = infos[st].r0, g = infos[st].g, dst = infos[st].dst;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          float l = l_r[mt][h2];
+          l += __shfl_xor_sync(0xffffffffu, l, 1);
+          l += __shfl_xor_sync(0xffffffffu, l, 2);
+          if (tig == 0) stat[warp * 16 * MT + mt * 16 + grp + 8 * h2] = l;
+        }
+      named_sync(1, kConsumers);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const int row = mt * 16 + grp + 8 * h2;
+          if (row >= rows) continue;
+          float l = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) l += stat[w * 16 * MT + row];
+          const int t = row / p.G, hq = g * p.G + (row - t * p.G);
+          const int col = warp * (D / 4) + 2 * tig;
+          if (dst < 0 && !p.own) {
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            __half* o = p.out + (int64_t)(r0 + t) * p.out_stride + (int64_t)hq * D + col;
+#pragma unroll
+            for (int i = 0; i < kNT; ++i)
+              *reinterpret_cast<__half2*>(o + i * 8) =
+                  __floats2half2_rn(O[mt][i][2 * h2] * inv, O[mt][i][2 * h2 + 1] * inv);
+          } else {
+            const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
+                                       : ((int64_t)cta * 2 + dst) * p.slot_rows + row;
+            float* o = (dst < 0 ? p.own : p.part) + at * D + col;
+#pragma unroll
+            for (int i = 0; i < kNT; ++i)
+              *reinterpret_cast<float2*>(o + i * 8) =
+                  make_float2(O[mt][i][2 * h2], O[mt][i][2 * h2 + 1]);
+            if (warp == 0 && tig == 0)
+              (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(m_r[mt][h2], l);
+          }
+        }
+      ++seg;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+  }
+}
+
+// ------------------------------------------------------------------- merging
+// A row's result from its pieces: sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
+// with M = max_c m_c, pieces in their order.  Block = 64 threads of two or one
+// columns by 4 groups that each take a quarter of the pieces (a long sequence
+// alone on the GPU is cut into 150 of them); the groups' sums are added in
+// order, so the bits do not depend on timing.
+template <int D>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedMergeParams q) {
+  constexpr int kV = D / 64;                 // columns per thread
+  const PagedAttnParams& p = q.a;
+  __shared__ float sacc[4][D + 2];
+  __shared__ PagedPiece cuts[512];
+  __shared__ int cut_row[512], wsum[8];
+  griddep_wait();
+  griddep_launch();
+  const int tid = threadIdx.x, grp = tid >> 6, c = (tid & 63) * kV;
+  int64_t items;
+  if (!q.prefix) {
+    // rows of the cut units before each CTA's (two CTAs a thread; nc <= 512)
+    int n2[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 2 * tid + k;
+      if (i < p.nc) {
+        cuts[i] = p.cut[i];
+        n2[k] = cuts[i].c0 >= 0 ? cuts[i].rows : 0;
+      }
+    }
+    int x = n2[0] + n2[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if ((tid & 31) >= o) x += y;
+    }
+    if ((tid & 31) == 31) wsum[tid >> 5] = x;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w < (tid >> 5)) x += wsum[w];
+      all += wsum[w];
+    }
+    cut_row[2 * tid] = x - n2[0] - n2[1];
+    cut_row[2 * tid + 1] = x - n2[1];
+    __syncthreads();
+    items = all;
+  } else {
+    items = (int64_t)p.N * p.Hq;
+  }
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    // pieces: own ones in slots of CTAs c0..c1 (or a whole one), then the prefix's
+    int c0, c1, s0, row, r, hq, pc0 = 0, pc1 = -1, ps0 = 0, prow = 0;
+    bool own_whole = false, pre_whole = false;
+    if (!q.prefix) {
+      int lo = 0, hi = p.nc;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cut_row[mid] <= item) lo = mid; else hi = mid;
+      }
+      const PagedPiece& u = cuts[lo];
+      const int tl = ((int)item - cut_row[lo]) / p.G, hh = (int)item - cut_row[lo] - tl * p.G;
+      c0 = u.c0;
+      c1 = u.c1;
+      s0 = u.s0;
+      row = tl / q.own_btok * 128 + tl % q.own_btok * p.G + hh;
+      r = u.r0 + tl;
+      hq = u.g * p.G + hh;
+    } else {
+      r = (int)(item / p.Hq);
+      hq = (int)(item - (int64_t)r * p.Hq);
+      const int g = hq / p.G, hh = hq - g * p.G;
+      const int4 f = p.row_info[(int64_t)r * p.Hkv + g];
+      if (f.x == -2) continue;               // a row behind the batch, or refused
+      own_whole = f.x == -1;
+      c0 = f.x;
+      c1 = f.y;
+      s0 = f.z;
+      row = f.w + hh;
+      // the prefix's unit of this row: pre_tok tokens in blocks of pre_btok
+      const int u = r / q.pre_tok, tl = r - u * q.pre_tok;
+      const int64_t us = ((int64_t)g * q.pre_units + u) * q.pre_tiles;
+      const int64_t T = (int64_t)p.Hkv * q.pre_units * q.pre_tiles;
+      pc0 = (int)(((us + 1) * q.pre_nc - 1) / T);
+      pc1 = (int)(((us + q.pre_tiles) * q.pre_nc - 1) / T);
+      pre_whole = pc0 == pc1;
+      ps0 = T * pc0 / q.pre_nc == us ? 0 : 1;
+      prow = tl / q.pre_btok * 128 + tl % q.pre_btok * p.G + hh;
+    }
+    const int n_own = own_whole ? 1 : c1 - c0 + 1;
+    const int n_all = n_own + (q.prefix ? pc1 - pc0 + 1 : 0);
+    auto piece = [&](int i, const float*& o, float2& ml) {
+      if (i < n_own) {
+        const int64_t at = own_whole ? (int64_t)r * p.Hq + hq
+                                     : ((int64_t)(c0 + i) * 2 + (i == 0 ? s0 : 0)) * p.slot_rows + row;
+        o = (own_whole ? p.own : p.part) + at * D;
+        ml = __ldcg((own_whole ? p.own_ml : p.ml) + at);
+      } else {
+        const int k = i - n_own;
+        const int64_t at = pre_whole ? (int64_t)r * p.Hq + hq
+                                     : ((int64_t)(pc0 + k) * 2 + (k == 0 ? ps0 : 0)) * q.pre_rows + prow;
+        o = (pre_whole ? q.pre_own : q.pre_part) + at * D;
+        ml = __ldcg((pre_whole ? q.pre_own_ml : q.pre_ml) + at);
+      }
+    };
+    const int i0 = grp * n_all / 4, i1 = (grp + 1) * n_all / 4;
+    float M = -INFINITY, l = 0.f, acc[kV];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) acc[k] = 0.f;
+    constexpr int kU = 4;                     // pieces' loads in flight
+    for (int i = i0; i < i1; i += kU) {
+      float v[kU][kV];
+      float2 ml[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (i + u < i1) {
+          const float* o;
+          piece(i + u, o, ml[u]);
+#pragma unroll
+          for (int k = 0; k < kV; ++k) v[u][k] = __ldcg(o + c + k);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (ml[u].x == -INFINITY) continue;
+        const float mn = fmaxf(M, ml[u].x);
+        const float so = M == -INFINITY ? 0.f : exp2f(M - mn), w = exp2f(ml[u].x - mn);
+        l = __fmaf_rn(w, ml[u].y, __fmul_rn(l, so));
+#pragma unroll
+        for (int k = 0; k < kV; ++k) acc[k] = __fmaf_rn(w, v[u][k], __fmul_rn(acc[k], so));
+        M = mn;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kV; ++k) sacc[grp][c + k] = acc[k];
+    if ((tid & 63) == 0) {
+      sacc[grp][D] = M;
+      sacc[grp][D + 1] = l;
+    }
+    __syncthreads();
+    if (grp == 0) {
+      float Mx = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) Mx = fmaxf(Mx, sacc[k][D]);
+      float lt = 0.f, o[kV];
+#pragma unroll
+      for (int k = 0; k < kV; ++k) o[k] = 0.f;
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) {
+        const float mg = sacc[gq][D];
+        const float w = mg == -INFINITY ? 0.f : exp2f(mg - Mx);
+        lt = __fmaf_rn(w, sacc[gq][D + 1], lt);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(w, sacc[gq][c + k], o[k]);
+      }
+      const float inv = lt > 0.f ? 1.f / lt : 0.f;
+      __half* d = p.out + (int64_t)r * p.out_stride + (int64_t)hq * D + c;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) d[k] = __float2half_rn(o[k] * inv);
+    }
+    __syncthreads();
+  }
+}
+
+template <int D, int MT>
+cudaError_t launch_few(const PagedAttnParams& p, cudaStream_t s, bool pdl) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.nc);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = FSmem<D, MT>::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_few_kernel<D, MT>, p);
+}
+
+template <int D, int MT>
+cudaError_t configure_one() {
+  return cudaFuncSetAttribute(paged_few_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)FSmem<D, MT>::kBytes);
+}
+
+int row_tiles(int slot_rows) { return slot_rows / 16; }
+
+}  // namespace
+
+bool paged_few_rows(int G, int64_t max_new) { return max_new * G <= kPagedFewRows; }
+
+size_t paged_few_part_rows(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows) {
+  const int64_t rows = max_new * G;
+  *nc = 2 * num_sms;
+  *slot_rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+  return (size_t)*nc * 2 * *slot_rows;
+}
+
+cudaError_t launch_paged_few(const PagedAttnParams& p, cudaStream_t s, bool pdl) {
+  if (p.max_new * p.G > p.slot_rows || p.nc < 1 || p.nc > 512) return cudaErrorInvalidValue;
+  const int mt = row_tiles(p.slot_rows);
+  if (p.D == 128)
+    return mt == 1 ? launch_few<128, 1>(p, s, pdl)
+                   : (mt == 2 ? launch_few<128, 2>(p, s, pdl) : launch_few<128, 4>(p, s, pdl));
+  if (p.D == 64)
+    return mt == 1 ? launch_few<64, 1>(p, s, pdl)
+                   : (mt == 2 ? launch_few<64, 2>(p, s, pdl) : launch_few<64, 4>(p, s, pdl));
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  const int64_t most = p.prefix ? (int64_t)p.a.N * p.a.Hq : (int64_t)p.a.nc * p.a.slot_rows;
+  const int64_t fit = (int64_t)num_sms * 8;
+  cfg.gridDim = dim3((unsigned)(most < fit ? most : fit));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (p.a.D == 128) return cudaLaunchKernelEx(&cfg, paged_merge_kernel<128>, p);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<64>, p);
+}
+
+cudaError_t configure_paged_few() {
+  cudaError_t e = configure_one<128, 1>();
+  if (e == cudaSuccess) e = configure_one<128, 2>();
+  if (e == cudaSuccess) e = configure_one<128, 4>();
+  if (e == cudaSuccess) e = configure_one<64, 1>();
+  if (e == cudaSuccess) e = configure_one<64, 2>();
+  if (e == cudaSuccess) e = configure_one<64, 4>();
+  return e;
+}
+
+}  // namespace blk

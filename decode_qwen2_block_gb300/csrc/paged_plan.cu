@@ -1,0 +1,215 @@
+// The bookkeeping of a paged K/V cache on the GPU: block tables, slot map and
+// positions of a step from the requests' lengths, and the copy of K/V rows
+// into their pages (the serving form of the KV append in the decoder block's
+// decode phase, §4 "three-phase split": new K/V follow the history).
+#include "common.cuh"
+#include "paged.h"
+
+namespace blk {
+namespace {
+
+constexpr int kPlanThreads = 512;
+
+// Exclusive sum over the block of one value per thread; `total` is the sum.
+__device__ __forceinline__ int64_t block_excl(int64_t v, int64_t* warp_sums, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();   // the sums of an earlier call have been read
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    const int64_t s = warp_sums[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+  return before + x - v;
+}
+
+// Last i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
+__device__ __forceinline__ int last_le(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// One step's plan.  With n_b new tokens after L_b slots, sequence b's rows
+// begin at sum of n over the sequences before it, it holds ceil(L_b / page)
+// pages and takes ceil((L_b + n_b) / page) less those from the free list,
+// beginning behind what the sequences before it took.  Both are sums over the
+// sequences, so every CTA forms them in shared memory by itself (B <= 4096
+// lengths, a few KB) and fills its share of the slots and table entries: one
+// launch, nothing waits on another CTA.  Pages of a row are formed from the
+// lengths and the free list, never read back from the table entries that this
+// launch writes.  Bound by latency: 64 decoding sequences are one CTA and
+// three round trips to L2.
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanParams p) {
+  extern __shared__ int sm[];
+  int* rs = sm;                  // [B + 1] first row, at most N
+  int* base = sm + p.B + 1;      // [B] first free page taken
+  uint8_t* bad = reinterpret_cast<uint8_t*>(base + p.B);   // [B] refused
+  __shared__ int64_t warp_sums[kPlanThreads / 32];
+  __shared__ int used_s;
+  griddep_wait();
+  griddep_launch();
+  const int tid = threadIdx.x;
+  const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  const int64_t cap = p.max_blocks << p.page_lg, mask = ((int64_t)1 << p.page_lg) - 1;
+  auto n_of = [&](int b) -> int64_t { return p.new_lens ? p.new_lens[b] : 1; };
+  if (tid == 0) used_s = 0;
+  int64_t rows = 0, total;
+  for (int b = b0; b < b1; ++b) {
+    const int64_t n = n_of(b);
+    rows += (n < 0 || n > p.N) ? 0 : n;
+  }
+  int64_t r = block_excl(rows, warp_sums, total);
+  int64_t need_sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int64_t n = n_of(b), L = p.cache_lens[b];
+    const bool n_ok = n >= 0 && n <= p.N;
+    const int64_t r1 = r + (n_ok ? n : 0);
+    const bool ok = n_ok && r1 <= p.N && L >= 0 && L <= cap && L + n <= cap;
+    rs[b] = (int)min(r, p.N);
+    bad[b] = !ok;
+    if (blockIdx.x == 0) p.row_start[b] = r;
+    if (ok) need_sum += ((L + n + mask) >> p.page_lg) - ((L + mask) >> p.page_lg);
+    r = r1;
+  }
+  if (tid == 0) {
+    rs[p.B] = (int)min(total, p.N);
+    if (blockIdx.x == 0) p.row_start[p.B] = total;
+  }
+  int64_t need_total;
+  int64_t take = block_excl(need_sum, warp_sums, need_total);
+  int top = 0;
+  bool any_bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const int64_t n = n_of(b), L = p.cache_lens[b];
+    const int64_t need =
+        bad[b] ? 0 : ((L + n + mask) >> p.page_lg) - ((L + mask) >> p.page_lg);
+    base[b] = (int)min(take, p.n_free);
+    if (need > 0) {
+      if (take + need > p.n_free) bad[b] = 1;
+      else top = (int)(take + need);
+    }
+    any_bad |= bad[b] != 0;
+    take += need;
+  }
+  if (top > 0) atomicMax(&used_s, top);
+  if (any_bad && blockIdx.x == 0) set_error(p.err, kDevPage);
+  __syncthreads();
+  const int used = used_s;
+  if (tid == 0 && blockIdx.x == 0) *p.used = used;
+  const int64_t gt = (int64_t)blockIdx.x * kPlanThreads + tid;
+  const int64_t gn = (int64_t)gridDim.x * kPlanThreads;
+  for (int64_t i = gt; i < p.N; i += gn) {
+    int64_t slot = -1, ps = 0;
+    if (i < rs[p.B]) {
+      const int b = last_le(rs, p.B, (int)i);
+      if (!bad[b]) {
+        const int64_t L = p.cache_lens[b];
+        ps = L + (i - rs[b]);
+        const int64_t blkno = ps >> p.page_lg, held = (L + mask) >> p.page_lg;
+        const int64_t pg = blkno < held ? p.table[(int64_t)b * p.max_blocks + blkno]
+                                        : p.free_pages[base[b] + (blkno - held)];
+        slot = pg < 0 ? -1 : (pg << p.page_lg) + (ps & mask);
+      }
+    }
+    p.slot_map[i] = slot;
+    p.pos[i] = ps;
+  }
+  for (int64_t u = gt; u < used; u += gn) {
+    const int b = last_le(base, p.B, (int)u);
+    const int64_t held = (p.cache_lens[b] + mask) >> p.page_lg;
+    p.table[(int64_t)b * p.max_blocks + held + (u - base[b])] = p.free_pages[u];
+  }
+}
+
+// Copies row r's K and V (Hkv heads of D) to slot slot_map[r].  A thread moves
+// the same 16 bytes of K and of V; bound by memory (2 x 2 x Hkv x D x 2 bytes a
+// row), kUnroll items in flight per thread.
+constexpr int kUnroll = 4;
+__global__ void __launch_bounds__(256) page_append_kernel(const PageAppendParams p) {
+  griddep_wait();
+  griddep_launch();
+  const int cpr = p.D >> 3;                       // 16-byte pieces of a head's row
+  const int per_row = p.Hkv * cpr;
+  const int64_t total = (int64_t)p.N * per_row;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  const int64_t mask = ((int64_t)1 << p.page_lg) - 1;
+  for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += step * kUnroll) {
+    uint4 kv[kUnroll], vv[kUnroll];
+    int64_t dst[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t i = i0 + u * step;
+      dst[u] = -1;
+      if (i < total) {
+        const int r = (int)(i / per_row), e = (int)(i - (int64_t)r * per_row);
+        const int h = e / cpr, c = e - h * cpr;
+        const int64_t slot = p.slot_map[r];
+        if (slot >= 0 && slot < p.n_slots) {
+          const int64_t pg = slot >> p.page_lg;
+          dst[u] = (((pg * p.Hkv + h) << p.page_lg) + (slot & mask)) * p.D + c * 8;
+          const int64_t src = r * p.row_stride + h * p.head_stride + c * 8;
+          kv[u] = *reinterpret_cast<const uint4*>(p.k + src);
+          vv[u] = *reinterpret_cast<const uint4*>(p.v + src);
+        } else if (slot != -1 && e == 0) {
+          set_error(p.err, kDevPage);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (dst[u] >= 0) {
+        *reinterpret_cast<uint4*>(p.k_pages + dst[u]) = kv[u];
+        *reinterpret_cast<uint4*>(p.v_pages + dst[u]) = vv[u];
+      }
+  }
+}
+
+template <typename K, typename P>
+cudaError_t launch(K kernel, int grid, int threads, size_t smem, cudaStream_t s, bool pdl,
+                   const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PagePlanParams& p, int num_sms, cudaStream_t s, bool pdl) {
+  // a CTA fills up to four slots a thread before another one pays
+  const int64_t want = (p.N + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  const int grid = (int)(want < 1 ? 1 : (want > num_sms ? num_sms : want));
+  const size_t smem = (size_t)(2 * p.B + 1) * sizeof(int) + p.B;   // 36 KB at 4096 sequences
+  return launch(page_plan_kernel, grid, kPlanThreads, smem, s, pdl, p);
+}
+
+cudaError_t launch_page_append(const PageAppendParams& p, int num_sms, cudaStream_t s, bool pdl) {
+  const int64_t total = (int64_t)p.N * p.Hkv * (p.D / 8);
+  const int64_t want = (total + 255) / 256, most = (int64_t)num_sms * 8;
+  const int grid = (int)(want < 1 ? 1 : (want > most ? most : want));
+  return launch(page_append_kernel, grid, 256, 0, s, pdl, p);
+}
+
+}  // namespace blk

@@ -13,9 +13,10 @@ import ctypes
 
 import torch
 
-from . import (BLK_ERR_SHAPE, BLK_OK, BlkError, Block, BlkQWeights, BlkWeights,
-               blk_decode_batch_stack, blk_decode_batch_stack_workspace_bytes, blk_decode_stack,
-               blk_decode_stack_q, blk_prefill_stack, blk_prefill_stack_workspace_bytes)
+from . import (BLK_ERR_CACHE_OVERFLOW, BLK_ERR_PAGE, BLK_ERR_SHAPE, BLK_OK, BlkError, Block,
+               BlkQWeights, BlkWeights, blk_decode_batch_stack,
+               blk_decode_batch_stack_workspace_bytes, blk_decode_stack, blk_decode_stack_q,
+               blk_prefill_stack, blk_prefill_stack_workspace_bytes, blk_step_paged_stack)
 
 
 class LayerStack:
@@ -161,6 +162,121 @@ class BatchStack:
         if rc != BLK_OK:
             raise BlkError(rc, "blk_decode_batch_stack")
         return out
+
+
+class PagedStack:
+    """Up to max_seqs sequences through a stack of decoder blocks over a paged
+    K/V cache: any number of new tokens per sequence and step (a prompt or a
+    chunk of it, drafts, one token), one library call for the step's plan
+    (blk_page_plan) and one for all layers (blk_step_paged_stack).
+
+    A sequence takes pages as it grows and gives them back with ``free``.
+    ``prefill_prefix`` computes a prefix that every sequence then begins with:
+    its pages are held once, and its keys are read once per step for the whole
+    batch.  The host knows the lengths it asked for, so no step waits for the
+    GPU."""
+
+    def __init__(self, shape, layer_weights, max_ctx: int, n_pages: int, page_size: int,
+                 max_seqs: int, max_rows: int, device="cuda"):
+        self.shape = shape
+        self.n_layers = len(layer_weights)
+        self.block = Block(shape, max_ctx, chain=True)
+        self.wdev = layer_weights
+        self.max_ctx, self.page, self.n_pages = max_ctx, page_size, n_pages
+        self.max_seqs, self.max_rows, self.device = max_seqs, max_rows, device
+        pool = (n_pages, shape.n_kv_heads, page_size, shape.head_dim)
+        self.pools = [(torch.zeros(pool, dtype=torch.float16, device=device),
+                       torch.zeros(pool, dtype=torch.float16, device=device))
+                      for _ in range(self.n_layers)]
+        self.max_blocks = -(-max_ctx // page_size)
+        self.table = torch.full((max_seqs, self.max_blocks), -1, dtype=torch.int32, device=device)
+        self.prefix = None                       # int32 pages of the shared prefix
+        self.prefix_ids: list[int] = []
+        self.lens = [0] * max_seqs               # slots of every sequence
+        self.pages: list[list[int]] = [[] for _ in range(max_seqs)]   # its own pages
+        self.free_ids = list(range(n_pages))
+        nbytes = self.block.step_paged_workspace_bytes(max_rows, max_seqs)
+        if nbytes == 0:
+            raise BlkError(BLK_ERR_SHAPE, "PagedStack: max_rows or max_seqs")
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        n = self.n_layers
+        self._w_arr = (BlkWeights * n)(*[Block.weights(w) for w in layer_weights])
+        self._k_arr = (ctypes.c_void_p * n)(*[k.data_ptr() for k, _ in self.pools])
+        self._v_arr = (ctypes.c_void_p * n)(*[v.data_ptr() for _, v in self.pools])
+
+    def _ints(self, values, dtype):
+        return torch.tensor(values, dtype=dtype).to(self.device, non_blocking=True)
+
+    def _run(self, table, lens, news, x, out, prefix, stream):
+        """Plans and runs one step of the sequences of `table`; returns (out, how many of
+        free_ids it took)."""
+        n, B = x.shape[0], len(lens)
+        need = [-(-(have + more) // self.page) - -(-have // self.page)
+                for have, more in zip(lens, news)]
+        if max(have + more for have, more in zip(lens, news)) > self.max_ctx:
+            raise BlkError(BLK_ERR_CACHE_OVERFLOW, "PagedStack.step")
+        if sum(need) > len(self.free_ids):
+            raise BlkError(BLK_ERR_PAGE, "PagedStack.step: no pages left")
+        if n != sum(news) or n > self.max_rows or min(news) < 0:
+            raise BlkError(BLK_ERR_SHAPE, "PagedStack.step: rows")
+        s = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(s):
+            i64 = torch.int64
+            lens_d, news_d = self._ints(lens, i64), self._ints(news, i64)
+            free_d = self._ints(self.free_ids[:sum(need)], torch.int32)
+            ints = torch.empty(2 * n + B + 2, dtype=i64, device=self.device)
+            slots, pos, used, start = ints.split((n, n, 1, B + 1))
+            out = torch.empty_like(x) if out is None else out
+            self.block.page_plan(self.page, lens_d, news_d, free_d, table, start, slots, pos, used,
+                                 stream=s)
+            batch = self.block.paged_batch(
+                start, lens_d, table, n, self.page, self.n_pages, max(news),
+                max(have + more for have, more in zip(lens, news)), prefix_pages=prefix)
+            self.block._paged_rows(batch, x, pos, slots, out)
+            rc = blk_step_paged_stack(self.block.handle, self._w_arr, self.n_layers, batch,
+                                      self._k_arr, self._v_arr, x.data_ptr(), pos.data_ptr(),
+                                      slots.data_ptr(), out.data_ptr(), self.ws.data_ptr(),
+                                      self.ws.numel(), s.cuda_stream)
+        if rc != BLK_OK:
+            raise BlkError(rc, "blk_step_paged_stack")
+        return out, need
+
+    def prefill_prefix(self, x, stream=None):
+        """Computes the shared prefix from its rows x (fp16 [P, hidden], P a multiple of
+        the page size) before any sequence has tokens; returns the last layer's rows."""
+        if any(self.lens) or self.prefix is not None or x.shape[0] % self.page:
+            raise BlkError(BLK_ERR_SHAPE, "PagedStack.prefill_prefix")
+        table = torch.full((1, self.max_blocks), -1, dtype=torch.int32, device=self.device)
+        out, need = self._run(table, [0], [x.shape[0]], x, None, None, stream)
+        self.prefix_ids = self.free_ids[:need[0]]
+        del self.free_ids[:need[0]]
+        s = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(s):
+            self.prefix = table[0, :need[0]].contiguous()
+            self.table[:, :need[0]] = self.prefix
+        self.lens = [x.shape[0]] * self.max_seqs
+        return out
+
+    def step(self, x, new_lens, out=None, stream=None):
+        """new_lens: new tokens of sequences 0, 1, ... (a list, at most max_seqs of them,
+        zeros allowed); x: fp16 [sum(new_lens), hidden], their rows back to back.
+        Returns the last layer's rows."""
+        B = len(new_lens)
+        if not 0 < B <= self.max_seqs or sum(new_lens) < 1:
+            raise BlkError(BLK_ERR_SHAPE, "PagedStack.step: new_lens")
+        out, need = self._run(self.table[:B], self.lens[:B], list(new_lens), x, out, self.prefix,
+                              stream)
+        for b, k in enumerate(need):
+            self.pages[b] += self.free_ids[:k]
+            del self.free_ids[:k]
+            self.lens[b] += new_lens[b]
+        return out
+
+    def free(self, b: int):
+        """Gives sequence b's own pages back; it begins anew behind the prefix."""
+        self.free_ids += self.pages[b]
+        self.pages[b] = []
+        self.lens[b] = len(self.prefix_ids) * self.page
 
 
 class QuantDecodeStack:

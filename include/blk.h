@@ -68,6 +68,8 @@ extern "C" {
 #define BLK_ERR_SCRATCH_LIMIT (-10)  /* shape needs more scratch than
                                         blk_decode_static's fixed array holds   */
 #define BLK_ERR_TOKEN (-11)          /* a token id outside [0, vocab)           */
+#define BLK_ERR_PAGE (-12)           /* a paged batch's sequence was refused:
+                                        its rows, length or pages do not fit    */
 
 /* Block shape.  Supported: head_dim 64 or 128; n_heads % n_kv_heads == 0 with
  * group size n_heads / n_kv_heads in {1, 2, 4, 6, 8, 16}; hidden a multiple
@@ -271,7 +273,8 @@ int blk_decode_static(blk_handle h, const blk_weights* w, const void* x,
 /* Synchronizes `stream`, then reports and clears the handle's device status
  * word: BLK_OK, BLK_ERR_DEVICE_TIMEOUT, BLK_ERR_POSITION (a kernel clamped
  * an out-of-range position id), BLK_ERR_TOKEN (blk_embed met an id outside
- * the vocabulary), or BLK_ERR_CUDA if the stream failed. */
+ * the vocabulary), BLK_ERR_PAGE (a paged call refused a sequence or met a bad
+ * page id), or BLK_ERR_CUDA if the stream failed. */
 int blk_check(blk_handle h, void* stream);
 
 /* Diagnostics of the failure path: launches one kernel that waits for the
@@ -292,7 +295,7 @@ int blk_wait_probe(blk_handle h, const void* flag, uint64_t limit_ns, void* stre
  * timed and blk_timing_collect returns BLK_ERR_WORKSPACE).  blk_timing_read
  * returns the totals of kernel id `kernel` (0 <= kernel < BLK_N_KERNELS) and
  * its name; BLK_ERR_SHAPE for an unknown id. */
-#define BLK_N_KERNELS 16
+#define BLK_N_KERNELS 24
 int blk_timing(blk_handle h, int on);
 int blk_timing_collect(blk_handle h, void* stream);
 int blk_timing_read(blk_handle h, int kernel, double* total_ms,
@@ -359,6 +362,118 @@ int blk_decode_batch_stack(blk_handle h, const blk_weights* w, int n_layers,
                            const int64_t* pos, const int64_t* cache_lens, int64_t B,
                            int64_t max_cache_len, void* out, void* ws, size_t ws_bytes,
                            void* stream);
+
+/* ---- paged K/V cache ---------------------------------------------------------
+ * Batched serving in which a sequence's slots lie in pages of a pool shared by
+ * all sequences, instead of max_ctx slots each: the K and V pools of a layer
+ * are device fp16 [n_pages][n_kv_heads][page_size][head_dim] (page_size 16, 32,
+ * 64 or 128), and slot s of sequence b is slot s % page_size of page
+ * block_table[b][s / page_size].  One block table serves every layer.  A step
+ * takes any number of new tokens per sequence: one (decode), a few (drafts to
+ * verify) or many (a chunk of a prompt), all sequences' rows back to back.
+ *
+ * Sequence b's rows are row_start[b] .. row_start[b + 1] - 1 of the batch; its
+ * t-th row sits in slot cache_lens[b] + t and sees slots
+ * [0, cache_lens[b] + t] (with blk_set_window the last W of them).  Lengths,
+ * row ranges and tables are read on the device, so a captured graph serves
+ * other lengths within the bounds of the batch.  A sequence whose row range,
+ * length or pages do not fit the batch is refused: its rows are not computed
+ * and the next blk_check reports BLK_ERR_PAGE; a page id outside the pool reads
+ * as zeros, is not written, and is reported likewise.
+ *
+ * Every call below returns BLK_OK, BLK_ERR_NULL, BLK_ERR_ALIGN, BLK_ERR_SHAPE (a
+ * size outside its range), BLK_ERR_CACHE_OVERFLOW, BLK_ERR_WORKSPACE or
+ * BLK_ERR_CUDA (also: the current device is not the handle's), checks before it
+ * enqueues anything, allocates nothing and is asynchronous on `stream`.  Calls
+ * in flight at the same time need workspaces of their own. */
+
+/* Block tables, slot map and positions of a step, on the GPU, from the
+ * requests' lengths:
+ *   cache_lens   device int64 [n_seqs] slots that each sequence holds
+ *   new_lens     device int64 [n_seqs] its new tokens (0 allowed), or NULL: 1 each
+ *   free_pages   device int32 [n_free] page ids to take, in order (NULL when n_free = 0)
+ *   block_table  device int32 [n_seqs][max_blocks]: entries [0, ceil(len / page_size))
+ *                are read, the entries that the new tokens need are written,
+ *                all others stay
+ *   row_start    device int64 [n_seqs + 1], written: sums of new_lens
+ *   slot_map     device int64 [n_rows], written: page * page_size + slot in the page
+ *   pos          device int64 [n_rows], written: the row's slot number
+ *   used         device int64 [1], written: how many of free_pages were taken
+ * n_rows (1 .. 2^20) is the size of the row arrays; rows at and behind
+ * row_start[n_seqs] get slot -1 and position 0 (a padded batch).  A sequence
+ * whose tokens do not fit n_rows, its table row or the free list (after those
+ * before it) takes no page and gets slots -1.  n_seqs is at most 4096. */
+int blk_page_plan(blk_handle h, int32_t page_size, int64_t n_seqs, const int64_t* cache_lens,
+                  const int64_t* new_lens, const int32_t* free_pages, int64_t n_free,
+                  int32_t* block_table, int64_t max_blocks, int64_t n_rows, int64_t* row_start,
+                  int64_t* slot_map, int64_t* pos, int64_t* used, void* stream);
+
+/* Copies n_rows (1 .. 2^20) rows of K and V into their slots.  k, v: device
+ * fp16, row r and head h at r * row_stride + h * head_stride elements (both
+ * multiples of 8, head_dim contiguous), so rows of a projection and slots of a
+ * contiguous cache [n_kv_heads][max_ctx][head_dim] are taken as they lie.  A row
+ * of slot -1 is left out; another slot outside the pool is left out and
+ * reported.  Of rows with equal slots any may win, piece by piece. */
+int blk_page_append(blk_handle h, const void* k, const void* v, int64_t row_stride,
+                    int64_t head_stride, const int64_t* slot_map, int64_t n_rows,
+                    int32_t page_size, int64_t n_pages, void* k_pages, void* v_pages,
+                    void* stream);
+
+typedef struct {
+  int64_t n_seqs, n_rows;       /* 1 .. 4096 sequences, 1 .. 2^20 rows                 */
+  int64_t max_new, max_len;     /* bounds of a sequence's new tokens, and of its slots
+                                   with the new ones (<= max_blocks * page_size)       */
+  const int64_t* row_start;     /* device [n_seqs + 1]                                 */
+  const int64_t* cache_lens;    /* device [n_seqs]                                     */
+  const int32_t* block_table;   /* device [n_seqs][max_blocks]                         */
+  int64_t max_blocks, n_pages;
+  const int32_t* prefix_pages;  /* device [prefix_len / page_size], or NULL            */
+  int64_t prefix_len;           /* slots of a shared prefix, a multiple of page_size; 0 */
+  int32_t page_size;
+} blk_paged_batch;
+
+/* Attention of the batch's rows over their paged caches (new K/V already in
+ * their slots): out[r] = softmax(q[r] . K / sqrt(head_dim)) V per query head.
+ *   q, out  device fp16, rows of [n_heads][head_dim] q_stride / out_stride
+ *           elements apart (multiples of 8); out must not overlap q.  Rows that
+ *           belong to no sequence are left as they were.
+ *   ws      blk_attn_paged_workspace_bytes(h, max_rows, max_seqs, with_prefix)
+ *           bytes or more, for any max_rows >= n_rows and max_seqs >= n_seqs
+ * With prefix_len > 0 the first prefix_len slots of every sequence are those of
+ * prefix_pages: their keys are read once for the whole batch, the block tables'
+ * entries for them are not read, and every sequence with rows must hold the
+ * whole prefix (cache_lens[b] >= prefix_len; refused otherwise).  A prefix does
+ * not go with a sliding window (BLK_ERR_SHAPE).  The result is that of the same
+ * batch without the prefix, up to the order of sums.
+ * Up to 64 rows (new tokens x query heads per kv head) per sequence run on the
+ * few-row kernel (K/V streamed once, mma.sync), more on the tcgen05 kernel.
+ * Slots that a row does not see may hold anything, unless another row of the
+ * same sequence sees them: values there must be finite. */
+size_t blk_attn_paged_workspace_bytes(blk_handle h, int64_t max_rows, int64_t max_seqs,
+                                      int with_prefix);
+int blk_attn_paged(blk_handle h, const blk_paged_batch* batch, const void* q, int64_t q_stride,
+                   const void* k_pages, const void* v_pages, void* out, int64_t out_stride,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/* One step of the block, or of a stack of n_layers blocks, for a paged batch:
+ * RMSNorm, QKV, RoPE at pos, the new K/V to the slots of slot_map, attention over
+ * the pages, o_proj, MLP.  x, out: device fp16 [n_rows, hidden] (out must not
+ * alias x); pos, slot_map: device int64 [n_rows] as blk_page_plan writes them
+ * (positions below the handle's max_ctx); k_pages, v_pages: the layer's pools
+ * (host arrays of them for the stack).  Rows that belong to no sequence come out
+ * undefined.  ws: blk_step_paged_workspace_bytes(h, max_rows, max_seqs,
+ * with_prefix) bytes for either call.  Agrees with blk_prefill_kv and blk_decode
+ * on each sequence within the tolerance. */
+size_t blk_step_paged_workspace_bytes(blk_handle h, int64_t max_rows, int64_t max_seqs,
+                                      int with_prefix);
+int blk_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* batch,
+                   const void* x, const int64_t* pos, const int64_t* slot_map, void* k_pages,
+                   void* v_pages, void* out, void* ws, size_t ws_bytes, void* stream);
+int blk_step_paged_stack(blk_handle h, const blk_weights* w, int n_layers,
+                         const blk_paged_batch* batch, void* const* k_pages,
+                         void* const* v_pages, const void* x, const int64_t* pos,
+                         const int64_t* slot_map, void* out, void* ws, size_t ws_bytes,
+                         void* stream);
 
 /* ---- around the block stack: embedding in, next token out ----------------
  * The inference flow of the MLIR-compilation page (§2.3 "LLM inference
