@@ -435,10 +435,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check_tensor(t, dtype, what, shape=None, contiguous=True):
-    """A tensor that the library reads or writes by its raw pointer: on the GPU, of
-    this type, (contiguous) and of this shape where one is given."""
-    if (t.dtype != dtype or not t.is_cuda or (shape is not None and tuple(t.shape) != shape) or
+def _check_tensor(t, dtype, what, shape, contiguous=True):
+    """A tensor that the library reads or writes by its raw pointer: on the GPU, of this
+    type and shape, and contiguous."""
+    if (t.dtype is not dtype or not t.is_cuda or t.shape != shape or
             (contiguous and not t.is_contiguous())):
         raise BlkError(BLK_ERR_SHAPE, f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}")
 
@@ -536,9 +536,15 @@ class Block:
 
     @staticmethod
     def _stream(stream):
+        if stream is not None:
+            return stream.cuda_stream
         import torch
-        s = torch.cuda.current_stream() if stream is None else stream
-        return s.cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a stream object around it, which takes
+        # 3 us, as long as a small kernel
+        return raw(torch._C._cuda_getDevice())
 
     def prefill(self, w: BlkWeights, x, pos, k_cache, v_cache, out, ws, k_new=None, v_new=None,
                 stream=None):

@@ -25,7 +25,7 @@ enum KernelId {
   kKRmsNorm = 0, kKGemmQKV, kKSplitReduce, kKAttnPrefill, kKGemmO, kKGemmGateUp,
   kKGemmDown, kKDecodeStep, kKAttnMerge, kKLmHead, kKArgmax, kKEmbed, kKDecodeAttnBatch,
   kKQkvFinish, kKDequant, kKReduceNorm, kKPagePlan, kKPageAppend, kKPagedFew, kKPagedMany,
-  kKPagedPrefix, kKPagedMerge, kKPagedSched, kKCount
+  kKPagedPrefix, kKPagedMerge, kKCount
 };
 static_assert(kKCount <= BLK_N_KERNELS, "kernel id table");
 const char* const kKernelNames[BLK_N_KERNELS] = {
@@ -33,7 +33,7 @@ const char* const kKernelNames[BLK_N_KERNELS] = {
     "gemm_gateup", "gemm_down", "decode_persistent", "attn_merge", "lm_head", "argmax_reduce",
     "embed", "decode_attn_batch", "qkv_finish", "dequant_weights", "splitk_reduce_norm",
     "page_plan", "page_append", "attn_paged_few", "attn_paged_many", "attn_paged_prefix",
-    "attn_paged_merge", "attn_paged_sched"};
+    "attn_paged_merge"};
 }  // namespace
 
 struct blk_handle_s {
@@ -1276,25 +1276,22 @@ int check_paged(blk_handle h, const blk_paged_batch* b) {
   return BLK_OK;
 }
 
-// Attention workspace: partials and (m, l) of the own parts, the cut units,
-// the many-row kernel's schedule; with a prefix also its partials and the
+// Attention workspace: partials and (m, l) of the own parts, the cut units;
+// with a prefix also its partials and the
 // whole units' parts by row and head.
 struct PagedWs {
-  size_t part, ml, cut, pref, unit, own, own_ml, info, ppart, pml, pown, pown_ml, total;
+  size_t part, ml, cut, own, own_ml, info, ppart, pml, pown, pown_ml, total;
 };
-PagedWs paged_ws(const blk_config& c, int64_t N, int64_t B, bool prefix, int num_sms) {
+PagedWs paged_ws(const blk_config& c, int64_t N, bool prefix, int num_sms) {
   const size_t D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads;
   const size_t few = (size_t)2 * num_sms * 2 * kPagedFewRows;
   const size_t many = (size_t)num_sms * 2 * kPagedManyRows;
   const size_t rows = few > many ? few : many;
-  const size_t units = (size_t)(N / (2 * paged_btok((int)(Hq / Hkv))) + B);
   PagedWs w;
   size_t o = 0;
   w.part = o; o = align_up(o + rows * D * 4);
   w.ml = o; o = align_up(o + rows * 8);
   w.cut = o; o = align_up(o + (size_t)2 * num_sms * sizeof(PagedPiece));
-  w.pref = o; o = align_up(o + (units + 2) * 8);
-  w.unit = o; o = align_up(o + units * sizeof(PagedUnit));
   w.own = w.own_ml = w.info = w.ppart = w.pml = w.pown = w.pown_ml = o;
   if (prefix) {
     w.own = o; o = align_up(o + (size_t)N * Hq * D * 4);
@@ -1315,7 +1312,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   const blk_config& c = h->cfg;
   const int D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads, G = Hq / Hkv;
   const bool prefix = b->prefix_len > 0;
-  const PagedWs lay = paged_ws(c, b->n_rows, b->n_seqs, prefix, h->num_sms);
+  const PagedWs lay = paged_ws(c, b->n_rows, prefix, h->num_sms);
   const int64_t page = b->page_size, heads = b->n_pages * Hkv;
   PagedManyParams m = {};
   PagedAttnParams& a = m.a;
@@ -1381,14 +1378,8 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
     paged_few_part_rows(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
     BLK_LAUNCH(tm, kKPagedFew, launch_paged_few(a, s, true));
   } else {
-    int64_t* pref = reinterpret_cast<int64_t*>(base + lay.pref) + 1;
-    PagedUnit* unit = reinterpret_cast<PagedUnit*>(base + lay.unit);
-    m.units = (int)(b->n_rows / (2 * m.btok) + b->n_seqs);
-    m.pref = pref;
-    m.unit = unit;
     a.nc = h->num_sms;
     a.slot_rows = kPagedManyRows;
-    BLK_LAUNCH(tm, kKPagedSched, launch_paged_sched(m, pref, unit, s, true));
     BLK_LAUNCH(tm, kKPagedMany, launch_paged_many(m, s, true));
   }
   mg.a = a;
@@ -1410,7 +1401,7 @@ int check_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int6
     if (st % 8) return BLK_ERR_ALIGN;
     if (st < width || st > (int64_t)1 << 32) return BLK_ERR_SHAPE;
   }
-  if (ws_bytes < paged_ws(h->cfg, b->n_rows, b->n_seqs, b->prefix_len > 0, h->num_sms).total)
+  if (ws_bytes < paged_ws(h->cfg, b->n_rows, b->prefix_len > 0, h->num_sms).total)
     return BLK_ERR_WORKSPACE;
   return BLK_OK;
 }
@@ -1422,7 +1413,7 @@ struct StepPagedWs {
   size_t xn16, q16, attn16, h32, hn16, act16, part32, k16, v16, attn, act[2], total;
 };
 int step_splits(int64_t N) { return N <= kFrMaxRows ? kMaxSplitsBatch : kMaxSplits; }
-StepPagedWs step_paged_ws(const blk_config& c, int64_t N, int64_t B, bool prefix, int num_sms) {
+StepPagedWs step_paged_ws(const blk_config& c, int64_t N, bool prefix, int num_sms) {
   const size_t H = c.hidden, D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads,
                I = c.intermediate;
   StepPagedWs w;
@@ -1438,7 +1429,7 @@ StepPagedWs step_paged_ws(const blk_config& c, int64_t N, int64_t B, bool prefix
   w.part32 = o; o = align_up(o + (size_t)step_splits(N) * N * nmax * 4);
   w.k16 = o; o = align_up(o + N * Hkv * D * 2);
   w.v16 = o; o = align_up(o + N * Hkv * D * 2);
-  w.attn = o; o = align_up(o + paged_ws(c, N, B, prefix, num_sms).total);
+  w.attn = o; o = align_up(o + paged_ws(c, N, prefix, num_sms).total);
   for (int i = 0; i < 2; ++i) { w.act[i] = o; o = align_up(o + N * H * 2); }
   w.total = o;
   return w;
@@ -1455,7 +1446,7 @@ int check_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* 
   for (const void* ptr : {x, k_pages, v_pages, out, ws})
     if (!aligned(ptr, 16)) return BLK_ERR_ALIGN;
   if (!aligned(pos, 8) || !aligned(slot_map, 8)) return BLK_ERR_ALIGN;
-  if (ws_bytes < step_paged_ws(h->cfg, b->n_rows, b->n_seqs, b->prefix_len > 0, h->num_sms).total)
+  if (ws_bytes < step_paged_ws(h->cfg, b->n_rows, b->prefix_len > 0, h->num_sms).total)
     return BLK_ERR_WORKSPACE;
   return BLK_OK;
 }
@@ -1467,7 +1458,7 @@ int run_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b,
                    void* out, unsigned char* base, cudaStream_t s, bool x_normed,
                    const __half* next_ln1) {
   const blk_config& c = h->cfg;
-  const StepPagedWs lay = step_paged_ws(c, b->n_rows, b->n_seqs, b->prefix_len > 0, h->num_sms);
+  const StepPagedWs lay = step_paged_ws(c, b->n_rows, b->prefix_len > 0, h->num_sms);
   __half* xn16 = reinterpret_cast<__half*>(base + lay.xn16);
   __half* q16 = reinterpret_cast<__half*>(base + lay.q16);
   __half* attn16 = reinterpret_cast<__half*>(base + lay.attn16);
@@ -1594,7 +1585,7 @@ size_t blk_attn_paged_workspace_bytes(blk_handle h, int64_t max_rows, int64_t ma
                                       int with_prefix) {
   if (!h || max_rows < 1 || max_rows > kMaxPagedRows || max_seqs < 1 || max_seqs > kMaxSeqs)
     return 0;
-  return paged_ws(h->cfg, max_rows, max_seqs, with_prefix != 0, h->num_sms).total;
+  return paged_ws(h->cfg, max_rows, with_prefix != 0, h->num_sms).total;
 }
 
 int blk_attn_paged(blk_handle h, const blk_paged_batch* batch, const void* q, int64_t q_stride,
@@ -1615,9 +1606,9 @@ size_t blk_step_paged_workspace_bytes(blk_handle h, int64_t max_rows, int64_t ma
   if (!h || max_rows < 1 || max_rows > kMaxPagedRows || max_seqs < 1 || max_seqs > kMaxSeqs)
     return 0;
   // few rows keep more split-K partials: enough for either side of that bound
-  const size_t a = step_paged_ws(h->cfg, max_rows, max_seqs, with_prefix != 0, h->num_sms).total;
+  const size_t a = step_paged_ws(h->cfg, max_rows, with_prefix != 0, h->num_sms).total;
   if (max_rows <= kFrMaxRows) return a;
-  const size_t b = step_paged_ws(h->cfg, kFrMaxRows, max_seqs, with_prefix != 0, h->num_sms).total;
+  const size_t b = step_paged_ws(h->cfg, kFrMaxRows, with_prefix != 0, h->num_sms).total;
   return a > b ? a : b;
 }
 
@@ -1647,8 +1638,7 @@ int blk_step_paged_stack(blk_handle h, const blk_weights* w, int n_layers,
     if (rc) return rc;
   }
   if (!on_device(h)) return BLK_ERR_CUDA;
-  const StepPagedWs lay = step_paged_ws(h->cfg, batch->n_rows, batch->n_seqs,
-                                        batch->prefix_len > 0, h->num_sms);
+  const StepPagedWs lay = step_paged_ws(h->cfg, batch->n_rows, batch->prefix_len > 0, h->num_sms);
   unsigned char* base = static_cast<unsigned char*>(ws);
   for (int l = 0; l < n_layers; ++l) {
     const void* in = l == 0 ? x : base + lay.act[(l - 1) % 2];

@@ -101,23 +101,15 @@ cudaError_t configure_paged_few();
 
 // Many rows: prompts and long runs of new tokens, and the shared prefix (its
 // rows are the whole batch's).  Units are 2 blocks of 128 / G tokens.
-struct PagedUnit {             // own parts: written by the schedule kernel
-  int b, tok, ntok, r0;        // sequence, first token, tokens, batch row of that token
-  int L, n, lo, hi;            // the sequence's; slots that some row sees: [lo, hi)
-};
 struct PagedManyParams {
   PagedAttnParams a;
   int prefix;                  // 1: the shared prefix's parts, of all N rows
   int btok;                    // tokens of a block
-  int units;                   // prefix: units of one kv head; own: at most this many
-  const int64_t* pref;         // own: [units + 1] tiles before each unit; pref[-1]: how many
-  const PagedUnit* unit;       // own: [units]
+  int units;                   // prefix: units of one kv head
 };
 inline int paged_btok(int G) { return 128 / G; }
 constexpr int kPagedManyRows = 256;     // partial rows of a slot
 constexpr int kPagedManyTile = 128;     // slots of a tile
-cudaError_t launch_paged_sched(const PagedManyParams& p, int64_t* pref, PagedUnit* unit,
-                               cudaStream_t s, bool pdl);
 cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl);
 cudaError_t configure_paged_many();
 

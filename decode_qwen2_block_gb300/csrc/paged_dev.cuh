@@ -6,6 +6,15 @@
 
 namespace blk {
 
+// mbar_wait for waits that are short and follow one another closely: the timer
+// (a slow read) is not consulted before the phase has been probed some times.
+__device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity, int* err) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, err);
+}
+
 // A sequence of the batch as the kernels take it: n = 0 when it has no rows
 // or is refused (and then `bad`): its row range, length and pages must fit the
 // batch before anything is formed from them.

@@ -69,6 +69,12 @@ __device__ __forceinline__ void st_zero16(uint32_t addr) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
 
+__device__ __forceinline__ float ex2(float x) {   // 2^x, relative error 2^-22; 2^-inf = 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 struct TileInfo {      // what the consumers need of a tile
   int slot0;           // its first slot
   int lo, hi;          // slots that some row of the unit sees: [lo, hi)
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* empty = full + S;
   uint64_t* q_empty = empty + S;
   __shared__ int64_t wsum[kThreads / 32];
-  __shared__ int start_b;
+  __shared__ int start_b, abort_s;
   __shared__ int64_t start_cum;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -133,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     fence_mbar_init();
     start_b = 0;
     start_cum = 0;
+    abort_s = 0;
   }
   // tiles of all sequences (one kv head), and those before this thread's
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (take) page = row[first >> p.page_lg];
         const bool in = page >= 0 && page < p.n_pages;
         if (take && !in) set_error(p.err, kDevPage);
-        if (it >= S && !mbar_wait(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
+        if (it >= S && !mbar_wait_near(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
         if (x == xa && seg >= QB &&
             !mbar_wait(&q_empty[qb], (uint32_t)(seg / QB - 1) & 1u, p.err))
           ok = false;
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       c.c0 = ok ? cut.c0 : -1;
     }
     const int st = it % S;
-    if (ok && it >= S && !mbar_wait(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
+    if (ok && it >= S && !mbar_wait_near(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       if (lane == 0) {
@@ -314,37 +321,43 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 
   // ---------------------------------------------------------------- consumers
-  const int grp = lane >> 2, tig = lane & 3;
+  const int grp = lane >> 2, tig = lane & 3, mm = lane >> 3;
   const int bs_lg = p.page_lg < 6 ? p.page_lg : 6;
   const int slab = warp * 16;
   const float sl2 = p.scale_log2;
   float m_r[MT][2], l_r[MT][2], O[MT][kNT][4];
   int last[MT][2], low[MT][2];
   int seg = 0;
-  // byte offset of (slot row r of the tile, 16-byte piece c) in a K or V tile of
-  // boxes [D / 64][bs slots][128 B] with the 128-byte swizzle
-  auto tile_off = [&](int r, int c) -> uint32_t {
-    const int box = r >> bs_lg, rr = r & ((1 << bs_lg) - 1);
-    return (uint32_t)(((box * (D / 64) + (c >> 3)) << (bs_lg + 7)) + rr * 128 +
-                      (((c & 7) ^ (rr & 7)) << 4));
+  // A K or V tile is boxes [D / 64][bs slots][128 B] with the 128-byte swizzle:
+  // row r, 16-byte piece c is at row_off(r) + (c / 8) half + ((c % 8 ^ r % 8) << 4).
+  const int half = 128 << bs_lg;
+  auto row_off = [&](int r) -> uint32_t {
+    return (uint32_t)((r >> bs_lg) * (D / 64) * half + (r & ((1 << bs_lg) - 1)) * 128);
   };
+  uint32_t k_off[4], v_col[kNT / 2], v_row[4];      // this lane's ldmatrix offsets
+  {
+    const int kr = slab + (mm >> 1) * 8 + (lane & 7);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) k_off[k] = row_off(kr) + (((k * 2 + (mm & 1)) ^ (kr & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < kNT / 2; ++i) {
+      const int c = warp * kNT + 2 * i + (mm >> 1);
+      v_col[i] = (c >> 3) * half + (((c & 7) ^ (lane & 7)) << 4) +
+                 ((mm & 1) * 8 + (lane & 7)) * 128;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v_row[k] = row_off(k * 16);
+  }
+  const uint32_t q_lane = ((mm & 1) * 8 + (lane & 7)) * Sm::kQStride + (mm >> 1) * 16;
+  const uint32_t p_lane = pbase + ((mm & 1) * 8 + (lane & 7)) * Sm::kPStride + (mm >> 1) * 16;
+  const uint32_t p_st = pbase + grp * Sm::kPStride + (slab + 2 * tig) * 2;
   for (int it = 0;; ++it) {
     const int st = it % S;
-    bool ok = mbar_wait(&full[st], (uint32_t)(it / S) & 1u, p.err);
-    ok = __all_sync(0xffffffffu, ok);
-    // the four warps agree on giving up: none stays behind at a barrier
-    int give_up;
-    asm volatile(
-        "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\t"
-        "bar.red.popc.u32 %0, 1, %2, a;\n\t}"
-        : "=r"(give_up)
-        : "r"(ok ? 0 : 1), "r"(kConsumers)
-        : "memory");
-    if (give_up) return;
+    if (!mbar_wait_near(&full[st], (uint32_t)(it / S) & 1u, p.err)) *(volatile int*)&abort_s = 1;
     const int flags = infos[st].flags;
     if (flags & 4) return;
     const int slot0 = infos[st].slot0, n = infos[st].n;
-    const int vlo = max(0, infos[st].lo - slot0), vhi = min(kTile, infos[st].hi - slot0);
+    const int vlo = infos[st].lo - slot0, vhi = infos[st].hi - slot0;   // seen: [vlo, vhi) of the tile
     const uint32_t kb = ring + st * 2 * Sm::kKV, vb = kb + Sm::kKV;
     if (flags & 1) {
       const int L = infos[st].L;
@@ -361,77 +374,84 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int i = 0; i < kNT; ++i) O[mt][i][2 * h2] = O[mt][i][2 * h2 + 1] = 0.f;
         }
     }
-    const uint32_t qs = qbase + (seg % QB) * Sm::kQBytes;
+    const uint32_t qs = qbase + (seg % QB) * Sm::kQBytes + q_lane;
     const bool active = slab < vhi && slab + 16 > vlo;
+    // every row sees every slot of this warp's 16: n - 1 slots from the end are
+    // behind the first row, windows begin at most n - 1 slots behind vlo
+    const bool clear = slab + 16 <= vhi - (n - 1) && slab >= (p.window > 0 ? vlo + (n - 1) : vlo);
     float sc[MT][2][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) sc[mt][k][0] = sc[mt][k][1] = sc[mt][k][2] = sc[mt][k][3] = 0.f;
-    const int mm = lane >> 3;
     if (active) {
       // S = Q K^T of this warp's 16 slots
-      const int kr = slab + (mm >> 1) * 8 + (lane & 7);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         uint32_t bk[4];
-        ldsm_x4(kb + tile_off(kr, ks * 2 + (mm & 1)), bk);
+        ldsm_x4(kb + k_off[ks & 3] + (ks >> 2) * half, bk);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           uint32_t a[4];
-          ldsm_x4(qs + (mt * 16 + (mm & 1) * 8 + (lane & 7)) * Sm::kQStride +
-                      (ks * 16 + (mm >> 1) * 8) * 2, a);
+          ldsm_x4(qs + mt * 16 * Sm::kQStride + ks * 32, a);
           mma16816(sc[mt][0], a, bk[0], bk[1]);
           mma16816(sc[mt][1], a, bk[2], bk[3]);
         }
       }
     }
-    // scores in log2 units, -inf where the row does not see the slot
+    // raw scores, -inf where the row does not see the slot; the warps' maxima meet
+    if (!clear) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float mx[2] = {-INFINITY, -INFINITY};
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = slab + k * 8 + 2 * tig + (e & 1), slot = slot0 + c, h2 = e >> 1;
-          const bool seen = c >= vlo && slot <= last[mt][h2] && slot >= low[mt][h2];
-          sc[mt][k][e] = active && seen ? sc[mt][k][e] * sl2 : -INFINITY;
-          mx[h2] = fmaxf(mx[h2], sc[mt][k][e]);
-        }
+          for (int e = 0; e < 4; ++e) {
+            const int c = slab + k * 8 + 2 * tig + (e & 1), slot = slot0 + c;
+            const bool seen =
+                active && c >= vlo && slot <= last[mt][e >> 1] && slot >= low[mt][e >> 1];
+            if (!seen) sc[mt][k][e] = -INFINITY;
+          }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
-        mx[h2] = fmaxf(mx[h2], __shfl_xor_sync(0xffffffffu, mx[h2], 1));
-        mx[h2] = fmaxf(mx[h2], __shfl_xor_sync(0xffffffffu, mx[h2], 2));
-        if (tig == 0) stat[warp * 16 * MT + mt * 16 + grp + 8 * h2] = mx[h2];
+        float mx = fmaxf(fmaxf(sc[mt][0][2 * h2], sc[mt][0][2 * h2 + 1]),
+                         fmaxf(sc[mt][1][2 * h2], sc[mt][1][2 * h2 + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (tig == 0) stat[warp * 16 * MT + mt * 16 + grp + 8 * h2] = mx;
       }
-    }
     named_sync(1, kConsumers);
+    // a wait that ran out stops all four warps here: the next flag is set behind the
+    // second barrier
+    if (*(volatile int*)&abort_s) return;
     if ((flags & 2) && lane == 0) mbar_arrive(&q_empty[seg % QB]);   // q has been used
     float corr[MT][2];
+    bool moved = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
         const int row = mt * 16 + grp + 8 * h2;
-        float mx = m_r[mt][h2];
+        float mx = stat[row];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) mx = fmaxf(mx, stat[w * 16 * MT + row]);
-        corr[mt][h2] = mx == -INFINITY ? 1.f : exp2f(m_r[mt][h2] - mx);
-        m_r[mt][h2] = mx;
+        for (int w = 1; w < 4; ++w) mx = fmaxf(mx, stat[w * 16 * MT + row]);
+        const float mn = fmaxf(m_r[mt][h2], mx * sl2);       // log2 units
+        corr[mt][h2] = mn == -INFINITY ? 1.f : ex2(m_r[mt][h2] - mn);
+        moved |= mn != m_r[mt][h2];
+        m_r[mt][h2] = mn;
+        const float nref = mn == -INFINITY ? 0.f : -mn;      // 2^-inf = 0
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float pv[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float s = sc[mt][k][2 * h2 + e];
-            pv[e] = s == -INFINITY ? 0.f : exp2f(s - mx);
-            sum += pv[e];
-          }
-          const __half2 ph = __floats2half2_rn(pv[0], pv[1]);
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(pbase + row * Sm::kPStride +
-                                                      (slab + k * 8 + 2 * tig) * 2),
+          const float e0 = ex2(fmaf(sc[mt][k][2 * h2], sl2, nref));
+          const float e1 = ex2(fmaf(sc[mt][k][2 * h2 + 1], sl2, nref));
+          sum += e0 + e1;
+          const __half2 ph = __floats2half2_rn(e0, e1);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_st + (mt * 16 + 8 * h2) * Sm::kPStride +
+                                                      k * 16),
                        "r"(*reinterpret_cast<const uint32_t*>(&ph))
                        : "memory");
         }
@@ -439,35 +459,34 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     if (active && (slab < vlo || slab + 16 > vhi)) {
       for (int i = lane; i < 16 * kCPR; i += 32) {
-        const int r = slab + i / kCPR;
-        if (r < vlo || r >= vhi) st_zero16(vb + tile_off(r, i % kCPR));
+        const int r = slab + i / kCPR, c = i % kCPR;
+        if (r < vlo || r >= vhi) st_zero16(vb + row_off(r) + (c >> 3) * half + (((c & 7) ^ (r & 7)) << 4));
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before a later copy there
     }
     named_sync(1, kConsumers);
+    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int i = 0; i < kNT; ++i) {
-        O[mt][i][0] *= corr[mt][0];
-        O[mt][i][1] *= corr[mt][0];
-        O[mt][i][2] *= corr[mt][1];
-        O[mt][i][3] *= corr[mt][1];
-      }
+        for (int i = 0; i < kNT; ++i) {
+          O[mt][i][0] *= corr[mt][0];
+          O[mt][i][1] *= corr[mt][0];
+          O[mt][i][2] *= corr[mt][1];
+          O[mt][i][3] *= corr[mt][1];
+        }
+    }
     // O += P V for this warp's D / 4 columns
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       if (ks * 16 >= vhi || ks * 16 + 16 <= vlo) continue;
       uint32_t bv[kNT / 2][4];
-      const int vr = ks * 16 + (mm & 1) * 8 + (lane & 7);
 #pragma unroll
-      for (int i = 0; i < kNT / 2; ++i)
-        ldsm_x4_t(vb + tile_off(vr, warp * kNT + 2 * i + (mm >> 1)), bv[i]);
+      for (int i = 0; i < kNT / 2; ++i) ldsm_x4_t(vb + v_row[ks] + v_col[i], bv[i]);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t a[4];
-        ldsm_x4(pbase + (mt * 16 + (mm & 1) * 8 + (lane & 7)) * Sm::kPStride +
-                    (ks * 16 + (mm >> 1) * 8) * 2, a);
+        ldsm_x4(p_lane + mt * 16 * Sm::kPStride + ks * 32, a);
 #pragma unroll
         for (int i = 0; i < kNT / 2; ++i) {
           mma16816(O[mt][2 * i], a, bv[i][0], bv[i][1]);
@@ -527,20 +546,20 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ------------------------------------------------------------------- merging
 // A row's result from its pieces: sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
-// with M = max_c m_c, pieces in their order.  Block = 64 threads of two or one
-// columns by 4 groups that each take a quarter of the pieces (a long sequence
-// alone on the GPU is cut into 150 of them); the groups' sums are added in
-// order, so the bits do not depend on timing.
-template <int D>
+// with M = max_c m_c, pieces in their order.  kWPR warps take a row, each a run of
+// its pieces (their sums are added in order, so the bits do not depend on
+// timing): eight where few rows have many pieces (one long sequence alone is cut
+// into 150), one where many rows have a few.
+template <int D, int kWPR>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedMergeParams q) {
-  constexpr int kV = D / 64;                 // columns per thread
+  constexpr int kV = D / 32;
   const PagedAttnParams& p = q.a;
-  __shared__ float sacc[4][D + 2];
+  __shared__ float sacc[kWPR > 1 ? 8 : 1][D + 2];
   __shared__ PagedPiece cuts[512];
   __shared__ int cut_row[512], wsum[8];
   griddep_wait();
   griddep_launch();
-  const int tid = threadIdx.x, grp = tid >> 6, c = (tid & 63) * kV;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane * kV;
   int64_t items;
   if (!q.prefix) {
     // rows of the cut units before each CTA's (two CTAs a thread; nc <= 512)
@@ -557,14 +576,14 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if ((tid & 31) >= o) x += y;
+      if (lane >= o) x += y;
     }
-    if ((tid & 31) == 31) wsum[tid >> 5] = x;
+    if (lane == 31) wsum[warp] = x;
     __syncthreads();
     int all = 0;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      if (w < (tid >> 5)) x += wsum[w];
+      if (w < warp) x += wsum[w];
       all += wsum[w];
     }
     cut_row[2 * tid] = x - n2[0] - n2[1];
@@ -574,7 +593,11 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   } else {
     items = (int64_t)p.N * p.Hq;
   }
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+  constexpr int kRows = 8 / kWPR;             // rows of a block at a time
+  for (int64_t item0 = (int64_t)blockIdx.x * kRows; item0 < items;
+       item0 += (int64_t)gridDim.x * kRows) {
+    const int64_t item = item0 + warp / kWPR;
+    if (kWPR == 1 && item >= items) break;
     // pieces: own ones in slots of CTAs c0..c1 (or a whole one), then the prefix's
     int c0, c1, s0, row, r, hq, pc0 = 0, pc1 = -1, ps0 = 0, prow = 0;
     bool own_whole = false, pre_whole = false;
@@ -629,7 +652,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
         ml = __ldcg((pre_whole ? q.pre_own_ml : q.pre_ml) + at);
       }
     };
-    const int i0 = grp * n_all / 4, i1 = (grp + 1) * n_all / 4;
+    const int wr = warp % kWPR;
+    const int i0 = wr * n_all / kWPR, i1 = (wr + 1) * n_all / kWPR;
     float M = -INFINITY, l = 0.f, acc[kV];
 #pragma unroll
     for (int k = 0; k < kV; ++k) acc[k] = 0.f;
@@ -643,8 +667,13 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
         if (i + u < i1) {
           const float* o;
           piece(i + u, o, ml[u]);
-#pragma unroll
-          for (int k = 0; k < kV; ++k) v[u][k] = __ldcg(o + c + k);
+          if constexpr (kV == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(o + c));
+            v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+          } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(o + c));
+            v[u][0] = x.x; v[u][1] = x.y;
+          }
         }
       }
 #pragma unroll
@@ -658,34 +687,36 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
         M = mn;
       }
     }
+    if constexpr (kWPR > 1) {
+      if (item0 > (int64_t)blockIdx.x * kRows) __syncthreads();   // sacc of the row before is read
 #pragma unroll
-    for (int k = 0; k < kV; ++k) sacc[grp][c + k] = acc[k];
-    if ((tid & 63) == 0) {
-      sacc[grp][D] = M;
-      sacc[grp][D + 1] = l;
-    }
-    __syncthreads();
-    if (grp == 0) {
-      float Mx = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) Mx = fmaxf(Mx, sacc[k][D]);
-      float lt = 0.f, o[kV];
-#pragma unroll
-      for (int k = 0; k < kV; ++k) o[k] = 0.f;
-#pragma unroll
-      for (int gq = 0; gq < 4; ++gq) {
-        const float mg = sacc[gq][D];
-        const float w = mg == -INFINITY ? 0.f : exp2f(mg - Mx);
-        lt = __fmaf_rn(w, sacc[gq][D + 1], lt);
-#pragma unroll
-        for (int k = 0; k < kV; ++k) o[k] = __fmaf_rn(w, sacc[gq][c + k], o[k]);
+      for (int k = 0; k < kV; ++k) sacc[warp][c + k] = acc[k];
+      if (lane == 0) {
+        sacc[warp][D] = M;
+        sacc[warp][D + 1] = l;
       }
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
-      __half* d = p.out + (int64_t)r * p.out_stride + (int64_t)hq * D + c;
+      __syncthreads();
+      if (warp != 0) continue;
+      M = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kV; ++k) d[k] = __float2half_rn(o[k] * inv);
+      for (int k = 0; k < 8; ++k) M = fmaxf(M, sacc[k][D]);
+      l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) acc[k] = 0.f;
+#pragma unroll
+      for (int w8 = 0; w8 < 8; ++w8) {
+        const float mg = sacc[w8][D];
+        const float w = mg == -INFINITY ? 0.f : exp2f(mg - M);
+        l = __fmaf_rn(w, sacc[w8][D + 1], l);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) acc[k] = __fmaf_rn(w, sacc[w8][c + k], acc[k]);
+      }
     }
-    __syncthreads();
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    __half* d = p.out + (int64_t)r * p.out_stride + (int64_t)hq * D + c;
+#pragma unroll
+    for (int k = 0; k < kV; k += 2)
+      *reinterpret_cast<__half2*>(d + k) = __floats2half2_rn(acc[k] * inv, acc[k + 1] * inv);
   }
 }
 
@@ -737,9 +768,12 @@ cudaError_t launch_paged_few(const PagedAttnParams& p, cudaStream_t s, bool pdl)
 
 cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const int64_t most = p.prefix ? (int64_t)p.a.N * p.a.Hq : (int64_t)p.a.nc * p.a.slot_rows;
-  const int64_t fit = (int64_t)num_sms * 8;
-  cfg.gridDim = dim3((unsigned)(most < fit ? most : fit));
+  // rows of a unit share its pieces: 8 warps a row while all of a CTA's rows at a
+  // time (the few-row kernel's without a prefix) are few
+  const bool deep = !p.prefix && p.a.slot_rows <= kPagedFewRows;
+  const int64_t rows = p.prefix ? (int64_t)p.a.N * p.a.Hq : (int64_t)p.a.nc * p.a.slot_rows;
+  const int64_t want = deep ? rows : (rows + 7) / 8, fit = (int64_t)num_sms * 8;
+  cfg.gridDim = dim3((unsigned)(want < fit ? want : fit));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -747,8 +781,11 @@ cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.a.D == 128) return cudaLaunchKernelEx(&cfg, paged_merge_kernel<128>, p);
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<64>, p);
+  if (p.a.D == 128)
+    return deep ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 8>, p)
+                : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 1>, p);
+  return deep ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 8>, p)
+              : cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 1>, p);
 }
 
 cudaError_t configure_paged_few() {

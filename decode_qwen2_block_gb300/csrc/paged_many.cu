@@ -6,17 +6,20 @@
 // score.  A unit is two blocks of 128 / G tokens, each with the G query heads of
 // one kv head: 256 rows that share every K/V tile of 128 slots.  The CTAs (one
 // per SM) take equal ranges of the line of all units' tiles, as the few-row
-// kernel does (see paged.h).  Ten warps:
+// kernel does (see paged.h).  Twelve warps:
 //   warp 0     producer: q of both blocks once per unit, then K and V tiles, page
 //              by page (each lane one box of 64 columns), into a ring of tiles.
-//   warp 1     MMA issuer (lane 0): S = Q K^T (M = N = 128) and O += P V for the
-//              two blocks in turn: S0 S1 | PV0 S0' | PV1 S1' | ..., so that one
-//              block's products run under the other's softmax.
-//   warps 2-5, 6-9   softmax of block 0 and 1, a thread per row: scores from TMEM,
+//   warps 1, 2 MMA issuers (lane 0) of block 0 and 1: S = Q K^T (M = N = 128), then in
+//              turn O += P V and the next tile's S, so that one block's products run
+//              under the other's softmax.  An issuer a block: issuing an MMA takes
+//              the thread as long as the MMA itself (64 clocks), so what one thread
+//              does in between (a wait, a commit: 250 clocks) leaves the tensor core
+//              idle; one issuer for both blocks took 4150 clocks a tile instead.
+//   warps 4-7, 8-11   softmax of block 0 and 1, a thread per row: scores from TMEM,
 //              online softmax in base 2 with lazy rescaling of O, P (fp16)
 //              over S's own columns (TMEM: S0 S1 O0 O1 = 512 columns).
-// MMAs of one thread execute in order: S_j+1 is written after PV_j has read P_j,
-// and a commit behind S_j+1 says that PV_j is complete too.
+// MMAs of one thread execute in order: a block's S_j+1 is written after its PV_j has
+// read P_j, and a commit behind S_j+1 says that PV_j is complete too.
 // Slots that no row of the unit sees have their V rows zeroed before PV (0 * NaN
 // is NaN).  Every wait is bounded.
 #include <math.h>
@@ -29,7 +32,12 @@
 namespace blk {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers: a softmax thread holds a row of 128 scores.  The block is launched
+// with 168 a thread (384 x 168 = 64512); warps 0-3 keep 72, the softmax warps take
+// 216: 128 x 72 + 256 x 216 = 64512.  configure_paged_many checks the 168.
+constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
+static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegsLaunch, "register split");
 constexpr int kTile = kPagedManyTile;
 constexpr int kInfos = 8;
 constexpr float kRescaleLog2 = 8.f;   // see the softmax
@@ -47,11 +55,12 @@ template <int D>
 struct MSmem {
   static constexpr int kQBlk = 128 * D * 2;                  // [D / 64][128 rows][128 B]
   static constexpr int kKV = kTile * D * 2;                  // K or V tile, the same form
-  static constexpr int kRing = D == 128 ? 5 : 8;
+  static constexpr int kRing = D == 128 ? 4 : 8;
   static constexpr int kRingOff = 2 * kQBlk;
-  static constexpr int kInfoOff = kRingOff + kRing * kKV;
+  static constexpr int kStageOff = kRingOff + kRing * kKV;   // 4 KB per softmax warp
+  static constexpr int kInfoOff = kStageOff + 8 * 4096;
   static constexpr int kBarOff = kInfoOff + kInfos * (int)sizeof(ManyInfo);
-  static constexpr int kEnd = kBarOff + (2 * kRing + 10) * 8 + 16;
+  static constexpr int kEnd = kBarOff + (2 * kRing + 8) * 8 + 16;
   static constexpr size_t kBytes = (size_t)kEnd + 1024;
   static constexpr uint32_t kSCol = 0, kOCol = 256;
   static_assert(kBarOff % 8 == 0 && kBytes <= 232448, "shared memory");
@@ -71,98 +80,84 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x; 2^-inf = 0
   return y;
 }
 
-// ------------------------------------------------------------------ schedule
-// The units of a ragged batch and the tiles before each, for one kv head: unit
-// u of sequence b are its tokens 2 btok u ...  One CTA; bound by latency (about
-// 3 us), for calls that take tens of microseconds.
-__global__ void __launch_bounds__(1024)
-    paged_sched_kernel(const __grid_constant__ PagedManyParams q, int64_t* pref, PagedUnit* unit) {
-  extern __shared__ int off[];          // [B + 1] units before each sequence
-  __shared__ int64_t wsum[32];
-  __shared__ int64_t run;
-  griddep_wait();
-  griddep_launch();
-  const PagedAttnParams& p = q.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int utok = 2 * q.btok;
-  auto scan = [&](int64_t v, int64_t& total) -> int64_t {   // exclusive, over the block
-    int64_t x = v;
+// Pairs of fp32 in one instruction, and the maximum of three.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// A unit of the own parts: tokens tok .. tok + ntok - 1 of a sequence.
+struct Unit {
+  int tok, ntok, r0;         // first token, tokens, batch row of the first
+  int L, lo, hi;             // the sequence's history; slots that some row sees: [lo, hi)
+};
+__device__ __forceinline__ Unit unit_of(const PagedAttnParams& p, const PagedSeq& s, int u, int utok) {
+  Unit x;
+  x.tok = u * utok;
+  x.ntok = min(utok, s.n - x.tok);
+  x.r0 = s.r0 + x.tok;
+  x.L = s.L;
+  x.lo = paged_lo(p, s.L + x.tok);
+  x.hi = s.L + x.tok + x.ntok;
+  return x;
+}
+__device__ __forceinline__ int unit_tiles(const Unit& x) {
+  return (x.hi + kTile - 1) / kTile - x.lo / kTile;
+}
+
+// Exclusive sum over the block of one value per thread; `total` is the sum.
+__device__ __forceinline__ int64_t block_excl(int64_t v, int64_t* warp_sums, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) wsum[warp] = x;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += wsum[w];
-      total += wsum[w];
-    }
-    return before + x - v;
-  };
-  const int per = (p.B + 1023) / 1024;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int64_t mine = 0, total;
-  bool bad = false;
-  for (int b = b0; b < b1; ++b) {
-    const PagedSeq s = load_seq(p, b);
-    mine += (s.n + utok - 1) / utok;
-    bad |= s.bad;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  if (bad) set_error(p.err, kDevPage);
-  int64_t at = scan(mine, total);
-  for (int b = b0; b < b1; ++b) {
-    off[b] = (int)min(at, (int64_t)q.units);
-    at += (load_seq(p, b).n + utok - 1) / utok;
-  }
-  // more units than rows allow: row ranges that overlap (the host's row_start is wrong)
-  const int R = (int)min(total, (int64_t)q.units);
-  if (total > q.units && tid == 0) set_error(p.err, kDevPage);
-  if (tid == 0) run = 0;
+  __syncthreads();   // the sums of an earlier call have been read
+  if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  for (int k0 = 0; k0 < R; k0 += 1024) {
-    const int k = k0 + tid;
-    int64_t tiles = 0;
-    if (k < R) {
-      int lo = 0, hi = p.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (off[mid] <= k) lo = mid; else hi = mid;
-      }
-      const PagedSeq s = load_seq(p, lo);
-      PagedUnit u;
-      u.b = lo;
-      u.tok = (k - off[lo]) * utok;
-      u.ntok = min(utok, s.n - u.tok);
-      u.r0 = s.r0 + u.tok;
-      u.L = s.L;
-      u.n = s.n;
-      u.lo = paged_lo(p, s.L + u.tok);
-      u.hi = s.L + u.tok + u.ntok;
-      unit[k] = u;
-      tiles = (u.hi + kTile - 1) / kTile - u.lo / kTile;
-    }
-    int64_t chunk;
-    const int64_t ex = scan(tiles, chunk);
-    if (k < R) pref[k] = run + ex;
-    __syncthreads();
-    if (tid == 0) run += chunk;
-    __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int64_t s = warp_sums[w];
+    if (w < warp) before += s;
+    total += s;
   }
-  if (tid == 0) {
-    pref[R] = run;
-    pref[-1] = R;
-  }
+  return before + x - v;
 }
 
 template <int D, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_many_kernel(const __grid_constant__ PagedManyParams q) {
   using Sm = MSmem<D>;
-  constexpr int R = Sm::kRing, H = D / 64;
+  // The commit behind a block's S of tile j says that everything it issued up to
+  // there is done: with both blocks' the K of tile j, the V of tile j - 1 and, at a
+  // piece's end, q are free.  The producer waits for that up to R / 2 tiles behind
+  // the issuers: R / 2 barriers in turn, so that no phase is overtaken.
+  constexpr int R = Sm::kRing, H = D / 64, kS = R / 2;
   const PagedAttnParams& p = q.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -170,27 +165,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = smem + Sm::kRingOff;
   volatile ManyInfo* infos = reinterpret_cast<volatile ManyInfo*>(smem + Sm::kInfoOff);
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + Sm::kBarOff);
-  uint64_t* kv_empty = kv_full + R;
-  uint64_t* q_full = kv_empty + R;
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_empty + 1;       // [2] S of a block in TMEM
-  uint64_t* p_full = s_full + 2;        // [2] its P in TMEM (O rescaled)
+  uint64_t* q_full = kv_full + R;
+  uint64_t* s_full = q_full + 1;        // [2][kS] S of a block in TMEM, tile j's at j % kS
+  uint64_t* p_full = s_full + 2 * kS;   // [2] P of a block in TMEM (O rescaled)
   uint64_t* o_full = p_full + 2;        // [2] O complete at the end of a piece
-  uint64_t* drain = o_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = o_full + 2;         // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&p.tm_q);
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
   griddep_wait();
   griddep_launch();
   // this CTA's range of the line of tiles
+  const int utok = 2 * q.btok;
   int64_t T1;
-  int n_units;
+  __shared__ int64_t wsum[kThreads / 32], start_cum;
+  __shared__ int start_b, start_u;
+  int64_t before = 0, mine = 0;
+  int k0 = 0, k1 = 0;
+  int* uoff = reinterpret_cast<int*>(smem);        // own: units before each sequence (the q area)
   if constexpr (kPrefix) {
-    n_units = q.units;
     T1 = (int64_t)q.units * ((p.prefix_len + kTile - 1) / kTile);
   } else {
-    n_units = (int)q.pref[-1];
-    T1 = q.pref[n_units];
+    // Every CTA sums the units' tiles itself: units of all sequences first (a run
+    // of sequences per thread), then their tiles (a run of units per thread).
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+    int64_t n = 0, R64;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+      const PagedSeq s = load_seq(p, b);
+      n += (s.n + utok - 1) / utok;
+      bad |= s.bad;
+    }
+    if (bad && cta == 0) set_error(p.err, kDevPage);
+    int64_t at = block_excl(n, wsum, R64);
+    for (int b = b0; b < b1; ++b) {
+      uoff[b] = (int)at;
+      at += (load_seq(p, b).n + utok - 1) / utok;
+    }
+    __syncthreads();
+    const int units = (int)R64, pu = (units + kThreads - 1) / kThreads;
+    k0 = min(units, (int)threadIdx.x * pu);
+    k1 = min(units, k0 + pu);
+    if (k0 < k1) {
+      int lo = 0, hi = p.B;            // last sequence with uoff <= k0: it has unit k0
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (uoff[mid] <= k0) lo = mid; else hi = mid;
+      }
+      PagedSeq s = load_seq(p, lo);
+      for (int k = k0, u = k0 - uoff[lo]; k < k1; ++k, ++u) {
+        while (u * utok >= s.n) {
+          s = load_seq(p, ++lo);
+          u = 0;
+        }
+        mine += unit_tiles(unit_of(p, s, u, utok));
+      }
+    }
+    before = block_excl(mine, wsum, T1);
   }
   const int64_t T = T1 * p.Hkv;
   int nc = p.nc;
@@ -203,19 +240,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && !kPrefix) p.cut[cta].c0 = -1;
     return;
   }
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < R; ++s) {
-      mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+  if constexpr (!kPrefix) {
+    const int64_t x = t0 % T1;
+    if (mine > 0 && before <= x && x < before + mine) {    // the range begins in this thread's run
+      int lo = 0, hi = p.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (uoff[mid] <= k0) lo = mid; else hi = mid;
+      }
+      PagedSeq s = load_seq(p, lo);
+      int64_t cum = before;
+      for (int u = k0 - uoff[lo];; ++u) {
+        while (u * utok >= s.n) {
+          s = load_seq(p, ++lo);
+          u = 0;
+        }
+        const int nt = unit_tiles(unit_of(p, s, u, utok));
+        if (x < cum + nt) {
+          start_b = lo;
+          start_u = u;
+          start_cum = cum;
+          break;
+        }
+        cum += nt;
+      }
     }
+    __syncthreads();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // uoff's place takes q by TMA
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < R; ++s) mbar_init(&kv_full[s], 1);
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    for (int k = 0; k < 2 * kS; ++k) mbar_init(&s_full[k], 1);
     for (int k = 0; k < 2; ++k) {
-      mbar_init(&s_full[k], 1);
-      mbar_init(&p_full[k], 4);
+      mbar_init(&p_full[k], 5);      // the softmax warps and the other block's issuer
       mbar_init(&o_full[k], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -231,268 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    // -------------------------------------------------------------- producer
-    const int ps_lg = p.page_lg, boxes = kTile >> ps_lg;     // pages of a tile
-    const uint32_t box_bytes = (128u << ps_lg);              // 64 columns of one page
-    int g = (int)(t0 / T1), k;
-    int64_t cum;                       // tiles before unit k
-    {
-      const int64_t x = t0 - (int64_t)g * T1;
-      if constexpr (kPrefix) {
-        const int64_t nt = (p.prefix_len + kTile - 1) / kTile;
-        k = (int)(x / nt);
-        cum = k * nt;
-      } else {
-        int lo = 0, hi = n_units;      // last unit with pref <= x: 32 probes a round
-        while (hi - lo > 1) {
-          const int step = (hi - lo + 31) / 32;
-          const int i = lo + (lane + 1) * step;
-          const bool le = i < hi && q.pref[i] <= x;
-          const int c = __popc(__ballot_sync(0xffffffffu, le));
-          const int nlo = lo + c * step;
-          hi = min(hi, nlo + step);
-          lo = nlo;
-        }
-        k = lo;
-        cum = q.pref[k];
-      }
-    }
-    int64_t lin = t0;
-    int it = 0, seg = 0, qn = 0, item = 0;   // tiles, pieces, q loads, ring items so far
-    bool ok = true;
-    PagedPiece cut;
-    cut.c0 = -1;
-    auto wait_slot = [&](int i) {      // ring item i's place is free
-      if (i >= R && !mbar_wait(&kv_empty[i % R], (uint32_t)(i / R - 1) & 1u, p.err)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-    };
-    while (lin < t1 && ok) {
-      if (k >= n_units) {
-        k = 0;
-        cum = 0;
-        ++g;
-      }
-      PagedUnit u;
-      if constexpr (kPrefix) {
-        u.b = 0;
-        u.tok = k * 2 * q.btok;
-        u.ntok = min(2 * q.btok, p.N - u.tok);
-        u.r0 = u.tok;
-        u.L = u.n = 0;
-        u.lo = 0;
-        u.hi = (int)p.prefix_len;
-      } else {
-        u = q.unit[k];
-      }
-      const int j0 = u.lo / kTile, nt = (u.hi + kTile - 1) / kTile - j0;
-      const int64_t us = (int64_t)g * T1 + cum;
-      const int xa = (int)(lin - us), xb = (int)min((int64_t)nt, t1 - us);
-      const bool whole = xa == 0 && xb == nt;
-      const int dst = whole ? -1 : (lin == t0 ? 0 : 1);
-      const bool two = u.ntok > q.btok;
-      if (xa == 0) {
-        if constexpr (kPrefix) {
-          // until the own parts' kernel says otherwise a row has no own part
-          for (int t = lane; t < u.ntok; t += 32)
-            p.row_info[(int64_t)(u.r0 + t) * p.Hkv + g] = make_int4(-2, 0, 0, 0);
-        } else {
-          const int c1 = whole ? cta : (int)(((us + nt) * nc - 1) / T);
-          if (!whole) {
-            cut.c0 = cta;
-            cut.c1 = c1;
-            cut.s0 = dst;
-            cut.rows = u.ntok * p.G;
-            cut.r0 = u.r0;
-            cut.g = g;
-          }
-          if (p.row_info)
-            for (int t = lane; t < u.ntok; t += 32)
-              p.row_info[(int64_t)(u.r0 + t) * p.Hkv + g] =
-                  make_int4(whole ? -1 : cta, c1, whole ? 0 : dst,
-                            t / q.btok * 128 + t % q.btok * p.G);
-        }
-      }
-      const int32_t* row = kPrefix ? p.prefix_pages : p.table + (int64_t)u.b * p.max_blocks;
-      for (int x = xa; x < xb && ok; ++x, ++it) {
-        const int slot0 = (j0 + x) * kTile;
-        // lane: half lane / 8 of the columns (D / 64 of them), page lane % 8 of the tile
-        const int i = lane & 7, half = lane >> 3, first = slot0 + (i << ps_lg);
-        const bool take = half < H && i < boxes && first < u.hi && first + (1 << ps_lg) > u.lo;
-        int64_t page = -1;
-        if (take) page = row[first >> ps_lg];
-        const bool in = page >= 0 && page < p.n_pages;
-        if (take && !in) set_error(p.err, kDevPage);
-        const int z = in ? (int)(page * p.Hkv + g) : (int)(p.n_pages * p.Hkv);   // zeros
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, take)) * box_bytes;
-        const int at = half * (kTile * 128) + ((i << ps_lg) * 128);
-        if (x == xa) {
-          if (seg > 0 && !mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.err)) ok = false;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          ++qn;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * q.btok * p.G * D * 2);
-            for (int blk = 0; blk < (two ? 2 : 1); ++blk)
-              for (int hh = 0; hh < H; ++hh)
-                tma_3d(smem + blk * Sm::kQBlk + hh * 16384, &p.tm_q, hh * 64, g * p.G,
-                       u.r0 + blk * q.btok, q_full);
-          }
-        }
-        wait_slot(item);
-        if (!ok) break;
-        if (lane == 0) {
-          volatile ManyInfo& f = infos[it % kInfos];
-          f.slot0 = slot0;
-          f.lo = u.lo;
-          f.hi = u.hi;
-          f.first = u.L + u.tok;
-          f.ntok = u.ntok;
-          f.r0 = u.r0;
-          f.g = g;
-          f.flags = (x == xa ? 1 : 0) | (x == xb - 1 ? 2 : 0) | (two ? 8 : 0);
-          f.dst = dst;
-          mbar_arrive_expect_tx(&kv_full[item % R], bytes);
-        }
-        __syncwarp();
-        if (take) tma_3d(ring + (item % R) * Sm::kKV + at, &p.tm_k, half * 64, 0, z, &kv_full[item % R]);
-        ++item;
-        wait_slot(item);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&kv_full[item % R], bytes);
-        __syncwarp();
-        if (take) tma_3d(ring + (item % R) * Sm::kKV + at, &p.tm_v, half * 64, 0, z, &kv_full[item % R]);
-        ++item;
-      }
-      lin = us + xb;
-      cum += nt;
-      ++k;
-      ++seg;
-    }
-    if (!kPrefix && lane == 0) {
-      volatile PagedPiece& c = p.cut[cta];
-      c.c1 = cut.c1;
-      c.s0 = cut.s0;
-      c.rows = cut.rows;
-      c.r0 = cut.r0;
-      c.g = cut.g;
-      c.c0 = ok ? cut.c0 : -1;
-    }
-    if (ok) wait_slot(item);
-    if (ok) {
-      if (lane == 0) {
-        infos[it % kInfos].flags = 4;
-        mbar_arrive(&kv_full[item % R]);
-      }
-    } else {
-      // copies in flight land before shared memory goes away
-      if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1u, nullptr);
-      for (int j = max(0, item - R); j < item; ++j)
-        mbar_wait(&kv_full[j % R], (uint32_t)(j / R) & 1u, nullptr);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = tc_idesc(128, kTile, 0), id_o = tc_idesc(128, D, 1);
-      const uint32_t qa = smem_u32(smem), ra = smem_u32(ring);
-      bool ok = true;
-      int seg = -1;                    // piece of the tile whose S was issued last
-      auto issue_s = [&](int blk, int it) {   // S of block blk, tile it
-        const uint32_t kb = ra + (2 * it % R) * Sm::kKV, qb = qa + blk * Sm::kQBlk;
-        const uint32_t tS = tmem + Sm::kSCol + blk * 128;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (ks >> 2) * 16384;
-          tc_mma(tS, tc_desc_kmajor(qb + o) + ((ks & 3) * 32 >> 4),
-                 tc_desc_kmajor(kb + o) + ((ks & 3) * 32 >> 4), id_s, ks != 0);
-        }
-      };
-      auto issue_pv = [&](int blk, int it, bool acc) {
-        const uint32_t vb = ra + ((2 * it + 1) % R) * Sm::kKV;
-        const uint32_t tP = tmem + Sm::kSCol + blk * 128, tO = tmem + Sm::kOCol + blk * 128;
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          tc_mma_ts(tO, tP + kk * 8, tc_desc_mnmajor(vb + kk * 16 * 128), id_o,
-                    acc || kk != 0);
-      };
-      // K of tile it has landed (and q of a new piece); its flags
-      auto begin = [&](int it) -> int {
-        const int i = 2 * it;
-        if (!mbar_wait(&kv_full[i % R], (uint32_t)(i / R) & 1u, p.err)) return -1;
-        const int f = infos[it % kInfos].flags;
-        if (f & 4) return f;
-        if (f & 1) {
-          ++seg;
-          if (!mbar_wait(q_full, (uint32_t)seg & 1u, p.err)) return -1;
-        }
-        return f;
-      };
-      auto end_s0 = [&](int it, int f) {
-        if (f & 4) mbar_arrive(&s_full[0]);
-        else {
-          issue_s(0, it);
-          tc_commit(&s_full[0]);
-        }
-      };
-      auto end_s1 = [&](int it, int f) {
-        if (f & 4) {
-          mbar_arrive(&s_full[1]);
-          return;
-        }
-        if (f & 8) {
-          issue_s(1, it);
-          tc_commit(&s_full[1]);
-        } else {
-          mbar_arrive(&s_full[1]);
-        }
-        tc_commit(&kv_empty[2 * it % R]);
-        if (f & 2) tc_commit(q_empty);
-      };
-      int f = begin(0);
-      ok = f >= 0;
-      if (ok) {
-        tc_fence_after();
-        end_s0(0, f);
-        end_s1(0, f);
-      }
-      for (int it = 0; ok && !(f & 4); ++it) {
-        const int vi = 2 * it + 1;
-        int fn = 0;
-        if (!mbar_wait(&p_full[0], (uint32_t)it & 1u, p.err) ||
-            !mbar_wait(&kv_full[vi % R], (uint32_t)(vi / R) & 1u, p.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        issue_pv(0, it, !(f & 1));
-        if (f & 2) tc_commit(&o_full[0]);
-        fn = begin(it + 1);
-        if (fn < 0) {
-          ok = false;
-          break;
-        }
-        end_s0(it + 1, fn);
-        if (!mbar_wait(&p_full[1], (uint32_t)it & 1u, p.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (f & 8) issue_pv(1, it, !(f & 1));
-        if (f & 2) {
-          if (f & 8) tc_commit(&o_full[1]);
-          else mbar_arrive(&o_full[1]);
-        }
-        tc_commit(&kv_empty[vi % R]);
-        end_s1(it + 1, fn);
-        f = fn;
-      }
-      // issued MMAs finish before TMEM and shared memory go away
-      tc_commit(drain);
-      mbar_wait(drain, 0, nullptr);
-    }
-  } else {
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
     // --------------------------------------------------------------- softmax
-    const int blk = (warp - 2) >> 2;
+    const int blk = (warp - 4) >> 2;
     const int qt = warp & 3;                     // TMEM lane quarter of this warp
     const int r = qt * 32 + lane;                // row of the block
     const uint32_t loff = (uint32_t)(qt * 32) << 16;
@@ -505,10 +309,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // decisions before a warp-collective TMEM access are uniform over the warp
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err));
+      return __all_sync(0xffffffffu, mbar_wait_near(bar, parity, p.err));
     };
     for (int it = 0; ok; ++it) {
-      if (!wait_all(&s_full[blk], (uint32_t)it & 1u)) { ok = false; break; }
+      if (!wait_all(&s_full[blk * kS + it % kS], (uint32_t)(it / kS) & 1u)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       volatile const ManyInfo& f = infos[it % kInfos];
       const int flags = f.flags;
@@ -530,8 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = -INFINITY;
         l = 0.f;
       }
-      // rows of V that no row of the unit sees: zero before PV (block 0 for both)
-      if (blk == 0 && (slot0 < lo || slot0 + kTile > hi)) {
+      // rows of V that no row of the unit sees: zero before PV (either block's warps
+      // write the zeros before their own PV)
+      if (slot0 < lo || slot0 + kTile > hi) {
         const int vi = 2 * it + 1;
         if (!wait_all(&kv_full[vi % R], (uint32_t)(vi / R) & 1u)) { ok = false; break; }
         if (slot0 + r < lo || slot0 + r >= hi) {
@@ -565,11 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < kTile; c += 4) {
-        a0 = fmaxf(a0, sv[c]);
-        a1 = fmaxf(a1, sv[c + 1]);
-        a2 = fmaxf(a2, sv[c + 2]);
-        a3 = fmaxf(a3, sv[c + 3]);
+      for (int c = 0; c < kTile; c += 8) {
+        a0 = max3(a0, sv[c], sv[c + 1]);
+        a1 = max3(a1, sv[c + 2], sv[c + 3]);
+        a2 = max3(a2, sv[c + 4], sv[c + 5]);
+        a3 = max3(a3, sv[c + 6], sv[c + 7]);
       }
       const float mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sl2;   // log2 units
       // A row's reference maximum moves (and O, l are rescaled) only when the
@@ -580,22 +388,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mn = move ? fmaxf(m, mx) : m;
       const float alpha = (m == -INFINITY || mn == m) ? 1.f : ex2(m - mn);
       const float nref = (mn == -INFINITY) ? 0.f : -mn;
-      float s0 = 0.f, s1 = 0.f;
+      const uint64_t sl22 = pack2(sl2, sl2), nref2 = pack2(nref, nref);
+      uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) {
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float e0 = ex2(fmaf(sv[c + 2 * i], sl2, nref));
-          const float e1 = ex2(fmaf(sv[c + 2 * i + 1], sl2, nref));
-          s0 += e0;
-          s1 += e1;
+          const float2 x = unpack2(fma2(pack2(sv[c + 2 * i], sv[c + 2 * i + 1]), sl22, nref2));
+          const float e0 = ex2(x.x), e1 = ex2(x.y);
+          if (i & 1) sum1 = add2(sum1, pack2(e0, e1));
+          else sum0 = add2(sum0, pack2(e0, e1));
           const __half2 h2 = __floats2half2_rn(e0, e1);
           pk[i] = *reinterpret_cast<const uint32_t*>(&h2);
         }
         tc_st16(tS + c / 2, pk);
       }
-      l = l * alpha + (s0 + s1);
+      const float2 sum = unpack2(add2(sum0, sum1));
+      l = l * alpha + (sum.x + sum.y);
       m = mn;
       if (move && !(flags & 1)) {       // (PV of the tile before is complete: S came behind it)
 #pragma unroll
@@ -617,17 +427,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_all(&o_full[blk], (uint32_t)seg & 1u)) { ok = false; break; }
         ++seg;
         tc_fence_after();
-        const bool row_ok = rt < q.btok && t < ntok;
-        const int hq = g * p.G + (r - rt * p.G);
-        if (dst < 0 && !p.own) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          __half* d = p.out + (int64_t)(r0 + t) * p.out_stride + (int64_t)hq * D;
+        // Rows go out through this warp's 4 KB of shared memory, 128 bytes of each of
+        // its 32 rows at a time (16-byte pieces XORed by the row), so that eight
+        // lanes store one row's piece: a lane per row stored 16 bytes in each of 32
+        // lines, and a unit's end took longer than two of its tiles.
+        uint8_t* stg = smem + Sm::kStageOff + (warp - 4) * 4096;
+        const bool fin = dst < 0 && !p.own;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        int64_t off[8];                  // element offsets of rows 4 i + lane / 8
+        const int inv_g = 65536 / p.G + 1;   // x / G = x inv_g >> 16 for x < 128
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            float ov[32];
-            tc_ld32(tO + c, ov);
-            tc_wait_ld();
-            if (row_ok) {
+        for (int i = 0; i < 8; ++i) {
+          const int ri = qt * 32 + 4 * i + (lane >> 3), ti = ri * inv_g >> 16;
+          const int tu = blk * q.btok + ti, hq = g * p.G + (ri - ti * p.G);
+          const int64_t at = fin       ? (int64_t)(r0 + tu) * p.out_stride + (int64_t)hq * D
+                             : dst < 0 ? ((int64_t)(r0 + tu) * p.Hq + hq) * D
+                                       : (((int64_t)cta * 2 + dst) * p.slot_rows + blk * 128 + ri) * D;
+          off[i] = ti < q.btok && tu < ntok ? at : -1;
+        }
+        if (!fin && rt < q.btok && t < ntok) {
+          const int hq = g * p.G + (r - rt * p.G);
+          const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
+                                     : ((int64_t)cta * 2 + dst) * p.slot_rows + blk * 128 + r;
+          (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(m, l);
+        }
+        float* fd = dst < 0 ? p.own : p.part;
+#pragma unroll 1
+        for (int c = 0; c < D; c += fin ? 64 : 32) {
+          float ov[32];
+          uint4* mine = reinterpret_cast<uint4*>(stg + lane * 128);
+          tc_ld32(tO + c, ov);
+          tc_wait_ld();
+          if (fin) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              if (hh) {
+                tc_ld32(tO + c + 32, ov);
+                tc_wait_ld();
+              }
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint4 w;
@@ -635,31 +472,269 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   hp[e] = __floats2half2_rn(ov[8 * k + 2 * e] * inv, ov[8 * k + 2 * e + 1] * inv);
-                *reinterpret_cast<uint4*>(d + c + 8 * k) = w;
+                mine[(hh * 4 + k) ^ (lane & 7)] = w;
               }
             }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mine[k ^ (lane & 7)] =
+                  make_uint4(__float_as_uint(ov[4 * k]), __float_as_uint(ov[4 * k + 1]),
+                             __float_as_uint(ov[4 * k + 2]), __float_as_uint(ov[4 * k + 3]));
           }
-        } else {
-          const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
-                                     : ((int64_t)cta * 2 + dst) * p.slot_rows + blk * 128 + r;
-          float* d = (dst < 0 ? p.own : p.part) + at * D;
+          __syncwarp();
+          const int pc = lane & 7;
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            float ov[32];
-            tc_ld32(tO + c, ov);
-            tc_wait_ld();
-            if (row_ok) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<float4*>(d + c + 4 * k) =
-                    make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+          for (int i = 0; i < 8; ++i) {
+            const int ri = 4 * i + (lane >> 3);
+            const uint4 w = *reinterpret_cast<const uint4*>(stg + ri * 128 + ((pc ^ (ri & 7)) << 4));
+            if (off[i] >= 0) {
+              if (fin) *reinterpret_cast<uint4*>(p.out + off[i] + c + pc * 8) = w;
+              else *reinterpret_cast<uint4*>(fd + off[i] + c + pc * 4) = w;
             }
           }
-          if (row_ok) (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(m, l);
+          __syncwarp();
         }
         tc_fence_before();
       }
     }
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
+    const int ps_lg = p.page_lg, boxes = kTile >> ps_lg;     // pages of a tile
+    const uint32_t box_bytes = (128u << ps_lg);              // 64 columns of one page
+    int g = (int)(t0 / T1);
+    int b, ui;                         // sequence (prefix: 0) and unit in it
+    int64_t cum;                       // tiles before that unit
+    int base32 = -1;
+    PagedSeq mys = {};
+    if constexpr (kPrefix) {
+      const int64_t nt = (p.prefix_len + kTile - 1) / kTile;
+      b = 0;
+      ui = (int)((t0 - (int64_t)g * T1) / nt);
+      cum = ui * nt;
+    } else {
+      b = start_b;
+      ui = start_u;
+      cum = start_cum;
+    }
+    int64_t lin = t0;
+    int it = 0, seg = 0, qn = 0, item = 0;   // tiles, pieces, q loads, ring items so far
+    bool ok = true;
+    PagedPiece cut;
+    cut.c0 = -1;
+    auto wait_s = [&](int j) {         // both S of tile j are done (j < 0: nothing to wait for)
+      if (j >= 0 &&
+          (!mbar_wait_near(&s_full[j % kS], (uint32_t)(j / kS) & 1u, p.err) ||
+           !mbar_wait_near(&s_full[kS + j % kS], (uint32_t)(j / kS) & 1u, p.err)))
+        ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    while (lin < t1 && ok) {
+      Unit u;
+      if constexpr (kPrefix) {
+        if (ui >= q.units) {
+          ui = 0;
+          cum = 0;
+          ++g;
+        }
+        u.tok = ui * utok;
+        u.ntok = min(utok, p.N - u.tok);
+        u.r0 = u.tok;
+        u.L = 0;
+        u.lo = 0;
+        u.hi = (int)p.prefix_len;
+      } else {
+        if (b >= p.B) {                // the next kv head begins again with the first sequence
+          b = 0;
+          ui = 0;
+          cum = 0;
+          ++g;
+        }
+        if ((b & ~31) != base32) {     // 32 sequences at a time, one per lane
+          base32 = b & ~31;
+          mys = base32 + lane < p.B ? load_seq(p, base32 + lane) : PagedSeq{};
+        }
+        PagedSeq s;
+        s.r0 = __shfl_sync(0xffffffffu, mys.r0, b & 31);
+        s.n = __shfl_sync(0xffffffffu, mys.n, b & 31);
+        s.L = __shfl_sync(0xffffffffu, mys.L, b & 31);
+        if (ui * utok >= s.n) {
+          ++b;
+          ui = 0;
+          continue;
+        }
+        u = unit_of(p, s, ui, utok);
+      }
+      const int j0 = u.lo / kTile, nt = (u.hi + kTile - 1) / kTile - j0;
+      const int64_t us = (int64_t)g * T1 + cum;
+      const int xa = (int)(lin - us), xb = (int)min((int64_t)nt, t1 - us);
+      const bool whole = xa == 0 && xb == nt;
+      const int dst = whole ? -1 : (lin == t0 ? 0 : 1);
+      const bool two = u.ntok > q.btok;
+      if (xa == 0) {
+        if constexpr (kPrefix) {
+          // until the own parts' kernel says otherwise a row has no own part
+          for (int t = lane; t < u.ntok; t += 32)
+            p.row_info[(int64_t)(u.r0 + t) * p.Hkv + g] = make_int4(-2, 0, 0, 0);
+        } else {
+          const int c1 = whole ? cta : (int)(((us + nt) * nc - 1) / T);
+          if (!whole) {
+            cut.c0 = cta;
+            cut.c1 = c1;
+            cut.s0 = dst;
+            cut.rows = u.ntok * p.G;
+            cut.r0 = u.r0;
+            cut.g = g;
+          }
+          if (p.row_info)
+            for (int t = lane; t < u.ntok; t += 32)
+              p.row_info[(int64_t)(u.r0 + t) * p.Hkv + g] =
+                  make_int4(whole ? -1 : cta, c1, whole ? 0 : dst,
+                            t / q.btok * 128 + t % q.btok * p.G);
+        }
+      }
+      const int32_t* row = kPrefix ? p.prefix_pages : p.table + (int64_t)b * p.max_blocks;
+      for (int x = xa; x < xb && ok; ++x, ++it) {
+        const int slot0 = (j0 + x) * kTile;
+        // lane: half lane / 8 of the columns (D / 64 of them), page lane % 8 of the tile
+        const int i = lane & 7, half = lane >> 3, first = slot0 + (i << ps_lg);
+        const bool take = half < H && i < boxes && first < u.hi && first + (1 << ps_lg) > u.lo;
+        int64_t page = -1;
+        if (take) page = row[first >> ps_lg];
+        const bool in = page >= 0 && page < p.n_pages;
+        if (take && !in) set_error(p.err, kDevPage);
+        const int z = in ? (int)(page * p.Hkv + g) : (int)(p.n_pages * p.Hkv);   // zeros
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, take)) * box_bytes;
+        const int at = half * (kTile * 128) + ((i << ps_lg) * 128);
+        wait_s(it - R / 2);           // K of that tile gives its place
+        if (!ok) break;
+        if (lane == 0) {
+          volatile ManyInfo& f = infos[it % kInfos];
+          f.slot0 = slot0;
+          f.lo = u.lo;
+          f.hi = u.hi;
+          f.first = u.L + u.tok;
+          f.ntok = u.ntok;
+          f.r0 = u.r0;
+          f.g = g;
+          f.flags = (x == xa ? 1 : 0) | (x == xb - 1 ? 2 : 0) | (two ? 8 : 0);
+          f.dst = dst;
+          mbar_arrive_expect_tx(&kv_full[item % R], bytes);
+        }
+        __syncwarp();
+        if (take) tma_3d(ring + (item % R) * Sm::kKV + at, &p.tm_k, half * 64, 0, z, &kv_full[item % R]);
+        ++item;
+        if (x == xa) {
+          wait_s(it - 1);             // q of the piece before is used up
+          if (!ok) break;
+          ++qn;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * q.btok * p.G * D * 2);
+            for (int blk = 0; blk < (two ? 2 : 1); ++blk)
+              for (int hh = 0; hh < H; ++hh)
+                tma_3d(smem + blk * Sm::kQBlk + hh * 16384, &p.tm_q, hh * 64, g * p.G,
+                       u.r0 + blk * q.btok, q_full);
+          }
+        }
+        wait_s(it - R / 2 + 1);       // V of the tile before that one
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&kv_full[item % R], bytes);
+        __syncwarp();
+        if (take) tma_3d(ring + (item % R) * Sm::kKV + at, &p.tm_v, half * 64, 0, z, &kv_full[item % R]);
+        ++item;
+      }
+      lin = us + xb;
+      cum += nt;
+      ++ui;
+      ++seg;
+    }
+    if (!kPrefix && lane == 0) {
+      volatile PagedPiece& c = p.cut[cta];
+      c.c1 = cut.c1;
+      c.s0 = cut.s0;
+      c.rows = cut.rows;
+      c.r0 = cut.r0;
+      c.g = cut.g;
+      c.c0 = ok ? cut.c0 : -1;
+    }
+    if (ok) wait_s(it - R / 2);
+    if (ok) {
+      if (lane == 0) {
+        infos[it % kInfos].flags = 4;
+        mbar_arrive(&kv_full[item % R]);
+      }
+    } else {
+      // copies in flight land before shared memory goes away
+      if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1u, nullptr);
+      for (int j = max(0, item - R); j < item; ++j)
+        mbar_wait(&kv_full[j % R], (uint32_t)(j / R) & 1u, nullptr);
+    }
+  } else if (warp < 3) {
+    // -------------------------------------------- MMA issuer of block warp - 1
+    if (lane == 0) {
+      constexpr uint32_t id_s = tc_idesc(128, kTile, 0), id_o = tc_idesc(128, D, 1);
+      const int blk = warp - 1;
+      const uint32_t qb = smem_u32(smem) + blk * Sm::kQBlk, ra = smem_u32(ring);
+      const uint32_t tS = tmem + Sm::kSCol + blk * 128, tO = tmem + Sm::kOCol + blk * 128;
+      int seg = -1;                    // piece of the tile whose S was issued last
+      auto landed = [&](int i) {       // ring item i
+        return mbar_wait_near(&kv_full[i % R], (uint32_t)(i / R) & 1u, p.err);
+      };
+      // S of tile it (flags f).  At the end of the range, or where the unit has no
+      // rows in this block, the commit alone.
+      auto start_s = [&](int it, int f) -> bool {
+        if (f & 1) {                   // a new piece: its q
+          ++seg;
+          if (!mbar_wait_near(q_full, (uint32_t)seg & 1u, p.err)) return false;
+        }
+        tc_fence_after();
+        if (!(f & 4) && (blk == 0 || (f & 8))) {
+          const uint32_t kb = ra + (2 * it % R) * Sm::kKV;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (ks >> 2) * 16384;
+            tc_mma(tS, tc_desc_kmajor(qb + o) + ((ks & 3) * 32 >> 4),
+                   tc_desc_kmajor(kb + o) + ((ks & 3) * 32 >> 4), id_s, ks != 0);
+          }
+        }
+        if (blk == 1 || it > 0) mbar_arrive(&p_full[1 - blk]);
+        tc_commit(&s_full[blk * kS + it % kS]);
+        return true;
+      };
+      // The issuers take turns, block 0 first, so that the blocks' softmaxes stay half
+      // a tile apart: issuing whenever P was there they fell into step (both softmaxes,
+      // then both blocks' products: 4500 clocks a tile).  The turn is an arrival on the
+      // other block's p_full: one wait for both.
+      int f = 0;
+      bool ok = landed(0);
+      if (ok) {
+        f = infos[0].flags;
+        ok = start_s(0, f);
+      }
+      for (int it = 0; ok && !(f & 4); ++it) {
+        // everything but P first: while the softmax works this thread has the time
+        if (!landed(2 * it + 1) || !landed(2 * it + 2)) break;
+        const int fn = infos[(it + 1) % kInfos].flags;
+        if (!mbar_wait_near(&p_full[blk], (uint32_t)it & 1u, p.err)) break;
+        tc_fence_after();
+        if (blk == 0 || (f & 8)) {
+          const uint32_t vb = ra + ((2 * it + 1) % R) * Sm::kKV;
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc_mma_ts(tO, tS + kk * 8, tc_desc_mnmajor(vb + kk * 16 * 128), id_o,
+                      !(f & 1) || kk != 0);
+        }
+        if (f & 2) tc_commit(&o_full[blk]);
+        if (!start_s(it + 1, fn)) break;
+        f = fn;
+      }
+      // issued MMAs finish before TMEM and shared memory go away
+      tc_commit(&drain[blk]);
+      mbar_wait(&drain[blk], 0, nullptr);
+    }
+  }
   }
   tc_fence_before();
   __syncthreads();
@@ -687,29 +762,18 @@ cudaError_t launch_many(const PagedManyParams& p, cudaStream_t s, bool pdl) {
 
 template <int D, bool kPrefix>
 cudaError_t configure_one() {
+  cudaFuncAttributes fa;
+  const cudaError_t e = cudaFuncGetAttributes(&fa, paged_many_kernel<D, kPrefix>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;   // see kRegsLaunch
   return cudaFuncSetAttribute(paged_many_kernel<D, kPrefix>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MSmem<D>::kBytes);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_sched(const PagedManyParams& p, int64_t* pref, PagedUnit* unit,
-                               cudaStream_t s, bool pdl) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(1024);
-  cfg.dynamicSmemBytes = (size_t)(p.a.B + 1) * sizeof(int);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_sched_kernel, p, pref, unit);
-}
-
 cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl) {
-  if (p.a.nc < 1 || p.a.nc > 512 || p.units < 1) return cudaErrorInvalidValue;
+  if (p.a.nc < 1 || p.a.nc > 512 || (p.prefix && p.units < 1)) return cudaErrorInvalidValue;
   if (p.a.D == 128)
     return p.prefix ? launch_many<128, true>(p, s, pdl) : launch_many<128, false>(p, s, pdl);
   if (p.a.D == 64)
