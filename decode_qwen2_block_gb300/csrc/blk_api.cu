@@ -1306,12 +1306,35 @@ PagedWs paged_ws(const blk_config& c, int64_t N, bool prefix, int num_sms) {
   return w;
 }
 
+// Whether a shared prefix gets a launch of its own: its keys are then read once for
+// all rows, which fill the tensor core's row blocks together, but every row's two
+// parts have to be merged.  Otherwise each sequence takes the prefix's pages with its
+// own (from L2).  Estimated in microseconds on 152 SMs: 10 for the launch and the
+// merge's start, 0.0125 a 128-slot tile of 256 rows on the many-row kernel, three
+// fp32 rows written and read at 3 TB/s; the few-row kernel passes 300 (16 rows) or
+// 200 (32) 64-slot tiles in one.  Of 72 measured batches (3 head layouts, 1 / 4 / 60 new
+// tokens, 8 - 64 sequences, prefixes of 1024 - 16384) the rule took the slower side of
+// six, by 5 % at most.  For instance 12 / 2 heads, one new token: 8 sequences behind
+// 1024 slots 10.9 us with their own against 17.4, 64 behind 8192 64 against 32.
+bool share_prefix(const blk_config& c, const blk_paged_batch* b) {
+  const int G = c.n_heads / c.n_kv_heads;
+  const int64_t utok = 2 * paged_btok(G), tiles = (b->prefix_len + kPagedManyTile - 1) / kPagedManyTile;
+  const double tile = 0.0125 * c.n_kv_heads * tiles;     // a unit of every kv head
+  const double alone = 10 + tile * ((b->n_rows + utok - 1) / utok) +
+                       (double)b->n_rows * c.n_heads * c.head_dim * 12 / 3e6;
+  const double with_own =
+      paged_few_rows(G, b->max_new)
+          ? b->n_seqs * c.n_kv_heads * tiles * 2 / (b->max_new * G <= 16 ? 300.0 : 200.0)
+          : tile * b->n_seqs * ((b->max_new + utok - 1) / utok);
+  return with_own > alone;
+}
+
 int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_t q_stride,
                    const void* k_pages, const void* v_pages, void* out, int64_t out_stride,
                    unsigned char* base, cudaStream_t s, Timer& tm) {
   const blk_config& c = h->cfg;
   const int D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads, G = Hq / Hkv;
-  const bool prefix = b->prefix_len > 0;
+  const bool prefix = b->prefix_len > 0 && share_prefix(c, b);
   const PagedWs lay = paged_ws(c, b->n_rows, prefix, h->num_sms);
   const int64_t page = b->page_size, heads = b->n_pages * Hkv;
   PagedManyParams m = {};
@@ -1322,6 +1345,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   a.table = b->block_table; a.prefix_pages = b->prefix_pages;
   a.max_blocks = b->max_blocks; a.n_pages = b->n_pages; a.window = h->window;
   a.max_len = b->max_len; a.prefix_len = b->prefix_len;
+  a.pre_here = prefix ? 0 : b->prefix_len;
   a.B = (int)b->n_seqs; a.N = (int)b->n_rows; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.G = G;
   a.page_lg = page_log2(page); a.max_new = (int)b->max_new;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));

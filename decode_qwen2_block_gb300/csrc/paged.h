@@ -50,14 +50,16 @@ cudaError_t launch_page_append(const PageAppendParams& p, int num_sms, cudaStrea
 // (a group of rows of one sequence and one kv head) are numbered in one line
 // and CTA i takes tiles [i T / n, (i + 1) T / n).  A unit inside one CTA is
 // finished there; of a cut unit every CTA leaves a partial (its unnormalised
-// O, maximum m in log2 units and sum l, fp32) in one of its two slots: slot 0
-// when the piece opens the CTA's range, else slot 1.
-struct PagedPiece {            // what merging needs of one cut unit
-  int c0, c1;                  // CTAs that hold its pieces, in order (c0 = -1: none)
-  int s0;                      // slot of the piece in c0 (0 in the others)
+// O, maximum m in log2 units and sum l, fp32) in one of its two slots: slot 1 of
+// the piece that begins the unit, slot 0 of those that go on.  In the line a unit
+// also has a head before its first tile, for what its begin and end cost.
+struct alignas(8) PagedPiece { // what merging needs of one cut unit
+  int c0;                      // first CTA that holds a piece of it (-1: no unit)
   int rows;                    // partial rows of the unit
+  int c1;                      // last CTA that holds a piece
   int r0;                      // batch row of its first token
   int g;                       // kv head
+  int pad;
 };
 
 struct PagedAttnParams {
@@ -75,7 +77,9 @@ struct PagedAttnParams {
   int64_t max_blocks, n_pages, window;
   int64_t max_len;             // slots of the longest sequence, new ones with it; it fits the
                                //   table's rows and 31 bits
-  int64_t prefix_len;          // slots below it are the shared prefix's
+  int64_t prefix_len;          // every sequence has at least the shared prefix's slots
+  int64_t pre_here;            // slots of it that the own parts take with them (their pages from
+                               //   prefix_pages); the others belong to the prefix's own launch
   int B, N, Hq, Hkv, D, G, page_lg, max_new;
   float scale_log2;
   int nc;                      // CTAs of the kernel
@@ -88,12 +92,12 @@ struct PagedAttnParams {
   // part is
   float* own;                  // [N][Hq][D]
   float2* own_ml;              // [N][Hq]
-  int4* row_info;              // [N][Hkv]: c0 (-1 whole, -2 no part), c1, s0, partial row of head 0
+  int4* row_info;              // [N][Hkv]: c0 (-1 whole, -2 no part), c1, 0, partial row of head 0
   int* err;
 };
 
 // Rows of one unit that the few-row kernel takes (16 per MMA row tile).
-constexpr int kPagedFewRows = 64;
+constexpr int kPagedFewRows = 32;
 bool paged_few_rows(int G, int64_t max_new);
 size_t paged_few_part_rows(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows);
 cudaError_t launch_paged_few(const PagedAttnParams& p, cudaStream_t s, bool pdl);
@@ -110,6 +114,10 @@ struct PagedManyParams {
 inline int paged_btok(int G) { return 128 / G; }
 constexpr int kPagedManyRows = 256;     // partial rows of a slot
 constexpr int kPagedManyTile = 128;     // slots of a tile
+#ifndef HEADMANY
+#define HEADMANY 3
+#endif
+constexpr int kPagedManyHead = HEADMANY;       // a unit's begin and end in the line, in tiles
 cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl);
 cudaError_t configure_paged_many();
 

@@ -34,11 +34,21 @@ __device__ __forceinline__ PagedSeq load_seq(const PagedAttnParams& p, int b) {
   return s;
 }
 
-// First slot that the rows from slot `first` on see here (the shared prefix's
-// slots are not a sequence's own).
+// First slot that the rows from slot `first` on see here (the prefix's slots only
+// where it has no launch of its own).
 __device__ __forceinline__ int paged_lo(const PagedAttnParams& p, int first) {
   const int64_t w = window_lo(p.window, first);
-  return (int)(w > p.prefix_len ? w : p.prefix_len);
+  const int64_t own = p.prefix_len - p.pre_here;
+  return (int)(w > own ? w : own);
+}
+
+// T * i / n and x / y of non-negative values, in 32 bits where they fit (a 64-bit
+// division takes some 100 clocks, and every CTA begins with a few).
+__device__ __forceinline__ int64_t range_of(int64_t T, int i, int n) {
+  return T < (1 << 20) ? (int64_t)((uint32_t)((uint32_t)T * (uint32_t)i) / (uint32_t)n) : T * i / n;
+}
+__device__ __forceinline__ int small_div(int64_t x, int64_t y) {
+  return ((x | y) >> 31) == 0 ? (int)((uint32_t)x / (uint32_t)y) : (int)(x / y);
 }
 
 }  // namespace blk

@@ -1,5 +1,5 @@
 // Attention over a paged K/V cache for few new rows per sequence (decode, or a
-// few drafted tokens): at most 64 rows (token, query head of the kv head's
+// few drafted tokens): at most 32 rows (token, query head of the kv head's
 // group) of one sequence share a pass over its K/V.
 //
 //   out[r, h] = softmax(q[r, h] . K / sqrt(D)) V  over the slots row r sees,
@@ -15,7 +15,7 @@
 //              TMA with the 128-byte swizzle; the unit's q rows come with its
 //              first tile as bulk copies into rows padded by 16 bytes.
 //   warps 0-3  16 slots each: S = Q K^T by mma.sync m16n8k16 (the rows are the M
-//              side: at most 64, a tcgen05 MMA's 128 rows would be padding),
+//              side: at most 32, a tcgen05 MMA's 128 rows would be padding),
 //              the row maxima meet in shared memory, P (fp16, in [0, 1]: the
 //              rounding is at most 2^-11 of a weight) goes there too, and each
 //              warp forms O for its quarter of the columns over all 64 slots.
@@ -36,6 +36,12 @@ namespace {
 constexpr int kTile = 64;            // slots of a tile
 constexpr int kConsumers = 128, kThreads = 160;
 constexpr int kMinTiles = 2;         // tiles that a CTA takes at least, where there are any
+// What a unit's beginning and end (q, the pieces' ends) count for in the line, in
+// tiles; they lie before its first tile.
+#ifndef HEADFEW
+#define HEADFEW 1
+#endif
+constexpr int kHead = HEADFEW;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -87,17 +93,16 @@ struct TileInfo {      // what the consumers need of a tile
 template <int D, int MT>
 struct FSmem {
   static constexpr int kKV = kTile * D * 2;                     // K or V of a tile
-  static constexpr int kStages = (MT == 4 ? 65536 : 98304) / (2 * kKV);
-  static constexpr int kQBufs = MT == 1 ? 2 : 1;
+  static constexpr int kStages = 98304 / (2 * kKV);
   static constexpr int kQStride = D * 2 + 16;                   // bytes (conflict-free ldmatrix)
   static constexpr int kQBytes = 16 * MT * kQStride;
   static constexpr int kPStride = kTile * 2 + 16;
   static constexpr int kQOff = kStages * 2 * kKV;
-  static constexpr int kPOff = kQOff + kQBufs * kQBytes;
-  static constexpr int kStatOff = kPOff + 16 * MT * kPStride;   // [4 warps][16 MT] floats
+  static constexpr int kPOff = kQOff + kQBytes;
+  static constexpr int kStatOff = kPOff + 16 * MT * kPStride;   // [16 MT][4 warps] floats
   static constexpr int kInfoOff = kStatOff + 4 * 16 * MT * 4;
   static constexpr int kBarOff = (kInfoOff + kStages * (int)sizeof(TileInfo) + 15) / 16 * 16;
-  static constexpr int kEnd = kBarOff + (2 * kStages + 2 * kQBufs) * 8 + 64;
+  static constexpr int kEnd = kBarOff + (2 * kStages + 1) * 8 + 64;
   static constexpr size_t kBytes = (size_t)kEnd + 1024;         // the ring is 1024-aligned
 };
 
@@ -105,12 +110,15 @@ __device__ __forceinline__ int seq_tiles(const PagedAttnParams& p, const PagedSe
   if (s.n == 0) return 0;
   return (s.L + s.n + kTile - 1) / kTile - paged_lo(p, s.L) / kTile;
 }
+__device__ __forceinline__ int seq_weight(const PagedAttnParams& p, const PagedSeq& s) {
+  return s.n == 0 ? 0 : seq_tiles(p, s) + kHead;
+}
 
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_few_kernel(const __grid_constant__ PagedAttnParams p) {
   using Sm = FSmem<D, MT>;
-  constexpr int S = Sm::kStages, QB = Sm::kQBufs;
+  constexpr int S = Sm::kStages;
   constexpr int kCPR = D / 8;           // 16-byte pieces of a row
   constexpr int kNT = D / 32;           // 8-column tiles of O per warp
   extern __shared__ uint8_t smem_raw[];
@@ -128,6 +136,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ int64_t start_cum;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if (tid == 0) {
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
   griddep_wait();
   griddep_launch();
   if (tid == 0) {
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 4);
     }
-    for (int s = 0; s < QB; ++s) mbar_init(&q_empty[s], 4);
+    mbar_init(q_empty, 4);
     fence_mbar_init();
     start_b = 0;
     start_cum = 0;
@@ -146,10 +158,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   int64_t mine = 0;
   bool bad = false;
+  // (the first 128 sequences go to the producer through P's place, still unused)
+  PagedSeq* first_seqs = reinterpret_cast<PagedSeq*>(smem + Sm::kPOff);
+  static_assert(sizeof(PagedSeq) * 128 <= 16 * MT * Sm::kPStride, "room for 128 sequences");
   for (int b = b0; b < b1; ++b) {
     const PagedSeq s = load_seq(p, b);
-    mine += seq_tiles(p, s);
+    mine += seq_weight(p, s);
     bad |= s.bad;
+    if (b < 128) first_seqs[b] = s;
   }
   if (bad && blockIdx.x == 0) set_error(p.err, kDevPage);
   int64_t inc = mine;
@@ -171,19 +187,20 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t enough = (T + kMinTiles - 1) / kMinTiles;
   const int nc = (int)(enough < p.nc ? (enough < 1 ? 1 : enough) : p.nc);
   const int cta = blockIdx.x;
-  const int64_t t0 = cta < nc ? T * cta / nc : T, t1 = cta < nc ? T * (cta + 1) / nc : T;
+  const int64_t t0 = cta < nc ? range_of(T, cta, nc) : T, t1 = cta < nc ? range_of(T, cta + 1, nc) : T;
   if (t0 >= t1) {   // (uniform over the CTA)
     if (tid == 0) p.cut[cta].c0 = -1;
     return;
   }
-  const int64_t x0 = t0 % T1;
+  const int g0 = small_div(t0, T1);
+  const int64_t x0 = t0 - g0 * T1;
   if (mine > 0 && before <= x0 && x0 < before + mine) {
     int64_t cum = before;
     int b = b0;
-    for (;; ++b) {
-      const int nt = seq_tiles(p, load_seq(p, b));
-      if (x0 < cum + nt) break;
-      cum += nt;
+    for (; b + 1 < b1; ++b) {
+      const int wt = seq_weight(p, load_seq(p, b));
+      if (x0 < cum + wt) break;
+      cum += wt;
     }
     start_b = b;
     start_cum = cum;
@@ -195,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int bs_lg = p.page_lg < 6 ? p.page_lg : 6, bs = 1 << bs_lg;   // slots of a box
     const int boxes = kTile >> bs_lg;
     const uint32_t box_bytes = (uint32_t)bs * D * 2;
-    int b = start_b, g = (int)(t0 / T1);
+    int b = start_b, g = g0;
     int64_t cum = start_cum, lin = t0;
     int it = 0, seg = 0, base32 = -1;
     PagedSeq mys = {};
@@ -210,7 +227,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if ((b & ~31) != base32) {
         base32 = b & ~31;
-        if (base32 + lane < p.B) mys = load_seq(p, base32 + lane);
+        if (it == 0 && seg == 0 && base32 < 128) mys = base32 + lane < p.B ? first_seqs[base32 + lane] : PagedSeq{};
+        else if (base32 + lane < p.B) mys = load_seq(p, base32 + lane);
         else mys = PagedSeq{};
       }
       PagedSeq s;
@@ -223,15 +241,22 @@ __global__ void __launch_bounds__(kThreads, 2)
         continue;
       }
       const int64_t us = (int64_t)g * T1 + cum;      // the unit's first tile in the line
-      const int xa = (int)(lin - us), xb = (int)min((int64_t)nt, t1 - us);
+      const int64_t ue = us + kHead + nt;
+      const int xa = (int)max((int64_t)0, lin - us - kHead);
+      const int xb = (int)min((int64_t)nt, t1 - us - kHead);
+      lin = ue;
+      cum += nt + kHead;
+      if (xb <= xa) {        // its head alone lies here
+        ++b;
+        continue;
+      }
       const bool whole = xa == 0 && xb == nt;
-      const int dst = whole ? -1 : (lin == t0 ? 0 : 1);
+      const int dst = whole ? -1 : (xa == 0 ? 1 : 0);
       if (xa == 0) {
-        const int c1 = whole ? cta : (int)(((us + nt) * nc - 1) / T);
+        const int c1 = whole ? cta : (int)((ue * nc - 1) / T);
         if (!whole) {
           cut.c0 = cta;
           cut.c1 = c1;
-          cut.s0 = dst;
           cut.rows = s.n * p.G;
           cut.r0 = s.r0;
           cut.g = g;
@@ -239,11 +264,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (p.row_info)
           for (int t = lane; t < s.n; t += 32)
             p.row_info[(int64_t)(s.r0 + t) * p.Hkv + g] =
-                make_int4(whole ? -1 : cta, c1, whole ? 0 : dst, t * p.G);
+                make_int4(whole ? -1 : cta, c1, 0, t * p.G);
       }
       const int lo = paged_lo(p, s.L), hi = s.L + s.n, j0 = lo / kTile;
       const int32_t* row = p.table + (int64_t)b * p.max_blocks;
-      const int qb = seg % QB;
       for (int x = xa; x < xb; ++x, ++it) {
         const int st = it % S;
         const int slot0 = (j0 + x) * kTile;
@@ -251,12 +275,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int i = lane & 15, first = slot0 + (i << bs_lg);
         const bool take = i < boxes && first < hi && first + bs > lo;
         int64_t page = -1;
-        if (take) page = row[first >> p.page_lg];
+        if (take) page = (first < p.pre_here ? p.prefix_pages : row)[first >> p.page_lg];
         const bool in = page >= 0 && page < p.n_pages;
         if (take && !in) set_error(p.err, kDevPage);
         if (it >= S && !mbar_wait_near(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
-        if (x == xa && seg >= QB &&
-            !mbar_wait(&q_empty[qb], (uint32_t)(seg / QB - 1) & 1u, p.err))
+        if (x == xa && seg > 0 && !mbar_wait_near(q_empty, (uint32_t)(seg - 1) & 1u, p.err))
           ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -285,20 +308,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         for (int r = lane; r < qrows; r += 32) {
           const int t = r / p.G, hh = r - t * p.G;
-          bulk_g2s(smem + Sm::kQOff + qb * Sm::kQBytes + r * Sm::kQStride,
+          bulk_g2s(smem + Sm::kQOff + r * Sm::kQStride,
                    p.q + (int64_t)(s.r0 + t) * p.q_stride + (int64_t)(g * p.G + hh) * D, D * 2,
                    &full[st]);
         }
       }
-      lin = us + xb;
-      cum += nt;
       ++b;
       ++seg;
     }
     if (lane == 0) {
       volatile PagedPiece& c = p.cut[cta];
       c.c1 = cut.c1;
-      c.s0 = cut.s0;
       c.rows = cut.rows;
       c.r0 = cut.r0;
       c.g = cut.g;
@@ -327,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float sl2 = p.scale_log2;
   float m_r[MT][2], l_r[MT][2], O[MT][kNT][4];
   int last[MT][2], low[MT][2];
-  int seg = 0;
+  uint32_t qf[D / 16][MT][4];          // the unit's q: A fragments
   // A K or V tile is boxes [D / 64][bs slots][128 B] with the 128-byte swizzle:
   // row r, 16-byte piece c is at row_off(r) + (c / 8) half + ((c % 8 ^ r % 8) << 4).
   const int half = 128 << bs_lg;
@@ -348,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int k = 0; k < 4; ++k) v_row[k] = row_off(k * 16);
   }
-  const uint32_t q_lane = ((mm & 1) * 8 + (lane & 7)) * Sm::kQStride + (mm >> 1) * 16;
+  const uint32_t q_lane = qbase + ((mm & 1) * 8 + (lane & 7)) * Sm::kQStride + (mm >> 1) * 16;
   const uint32_t p_lane = pbase + ((mm & 1) * 8 + (lane & 7)) * Sm::kPStride + (mm >> 1) * 16;
   const uint32_t p_st = pbase + grp * Sm::kPStride + (slab + 2 * tig) * 2;
   for (int it = 0;; ++it) {
@@ -374,7 +394,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int i = 0; i < kNT; ++i) O[mt][i][2 * h2] = O[mt][i][2 * h2 + 1] = 0.f;
         }
     }
-    const uint32_t qs = qbase + (seg % QB) * Sm::kQBytes + q_lane;
+    if (flags & 1) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) ldsm_x4(q_lane + mt * 16 * Sm::kQStride + ks * 32, qf[ks][mt]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty);       // q's place is free
+    }
     const bool active = slab < vhi && slab + 16 > vlo;
     // every row sees every slot of this warp's 16: n - 1 slots from the end are
     // behind the first row, windows begin at most n - 1 slots behind vlo
@@ -392,10 +419,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         ldsm_x4(kb + k_off[ks & 3] + (ks >> 2) * half, bk);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          uint32_t a[4];
-          ldsm_x4(qs + mt * 16 * Sm::kQStride + ks * 32, a);
-          mma16816(sc[mt][0], a, bk[0], bk[1]);
-          mma16816(sc[mt][1], a, bk[2], bk[3]);
+          mma16816(sc[mt][0], qf[ks][mt], bk[0], bk[1]);
+          mma16816(sc[mt][1], qf[ks][mt], bk[2], bk[3]);
         }
       }
     }
@@ -421,13 +446,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                          fmaxf(sc[mt][1][2 * h2], sc[mt][1][2 * h2 + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (tig == 0) stat[warp * 16 * MT + mt * 16 + grp + 8 * h2] = mx;
+        if (tig == 0) stat[(mt * 16 + grp + 8 * h2) * 4 + warp] = mx;
       }
     named_sync(1, kConsumers);
     // a wait that ran out stops all four warps here: the next flag is set behind the
     // second barrier
     if (*(volatile int*)&abort_s) return;
-    if ((flags & 2) && lane == 0) mbar_arrive(&q_empty[seg % QB]);   // q has been used
     float corr[MT][2];
     bool moved = false;
 #pragma unroll
@@ -435,9 +459,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
         const int row = mt * 16 + grp + 8 * h2;
-        float mx = stat[row];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) mx = fmaxf(mx, stat[w * 16 * MT + row]);
+        const float4 m4 = *reinterpret_cast<const float4*>(stat + row * 4);
+        const float mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
         const float mn = fmaxf(m_r[mt][h2], mx * sl2);       // log2 units
         corr[mt][h2] = mn == -INFINITY ? 1.f : ex2(m_r[mt][h2] - mn);
         moved |= mn != m_r[mt][h2];
@@ -504,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           float l = l_r[mt][h2];
           l += __shfl_xor_sync(0xffffffffu, l, 1);
           l += __shfl_xor_sync(0xffffffffu, l, 2);
-          if (tig == 0) stat[warp * 16 * MT + mt * 16 + grp + 8 * h2] = l;
+          if (tig == 0) stat[(mt * 16 + grp + 8 * h2) * 4 + warp] = l;
         }
       named_sync(1, kConsumers);
 #pragma unroll
@@ -513,9 +536,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int h2 = 0; h2 < 2; ++h2) {
           const int row = mt * 16 + grp + 8 * h2;
           if (row >= rows) continue;
-          float l = 0.f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) l += stat[w * 16 * MT + row];
+          const float4 l4 = *reinterpret_cast<const float4*>(stat + row * 4);
+          const float l = (l4.x + l4.y) + (l4.z + l4.w);
           const int t = row / p.G, hq = g * p.G + (row - t * p.G);
           const int col = warp * (D / 4) + 2 * tig;
           if (dst < 0 && !p.own) {
@@ -537,7 +559,6 @@ __global__ void __launch_bounds__(kThreads, 2)
               (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(m_r[mt][h2], l);
           }
         }
-      ++seg;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
@@ -555,7 +576,6 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   constexpr int kV = D / 32;
   const PagedAttnParams& p = q.a;
   __shared__ float sacc[kWPR > 1 ? 8 : 1][D + 2];
-  __shared__ PagedPiece cuts[512];
   __shared__ int cut_row[512], wsum[8];
   griddep_wait();
   griddep_launch();
@@ -568,8 +588,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
     for (int k = 0; k < 2; ++k) {
       const int i = 2 * tid + k;
       if (i < p.nc) {
-        cuts[i] = p.cut[i];
-        n2[k] = cuts[i].c0 >= 0 ? cuts[i].rows : 0;
+        const int2 h = *reinterpret_cast<const int2*>(&p.cut[i]);     // c0, rows
+        n2[k] = h.x >= 0 ? h.y : 0;
       }
     }
     int x = n2[0] + n2[1];
@@ -597,21 +617,21 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   for (int64_t item0 = (int64_t)blockIdx.x * kRows; item0 < items;
        item0 += (int64_t)gridDim.x * kRows) {
     const int64_t item = item0 + warp / kWPR;
-    if (kWPR == 1 && item >= items) break;
+    const bool here = item < items;
+    if (kWPR == 1 && !here) break;
     // pieces: own ones in slots of CTAs c0..c1 (or a whole one), then the prefix's
-    int c0, c1, s0, row, r, hq, pc0 = 0, pc1 = -1, ps0 = 0, prow = 0;
+    int c0, c1, row, r, hq, pc0 = 0, pc1 = -1, prow = 0;
     bool own_whole = false, pre_whole = false;
     if (!q.prefix) {
       int lo = 0, hi = p.nc;
-      while (hi - lo > 1) {
+      while (hi - lo > 1) {          // (an item behind the last takes no piece)
         const int mid = (lo + hi) >> 1;
         if (cut_row[mid] <= item) lo = mid; else hi = mid;
       }
-      const PagedPiece& u = cuts[lo];
+      const PagedPiece u = p.cut[lo];
       const int tl = ((int)item - cut_row[lo]) / p.G, hh = (int)item - cut_row[lo] - tl * p.G;
       c0 = u.c0;
       c1 = u.c1;
-      s0 = u.s0;
       row = tl / q.own_btok * 128 + tl % q.own_btok * p.G + hh;
       r = u.r0 + tl;
       hq = u.g * p.G + hh;
@@ -624,30 +644,34 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
       own_whole = f.x == -1;
       c0 = f.x;
       c1 = f.y;
-      s0 = f.z;
       row = f.w + hh;
       // the prefix's unit of this row: pre_tok tokens in blocks of pre_btok
       const int u = r / q.pre_tok, tl = r - u * q.pre_tok;
-      const int64_t us = ((int64_t)g * q.pre_units + u) * q.pre_tiles;
-      const int64_t T = (int64_t)p.Hkv * q.pre_units * q.pre_tiles;
-      pc0 = (int)(((us + 1) * q.pre_nc - 1) / T);
-      pc1 = (int)(((us + q.pre_tiles) * q.pre_nc - 1) / T);
+      const int64_t w = q.pre_tiles + kPagedManyHead;
+      const int64_t ue = ((int64_t)g * q.pre_units + u + 1) * w, T = p.Hkv * q.pre_units * w;
+      const int64_t x0 = (ue - q.pre_tiles + 1) * q.pre_nc - 1, x1 = ue * q.pre_nc - 1;
+      if (T * q.pre_nc < ((int64_t)1 << 31)) {       // (a 64-bit division takes 100 clocks)
+        pc0 = (int)x0 / (int)T;
+        pc1 = (int)x1 / (int)T;
+      } else {
+        pc0 = (int)(x0 / T);
+        pc1 = (int)(x1 / T);
+      }
       pre_whole = pc0 == pc1;
-      ps0 = T * pc0 / q.pre_nc == us ? 0 : 1;
       prow = tl / q.pre_btok * 128 + tl % q.pre_btok * p.G + hh;
     }
     const int n_own = own_whole ? 1 : c1 - c0 + 1;
-    const int n_all = n_own + (q.prefix ? pc1 - pc0 + 1 : 0);
+    const int n_all = !here ? 0 : n_own + (q.prefix ? pc1 - pc0 + 1 : 0);
     auto piece = [&](int i, const float*& o, float2& ml) {
       if (i < n_own) {
         const int64_t at = own_whole ? (int64_t)r * p.Hq + hq
-                                     : ((int64_t)(c0 + i) * 2 + (i == 0 ? s0 : 0)) * p.slot_rows + row;
+                                     : ((int64_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.slot_rows + row;
         o = (own_whole ? p.own : p.part) + at * D;
         ml = __ldcg((own_whole ? p.own_ml : p.ml) + at);
       } else {
         const int k = i - n_own;
         const int64_t at = pre_whole ? (int64_t)r * p.Hq + hq
-                                     : ((int64_t)(pc0 + k) * 2 + (k == 0 ? ps0 : 0)) * q.pre_rows + prow;
+                                     : ((int64_t)(pc0 + k) * 2 + (k == 0 ? 1 : 0)) * q.pre_rows + prow;
         o = (pre_whole ? q.pre_own : q.pre_part) + at * D;
         ml = __ldcg((pre_whole ? q.pre_own_ml : q.pre_ml) + at);
       }
@@ -657,7 +681,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
     float M = -INFINITY, l = 0.f, acc[kV];
 #pragma unroll
     for (int k = 0; k < kV; ++k) acc[k] = 0.f;
-    constexpr int kU = 4;                     // pieces' loads in flight
+    constexpr int kU = 4;                     // pieces' loads in flight (8: fewer warps fit, slower)
     for (int i = i0; i < i1; i += kU) {
       float v[kU][kV];
       float2 ml[kU];
@@ -688,28 +712,30 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
       }
     }
     if constexpr (kWPR > 1) {
-      if (item0 > (int64_t)blockIdx.x * kRows) __syncthreads();   // sacc of the row before is read
+      __syncthreads();                        // sacc of the rows before is read
+      if (here) {
 #pragma unroll
-      for (int k = 0; k < kV; ++k) sacc[warp][c + k] = acc[k];
-      if (lane == 0) {
-        sacc[warp][D] = M;
-        sacc[warp][D + 1] = l;
+        for (int k = 0; k < kV; ++k) sacc[warp][c + k] = acc[k];
+        if (lane == 0) {
+          sacc[warp][D] = M;
+          sacc[warp][D + 1] = l;
+        }
       }
       __syncthreads();
-      if (warp != 0) continue;
+      if (wr != 0 || !here) continue;
       M = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) M = fmaxf(M, sacc[k][D]);
+      for (int k = 0; k < kWPR; ++k) M = fmaxf(M, sacc[warp + k][D]);
       l = 0.f;
 #pragma unroll
       for (int k = 0; k < kV; ++k) acc[k] = 0.f;
 #pragma unroll
-      for (int w8 = 0; w8 < 8; ++w8) {
-        const float mg = sacc[w8][D];
+      for (int k = 0; k < kWPR; ++k) {
+        const float mg = sacc[warp + k][D];
         const float w = mg == -INFINITY ? 0.f : exp2f(mg - M);
-        l = __fmaf_rn(w, sacc[w8][D + 1], l);
+        l = __fmaf_rn(w, sacc[warp + k][D + 1], l);
 #pragma unroll
-        for (int k = 0; k < kV; ++k) acc[k] = __fmaf_rn(w, sacc[w8][c + k], acc[k]);
+        for (int e = 0; e < kV; ++e) acc[e] = __fmaf_rn(w, sacc[warp + k][c + e], acc[e]);
       }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -750,7 +776,7 @@ bool paged_few_rows(int G, int64_t max_new) { return max_new * G <= kPagedFewRow
 size_t paged_few_part_rows(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows) {
   const int64_t rows = max_new * G;
   *nc = 2 * num_sms;
-  *slot_rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+  *slot_rows = rows <= 16 ? 16 : 32;
   return (size_t)*nc * 2 * *slot_rows;
 }
 
@@ -758,21 +784,22 @@ cudaError_t launch_paged_few(const PagedAttnParams& p, cudaStream_t s, bool pdl)
   if (p.max_new * p.G > p.slot_rows || p.nc < 1 || p.nc > 512) return cudaErrorInvalidValue;
   const int mt = row_tiles(p.slot_rows);
   if (p.D == 128)
-    return mt == 1 ? launch_few<128, 1>(p, s, pdl)
-                   : (mt == 2 ? launch_few<128, 2>(p, s, pdl) : launch_few<128, 4>(p, s, pdl));
+    return mt == 1 ? launch_few<128, 1>(p, s, pdl) : launch_few<128, 2>(p, s, pdl);
   if (p.D == 64)
-    return mt == 1 ? launch_few<64, 1>(p, s, pdl)
-                   : (mt == 2 ? launch_few<64, 2>(p, s, pdl) : launch_few<64, 4>(p, s, pdl));
+    return mt == 1 ? launch_few<64, 1>(p, s, pdl) : launch_few<64, 2>(p, s, pdl);
   return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  // rows of a unit share its pieces: 8 warps a row while all of a CTA's rows at a
-  // time (the few-row kernel's without a prefix) are few
-  const bool deep = !p.prefix && p.a.slot_rows <= kPagedFewRows;
+  // The fewer rows there are to merge, the more warps take one.
+  const int64_t units = (int64_t)p.a.B * p.a.Hkv;
+  const int64_t cut = p.prefix                           ? (int64_t)p.a.N * p.a.Hq     // rows at most
+                      : p.a.slot_rows > kPagedFewRows ? (int64_t)p.a.nc * p.a.slot_rows
+                      : (units < p.a.nc ? units : p.a.nc) * p.a.max_new * p.a.G;
+  const int wpr = cut > 16 * num_sms ? 1 : cut > 4 * num_sms ? 2 : 8;
   const int64_t rows = p.prefix ? (int64_t)p.a.N * p.a.Hq : (int64_t)p.a.nc * p.a.slot_rows;
-  const int64_t want = deep ? rows : (rows + 7) / 8, fit = (int64_t)num_sms * 8;
+  const int64_t want = (rows * wpr + 7) / 8, fit = (int64_t)num_sms * 8;
   cfg.gridDim = dim3((unsigned)(want < fit ? want : fit));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
@@ -782,19 +809,19 @@ cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (p.a.D == 128)
-    return deep ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 8>, p)
-                : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 1>, p);
-  return deep ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 8>, p)
-              : cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 1>, p);
+    return wpr == 1   ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 1>, p)
+           : wpr == 2 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 2>, p)
+                      : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 8>, p);
+  return wpr == 1   ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 1>, p)
+         : wpr == 2 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 2>, p)
+                    : cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 8>, p);
 }
 
 cudaError_t configure_paged_few() {
   cudaError_t e = configure_one<128, 1>();
   if (e == cudaSuccess) e = configure_one<128, 2>();
-  if (e == cudaSuccess) e = configure_one<128, 4>();
   if (e == cudaSuccess) e = configure_one<64, 1>();
   if (e == cudaSuccess) e = configure_one<64, 2>();
-  if (e == cudaSuccess) e = configure_one<64, 4>();
   return e;
 }
 

@@ -42,6 +42,7 @@ constexpr int kTile = kPagedManyTile;
 constexpr int kInfos = 8;
 constexpr float kRescaleLog2 = 8.f;   // see the softmax
 constexpr int kMinTiles = 2;
+constexpr int kHead = kPagedManyHead;
 
 struct ManyInfo {
   int slot0, lo, hi;         // first slot; slots that some row sees: [lo, hi)
@@ -55,12 +56,12 @@ template <int D>
 struct MSmem {
   static constexpr int kQBlk = 128 * D * 2;                  // [D / 64][128 rows][128 B]
   static constexpr int kKV = kTile * D * 2;                  // K or V tile, the same form
-  static constexpr int kRing = D == 128 ? 4 : 8;
+  static constexpr int kRing = D == 128 ? 5 : 8;
+  static constexpr int kS = (kRing + 1) / 2;                 // see the kernel
   static constexpr int kRingOff = 2 * kQBlk;
-  static constexpr int kStageOff = kRingOff + kRing * kKV;   // 4 KB per softmax warp
-  static constexpr int kInfoOff = kStageOff + 8 * 4096;
+  static constexpr int kInfoOff = kRingOff + kRing * kKV;
   static constexpr int kBarOff = kInfoOff + kInfos * (int)sizeof(ManyInfo);
-  static constexpr int kEnd = kBarOff + (2 * kRing + 8) * 8 + 16;
+  static constexpr int kEnd = kBarOff + (kRing + 2 * kS + 7) * 8 + 16;
   static constexpr size_t kBytes = (size_t)kEnd + 1024;
   static constexpr uint32_t kSCol = 0, kOCol = 256;
   static_assert(kBarOff % 8 == 0 && kBytes <= 232448, "shared memory");
@@ -78,6 +79,18 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x; 2^-inf = 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 32 bytes; `wide`: dst is 32-byte aligned (else 16).
+__device__ __forceinline__ void st_global32(void* dst, const uint32_t* v, bool wide) {
+  if (!wide) {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Pairs of fp32 in one instruction, and the maximum of three.
@@ -153,11 +166,12 @@ template <int D, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_many_kernel(const __grid_constant__ PagedManyParams q) {
   using Sm = MSmem<D>;
-  // The commit behind a block's S of tile j says that everything it issued up to
-  // there is done: with both blocks' the K of tile j, the V of tile j - 1 and, at a
-  // piece's end, q are free.  The producer waits for that up to R / 2 tiles behind
-  // the issuers: R / 2 barriers in turn, so that no phase is overtaken.
-  constexpr int R = Sm::kRing, H = D / 64, kS = R / 2;
+  // Ring item 2 j is K of tile j, item 2 j + 1 its V.  The commit behind a block's S of
+  // tile j says that everything it issued up to there is done: with both blocks'
+  // the items up to 2 j and, at a piece's end, q are free.  The producer waits for
+  // that, for item i with j = (i - R + 1) / 2, at most kS - 1 tiles behind the
+  // issuers: kS barriers in turn, so that no phase is overtaken.
+  constexpr int R = Sm::kRing, H = D / 64, kS = Sm::kS;
   const PagedAttnParams& p = q.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -189,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int k0 = 0, k1 = 0;
   int* uoff = reinterpret_cast<int*>(smem);        // own: units before each sequence (the q area)
   if constexpr (kPrefix) {
-    T1 = (int64_t)q.units * ((p.prefix_len + kTile - 1) / kTile);
+    T1 = (int64_t)q.units * ((p.prefix_len + kTile - 1) / kTile + kHead);
   } else {
     // Every CTA sums the units' tiles itself: units of all sequences first (a run
     // of sequences per thread), then their tiles (a run of units per thread).
@@ -224,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s = load_seq(p, ++lo);
           u = 0;
         }
-        mine += unit_tiles(unit_of(p, s, u, utok));
+        mine += unit_tiles(unit_of(p, s, u, utok)) + kHead;
       }
     }
     before = block_excl(mine, wsum, T1);
@@ -235,13 +249,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t enough = (T + kMinTiles - 1) / kMinTiles;
     nc = (int)(enough < p.nc ? (enough < 1 ? 1 : enough) : p.nc);
   }
-  const int64_t t0 = cta < nc ? T * cta / nc : T, t1 = cta < nc ? T * (cta + 1) / nc : T;
+  const int64_t t0 = cta < nc ? range_of(T, cta, nc) : T;
+  const int64_t t1 = cta < nc ? range_of(T, cta + 1, nc) : T;
   if (t0 >= t1) {
     if (threadIdx.x == 0 && !kPrefix) p.cut[cta].c0 = -1;
     return;
   }
+  const int g0 = small_div(t0, T1);
   if constexpr (!kPrefix) {
-    const int64_t x = t0 % T1;
+    const int64_t x = t0 - g0 * T1;
     if (mine > 0 && before <= x && x < before + mine) {    // the range begins in this thread's run
       int lo = 0, hi = p.B;
       while (hi - lo > 1) {
@@ -255,14 +271,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           s = load_seq(p, ++lo);
           u = 0;
         }
-        const int nt = unit_tiles(unit_of(p, s, u, utok));
-        if (x < cum + nt) {
+        const int wt = unit_tiles(unit_of(p, s, u, utok)) + kHead;
+        if (x < cum + wt) {
           start_b = lo;
           start_u = u;
           start_cum = cum;
           break;
         }
-        cum += nt;
+        cum += wt;
       }
     }
     __syncthreads();
@@ -304,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + Sm::kOCol + blk * 128 + loff;
     const float sl2 = p.scale_log2;
     const int rt = r / p.G;                      // token of the row in its block
+    const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.out_stride % 16 == 0;
     float m = -INFINITY, l = 0.f;
     int seg = 0;
     bool ok = true;
@@ -332,25 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const int t = blk * q.btok + rt;           // token of the unit
+      const bool row_ok = rt < q.btok && t < ntok;
       const int last = kPrefix ? hi - 1 : first + min(t, ntok - 1);
       if (flags & 1) {
         m = -INFINITY;
         l = 0.f;
-      }
-      // rows of V that no row of the unit sees: zero before PV (either block's warps
-      // write the zeros before their own PV)
-      if (slot0 < lo || slot0 + kTile > hi) {
-        const int vi = 2 * it + 1;
-        if (!wait_all(&kv_full[vi % R], (uint32_t)(vi / R) & 1u)) { ok = false; break; }
-        if (slot0 + r < lo || slot0 + r >= hi) {
-          uint8_t* vrow = ring + (vi % R) * Sm::kKV + (size_t)r * 128;
-#pragma unroll
-          for (int hh = 0; hh < H; ++hh)
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<uint4*>(vrow + hh * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       float sv[kTile];
 #pragma unroll
@@ -383,11 +386,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A row's reference maximum moves (and O, l are rescaled) only when the
       // maximum grew by more than 2^8 since: P <= 256 fits fp16, and 1 / l at the
       // end makes the choice exact.
-      const bool need = (m == -INFINITY) ? (mx != -INFINITY) : (mx - m > kRescaleLog2);
+      // (Rows of no token hold whatever lay there: they take no part, or the moment
+      // of a move, and with it the rounding of P, would differ from call to call.)
+      const bool need = row_ok && ((m == -INFINITY) ? (mx != -INFINITY) : (mx - m > kRescaleLog2));
       const bool move = __any_sync(0xffffffffu, need);
       const float mn = move ? fmaxf(m, mx) : m;
       const float alpha = (m == -INFINITY || mn == m) ? 1.f : ex2(m - mn);
       const float nref = (mn == -INFINITY) ? 0.f : -mn;
+      if (move && !(flags & 1)) {       // (PV of the tile before is complete: S came behind it)
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float ov[32];
+          tc_ld32(tO + c, ov);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] *= alpha;
+          tc_st32(tO + c, ov);
+        }
+      }
+      const int r0 = f.r0, g = f.g, dst = f.dst;
       const uint64_t sl22 = pack2(sl2, sl2), nref2 = pack2(nref, nref);
       uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
@@ -404,96 +421,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_st16(tS + c / 2, pk);
       }
+      if (slot0 < lo || slot0 + kTile > hi) {
+        // rows of V that no row of the unit sees are zero before PV (either block's
+        // warps write the zeros before their own PV)
+        const int vi = 2 * it + 1;
+        ok = wait_all(&kv_full[vi % R], (uint32_t)(vi / R) & 1u);
+        if (slot0 + r < lo || slot0 + r >= hi) {
+          uint8_t* vrow = ring + (vi % R) * Sm::kKV + (size_t)r * 128;
+#pragma unroll
+          for (int hh = 0; hh < H; ++hh)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(vrow + hh * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[blk]);
       const float2 sum = unpack2(add2(sum0, sum1));
       l = l * alpha + (sum.x + sum.y);
       m = mn;
-      if (move && !(flags & 1)) {       // (PV of the tile before is complete: S came behind it)
+      if (flags & 2) {
+        if (!wait_all(&o_full[blk], (uint32_t)seg & 1u)) { ok = false; break; }
+        ++seg;
+        tc_fence_after();
+        const int hq = g * p.G + (r - rt * p.G);
+        const bool fin = dst < 0 && !p.own;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
+                                   : ((int64_t)cta * 2 + dst) * p.slot_rows + blk * 128 + r;
+        if (!fin && row_ok) (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(m, l);
+        __half* ho = p.out + (int64_t)(r0 + t) * p.out_stride + (int64_t)hq * D;
+        float* fo = (dst < 0 ? p.own : p.part) + at * D;
+        // a lane stores its own row, 32 bytes (a whole sector) at a time
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           float ov[32];
           tc_ld32(tO + c, ov);
           tc_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] *= alpha;
-          tc_st32(tO + c, ov);
-        }
-      }
-      tc_wait_st();
-      tc_fence_before();
-      const int r0 = f.r0, g = f.g, dst = f.dst;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[blk]);
-      if (flags & 2) {
-        if (!wait_all(&o_full[blk], (uint32_t)seg & 1u)) { ok = false; break; }
-        ++seg;
-        tc_fence_after();
-        // Rows go out through this warp's 4 KB of shared memory, 128 bytes of each of
-        // its 32 rows at a time (16-byte pieces XORed by the row), so that eight
-        // lanes store one row's piece: a lane per row stored 16 bytes in each of 32
-        // lines, and a unit's end took longer than two of its tiles.
-        uint8_t* stg = smem + Sm::kStageOff + (warp - 4) * 4096;
-        const bool fin = dst < 0 && !p.own;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        int64_t off[8];                  // element offsets of rows 4 i + lane / 8
-        const int inv_g = 65536 / p.G + 1;   // x / G = x inv_g >> 16 for x < 128
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int ri = qt * 32 + 4 * i + (lane >> 3), ti = ri * inv_g >> 16;
-          const int tu = blk * q.btok + ti, hq = g * p.G + (ri - ti * p.G);
-          const int64_t at = fin       ? (int64_t)(r0 + tu) * p.out_stride + (int64_t)hq * D
-                             : dst < 0 ? ((int64_t)(r0 + tu) * p.Hq + hq) * D
-                                       : (((int64_t)cta * 2 + dst) * p.slot_rows + blk * 128 + ri) * D;
-          off[i] = ti < q.btok && tu < ntok ? at : -1;
-        }
-        if (!fin && rt < q.btok && t < ntok) {
-          const int hq = g * p.G + (r - rt * p.G);
-          const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
-                                     : ((int64_t)cta * 2 + dst) * p.slot_rows + blk * 128 + r;
-          (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(m, l);
-        }
-        float* fd = dst < 0 ? p.own : p.part;
-#pragma unroll 1
-        for (int c = 0; c < D; c += fin ? 64 : 32) {
-          float ov[32];
-          uint4* mine = reinterpret_cast<uint4*>(stg + lane * 128);
-          tc_ld32(tO + c, ov);
-          tc_wait_ld();
+          if (!row_ok) continue;
           if (fin) {
+            uint32_t w[16];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              if (hh) {
-                tc_ld32(tO + c + 32, ov);
-                tc_wait_ld();
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint4 w;
-                __half2* hp = reinterpret_cast<__half2*>(&w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  hp[e] = __floats2half2_rn(ov[8 * k + 2 * e] * inv, ov[8 * k + 2 * e + 1] * inv);
-                mine[(hh * 4 + k) ^ (lane & 7)] = w;
-              }
+            for (int k = 0; k < 16; ++k) {
+              const __half2 h2 = __floats2half2_rn(ov[2 * k] * inv, ov[2 * k + 1] * inv);
+              w[k] = *reinterpret_cast<const uint32_t*>(&h2);
             }
+            st_global32(ho + c, w, wide);
+            st_global32(ho + c + 16, w + 8, wide);
           } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mine[k ^ (lane & 7)] =
-                  make_uint4(__float_as_uint(ov[4 * k]), __float_as_uint(ov[4 * k + 1]),
-                             __float_as_uint(ov[4 * k + 2]), __float_as_uint(ov[4 * k + 3]));
+            for (int k = 0; k < 4; ++k)
+              st_global32(fo + c + 8 * k, reinterpret_cast<const uint32_t*>(ov) + 8 * k, true);
           }
-          __syncwarp();
-          const int pc = lane & 7;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int ri = 4 * i + (lane >> 3);
-            const uint4 w = *reinterpret_cast<const uint4*>(stg + ri * 128 + ((pc ^ (ri & 7)) << 4));
-            if (off[i] >= 0) {
-              if (fin) *reinterpret_cast<uint4*>(p.out + off[i] + c + pc * 8) = w;
-              else *reinterpret_cast<uint4*>(fd + off[i] + c + pc * 4) = w;
-            }
-          }
-          __syncwarp();
         }
         tc_fence_before();
       }
@@ -504,16 +486,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- producer
     const int ps_lg = p.page_lg, boxes = kTile >> ps_lg;     // pages of a tile
     const uint32_t box_bytes = (128u << ps_lg);              // 64 columns of one page
-    int g = (int)(t0 / T1);
+    int g = g0;
     int b, ui;                         // sequence (prefix: 0) and unit in it
     int64_t cum;                       // tiles before that unit
     int base32 = -1;
     PagedSeq mys = {};
     if constexpr (kPrefix) {
-      const int64_t nt = (p.prefix_len + kTile - 1) / kTile;
+      const int64_t w = (p.prefix_len + kTile - 1) / kTile + kHead;
       b = 0;
-      ui = (int)((t0 - (int64_t)g * T1) / nt);
-      cum = ui * nt;
+      ui = small_div(t0 - g * T1, w);
+      cum = ui * w;
     } else {
       b = start_b;
       ui = start_u;
@@ -569,9 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int j0 = u.lo / kTile, nt = (u.hi + kTile - 1) / kTile - j0;
       const int64_t us = (int64_t)g * T1 + cum;
-      const int xa = (int)(lin - us), xb = (int)min((int64_t)nt, t1 - us);
+      const int64_t ue = us + kHead + nt;
+      const int xa = (int)max((int64_t)0, lin - us - kHead);
+      const int xb = (int)min((int64_t)nt, t1 - us - kHead);
+      lin = ue;
+      cum += nt + kHead;
+      ++ui;
+      if (xb <= xa) continue;          // its head alone lies here
       const bool whole = xa == 0 && xb == nt;
-      const int dst = whole ? -1 : (lin == t0 ? 0 : 1);
+      const int dst = whole ? -1 : (xa == 0 ? 1 : 0);
       const bool two = u.ntok > q.btok;
       if (xa == 0) {
         if constexpr (kPrefix) {
@@ -579,11 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = lane; t < u.ntok; t += 32)
             p.row_info[(int64_t)(u.r0 + t) * p.Hkv + g] = make_int4(-2, 0, 0, 0);
         } else {
-          const int c1 = whole ? cta : (int)(((us + nt) * nc - 1) / T);
+          const int c1 = whole ? cta : (int)((ue * nc - 1) / T);
           if (!whole) {
             cut.c0 = cta;
             cut.c1 = c1;
-            cut.s0 = dst;
             cut.rows = u.ntok * p.G;
             cut.r0 = u.r0;
             cut.g = g;
@@ -591,24 +578,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.row_info)
             for (int t = lane; t < u.ntok; t += 32)
               p.row_info[(int64_t)(u.r0 + t) * p.Hkv + g] =
-                  make_int4(whole ? -1 : cta, c1, whole ? 0 : dst,
+                  make_int4(whole ? -1 : cta, c1, 0,
                             t / q.btok * 128 + t % q.btok * p.G);
         }
       }
       const int32_t* row = kPrefix ? p.prefix_pages : p.table + (int64_t)b * p.max_blocks;
+      const int64_t pre = kPrefix ? 0 : p.pre_here;
       for (int x = xa; x < xb && ok; ++x, ++it) {
         const int slot0 = (j0 + x) * kTile;
         // lane: half lane / 8 of the columns (D / 64 of them), page lane % 8 of the tile
         const int i = lane & 7, half = lane >> 3, first = slot0 + (i << ps_lg);
         const bool take = half < H && i < boxes && first < u.hi && first + (1 << ps_lg) > u.lo;
         int64_t page = -1;
-        if (take) page = row[first >> ps_lg];
+        if (take) page = (first < pre ? p.prefix_pages : row)[first >> ps_lg];
         const bool in = page >= 0 && page < p.n_pages;
         if (take && !in) set_error(p.err, kDevPage);
         const int z = in ? (int)(page * p.Hkv + g) : (int)(p.n_pages * p.Hkv);   // zeros
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, take)) * box_bytes;
         const int at = half * (kTile * 128) + ((i << ps_lg) * 128);
-        wait_s(it - R / 2);           // K of that tile gives its place
+        wait_s((item - R + 1) >> 1);   // (arithmetic shift: below 0 nothing to wait for)
         if (!ok) break;
         if (lane == 0) {
           volatile ManyInfo& f = infos[it % kInfos];
@@ -638,28 +626,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                        u.r0 + blk * q.btok, q_full);
           }
         }
-        wait_s(it - R / 2 + 1);       // V of the tile before that one
+        wait_s((item - R + 1) >> 1);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&kv_full[item % R], bytes);
         __syncwarp();
         if (take) tma_3d(ring + (item % R) * Sm::kKV + at, &p.tm_v, half * 64, 0, z, &kv_full[item % R]);
         ++item;
       }
-      lin = us + xb;
-      cum += nt;
-      ++ui;
       ++seg;
     }
     if (!kPrefix && lane == 0) {
       volatile PagedPiece& c = p.cut[cta];
       c.c1 = cut.c1;
-      c.s0 = cut.s0;
       c.rows = cut.rows;
       c.r0 = cut.r0;
       c.g = cut.g;
       c.c0 = ok ? cut.c0 : -1;
     }
-    if (ok) wait_s(it - R / 2);
+    if (ok) wait_s((item - R + 1) >> 1);
     if (ok) {
       if (lane == 0) {
         infos[it % kInfos].flags = 4;

@@ -143,38 +143,39 @@ constexpr int kUnroll = 4;
 __global__ void __launch_bounds__(256) page_append_kernel(const PageAppendParams p) {
   griddep_wait();
   griddep_launch();
-  const int cpr = p.D >> 3;                       // 16-byte pieces of a head's row
-  const int per_row = p.Hkv * cpr;
-  const int64_t total = (int64_t)p.N * per_row;
+  const uint32_t cpr = p.D >> 3;                  // 16-byte pieces of a head's row
+  const uint32_t per_row = p.Hkv * cpr;
+  const int64_t total = (int64_t)p.N * per_row;   // < 2^32: checked by the launcher
   const int64_t step = (int64_t)gridDim.x * 256;
   const int64_t mask = ((int64_t)1 << p.page_lg) - 1;
   for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += step * kUnroll) {
     uint4 kv[kUnroll], vv[kUnroll];
-    int64_t dst[kUnroll];
+    int64_t slot[kUnroll], to[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t i = i0 + u * step;
-      dst[u] = -1;
-      if (i < total) {
-        const int r = (int)(i / per_row), e = (int)(i - (int64_t)r * per_row);
-        const int h = e / cpr, c = e - h * cpr;
-        const int64_t slot = p.slot_map[r];
-        if (slot >= 0 && slot < p.n_slots) {
-          const int64_t pg = slot >> p.page_lg;
-          dst[u] = (((pg * p.Hkv + h) << p.page_lg) + (slot & mask)) * p.D + c * 8;
-          const int64_t src = r * p.row_stride + h * p.head_stride + c * 8;
-          kv[u] = *reinterpret_cast<const uint4*>(p.k + src);
-          vv[u] = *reinterpret_cast<const uint4*>(p.v + src);
-        } else if (slot != -1 && e == 0) {
-          set_error(p.err, kDevPage);
+      slot[u] = -1;
+      if (i < total) {       // the rows are there whatever their slots: nothing waits for these
+        const uint32_t r = (uint32_t)i / per_row, e = (uint32_t)i - r * per_row;
+        const uint32_t h = e / cpr, c = e - h * cpr;
+        slot[u] = p.slot_map[r];
+        const int64_t src = (int64_t)r * p.row_stride + h * p.head_stride + c * 8;
+        kv[u] = __ldcs(reinterpret_cast<const uint4*>(p.k + src));
+        vv[u] = __ldcs(reinterpret_cast<const uint4*>(p.v + src));
+        to[u] = ((int64_t)h << p.page_lg) * p.D + c * 8;
+        if (slot[u] != -1 && (slot[u] < 0 || slot[u] >= p.n_slots)) {
+          if (e == 0) set_error(p.err, kDevPage);
+          slot[u] = -1;
         }
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (dst[u] >= 0) {
-        *reinterpret_cast<uint4*>(p.k_pages + dst[u]) = kv[u];
-        *reinterpret_cast<uint4*>(p.v_pages + dst[u]) = vv[u];
+      if (slot[u] >= 0) {
+        const int64_t dst =
+            (((slot[u] >> p.page_lg) * p.Hkv << p.page_lg) + (slot[u] & mask)) * p.D + to[u];
+        *reinterpret_cast<uint4*>(p.k_pages + dst) = kv[u];
+        *reinterpret_cast<uint4*>(p.v_pages + dst) = vv[u];
       }
   }
 }
@@ -207,6 +208,7 @@ cudaError_t launch_page_plan(const PagePlanParams& p, int num_sms, cudaStream_t 
 
 cudaError_t launch_page_append(const PageAppendParams& p, int num_sms, cudaStream_t s, bool pdl) {
   const int64_t total = (int64_t)p.N * p.Hkv * (p.D / 8);
+  if (total >= (int64_t)1 << 32) return cudaErrorInvalidValue;
   const int64_t want = (total + 255) / 256, most = (int64_t)num_sms * 8;
   const int grid = (int)(want < 1 ? 1 : (want > most ? most : want));
   return launch(page_append_kernel, grid, 256, 0, s, pdl, p);

@@ -252,30 +252,58 @@ def test_window(window, top):
     check_rows(x, out, window)
 
 
-@pytest.mark.parametrize("heads,kv,dim", HEADS)
-@pytest.mark.parametrize("prefix,page", [(16, 16), (128, 64), (1040, 16), (640, 128)])
-@pytest.mark.parametrize("top", [1, 3, 150])
-def test_shared_prefix(heads, kv, dim, prefix, page, top):
-    """The prefix's keys are read once for all rows; sequences that hold nothing but the
-    prefix, and table entries for it that are junk."""
+def prefix_launches(b, run):
+    """How many prefix launches a call of run() makes."""
+    before = b.timing_table().get("attn_paged_prefix", (0, 0))[1]
+    b.timing(True)
+    out = run()
+    b.timing_collect()
+    b.timing(False)
+    return out, b.timing_table().get("attn_paged_prefix", (0, 0))[1] - before
+
+
+def shared_prefix(heads, kv, dim, prefix, page, top, seqs, own_launch):
+    """seqs sequences behind one prefix, some of which hold nothing else; table entries for
+    the prefix are junk.  The prefix gets a launch of its own where that pays."""
     rng = random.Random(prefix + top)
-    hist = [prefix + h for h in (0, 1, 17, 64, 100, 300, 0)]
+    hist = [prefix + (0, 1, 17, 64, 100, 300, 0)[i % 7] for i in range(seqs)]
     new = [rng.randint(1, top) for _ in hist]
     new[4] = 0
     x = Batch(heads, kv, dim, page, hist, new, seed=top, prefix=prefix, pad_rows=2)
     keep = x.table.clone()
     x.table[:, :prefix // page] = -3
-    out, b = run_attention(x)
+    b = block(heads, kv, dim)
+    (out, _), n = prefix_launches(b, lambda: run_attention(x, max_new=top))
     b.check()
+    assert n == own_launch
     x.table = keep
     check_rows(x, out)
 
 
+@pytest.mark.parametrize("heads,kv,dim", HEADS)
+@pytest.mark.parametrize("prefix,page", [(16, 16), (128, 64), (1040, 16)])
+@pytest.mark.parametrize("top", [1, 3, 150])
+def test_short_shared_prefix(heads, kv, dim, prefix, page, top):
+    shared_prefix(heads, kv, dim, prefix, page, top, 7, 0)
+
+
+@pytest.mark.parametrize("heads,kv,dim,prefix,page,top,seqs", [
+    (12, 2, 128, 1040, 16, 1, 130), (12, 2, 128, 4096, 64, 4, 40), (12, 2, 128, 7056, 16, 30, 70),
+    (32, 2, 128, 2064, 16, 1, 70), (32, 2, 128, 9600, 128, 2, 30), (4, 2, 64, 2048, 32, 1, 100),
+    (16, 16, 64, 2064, 16, 1, 16), (16, 16, 64, 2048, 128, 9, 16), (16, 16, 64, 3088, 16, 40, 20),
+    (8, 4, 128, 2080, 32, 1, 60), (32, 8, 64, 2064, 16, 5, 30), (16, 2, 64, 4128, 32, 1, 40)])
+def test_long_shared_prefix(heads, kv, dim, prefix, page, top, seqs):
+    shared_prefix(heads, kv, dim, prefix, page, top, seqs, 1)
+
+
 def test_shared_prefix_equals_the_same_batch_without_it():
-    x = Batch(12, 2, 128, 64, [640 + h for h in (0, 5, 70, 300)], [1, 2, 1, 3], seed=4, prefix=640)
-    a, b = run_attention(x)
-    c, _ = run_attention(x, prefix_pages=None)
+    x = Batch(12, 2, 128, 64, [2048 + h for h in (0, 5, 70, 300)] * 20, [1, 2, 1, 3] * 20, seed=4,
+              prefix=2048)
+    b = block(12, 2, 128)
+    (a, _), n = prefix_launches(b, lambda: run_attention(x))
+    (c, _), m = prefix_launches(b, lambda: run_attention(x, prefix_pages=None))
     b.check()
+    assert (n, m) == (1, 0)
     check_rows(x, a)
     check_rows(x, c)
 
@@ -352,12 +380,14 @@ def test_refused_sequences_leave_their_rows_and_the_others_are_served(top):
     with pytest.raises(blk.BlkError):
         b.check()
     check_rows(x, out, skip=[2])
-    x = Batch(12, 2, 128, 16, [64, 65, 64], [1, top, 1], seed=9, prefix=64)
-    x.lens[0] = 63
-    out, b = run_attention(x)
-    with pytest.raises(blk.BlkError):
-        b.check()
-    check_rows(x, out, skip=[0])
+    for prefix, seqs in ((64, 3), (4096, 60)):
+        x = Batch(12, 2, 128, 64, [prefix, prefix + 1, prefix] * (seqs // 3),
+                  [1, top if seqs < 9 else 3, 1] * (seqs // 3), seed=9, prefix=prefix)
+        x.lens[0] = prefix - 1
+        out, b = run_attention(x)
+        with pytest.raises(blk.BlkError):
+            b.check()
+        check_rows(x, out, skip=[0])
 
 
 @pytest.mark.parametrize("top", [1, 60])
@@ -377,7 +407,7 @@ def test_a_bad_page_reads_as_zeros_and_is_reported(top, bad):
 
 
 @pytest.mark.parametrize("top", [1, 4, 40])
-@pytest.mark.parametrize("prefix", [0, 128])
+@pytest.mark.parametrize("prefix", [0, 128, 32768])
 def test_a_captured_graph_serves_other_lengths(top, prefix):
     """Lengths, row ranges and tables are the device's: a graph captured at one step
     replays the next, on its own stream, with the same bits as the call itself."""
@@ -450,13 +480,16 @@ def test_two_streams_with_their_own_workspaces():
         check_rows(x, out)
 
 
-def test_strided_output_and_the_gaps_between_rows():
-    x = Batch(12, 2, 128, 64, [70, 200], [2, 90], seed=13)
-    wide = torch.full((x.rows, 12 * 128 + 64), MARK, dtype=torch.float16, device="cuda")
-    out, b = run_attention(x, out=wide[:, 32:32 + 12 * 128].unflatten(1, (12, 128)))
+@pytest.mark.parametrize("top", [2, 90])
+@pytest.mark.parametrize("first,width", [(32, 64), (8, 24), (0, 8)])
+def test_strided_output_and_the_gaps_between_rows(top, first, width):
+    """Rows at 16-byte boundaries only, too."""
+    x = Batch(12, 2, 128, 64, [70, 200], [2, top], seed=13)
+    wide = torch.full((x.rows, 12 * 128 + width), MARK, dtype=torch.float16, device="cuda")
+    out, b = run_attention(x, out=wide[:, first:first + 12 * 128].unflatten(1, (12, 128)))
     b.check()
     check_rows(x, out)
-    assert (wide[:, :32] == MARK).all() and (wide[:, 32 + 12 * 128:] == MARK).all()
+    assert (wide[:, :first] == MARK).all() and (wide[:, first + 12 * 128:] == MARK).all()
 
 
 def test_argument_errors():
