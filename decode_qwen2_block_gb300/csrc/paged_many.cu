@@ -35,21 +35,27 @@ namespace {
 constexpr int kThreads = 384;
 // Registers: a softmax thread holds a row of 128 scores.  The block is launched
 // with 168 a thread (384 x 168 = 64512); warps 0-3 keep 72, the softmax warps take
-// 216: 128 x 72 + 256 x 216 = 64512.  configure_paged_many checks the 168.
-constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
-static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegsLaunch, "register split");
+// 216 (with the prefix's simpler producer 88 and 208 spill less): 128 x 72 + 256 x
+// 216 = 128 x 88 + 256 x 208 = 64512.  configure_paged_many checks the 168.
+constexpr int kRegsLaunch = 168;
+template <bool kPrefix>
+struct Regs {
+  static constexpr int kFew = kPrefix ? 88 : 72, kMany = kPrefix ? 208 : 216;
+  static_assert(128 * kFew + 256 * kMany <= kThreads * kRegsLaunch, "register split");
+};
 constexpr int kTile = kPagedManyTile;
 constexpr int kInfos = 8;
 constexpr float kRescaleLog2 = 8.f;   // see the softmax
 constexpr int kMinTiles = 2;
 constexpr int kHead = kPagedManyHead;
 
-struct ManyInfo {
+struct alignas(16) ManyInfo {
+  int flags;                 // 1 first tile of the piece, 2 last, 4 the end, 8 block 1 has rows
   int slot0, lo, hi;         // first slot; slots that some row sees: [lo, hi)
   int first;                 // slot of the unit's first token
-  int ntok, r0, tok0, g;     // tokens, batch row of the first, its number, kv head
-  int flags;                 // 1 first tile of the piece, 2 last, 4 the end, 8 block 1 has rows
+  int ntok, r0, g;           // tokens, batch row of the first, kv head
   int dst;                   // -1 whole, else the partial slot
+  int pad[3];
 };
 
 template <int D>
@@ -74,6 +80,14 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x,
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ int4 lds128(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ float ex2(float x) {   // 2^x; 2^-inf = 0
   float y;
@@ -187,103 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
-  if (threadIdx.x == 0) {
-    prefetch_tmap(&p.tm_q);
-    prefetch_tmap(&p.tm_k);
-    prefetch_tmap(&p.tm_v);
-  }
-  griddep_wait();
-  griddep_launch();
-  // this CTA's range of the line of tiles
-  const int utok = 2 * q.btok;
-  int64_t T1;
-  __shared__ int64_t wsum[kThreads / 32], start_cum;
-  __shared__ int start_b, start_u;
-  int64_t before = 0, mine = 0;
-  int k0 = 0, k1 = 0;
-  int* uoff = reinterpret_cast<int*>(smem);        // own: units before each sequence (the q area)
-  if constexpr (kPrefix) {
-    T1 = (int64_t)q.units * ((p.prefix_len + kTile - 1) / kTile + kHead);
-  } else {
-    // Every CTA sums the units' tiles itself: units of all sequences first (a run
-    // of sequences per thread), then their tiles (a run of units per thread).
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-    int64_t n = 0, R64;
-    bool bad = false;
-    for (int b = b0; b < b1; ++b) {
-      const PagedSeq s = load_seq(p, b);
-      n += (s.n + utok - 1) / utok;
-      bad |= s.bad;
-    }
-    if (bad && cta == 0) set_error(p.err, kDevPage);
-    int64_t at = block_excl(n, wsum, R64);
-    for (int b = b0; b < b1; ++b) {
-      uoff[b] = (int)at;
-      at += (load_seq(p, b).n + utok - 1) / utok;
-    }
-    __syncthreads();
-    const int units = (int)R64, pu = (units + kThreads - 1) / kThreads;
-    k0 = min(units, (int)threadIdx.x * pu);
-    k1 = min(units, k0 + pu);
-    if (k0 < k1) {
-      int lo = 0, hi = p.B;            // last sequence with uoff <= k0: it has unit k0
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (uoff[mid] <= k0) lo = mid; else hi = mid;
-      }
-      PagedSeq s = load_seq(p, lo);
-      for (int k = k0, u = k0 - uoff[lo]; k < k1; ++k, ++u) {
-        while (u * utok >= s.n) {
-          s = load_seq(p, ++lo);
-          u = 0;
-        }
-        mine += unit_tiles(unit_of(p, s, u, utok)) + kHead;
-      }
-    }
-    before = block_excl(mine, wsum, T1);
-  }
-  const int64_t T = T1 * p.Hkv;
-  int nc = p.nc;
-  if constexpr (!kPrefix) {
-    const int64_t enough = (T + kMinTiles - 1) / kMinTiles;
-    nc = (int)(enough < p.nc ? (enough < 1 ? 1 : enough) : p.nc);
-  }
-  const int64_t t0 = cta < nc ? range_of(T, cta, nc) : T;
-  const int64_t t1 = cta < nc ? range_of(T, cta + 1, nc) : T;
-  if (t0 >= t1) {
-    if (threadIdx.x == 0 && !kPrefix) p.cut[cta].c0 = -1;
-    return;
-  }
-  const int g0 = small_div(t0, T1);
-  if constexpr (!kPrefix) {
-    const int64_t x = t0 - g0 * T1;
-    if (mine > 0 && before <= x && x < before + mine) {    // the range begins in this thread's run
-      int lo = 0, hi = p.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (uoff[mid] <= k0) lo = mid; else hi = mid;
-      }
-      PagedSeq s = load_seq(p, lo);
-      int64_t cum = before;
-      for (int u = k0 - uoff[lo];; ++u) {
-        while (u * utok >= s.n) {
-          s = load_seq(p, ++lo);
-          u = 0;
-        }
-        const int wt = unit_tiles(unit_of(p, s, u, utok)) + kHead;
-        if (x < cum + wt) {
-          start_b = lo;
-          start_u = u;
-          start_cum = cum;
-          break;
-        }
-        cum += wt;
-      }
-    }
-    __syncthreads();
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // uoff's place takes q by TMA
-  }
+  // what needs nothing of the kernels before: barriers, TMEM, tensor maps
   if (threadIdx.x == 0) {
     for (int s = 0; s < R; ++s) mbar_init(&kv_full[s], 1);
     mbar_init(q_full, 1);
@@ -304,13 +222,125 @@ __global__ void __launch_bounds__(kThreads, 1)
         : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&p.tm_q);
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
+  griddep_wait();
+  griddep_launch();
+  // this CTA's range of the line of tiles
+  const int utok = 2 * q.btok;
+  int64_t T1;
+  __shared__ int64_t wsum[kThreads / 32], start_cum;
+  __shared__ int start_b, start_u;
+  int64_t before = 0, mine = 0;
+  int k0 = 0, k1 = 0;
+  // own: units before each sequence, and the sequences where a thread has one each (in
+  // the q area, until q comes)
+  int* uoff = reinterpret_cast<int*>(smem);
+  PagedSeq* seqs = reinterpret_cast<PagedSeq*>(smem + (kMaxSeqs + 16) * 4);
+  static_assert((kMaxSeqs + 16) * 4 + kThreads * sizeof(PagedSeq) <= 2 * Sm::kQBlk, "q area");
+  const bool few_seqs = p.B <= kThreads;
+  auto seq = [&](int b) { return few_seqs ? seqs[b] : load_seq(p, b); };
+  if constexpr (kPrefix) {
+    T1 = (int64_t)q.units * ((p.prefix_len + kTile - 1) / kTile + kHead);
+  } else {
+    // Every CTA sums the units' tiles itself: units of all sequences first (a run
+    // of sequences per thread), then their tiles (a run of units per thread).
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+    int64_t n = 0, R64;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+      const PagedSeq s = load_seq(p, b);
+      n += (s.n + utok - 1) / utok;
+      bad |= s.bad;
+      if (few_seqs) seqs[b] = s;
+    }
+    if (bad && cta == 0) set_error(p.err, kDevPage);
+    int64_t at = block_excl(n, wsum, R64);
+    for (int b = b0; b < b1; ++b) {
+      uoff[b] = (int)at;
+      at += (seq(b).n + utok - 1) / utok;
+    }
+    __syncthreads();
+    const int units = (int)R64, pu = (units + kThreads - 1) / kThreads;
+    k0 = min(units, (int)threadIdx.x * pu);
+    k1 = min(units, k0 + pu);
+    if (k0 < k1) {
+      int lo = 0, hi = p.B;            // last sequence with uoff <= k0: it has unit k0
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (uoff[mid] <= k0) lo = mid; else hi = mid;
+      }
+      PagedSeq s = seq(lo);
+      for (int k = k0, u = k0 - uoff[lo]; k < k1; ++k, ++u) {
+        while (u * utok >= s.n) {
+          s = seq(++lo);
+          u = 0;
+        }
+        mine += unit_tiles(unit_of(p, s, u, utok)) + kHead;
+      }
+    }
+    before = block_excl(mine, wsum, T1);
+  }
+  const int64_t T = T1 * p.Hkv;
+  int nc = p.nc;
+  if constexpr (!kPrefix) {
+    const int64_t enough = (T + kMinTiles - 1) / kMinTiles;
+    nc = (int)(enough < p.nc ? (enough < 1 ? 1 : enough) : p.nc);
+  }
+  const int64_t t0 = cta < nc ? range_of(T, cta, nc) : T;
+  const int64_t t1 = cta < nc ? range_of(T, cta + 1, nc) : T;
+  if (t0 >= t1) {
+    if (threadIdx.x == 0 && !kPrefix) p.cut[cta].c0 = -1;
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+      tc_fence_after();
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot),
+                   "r"(512u)
+                   : "memory");
+    }
+    return;
+  }
+  const int g0 = small_div(t0, T1);
+  if constexpr (!kPrefix) {
+    const int64_t x = t0 - g0 * T1;
+    if (mine > 0 && before <= x && x < before + mine) {    // the range begins in this thread's run
+      int lo = 0, hi = p.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (uoff[mid] <= k0) lo = mid; else hi = mid;
+      }
+      PagedSeq s = seq(lo);
+      int64_t cum = before;
+      for (int u = k0 - uoff[lo];; ++u) {
+        while (u * utok >= s.n) {
+          s = seq(++lo);
+          u = 0;
+        }
+        const int wt = unit_tiles(unit_of(p, s, u, utok)) + kHead;
+        if (x < cum + wt) {
+          start_b = lo;
+          start_u = u;
+          start_cum = cum;
+          break;
+        }
+        cum += wt;
+      }
+    }
+    __syncthreads();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // uoff's place takes q by TMA
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kPrefix>::kMany));
     // --------------------------------------------------------------- softmax
     const int blk = (warp - 4) >> 2;
     const int qt = warp & 3;                     // TMEM lane quarter of this warp
@@ -322,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rt = r / p.G;                      // token of the row in its block
     const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.out_stride % 16 == 0;
     float m = -INFINITY, l = 0.f;
-    int seg = 0;
+    int seg = 0, last = 0, low = 0;              // slots that the row sees: [low, last]
+    bool row_ok = false;                         // the row is a token's
     bool ok = true;
     // decisions before a warp-collective TMEM access are uniform over the warp
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
@@ -334,12 +365,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      volatile const ManyInfo& f = infos[it % kInfos];
-      const int flags = f.flags;
+      // the scores and the tile's description on their way together
+      float sv[kTile];
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tc_ld32(tS + c, sv + c);
+      const uint32_t fi = smem_u32(const_cast<ManyInfo*>(&infos[it % kInfos]));
+      const int4 fa = lds128(fi), fb = lds128(fi + 16);
+      const int flags = fa.x, slot0 = fa.y, lo = fa.z, hi = fa.w;
+      const int first = fb.x, ntok = fb.y;
+      tc_wait_ld();
       if (flags & 4) break;
-      const int slot0 = f.slot0, lo = f.lo, hi = f.hi, first = f.first, ntok = f.ntok;
-      const bool here = blk == 0 || (flags & 8);
-      if (!here) {       // the unit has no rows in block 1
+      if (blk == 1 && !(flags & 8)) {    // the unit has no rows in block 1
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[blk]);
         if (flags & 2) {
@@ -348,17 +384,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      const int t = blk * q.btok + rt;           // token of the unit
-      const bool row_ok = rt < q.btok && t < ntok;
-      const int last = kPrefix ? hi - 1 : first + min(t, ntok - 1);
-      if (flags & 1) {
+      if (flags & 1) {                   // a new piece
+        const int t = blk * q.btok + rt; // token of the unit
+        row_ok = rt < q.btok && t < ntok;
+        last = kPrefix ? hi - 1 : first + min(t, ntok - 1);
+        low = kPrefix ? 0 : max(lo, (int)window_lo(p.window, last));
         m = -INFINITY;
         l = 0.f;
       }
-      float sv[kTile];
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) tc_ld32(tS + c, sv + c);
-      tc_wait_ld();
       const int first_last = kPrefix ? hi - 1 : first + blk * q.btok;   // of the block's first row
       if (slot0 + kTile - 1 > first_last) {      // some row sees less than the tile
         const int lim = last - slot0;
@@ -366,13 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kTile; ++c)
           if (c > lim) sv[c] = -INFINITY;
       }
-      if (!kPrefix) {
-        const int low = max(lo, (int)window_lo(p.window, last)) - slot0;
-        if (__any_sync(0xffffffffu, low > 0)) {
+      if (!kPrefix && (slot0 < lo || p.window > 0)) {
+        const int lim = low - slot0;
 #pragma unroll
-          for (int c = 0; c < kTile; ++c)
-            if (c < low) sv[c] = -INFINITY;
-        }
+        for (int c = 0; c < kTile; ++c)
+          if (c < lim) sv[c] = -INFINITY;
       }
       float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
 #pragma unroll
@@ -390,21 +421,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       // of a move, and with it the rounding of P, would differ from call to call.)
       const bool need = row_ok && ((m == -INFINITY) ? (mx != -INFINITY) : (mx - m > kRescaleLog2));
       const bool move = __any_sync(0xffffffffu, need);
-      const float mn = move ? fmaxf(m, mx) : m;
-      const float alpha = (m == -INFINITY || mn == m) ? 1.f : ex2(m - mn);
-      const float nref = (mn == -INFINITY) ? 0.f : -mn;
-      if (move && !(flags & 1)) {       // (PV of the tile before is complete: S came behind it)
+      if (move) {
+        const float mn = fmaxf(m, mx);
+        const float alpha = (m == -INFINITY || mn == m) ? 1.f : ex2(m - mn);
+        m = mn;
+        l *= alpha;
+        if (!(flags & 1)) {             // (PV of the tile before is complete: S came behind it)
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float ov[32];
-          tc_ld32(tO + c, ov);
-          tc_wait_ld();
+          for (int c = 0; c < D; c += 32) {
+            float ov[32];
+            tc_ld32(tO + c, ov);
+            tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] *= alpha;
-          tc_st32(tO + c, ov);
+            for (int i = 0; i < 32; ++i) ov[i] *= alpha;
+            tc_st32(tO + c, ov);
+          }
         }
       }
-      const int r0 = f.r0, g = f.g, dst = f.dst;
+      const float nref = (m == -INFINITY) ? 0.f : -m;
       const uint64_t sl22 = pack2(sl2, sl2), nref2 = pack2(nref, nref);
       uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
@@ -441,13 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[blk]);
       const float2 sum = unpack2(add2(sum0, sum1));
-      l = l * alpha + (sum.x + sum.y);
-      m = mn;
+      l += sum.x + sum.y;
       if (flags & 2) {
         if (!wait_all(&o_full[blk], (uint32_t)seg & 1u)) { ok = false; break; }
         ++seg;
         tc_fence_after();
-        const int hq = g * p.G + (r - rt * p.G);
+        const int t = blk * q.btok + rt, r0 = fb.z, g = fb.w, hq = g * p.G + (r - rt * p.G);
+        const int dst = lds128(fi + 32).x;
         const bool fin = dst < 0 && !p.own;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
@@ -481,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kPrefix>::kFew));
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     const int ps_lg = p.page_lg, boxes = kTile >> ps_lg;     // pages of a tile
@@ -536,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if ((b & ~31) != base32) {     // 32 sequences at a time, one per lane
           base32 = b & ~31;
-          mys = base32 + lane < p.B ? load_seq(p, base32 + lane) : PagedSeq{};
+          mys = base32 + lane < p.B ? (seg == 0 ? seq(base32 + lane) : load_seq(p, base32 + lane))
+                                    : PagedSeq{};
         }
         PagedSeq s;
         s.r0 = __shfl_sync(0xffffffffu, mys.r0, b & 31);
