@@ -435,6 +435,24 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """The current stream's handle.  Without a stream object around it: that takes 3 us,
+    as long as a small kernel."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            device = torch._C._cuda_getDevice
+            _raw_stream = lambda: raw(device())  # noqa: E731
+    return _raw_stream()
+
+
 def _check_tensor(t, dtype, what, shape, contiguous=True):
     """A tensor that the library reads or writes by its raw pointer: on the GPU, of this
     type and shape, and contiguous."""
@@ -450,12 +468,16 @@ class Block:
     intermediate, has_qkv_bias, rms_eps, rope_theta."""
 
     def __init__(self, shape, max_ctx: int, chain: bool = False):
+        global torch          # for the methods: this module itself loads without it
+        import torch
         self.shape = shape
         self.max_ctx = int(max_ctx)
         self.cfg = BlkConfig(shape.hidden, shape.n_heads, shape.n_kv_heads, shape.head_dim,
                              shape.intermediate, shape.rms_eps, shape.rope_theta, self.max_ctx,
                              1 if shape.has_qkv_bias else 0)
         self.handle = blk_create(self.cfg)
+        self._heads = (shape.n_heads, shape.head_dim)          # of q rows
+        self._kv_heads = (shape.n_kv_heads, shape.head_dim)
         if chain:
             blk_set_flags(self.handle, BLK_FLAG_CHAIN)
 
@@ -536,15 +558,7 @@ class Block:
 
     @staticmethod
     def _stream(stream):
-        if stream is not None:
-            return stream.cuda_stream
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:
-            return torch.cuda.current_stream().cuda_stream
-        # the current stream's handle without a stream object around it, which takes
-        # 3 us, as long as a small kernel
-        return raw(torch._C._cuda_getDevice())
+        return _current_stream() if stream is None else stream.cuda_stream
 
     def prefill(self, w: BlkWeights, x, pos, k_cache, v_cache, out, ws, k_new=None, v_new=None,
                 stream=None):
@@ -593,13 +607,15 @@ class Block:
         int32, taken from the front (used[0] of them); block_table: int32 [B,
         max_blocks], the new pages' entries written; row_start int64 [B + 1],
         slot_map and pos int64 [n_rows], used int64 [1]: written."""
-        import torch
         B, n = cache_lens.numel(), slot_map.numel()
-        for t, shape, what in ((cache_lens, (B,), "cache_lens"), (row_start, (B + 1,), "row_start"),
-                               (slot_map, (n,), "slot_map"), (pos, (n,), "pos"), (used, (1,), "used")):
-            _check_tensor(t, torch.int64, what, shape)
+        i64 = torch.int64
+        _check_tensor(cache_lens, i64, "cache_lens", (B,))
+        _check_tensor(row_start, i64, "row_start", (B + 1,))
+        _check_tensor(slot_map, i64, "slot_map", (n,))
+        _check_tensor(pos, i64, "pos", (n,))
+        _check_tensor(used, i64, "used", (1,))
         if new_lens is not None:
-            _check_tensor(new_lens, torch.int64, "new_lens", (B,))
+            _check_tensor(new_lens, i64, "new_lens", (B,))
         _check_tensor(free_pages, torch.int32, "free_pages", (free_pages.numel(),))
         if block_table.dim() != 2:
             raise BlkError(BLK_ERR_SHAPE, "block_table")
@@ -612,30 +628,28 @@ class Block:
             raise BlkError(rc, "blk_page_plan")
 
     def _pools(self, k_pages, v_pages):
-        import torch
-        s = self.cfg
-        if k_pages.dim() != 4:
-            raise BlkError(BLK_ERR_SHAPE, "k_pages")
-        shape = (k_pages.shape[0], s.n_kv_heads, k_pages.shape[2], s.head_dim)
+        shape = k_pages.shape
+        if len(shape) != 4 or (shape[1], shape[3]) != self._kv_heads:
+            raise BlkError(BLK_ERR_SHAPE, f"k_pages: {tuple(shape)}")
         _check_tensor(k_pages, torch.float16, "k_pages", shape)
         _check_tensor(v_pages, torch.float16, "v_pages", shape)
+        return shape[0], shape[2]
 
     def page_append(self, k, v, slot_map, k_pages, v_pages, stream=None):
         """Rows of k and v (fp16 [n, n_kv_heads, head_dim], the last dimension
         contiguous, both with the same strides) into the slots of slot_map (int64
         [n]; -1 leaves a row out)."""
-        import torch
-        s = self.cfg
-        self._pools(k_pages, v_pages)
+        n_pages, page = self._pools(k_pages, v_pages)
         n = slot_map.numel()
         _check_tensor(slot_map, torch.int64, "slot_map", (n,))
-        for t, what in ((k, "k"), (v, "v")):
-            _check_tensor(t, torch.float16, what, (n, s.n_kv_heads, s.head_dim), contiguous=False)
+        shape = (n, *self._kv_heads)
+        _check_tensor(k, torch.float16, "k", shape, contiguous=False)
+        _check_tensor(v, torch.float16, "v", shape, contiguous=False)
         st = k.stride()
         if st != v.stride() or st[2] != 1:
             raise BlkError(BLK_ERR_SHAPE, "page_append: strides")
         rc = blk_page_append(self.handle, k.data_ptr(), v.data_ptr(), st[0], st[1],
-                             slot_map.data_ptr(), n, k_pages.shape[2], k_pages.shape[0],
+                             slot_map.data_ptr(), n, page, n_pages,
                              k_pages.data_ptr(), v_pages.data_ptr(), self._stream(stream))
         if rc != BLK_OK:
             raise BlkError(rc, "blk_page_append")
@@ -646,7 +660,6 @@ class Block:
         int64 [B], block_table int32 [B, max_blocks] (device); max_new and max_len bound
         a sequence's new tokens and its slots with them; prefix_pages: int32 pages
         whose slots begin every sequence (a shared prefix), or None."""
-        import torch
         B = cache_lens.numel()
         _check_tensor(cache_lens, torch.int64, "cache_lens", (B,))
         _check_tensor(row_start, torch.int64, "row_start", (B + 1,))
@@ -667,24 +680,22 @@ class Block:
         return blk_attn_paged_workspace_bytes(self.handle, max_rows, max_seqs, prefix)
 
     def _paged_pools(self, batch, k_pages, v_pages):
-        self._pools(k_pages, v_pages)
-        if (k_pages.shape[0], k_pages.shape[2]) != (batch.n_pages, batch.page_size):
+        if self._pools(k_pages, v_pages) != (batch.n_pages, batch.page_size):
             raise BlkError(BLK_ERR_SHAPE, "the pools are not those of the batch")
 
     def attn_paged(self, batch: BlkPagedBatch, q, k_pages, v_pages, out, ws, stream=None):
         """Attention of the batch's rows: q, out fp16 [n_rows, n_heads, head_dim], heads
         contiguous, rows at any stride."""
-        import torch
-        s = self.cfg
         self._paged_pools(batch, k_pages, v_pages)
-        for t, what in ((q, "q"), (out, "out")):
-            _check_tensor(t, torch.float16, what, (batch.n_rows, s.n_heads, s.head_dim),
-                          contiguous=False)
-            if t.stride()[1:] != (s.head_dim, 1):
-                raise BlkError(BLK_ERR_SHAPE, what)
-        rc = blk_attn_paged(self.handle, batch, q.data_ptr(), q.stride(0), k_pages.data_ptr(),
-                            v_pages.data_ptr(), out.data_ptr(), out.stride(0), ws.data_ptr(),
-                            ws.numel() * ws.element_size(), self._stream(stream))
+        shape, rows = (batch.n_rows, *self._heads), (self._heads[1], 1)
+        _check_tensor(q, torch.float16, "q", shape, contiguous=False)
+        _check_tensor(out, torch.float16, "out", shape, contiguous=False)
+        sq, so = q.stride(), out.stride()
+        if sq[1:] != rows or so[1:] != rows:
+            raise BlkError(BLK_ERR_SHAPE, f"attn_paged: strides {sq}, {so}")
+        rc = blk_attn_paged(self.handle, batch, q.data_ptr(), sq[0], k_pages.data_ptr(),
+                            v_pages.data_ptr(), out.data_ptr(), so[0], ws.data_ptr(),
+                            ws.nbytes, self._stream(stream))
         if rc != BLK_OK:
             raise BlkError(rc, "blk_attn_paged")
 
@@ -705,7 +716,6 @@ class Block:
             raise BlkError(rc, "blk_step_paged")
 
     def _paged_rows(self, batch, x, pos, slot_map, out):
-        import torch
         for t, what in ((x, "x"), (out, "out")):
             _check_tensor(t, torch.float16, what, (batch.n_rows, self.cfg.hidden))
         for t, what in ((pos, "pos"), (slot_map, "slot_map")):

@@ -373,7 +373,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t p_st = pbase + grp * Sm::kPStride + (slab + 2 * tig) * 2;
   for (int it = 0;; ++it) {
     const int st = it % S;
-    if (!mbar_wait_near(&full[st], (uint32_t)(it / S) & 1u, p.err)) *(volatile int*)&abort_s = 1;
+    if (!__all_sync(0xffffffffu, mbar_wait_near(&full[st], (uint32_t)(it / S) & 1u, p.err))) {
+      // the wait ran out: the other warps, at the first barrier or on their way there,
+      // find the flag behind it; nobody waits for this one
+      if (lane == 0) *(volatile int*)&abort_s = 1;
+      __threadfence_block();
+      asm volatile("bar.arrive 1, %0;" ::"r"(kConsumers) : "memory");
+      return;
+    }
     const int flags = infos[st].flags;
     if (flags & 4) return;
     const int slot0 = infos[st].slot0, n = infos[st].n;
@@ -449,9 +456,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (tig == 0) stat[(mt * 16 + grp + 8 * h2) * 4 + warp] = mx;
       }
     named_sync(1, kConsumers);
-    // a wait that ran out stops all four warps here: the next flag is set behind the
-    // second barrier
-    if (*(volatile int*)&abort_s) return;
+    if (*(volatile int*)&abort_s) return;       // (set before a warp's arrival, see above)
     float corr[MT][2];
     bool moved = false;
 #pragma unroll

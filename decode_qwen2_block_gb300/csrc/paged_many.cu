@@ -350,7 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + Sm::kOCol + blk * 128 + loff;
     const float sl2 = p.scale_log2;
     const int rt = r / p.G;                      // token of the row in its block
+    // 32-byte stores where the rows allow them (pointers are 16-byte aligned, as the
+    // workspace's parts are with respect to one another by 256)
     const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.out_stride % 16 == 0;
+    const bool wide_part = reinterpret_cast<uintptr_t>(p.part) % 32 == 0;
     float m = -INFINITY, l = 0.f;
     int seg = 0, last = 0, low = 0;              // slots that the row sees: [low, last]
     bool row_ok = false;                         // the row is a token's
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
 #pragma unroll
             for (int c = 0; c < D; c += 8)
-              st_global32(fo + c, reinterpret_cast<const uint32_t*>(ov) + c, true);
+              st_global32(fo + c, reinterpret_cast<const uint32_t*>(ov) + c, wide_part);
           }
         }
         tc_fence_before();

@@ -160,13 +160,14 @@ def test_append_reports_a_slot_outside_the_pool_and_writes_nothing_there():
 
 
 # ----------------------------------------------------------------- attention
-def run_attention(x, window=0, out=None, stream=None, **kw):
+def run_attention(x, window=0, out=None, stream=None, shift=0, **kw):
     b = block(x.heads, x.kv, x.dim, window)
     d = x.descriptor(b, **kw)
     if out is None:
         out = torch.full((x.rows, x.heads, x.dim), MARK, dtype=torch.float16, device="cuda")
     nb = b.attn_paged_workspace_bytes(x.rows, len(x.hist), prefix=d.prefix_len > 0)
-    ws = torch.full((nb,), 255, dtype=torch.uint8, device="cuda")     # NaN wherever it is read
+    ws = torch.full((nb + 32,), 255, dtype=torch.uint8, device="cuda")     # NaN wherever it is read
+    ws = ws[shift:shift + nb]
     b.attn_paged(d, x.q, x.k_pages, x.v_pages, out, ws, stream=stream)
     return out, b
 
@@ -186,7 +187,8 @@ def check_rows(x, out, window=0, skip=()):
     assert (out[at:] == MARK).all(), "rows behind the batch stay"
 
 
-HEADS = [(12, 2, 128), (32, 2, 128), (4, 2, 64), (16, 16, 64), (8, 4, 128), (32, 8, 64), (16, 2, 64)]
+HEADS = [(12, 2, 128), (32, 2, 128), (4, 2, 64), (16, 16, 64), (8, 4, 128), (32, 8, 64), (16, 2, 64),
+         (4, 4, 128), (16, 1, 64)]
 
 
 @pytest.mark.parametrize("heads,kv,dim", HEADS)
@@ -490,6 +492,50 @@ def test_strided_output_and_the_gaps_between_rows(top, first, width):
     b.check()
     check_rows(x, out)
     assert (wide[:, :first] == MARK).all() and (wide[:, first + 12 * 128:] == MARK).all()
+
+
+@pytest.mark.parametrize("new,prefix", [([1, 3, 1], 0), ([60, 3, 90], 0), ([1, 3, 1] * 40, 4096)])
+def test_a_workspace_at_a_16_byte_boundary(new, prefix):
+    x = Batch(12, 2, 128, 64, [prefix + h for h in (900, 4000, 0)] * (len(new) // 3), new, seed=15,
+              prefix=prefix)
+    out, b = run_attention(x, shift=16)
+    b.check()
+    check_rows(x, out)
+
+
+@pytest.mark.parametrize("top", [1, 5, 70])
+def test_rows_before_the_first_sequence_and_idle_batches(top):
+    """Row ranges that begin behind the batch's first rows; no sequence with rows at all."""
+    x = Batch(12, 2, 128, 64, [100, 7], [1, top], seed=16, pad_rows=4)
+    x.row_start += 3
+    x.q[3:3 + x.n] = x.q[:x.n].clone()
+    out, b = run_attention(x)
+    b.check()
+    assert (out[:3] == MARK).all()
+    x.q = x.q[3:]
+    x.rows -= 3
+    check_rows(x, out[3:])
+    for prefix in (0, 8192):
+        x = Batch(12, 2, 128, 64, [prefix + 5] * 80, [0] * 80, seed=17, prefix=prefix, pad_rows=top)
+        out, b = run_attention(x, max_new=top)
+        b.check()
+        assert (out == MARK).all()
+
+
+@pytest.mark.parametrize("top", [2, 50])
+def test_more_new_tokens_than_announced_are_refused(top):
+    x = Batch(12, 2, 128, 64, [100, 7, 30], [1, top, 1], seed=18)
+    out, b = run_attention(x, max_new=top - 1)
+    with pytest.raises(blk.BlkError) as e:
+        b.check()
+    assert e.value.status == blk.BLK_ERR_PAGE
+    check_rows(x, out, skip=[1])
+    # row ranges that run backwards or past the batch
+    x.row_start[1] = x.rows + 5
+    out, b = run_attention(x)
+    with pytest.raises(blk.BlkError):
+        b.check()
+    assert (out[:1 + top] == MARK).all()
 
 
 def test_argument_errors():
