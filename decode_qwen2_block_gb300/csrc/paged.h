@@ -114,10 +114,7 @@ struct PagedManyParams {
 inline int paged_btok(int G) { return 128 / G; }
 constexpr int kPagedManyRows = 256;     // partial rows of a slot
 constexpr int kPagedManyTile = 128;     // slots of a tile
-#ifndef HEADMANY
-#define HEADMANY 3
-#endif
-constexpr int kPagedManyHead = HEADMANY;       // a unit's begin and end in the line, in tiles
+constexpr int kPagedManyHead = 3;       // a unit's begin and end in the line, in tiles
 cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl);
 cudaError_t configure_paged_many();
 

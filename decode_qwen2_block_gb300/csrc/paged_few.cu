@@ -35,13 +35,9 @@ namespace {
 
 constexpr int kTile = 64;            // slots of a tile
 constexpr int kConsumers = 128, kThreads = 160;
-constexpr int kMinTiles = 2;         // tiles that a CTA takes at least, where there are any
 // What a unit's beginning and end (q, the pieces' ends) count for in the line, in
 // tiles; they lie before its first tile.
-#ifndef HEADFEW
-#define HEADFEW 1
-#endif
-constexpr int kHead = HEADFEW;
+constexpr int kHead = 1;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -184,8 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   before += inc - mine;
   const int64_t T = T1 * p.Hkv;
-  const int64_t enough = (T + kMinTiles - 1) / kMinTiles;
-  const int nc = (int)(enough < p.nc ? (enough < 1 ? 1 : enough) : p.nc);
+  const int nc = (int)(T < p.nc ? (T < 1 ? 1 : T) : p.nc);
   const int cta = blockIdx.x;
   const int64_t t0 = cta < nc ? range_of(T, cta, nc) : T, t1 = cta < nc ? range_of(T, cta + 1, nc) : T;
   if (t0 >= t1) {   // (uniform over the CTA)
@@ -578,13 +573,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 // into 150), one where many rows have a few.
 template <int D, int kWPR>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedMergeParams q) {
-  constexpr int kV = D / 32;
+  // a row's lanes: half a warp where rows are many (two rows' pieces in flight per warp)
+  constexpr int kLanes = kWPR == 1 ? 16 : 32, kV = D / kLanes;     // columns per lane
   const PagedAttnParams& p = q.a;
   __shared__ float sacc[kWPR > 1 ? 8 : 1][D + 2];
   __shared__ int cut_row[512], wsum[8];
   griddep_wait();
   griddep_launch();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane * kV;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = (lane % kLanes) * kV;
   int64_t items;
   if (!q.prefix) {
     // rows of the cut units before each CTA's (two CTAs a thread; nc <= 512)
@@ -618,14 +615,14 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   } else {
     items = (int64_t)p.N * p.Hq;
   }
-  constexpr int kRows = 8 / kWPR;             // rows of a block at a time
+  constexpr int kRows = 256 / kLanes / kWPR;  // rows of a block at a time
   for (int64_t item0 = (int64_t)blockIdx.x * kRows; item0 < items;
        item0 += (int64_t)gridDim.x * kRows) {
-    const int64_t item = item0 + warp / kWPR;
-    const bool here = item < items;
+    const int64_t item = item0 + tid / kLanes / kWPR;
+    bool here = item < items;                 // (a block's warps stay together: barriers below)
     if (kWPR == 1 && !here) break;
     // pieces: own ones in slots of CTAs c0..c1 (or a whole one), then the prefix's
-    int c0, c1, row, r, hq, pc0 = 0, pc1 = -1, prow = 0;
+    int c0 = 0, c1 = 0, row = 0, r = 0, hq = 0, pc0 = 0, pc1 = -1, prow = 0;
     bool own_whole = false, pre_whole = false;
     if (!q.prefix) {
       int lo = 0, hi = p.nc;
@@ -644,8 +641,9 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
       r = (int)(item / p.Hq);
       hq = (int)(item - (int64_t)r * p.Hq);
       const int g = hq / p.G, hh = hq - g * p.G;
-      const int4 f = p.row_info[(int64_t)r * p.Hkv + g];
-      if (f.x == -2) continue;               // a row behind the batch, or refused
+      const int4 f = here ? p.row_info[(int64_t)r * p.Hkv + g] : make_int4(-2, 0, 0, 0);
+      here = f.x != -2;                      // else a row behind the batch, or refused
+      if (kWPR == 1 && !here) continue;
       own_whole = f.x == -1;
       c0 = f.x;
       c1 = f.y;
@@ -696,12 +694,15 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
         if (i + u < i1) {
           const float* o;
           piece(i + u, o, ml[u]);
-          if constexpr (kV == 4) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(o + c));
-            v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
-          } else {
+          if constexpr (kV == 2) {
             const float2 x = __ldcg(reinterpret_cast<const float2*>(o + c));
             v[u][0] = x.x; v[u][1] = x.y;
+          } else {
+#pragma unroll
+            for (int e = 0; e < kV; e += 4) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(o + c + e));
+              v[u][e] = x.x; v[u][e + 1] = x.y; v[u][e + 2] = x.z; v[u][e + 3] = x.w;
+            }
           }
         }
       }
@@ -804,7 +805,8 @@ cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStrea
                       : (units < p.a.nc ? units : p.a.nc) * p.a.max_new * p.a.G;
   const int wpr = cut > 16 * num_sms ? 1 : cut > 4 * num_sms ? 2 : 8;
   const int64_t rows = p.prefix ? (int64_t)p.a.N * p.a.Hq : (int64_t)p.a.nc * p.a.slot_rows;
-  const int64_t want = (rows * wpr + 7) / 8, fit = (int64_t)num_sms * 8;
+  const int64_t per = wpr == 1 ? 16 : 8 / wpr, want = (rows + per - 1) / per;
+  const int64_t fit = (int64_t)num_sms * 8;
   cfg.gridDim = dim3((unsigned)(want < fit ? want : fit));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
