@@ -708,19 +708,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // S of tile it (flags f).  At the end of the range, or where the unit has no
       // rows in this block, the commit alone.
-      auto start_s = [&](int it, int f) -> bool {
+      // Descriptors: their low words hold the address, so a step adds to those (kd_lo:
+      // K of tile it, formed before the waits).
+      const uint32_t d_hi = (uint32_t)(tc_desc_kmajor(0) >> 32);
+      const uint32_t q_lo = (uint32_t)tc_desc_kmajor(qb), r_lo = (uint32_t)tc_desc_kmajor(ra);
+      const uint32_t v_hi = (uint32_t)(tc_desc_mnmajor(0) >> 32), rv_lo = (uint32_t)tc_desc_mnmajor(ra);
+      auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
+      auto start_s = [&](int it, int f, uint32_t kd_lo) -> bool {
         if (f & 1) {                   // a new piece: its q
           ++seg;
           if (!mbar_wait_near(q_full, (uint32_t)seg & 1u, p.err)) return false;
         }
         tc_fence_after();
         if (!(f & 4) && (blk == 0 || (f & 8))) {
-          const uint32_t kb = ra + (2 * it % R) * Sm::kKV;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t o = (ks >> 2) * 16384;
-            tc_mma(tS, tc_desc_kmajor(qb + o) + ((ks & 3) * 32 >> 4),
-                   tc_desc_kmajor(kb + o) + ((ks & 3) * 32 >> 4), id_s, ks != 0);
+            const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+            tc_mma(tS, desc(d_hi, q_lo + o), desc(d_hi, kd_lo + o), id_s, ks != 0);
           }
         }
         if (blk == 1 || it > 0) mbar_arrive(&p_full[1 - blk]);
@@ -735,23 +739,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = landed(0);
       if (ok) {
         f = infos[0].flags;
-        ok = start_s(0, f);
+        ok = start_s(0, f, r_lo);
       }
       for (int it = 0; ok && !(f & 4); ++it) {
         // everything but P first: while the softmax works this thread has the time
         if (!landed(2 * it + 1) || !landed(2 * it + 2)) break;
         const int fn = infos[(it + 1) % kInfos].flags;
+        const uint32_t vd_lo = rv_lo + ((2 * it + 1) % R) * (Sm::kKV >> 4);
+        const uint32_t kd_lo = r_lo + ((2 * it + 2) % R) * (Sm::kKV >> 4);
         if (!mbar_wait_near(&p_full[blk], (uint32_t)it & 1u, p.err)) break;
         tc_fence_after();
         if (blk == 0 || (f & 8)) {
-          const uint32_t vb = ra + ((2 * it + 1) % R) * Sm::kKV;
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            tc_mma_ts(tO, tS + kk * 8, tc_desc_mnmajor(vb + kk * 16 * 128), id_o,
+            tc_mma_ts(tO, tS + kk * 8, desc(v_hi, vd_lo + (kk * 16 * 128 >> 4)), id_o,
                       !(f & 1) || kk != 0);
         }
         if (f & 2) tc_commit(&o_full[blk]);
-        if (!start_s(it + 1, fn)) break;
+        if (!start_s(it + 1, fn, kd_lo)) break;
         f = fn;
       }
       // issued MMAs finish before TMEM and shared memory go away
