@@ -1399,7 +1399,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   if (few) {
     a.tm_k = few_k;
     a.tm_v = few_v;
-    paged_few_part_rows(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
+    paged_few_slots(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
     BLK_LAUNCH(tm, kKPagedFew, launch_paged_few(a, s, true));
   } else {
     a.nc = h->num_sms;

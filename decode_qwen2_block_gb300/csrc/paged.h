@@ -99,7 +99,8 @@ struct PagedAttnParams {
 // Rows of one unit that the few-row kernel takes (16 per MMA row tile).
 constexpr int kPagedFewRows = 32;
 bool paged_few_rows(int G, int64_t max_new);
-size_t paged_few_part_rows(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows);
+// CTAs of the kernel and partial rows of a slot.
+void paged_few_slots(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows);
 cudaError_t launch_paged_few(const PagedAttnParams& p, cudaStream_t s, bool pdl);
 cudaError_t configure_paged_few();
 

@@ -96,10 +96,12 @@ struct FSmem {
   static constexpr int kQOff = kStages * 2 * kKV;
   static constexpr int kPOff = kQOff + kQBytes;
   static constexpr int kStatOff = kPOff + 16 * MT * kPStride;   // [16 MT][4 warps] floats
-  static constexpr int kInfoOff = kStatOff + 4 * 16 * MT * 4;
+  static constexpr int kSumOff = kStatOff + 4 * 16 * MT * 4;    // [16 MT][4 warps] floats
+  static constexpr int kInfoOff = kSumOff + 4 * 16 * MT * 4;
   static constexpr int kBarOff = (kInfoOff + kStages * (int)sizeof(TileInfo) + 15) / 16 * 16;
   static constexpr int kEnd = kBarOff + (2 * kStages + 1) * 8 + 64;
   static constexpr size_t kBytes = (size_t)kEnd + 1024;         // the ring is 1024-aligned
+  static_assert(kBytes + 2048 <= 233472 / 2, "two CTAs per SM");   // (1 KB the system's, statics)
 };
 
 __device__ __forceinline__ int seq_tiles(const PagedAttnParams& p, const PagedSeq& s) {
@@ -122,7 +124,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_u32(smem), qbase = smem_u32(smem + Sm::kQOff),
                  pbase = smem_u32(smem + Sm::kPOff);
-  float* stat = reinterpret_cast<float*>(smem + Sm::kStatOff);
+  float* stat = reinterpret_cast<float*>(smem + Sm::kStatOff);   // the warps' row maxima
+  // the warps' row sums at a piece's end: apart, as a warp that has read its own goes on
+  // to the next tile's maxima while others still read (the next sums are two barriers off)
+  float* stat_l = reinterpret_cast<float*>(smem + Sm::kSumOff);
   volatile TileInfo* infos = reinterpret_cast<volatile TileInfo*>(smem + Sm::kInfoOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Sm::kBarOff);
   uint64_t* empty = full + S;
@@ -527,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           float l = l_r[mt][h2];
           l += __shfl_xor_sync(0xffffffffu, l, 1);
           l += __shfl_xor_sync(0xffffffffu, l, 2);
-          if (tig == 0) stat[(mt * 16 + grp + 8 * h2) * 4 + warp] = l;
+          if (tig == 0) stat_l[(mt * 16 + grp + 8 * h2) * 4 + warp] = l;
         }
       named_sync(1, kConsumers);
 #pragma unroll
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int h2 = 0; h2 < 2; ++h2) {
           const int row = mt * 16 + grp + 8 * h2;
           if (row >= rows) continue;
-          const float4 l4 = *reinterpret_cast<const float4*>(stat + row * 4);
+          const float4 l4 = *reinterpret_cast<const float4*>(stat_l + row * 4);
           const float l = (l4.x + l4.y) + (l4.z + l4.w);
           const int t = row / p.G, hq = g * p.G + (row - t * p.G);
           const int col = warp * (D / 4) + 2 * tig;
@@ -773,22 +778,18 @@ cudaError_t configure_one() {
                               (int)FSmem<D, MT>::kBytes);
 }
 
-int row_tiles(int slot_rows) { return slot_rows / 16; }
-
 }  // namespace
 
 bool paged_few_rows(int G, int64_t max_new) { return max_new * G <= kPagedFewRows; }
 
-size_t paged_few_part_rows(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows) {
-  const int64_t rows = max_new * G;
+void paged_few_slots(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows) {
   *nc = 2 * num_sms;
-  *slot_rows = rows <= 16 ? 16 : 32;
-  return (size_t)*nc * 2 * *slot_rows;
+  *slot_rows = max_new * G <= 16 ? 16 : 32;
 }
 
 cudaError_t launch_paged_few(const PagedAttnParams& p, cudaStream_t s, bool pdl) {
   if (p.max_new * p.G > p.slot_rows || p.nc < 1 || p.nc > 512) return cudaErrorInvalidValue;
-  const int mt = row_tiles(p.slot_rows);
+  const int mt = p.slot_rows / 16;
   if (p.D == 128)
     return mt == 1 ? launch_few<128, 1>(p, s, pdl) : launch_few<128, 2>(p, s, pdl);
   if (p.D == 64)

@@ -328,6 +328,21 @@ def test_many_short_sequences():
     check_rows(x, out)
 
 
+@pytest.mark.parametrize("heads,kv,dim,top", [(16, 1, 64, 2), (12, 2, 128, 2), (8, 4, 128, 1)])
+def test_short_pieces_one_after_another_give_the_same_bits(heads, kv, dim, top):
+    """Every tile ends a piece: a warp is in the next piece's maxima while another still
+    finishes the one before."""
+    rng = random.Random(21)
+    hist = [rng.randint(0, 62) for _ in range(2000)]
+    x = Batch(heads, kv, dim, 32, hist, [rng.randint(1, top) for _ in hist], seed=21)
+    first, b = run_attention(x)
+    b.check()
+    check_rows(x, first)
+    for _ in range(20):
+        out, _ = run_attention(x)
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16))
+
+
 @pytest.mark.parametrize("top", [1, 100])
 def test_scores_of_any_size(top):
     """Rows whose scores reach +-1000: the running maximum keeps every weight in range."""
@@ -601,3 +616,14 @@ def test_argument_errors():
             b.attn_paged(d, bad.get("q", x.q), bad.get("k", x.k_pages), x.v_pages,
                          bad.get("out", out), ws)
         assert e.value.status == S
+    for bad in (ws.cpu(), torch.empty((nb, 2), dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(blk.BlkError) as e:
+            b.attn_paged(d, x.q, x.k_pages, x.v_pages, out, bad)
+        assert e.value.status == blk.BLK_ERR_WORKSPACE
+    b._device += 1                             # tensors of another GPU than the block's
+    try:
+        with pytest.raises(blk.BlkError) as e:
+            b.attn_paged(d, x.q, x.k_pages, x.v_pages, out, ws)
+        assert e.value.status == S
+    finally:
+        b._device -= 1
