@@ -453,14 +453,6 @@ def _current_stream() -> int:
     return _raw_stream()
 
 
-def _check_tensor(t, dtype, what, shape, contiguous=True):
-    """A tensor that the library reads or writes by its raw pointer: on the GPU, of this
-    type and shape, and contiguous."""
-    if (t.dtype is not dtype or not t.is_cuda or t.shape != shape or
-            (contiguous and not t.is_contiguous())):
-        raise BlkError(BLK_ERR_SHAPE, f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}")
-
-
 class Block:
     """One block shape on the current CUDA device.
 
@@ -478,6 +470,7 @@ class Block:
         self.handle = blk_create(self.cfg)
         self._heads = (shape.n_heads, shape.head_dim)          # of q rows
         self._kv_heads = (shape.n_kv_heads, shape.head_dim)
+        self._device = torch.cuda.current_device()
         if chain:
             blk_set_flags(self.handle, BLK_FLAG_CHAIN)
 
@@ -599,6 +592,13 @@ class Block:
 
     # ---- paged cache: pools [n_pages, n_kv_heads, page_size, head_dim] fp16
 
+    def _tensor(self, t, dtype, what, shape, contiguous=True):
+        """A tensor that the library reads or writes by its raw pointer: on this block's
+        GPU, of this type and shape, and contiguous."""
+        if (t.dtype is not dtype or t.get_device() != self._device or t.shape != shape or
+                (contiguous and not t.is_contiguous())):
+            raise BlkError(BLK_ERR_SHAPE, f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}")
+
     def page_plan(self, page_size: int, cache_lens, new_lens, free_pages, block_table, row_start,
                   slot_map, pos, used, stream=None):
         """Block tables, slot map and positions of a step from the requests' lengths.
@@ -609,17 +609,17 @@ class Block:
         slot_map and pos int64 [n_rows], used int64 [1]: written."""
         B, n = cache_lens.numel(), slot_map.numel()
         i64 = torch.int64
-        _check_tensor(cache_lens, i64, "cache_lens", (B,))
-        _check_tensor(row_start, i64, "row_start", (B + 1,))
-        _check_tensor(slot_map, i64, "slot_map", (n,))
-        _check_tensor(pos, i64, "pos", (n,))
-        _check_tensor(used, i64, "used", (1,))
+        self._tensor(cache_lens, i64, "cache_lens", (B,))
+        self._tensor(row_start, i64, "row_start", (B + 1,))
+        self._tensor(slot_map, i64, "slot_map", (n,))
+        self._tensor(pos, i64, "pos", (n,))
+        self._tensor(used, i64, "used", (1,))
         if new_lens is not None:
-            _check_tensor(new_lens, i64, "new_lens", (B,))
-        _check_tensor(free_pages, torch.int32, "free_pages", (free_pages.numel(),))
+            self._tensor(new_lens, i64, "new_lens", (B,))
+        self._tensor(free_pages, torch.int32, "free_pages", (free_pages.numel(),))
         if block_table.dim() != 2:
             raise BlkError(BLK_ERR_SHAPE, "block_table")
-        _check_tensor(block_table, torch.int32, "block_table", (B, block_table.shape[1]))
+        self._tensor(block_table, torch.int32, "block_table", (B, block_table.shape[1]))
         rc = blk_page_plan(self.handle, page_size, B, cache_lens.data_ptr(), _ptr(new_lens),
                            free_pages.data_ptr(), free_pages.numel(), block_table.data_ptr(),
                            block_table.shape[1], n, row_start.data_ptr(), slot_map.data_ptr(),
@@ -631,8 +631,8 @@ class Block:
         shape = k_pages.shape
         if len(shape) != 4 or (shape[1], shape[3]) != self._kv_heads:
             raise BlkError(BLK_ERR_SHAPE, f"k_pages: {tuple(shape)}")
-        _check_tensor(k_pages, torch.float16, "k_pages", shape)
-        _check_tensor(v_pages, torch.float16, "v_pages", shape)
+        self._tensor(k_pages, torch.float16, "k_pages", shape)
+        self._tensor(v_pages, torch.float16, "v_pages", shape)
         return shape[0], shape[2]
 
     def page_append(self, k, v, slot_map, k_pages, v_pages, stream=None):
@@ -641,10 +641,10 @@ class Block:
         [n]; -1 leaves a row out)."""
         n_pages, page = self._pools(k_pages, v_pages)
         n = slot_map.numel()
-        _check_tensor(slot_map, torch.int64, "slot_map", (n,))
+        self._tensor(slot_map, torch.int64, "slot_map", (n,))
         shape = (n, *self._kv_heads)
-        _check_tensor(k, torch.float16, "k", shape, contiguous=False)
-        _check_tensor(v, torch.float16, "v", shape, contiguous=False)
+        self._tensor(k, torch.float16, "k", shape, contiguous=False)
+        self._tensor(v, torch.float16, "v", shape, contiguous=False)
         st = k.stride()
         if st != v.stride() or st[2] != 1:
             raise BlkError(BLK_ERR_SHAPE, "page_append: strides")
@@ -661,14 +661,14 @@ class Block:
         a sequence's new tokens and its slots with them; prefix_pages: int32 pages
         whose slots begin every sequence (a shared prefix), or None."""
         B = cache_lens.numel()
-        _check_tensor(cache_lens, torch.int64, "cache_lens", (B,))
-        _check_tensor(row_start, torch.int64, "row_start", (B + 1,))
+        self._tensor(cache_lens, torch.int64, "cache_lens", (B,))
+        self._tensor(row_start, torch.int64, "row_start", (B + 1,))
         if block_table.dim() != 2:
             raise BlkError(BLK_ERR_SHAPE, "block_table")
-        _check_tensor(block_table, torch.int32, "block_table", (B, block_table.shape[1]))
+        self._tensor(block_table, torch.int32, "block_table", (B, block_table.shape[1]))
         pre = 0
         if prefix_pages is not None:
-            _check_tensor(prefix_pages, torch.int32, "prefix_pages", (prefix_pages.numel(),))
+            self._tensor(prefix_pages, torch.int32, "prefix_pages", (prefix_pages.numel(),))
             pre = prefix_pages.numel() * page_size
         b = BlkPagedBatch(B, n_rows, max_new, max_len, row_start.data_ptr(), cache_lens.data_ptr(),
                           block_table.data_ptr(), block_table.shape[1], n_pages,
@@ -679,17 +679,19 @@ class Block:
     def attn_paged_workspace_bytes(self, max_rows: int, max_seqs: int, prefix: bool = True) -> int:
         return blk_attn_paged_workspace_bytes(self.handle, max_rows, max_seqs, prefix)
 
-    def _paged_pools(self, batch, k_pages, v_pages):
+    def _paged_pools(self, batch, k_pages, v_pages, ws):
         if self._pools(k_pages, v_pages) != (batch.n_pages, batch.page_size):
             raise BlkError(BLK_ERR_SHAPE, "the pools are not those of the batch")
+        if ws.get_device() != self._device or not ws.is_contiguous():
+            raise BlkError(BLK_ERR_WORKSPACE, f"workspace {tuple(ws.shape)} on {ws.device}")
 
     def attn_paged(self, batch: BlkPagedBatch, q, k_pages, v_pages, out, ws, stream=None):
         """Attention of the batch's rows: q, out fp16 [n_rows, n_heads, head_dim], heads
         contiguous, rows at any stride."""
-        self._paged_pools(batch, k_pages, v_pages)
+        self._paged_pools(batch, k_pages, v_pages, ws)
         shape, rows = (batch.n_rows, *self._heads), (self._heads[1], 1)
-        _check_tensor(q, torch.float16, "q", shape, contiguous=False)
-        _check_tensor(out, torch.float16, "out", shape, contiguous=False)
+        self._tensor(q, torch.float16, "q", shape, contiguous=False)
+        self._tensor(out, torch.float16, "out", shape, contiguous=False)
         sq, so = q.stride(), out.stride()
         if sq[1:] != rows or so[1:] != rows:
             raise BlkError(BLK_ERR_SHAPE, f"attn_paged: strides {sq}, {so}")
@@ -706,20 +708,19 @@ class Block:
                    out, ws, stream=None):
         """One block step of the batch: x, out fp16 [n_rows, hidden]; pos, slot_map as
         page_plan writes them."""
-        self._paged_pools(batch, k_pages, v_pages)
+        self._paged_pools(batch, k_pages, v_pages, ws)
         self._paged_rows(batch, x, pos, slot_map, out)
         rc = blk_step_paged(self.handle, w, batch, x.data_ptr(), pos.data_ptr(),
                             slot_map.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                            out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                            self._stream(stream))
+                            out.data_ptr(), ws.data_ptr(), ws.nbytes, self._stream(stream))
         if rc != BLK_OK:
             raise BlkError(rc, "blk_step_paged")
 
     def _paged_rows(self, batch, x, pos, slot_map, out):
         for t, what in ((x, "x"), (out, "out")):
-            _check_tensor(t, torch.float16, what, (batch.n_rows, self.cfg.hidden))
+            self._tensor(t, torch.float16, what, (batch.n_rows, self.cfg.hidden))
         for t, what in ((pos, "pos"), (slot_map, "slot_map")):
-            _check_tensor(t, torch.int64, what, (batch.n_rows,))
+            self._tensor(t, torch.int64, what, (batch.n_rows,))
 
     def embed(self, table, ids, x, stream=None):
         """x[t] = table[ids[t]] (fp16 [vocab, hidden] table, int64 ids)."""

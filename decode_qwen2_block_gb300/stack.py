@@ -172,9 +172,9 @@ class PagedStack:
 
     A sequence takes pages as it grows and gives them back with ``free``.
     ``prefill_prefix`` computes a prefix that every sequence then begins with:
-    its pages are held once, and its keys are read once per step for the whole
-    batch.  The host knows the lengths it asked for, so no step waits for the
-    GPU."""
+    its pages are held once, and a step reads its keys once for the whole batch
+    where that pays.  The host knows the lengths it asked for, so no step waits
+    for the GPU.  Steps follow one another whatever streams they are given."""
 
     def __init__(self, shape, layer_weights, max_ctx: int, n_pages: int, page_size: int,
                  max_seqs: int, max_rows: int, device="cuda"):
@@ -185,6 +185,7 @@ class PagedStack:
         self.max_ctx, self.page, self.n_pages = max_ctx, page_size, n_pages
         self.max_seqs, self.max_rows, self.device = max_seqs, max_rows, device
         pool = (n_pages, shape.n_kv_heads, page_size, shape.head_dim)
+        self._last = torch.cuda.current_stream()  # the buffers' stream, then the last step's
         self.pools = [(torch.zeros(pool, dtype=torch.float16, device=device),
                        torch.zeros(pool, dtype=torch.float16, device=device))
                       for _ in range(self.n_layers)]
@@ -220,6 +221,9 @@ class PagedStack:
         if n != sum(news) or n > self.max_rows or min(news) < 0:
             raise BlkError(BLK_ERR_SHAPE, "PagedStack.step: rows")
         s = torch.cuda.current_stream() if stream is None else stream
+        if s != self._last:
+            s.wait_stream(self._last)
+            self._last = s
         with torch.cuda.stream(s):
             i64 = torch.int64
             lens_d, news_d = self._ints(lens, i64), self._ints(news, i64)

@@ -440,13 +440,14 @@ typedef struct {
  *   ws      blk_attn_paged_workspace_bytes(h, max_rows, max_seqs, with_prefix)
  *           bytes or more, for any max_rows >= n_rows and max_seqs >= n_seqs
  * With prefix_len > 0 the first prefix_len slots of every sequence are those of
- * prefix_pages: their keys are read once for the whole batch, the block tables'
- * entries for them are not read, and every sequence with rows must hold the
+ * prefix_pages: the block tables' entries for them are not read, and every sequence with rows must hold the
  * whole prefix (cache_lens[b] >= prefix_len; refused otherwise).  A prefix does
  * not go with a sliding window (BLK_ERR_SHAPE).  The result is that of the same
  * batch without the prefix, up to the order of sums.
- * Up to 64 rows (new tokens x query heads per kv head) per sequence run on the
- * few-row kernel (K/V streamed once, mma.sync), more on the tcgen05 kernel.
+ * Up to 32 rows (max_new x query heads per kv head) per sequence run on the
+ * few-row kernel (K/V streamed once, mma.sync), more on the tcgen05 kernel; the
+ * prefix gets a launch of its own where reading its keys once pays for it, and
+ * is taken with each sequence's own slots otherwise.
  * Slots that a row does not see may hold anything, unless another row of the
  * same sequence sees them: values there must be finite. */
 size_t blk_attn_paged_workspace_bytes(blk_handle h, int64_t max_rows, int64_t max_seqs,

@@ -239,6 +239,28 @@ def test_paged_stack_serves_like_contiguous_caches(prefix):
     assert sorted(pg.free_ids + pg.prefix_ids + sum(pg.pages, [])) == list(range(30))
 
 
+def test_paged_stack_steps_on_changing_streams():
+    """Each step on another stream than the last, nothing waiting between them: the bits of
+    the same steps on one stream."""
+    s = synth.TINY
+    wd = _layers(s, 3, 37)
+    x = to_dev(synth.hidden_input(s, 200, seed=37))
+    news = [[40, 3], [1, 20], [1, 1], [30, 1], [1, 1]]
+    torch.cuda.synchronize()
+    results = []
+    for many in (False, True):
+        streams = [torch.cuda.Stream() for _ in range(3)] if many else [torch.cuda.current_stream()]
+        pg = PagedStack(s, wd, 128, 30, 16, 2, 64)
+        at, outs = 0, []
+        for i, new in enumerate(news):
+            outs.append(pg.step(x[at:at + sum(new)], new, stream=streams[i % len(streams)]))
+            at += sum(new)
+        torch.cuda.synchronize()
+        pg.block.check()
+        results.append(torch.cat(outs))
+    assert torch.equal(results[0].view(torch.int16), results[1].view(torch.int16))
+
+
 def test_paged_stack_refuses_what_does_not_fit():
     s = synth.TINY
     pg = PagedStack(s, _layers(s, 1, 34), 64, 5, 16, 2, 100)
