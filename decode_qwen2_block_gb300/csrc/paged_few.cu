@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        if (ml[u].x == -INFINITY) continue;
+        if (ml[u].y == 0.f) continue;         // nothing seen there (a sum of NaN goes on)
         const float mn = fmaxf(M, ml[u].x);
         const float so = M == -INFINITY ? 0.f : exp2f(M - mn), w = exp2f(ml[u].x - mn);
         l = __fmaf_rn(w, ml[u].y, __fmul_rn(l, so));

@@ -343,6 +343,25 @@ def test_short_pieces_one_after_another_give_the_same_bits(heads, kv, dim, top):
         assert torch.equal(out.view(torch.int16), first.view(torch.int16))
 
 
+@pytest.mark.parametrize("top", [1, 4, 40])
+@pytest.mark.parametrize("prefix", [0, 8192])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_row_of_nan_stays_nan_and_alone(top, prefix, value):
+    """A query that is not finite, in a sequence inside one CTA and in one cut over many
+    (an infinite score's weight is 2^(inf - inf))."""
+    hist = [prefix + h for h in (3, 9000, 500)] * (1 if prefix == 0 else 30)
+    x = Batch(12, 2, 128, 64, hist, [top, 1, top] * (len(hist) // 3), seed=22, prefix=prefix)
+    want, bound = x.reference()
+    x.q[0, 3] = value
+    x.q[top, 7] = value
+    x.q[2 * top, 11] = value
+    out, b = run_attention(x)
+    b.check()
+    off, bad = (out.double() - want).abs() <= bound, torch.zeros(x.rows, 12, dtype=torch.bool)
+    bad[0, 3] = bad[top, 7] = bad[2 * top, 11] = True
+    assert out[bad].isnan().all() and off[~bad].all()
+
+
 @pytest.mark.parametrize("top", [1, 100])
 def test_scores_of_any_size(top):
     """Rows whose scores reach +-1000: the running maximum keeps every weight in range."""
