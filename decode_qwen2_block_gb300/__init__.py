@@ -596,7 +596,7 @@ class Block:
         """A tensor that the library reads or writes by its raw pointer: on this block's
         GPU, of this type and shape, and contiguous."""
         if (t.dtype is not dtype or t.get_device() != self._device or t.shape != shape or
-                (contiguous and not t.is_contiguous())):
+                contiguous and not t.is_contiguous()):
             raise BlkError(BLK_ERR_SHAPE, f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}")
 
     def page_plan(self, page_size: int, cache_lens, new_lens, free_pages, block_table, row_start,
@@ -607,33 +607,35 @@ class Block:
         int32, taken from the front (used[0] of them); block_table: int32 [B,
         max_blocks], the new pages' entries written; row_start int64 [B + 1],
         slot_map and pos int64 [n_rows], used int64 [1]: written."""
-        B, n = cache_lens.numel(), slot_map.numel()
-        i64 = torch.int64
-        self._tensor(cache_lens, i64, "cache_lens", (B,))
-        self._tensor(row_start, i64, "row_start", (B + 1,))
-        self._tensor(slot_map, i64, "slot_map", (n,))
-        self._tensor(pos, i64, "pos", (n,))
-        self._tensor(used, i64, "used", (1,))
-        if new_lens is not None:
-            self._tensor(new_lens, i64, "new_lens", (B,))
-        self._tensor(free_pages, torch.int32, "free_pages", (free_pages.numel(),))
-        if block_table.dim() != 2:
-            raise BlkError(BLK_ERR_SHAPE, "block_table")
-        self._tensor(block_table, torch.int32, "block_table", (B, block_table.shape[1]))
-        rc = blk_page_plan(self.handle, page_size, B, cache_lens.data_ptr(), _ptr(new_lens),
-                           free_pages.data_ptr(), free_pages.numel(), block_table.data_ptr(),
-                           block_table.shape[1], n, row_start.data_ptr(), slot_map.data_ptr(),
-                           pos.data_ptr(), used.data_ptr(), self._stream(stream))
+        B, n, n_free = cache_lens.numel(), slot_map.numel(), free_pages.numel()
+        i64, dev = torch.int64, self._device
+        # (a loop of its own: a call per array takes as long again as the kernel)
+        for t, k in ((cache_lens, B), (row_start, B + 1), (slot_map, n), (pos, n), (used, 1),
+                     (cache_lens if new_lens is None else new_lens, B)):
+            if (t.dtype is not i64 or t.get_device() != dev or t.numel() != k or
+                    not t.is_contiguous()):
+                raise BlkError(BLK_ERR_SHAPE, f"page_plan: {tuple(t.shape)} {t.dtype} on "
+                               f"{t.device}, not int64 [{k}]")
+        self._tensor(free_pages, torch.int32, "free_pages", (n_free,))
+        shape = block_table.shape
+        if len(shape) != 2 or shape[0] != B:
+            raise BlkError(BLK_ERR_SHAPE, f"block_table: {tuple(shape)}")
+        self._tensor(block_table, torch.int32, "block_table", shape)
+        rc = blk_page_plan(self.handle, page_size, B, cache_lens.data_ptr(),
+                           None if new_lens is None else new_lens.data_ptr(),
+                           free_pages.data_ptr(), n_free, block_table.data_ptr(), shape[1], n,
+                           row_start.data_ptr(), slot_map.data_ptr(), pos.data_ptr(),
+                           used.data_ptr(), self._stream(stream))
         if rc != BLK_OK:
             raise BlkError(rc, "blk_page_plan")
 
     def _pools(self, k_pages, v_pages):
         shape = k_pages.shape
-        if len(shape) != 4 or (shape[1], shape[3]) != self._kv_heads:
+        if len(shape) != 4 or shape[1::2] != self._kv_heads:
             raise BlkError(BLK_ERR_SHAPE, f"k_pages: {tuple(shape)}")
         self._tensor(k_pages, torch.float16, "k_pages", shape)
         self._tensor(v_pages, torch.float16, "v_pages", shape)
-        return shape[0], shape[2]
+        return shape[::2]
 
     def page_append(self, k, v, slot_map, k_pages, v_pages, stream=None):
         """Rows of k and v (fp16 [n, n_kv_heads, head_dim], the last dimension
