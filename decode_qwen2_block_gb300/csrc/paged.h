@@ -59,7 +59,6 @@ struct alignas(8) PagedPiece { // what merging needs of one cut unit
   int c1;                      // last CTA that holds a piece
   int r0;                      // batch row of its first token
   int g;                       // kv head
-  int pad;
 };
 
 struct PagedAttnParams {
@@ -96,7 +95,9 @@ struct PagedAttnParams {
   int* err;
 };
 
-// Rows of one unit that the few-row kernel takes (16 per MMA row tile).
+// Rows of one unit that the few-row kernel takes (16 per MMA row tile): at 30 rows it
+// takes 32 us for what takes the many-row kernel 36, with 64 rows (four row tiles) it
+// was the slower one.
 constexpr int kPagedFewRows = 32;
 bool paged_few_rows(int G, int64_t max_new);
 // CTAs of the kernel and partial rows of a slot.
@@ -115,7 +116,8 @@ struct PagedManyParams {
 inline int paged_btok(int G) { return 128 / G; }
 constexpr int kPagedManyRows = 256;     // partial rows of a slot
 constexpr int kPagedManyTile = 128;     // slots of a tile
-constexpr int kPagedManyHead = 3;       // a unit's begin and end in the line, in tiles
+// A unit's begin and end in the line, in tiles (8 prompts: 1 84 us, 3 81, 5 85).
+constexpr int kPagedManyHead = 3;
 cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl);
 cudaError_t configure_paged_many();
 

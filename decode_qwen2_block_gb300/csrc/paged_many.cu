@@ -22,6 +22,13 @@
 // read P_j, and a commit behind S_j+1 says that PV_j is complete too.
 // Slots that no row of the unit sees have their V rows zeroed before PV (0 * NaN
 // is NaN).  Every wait is bounded.
+//
+// Measured with the merge, in a graph, 12 heads on 2 kv heads of 128: 8 prompts of 700 -
+// 2000 tokens 80 us (645 TFLOP/s; the kernel alone 686), 512 tokens behind 3584 slots
+// 28 us.  A tile takes ~3400 clocks of 2048 for its 32 MMAs: S = Q K^T reads 128 bytes
+// of shared memory per clock, all there is, while the next tiles' 64 KB arrive.  A
+// unit's begin and end take some 3000 clocks, a launch 6 us before its first tile is
+// there.
 #include <math.h>
 
 #include "common.cuh"
@@ -46,7 +53,7 @@ struct Regs {
 constexpr int kTile = kPagedManyTile;
 constexpr int kInfos = 8;
 constexpr float kRescaleLog2 = 8.f;   // see the softmax
-constexpr int kMinTiles = 2;
+constexpr int kMinTiles = 2;          // of a CTA: a piece of less is all begin and end
 constexpr int kHead = kPagedManyHead;
 
 struct alignas(16) ManyInfo {
