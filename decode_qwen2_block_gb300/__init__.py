@@ -3,7 +3,9 @@
 The binding only marshals arguments: every step of the block runs in the
 library's CUDA kernels (see include/blk.h for the contract).  It loads the
 in-tree ``libblk.so`` and raises if it has not been built; there is no CPU or
-PyTorch fallback.
+PyTorch fallback.  ``Block``'s calls on a paged cache, which a serving step makes
+several times on a few rows, check and pass their tensors in ``_native.so``
+(csrc/binding.cpp).
 
 Low-level functions carry the C names (``blk_create``, ``blk_prefill``,
 ``blk_prefill_kv``, ``blk_decode``, ...) and take plain integers for device
@@ -460,7 +462,7 @@ class Block:
     intermediate, has_qkv_bias, rms_eps, rope_theta."""
 
     def __init__(self, shape, max_ctx: int, chain: bool = False):
-        global torch          # for the methods: this module itself loads without it
+        global torch, _native   # for the methods: this module itself loads without them
         import torch
         self.shape = shape
         self.max_ctx = int(max_ctx)
@@ -468,9 +470,9 @@ class Block:
                              shape.intermediate, shape.rms_eps, shape.rope_theta, self.max_ctx,
                              1 if shape.has_qkv_bias else 0)
         self.handle = blk_create(self.cfg)
-        self._heads = (shape.n_heads, shape.head_dim)          # of q rows
-        self._kv_heads = (shape.n_kv_heads, shape.head_dim)
+        from . import _native   # (calls the library that blk_create has loaded)
         self._device = torch.cuda.current_device()
+        self._args = (self.handle, self._device, shape.n_heads, shape.n_kv_heads, shape.head_dim)
         if chain:
             blk_set_flags(self.handle, BLK_FLAG_CHAIN)
 
@@ -478,6 +480,7 @@ class Block:
         if getattr(self, "handle", None):
             blk_destroy(self.handle)
             self.handle = None
+            self._args = (None, *self._args[1:])
 
     def __del__(self):
         try:
@@ -607,54 +610,16 @@ class Block:
         int32, taken from the front (used[0] of them); block_table: int32 [B,
         max_blocks], the new pages' entries written; row_start int64 [B + 1],
         slot_map and pos int64 [n_rows], used int64 [1]: written."""
-        B, n, n_free = cache_lens.numel(), slot_map.numel(), free_pages.numel()
-        i64, dev = torch.int64, self._device
-        # (a loop of its own: a call per array takes as long again as the kernel)
-        for t, k in ((cache_lens, B), (row_start, B + 1), (slot_map, n), (pos, n), (used, 1),
-                     (cache_lens if new_lens is None else new_lens, B)):
-            if (t.dtype is not i64 or t.get_device() != dev or t.numel() != k or
-                    not t.is_contiguous()):
-                raise BlkError(BLK_ERR_SHAPE, f"page_plan: {tuple(t.shape)} {t.dtype} on "
-                               f"{t.device}, not int64 [{k}]")
-        self._tensor(free_pages, torch.int32, "free_pages", (n_free,))
-        shape = block_table.shape
-        if len(shape) != 2 or shape[0] != B:
-            raise BlkError(BLK_ERR_SHAPE, f"block_table: {tuple(shape)}")
-        self._tensor(block_table, torch.int32, "block_table", shape)
-        rc = blk_page_plan(self.handle, page_size, B, cache_lens.data_ptr(),
-                           None if new_lens is None else new_lens.data_ptr(),
-                           free_pages.data_ptr(), n_free, block_table.data_ptr(), shape[1], n,
-                           row_start.data_ptr(), slot_map.data_ptr(), pos.data_ptr(),
-                           used.data_ptr(), self._stream(stream))
-        if rc != BLK_OK:
-            raise BlkError(rc, "blk_page_plan")
-
-    def _pools(self, k_pages, v_pages):
-        shape = k_pages.shape
-        if len(shape) != 4 or shape[1::2] != self._kv_heads:
-            raise BlkError(BLK_ERR_SHAPE, f"k_pages: {tuple(shape)}")
-        self._tensor(k_pages, torch.float16, "k_pages", shape)
-        self._tensor(v_pages, torch.float16, "v_pages", shape)
-        return shape[::2]
+        _native.page_plan(self._args, page_size, cache_lens, new_lens, free_pages, block_table,
+                          row_start, slot_map, pos, used,
+                          None if stream is None else stream.cuda_stream)
 
     def page_append(self, k, v, slot_map, k_pages, v_pages, stream=None):
         """Rows of k and v (fp16 [n, n_kv_heads, head_dim], the last dimension
         contiguous, both with the same strides) into the slots of slot_map (int64
         [n]; -1 leaves a row out)."""
-        n_pages, page = self._pools(k_pages, v_pages)
-        n = slot_map.numel()
-        self._tensor(slot_map, torch.int64, "slot_map", (n,))
-        shape = (n, *self._kv_heads)
-        self._tensor(k, torch.float16, "k", shape, contiguous=False)
-        self._tensor(v, torch.float16, "v", shape, contiguous=False)
-        st = k.stride()
-        if st != v.stride() or st[2] != 1:
-            raise BlkError(BLK_ERR_SHAPE, "page_append: strides")
-        rc = blk_page_append(self.handle, k.data_ptr(), v.data_ptr(), st[0], st[1],
-                             slot_map.data_ptr(), n, page, n_pages,
-                             k_pages.data_ptr(), v_pages.data_ptr(), self._stream(stream))
-        if rc != BLK_OK:
-            raise BlkError(rc, "blk_page_append")
+        _native.page_append(self._args, k, v, slot_map, k_pages, v_pages,
+                            None if stream is None else stream.cuda_stream)
 
     def paged_batch(self, row_start, cache_lens, block_table, n_rows: int, page_size: int,
                     n_pages: int, max_new: int, max_len: int, prefix_pages=None) -> BlkPagedBatch:
@@ -681,27 +646,11 @@ class Block:
     def attn_paged_workspace_bytes(self, max_rows: int, max_seqs: int, prefix: bool = True) -> int:
         return blk_attn_paged_workspace_bytes(self.handle, max_rows, max_seqs, prefix)
 
-    def _paged_pools(self, batch, k_pages, v_pages, ws):
-        if self._pools(k_pages, v_pages) != (batch.n_pages, batch.page_size):
-            raise BlkError(BLK_ERR_SHAPE, "the pools are not those of the batch")
-        if ws.get_device() != self._device or not ws.is_contiguous():
-            raise BlkError(BLK_ERR_WORKSPACE, f"workspace {tuple(ws.shape)} on {ws.device}")
-
     def attn_paged(self, batch: BlkPagedBatch, q, k_pages, v_pages, out, ws, stream=None):
         """Attention of the batch's rows: q, out fp16 [n_rows, n_heads, head_dim], heads
         contiguous, rows at any stride."""
-        self._paged_pools(batch, k_pages, v_pages, ws)
-        shape, rows = (batch.n_rows, *self._heads), (self._heads[1], 1)
-        self._tensor(q, torch.float16, "q", shape, contiguous=False)
-        self._tensor(out, torch.float16, "out", shape, contiguous=False)
-        sq, so = q.stride(), out.stride()
-        if sq[1:] != rows or so[1:] != rows:
-            raise BlkError(BLK_ERR_SHAPE, f"attn_paged: strides {sq}, {so}")
-        rc = blk_attn_paged(self.handle, batch, q.data_ptr(), sq[0], k_pages.data_ptr(),
-                            v_pages.data_ptr(), out.data_ptr(), so[0], ws.data_ptr(),
-                            ws.nbytes, self._stream(stream))
-        if rc != BLK_OK:
-            raise BlkError(rc, "blk_attn_paged")
+        _native.attn_paged(self._args, batch, q, k_pages, v_pages, out, ws,
+                           None if stream is None else stream.cuda_stream)
 
     def step_paged_workspace_bytes(self, max_rows: int, max_seqs: int, prefix: bool = True) -> int:
         return blk_step_paged_workspace_bytes(self.handle, max_rows, max_seqs, prefix)
@@ -710,8 +659,12 @@ class Block:
                    out, ws, stream=None):
         """One block step of the batch: x, out fp16 [n_rows, hidden]; pos, slot_map as
         page_plan writes them."""
-        self._paged_pools(batch, k_pages, v_pages, ws)
+        shape = (batch.n_pages, self.cfg.n_kv_heads, batch.page_size, self.cfg.head_dim)
+        self._tensor(k_pages, torch.float16, "k_pages", shape)
+        self._tensor(v_pages, torch.float16, "v_pages", shape)
         self._paged_rows(batch, x, pos, slot_map, out)
+        if ws.get_device() != self._device or not ws.is_contiguous():
+            raise BlkError(BLK_ERR_WORKSPACE, f"workspace {tuple(ws.shape)} on {ws.device}")
         rc = blk_step_paged(self.handle, w, batch, x.data_ptr(), pos.data_ptr(),
                             slot_map.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                             out.data_ptr(), ws.data_ptr(), ws.nbytes, self._stream(stream))

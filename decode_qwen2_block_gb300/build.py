@@ -1,20 +1,26 @@
 """Builds libblk.so in-tree with nvcc for sm_103a (GB300).
 
 Each .cu file compiles to an object in parallel, then one shared library is
-linked.  No CMake, no torch extension machinery.
+linked; beside it the Python module of csrc/binding.cpp, against torch's headers,
+which calls that library.  No CMake, no torch extension machinery.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libblk.so")
+NATIVE = os.path.join(HERE, "_native.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
+CUDA = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -28,41 +34,55 @@ def sources():
 def _deps():
     files = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     files.append(os.path.join(os.path.dirname(HERE), "include", "blk.h"))
-    files.append(os.path.abspath(__file__))
+    files += [BINDING, os.path.abspath(__file__)]
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _run(cmd, what, verbose=False):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0 or verbose:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(what)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
 
     def compile_one(src):
-        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = [NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0 or verbose:
-            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
+        obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
+        if src == BINDING:
+            inc = os.path.join(torch_dir, "include")
+            _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", inc, "-I",
+                  os.path.join(inc, "torch", "csrc", "api", "include"), "-I",
+                  sysconfig.get_paths()["include"], "-I", os.path.join(CUDA, "include"), "-c", src,
+                  "-o", obj], "g++ failed on binding.cpp", verbose)
+        else:
+            _run([NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj],
+                 f"nvcc failed on {os.path.basename(src)}", verbose)
         return obj
 
-    with ThreadPoolExecutor(max(1, min(len(sources()), os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(compile_one, sources()))
+    files = sources() + [BINDING]
+    with ThreadPoolExecutor(max(1, min(len(files), os.cpu_count() or 1))) as ex:
+        *objs, binding = ex.map(compile_one, files)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-        raise RuntimeError("link of libblk.so failed")
+    _run([NVCC, *ARCH, "-shared", "-o", tmp, *objs], "link of libblk.so failed")
     os.replace(tmp, LIB)
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, binding, "-L", HERE, "-l:libblk.so", "-Wl,-rpath,$ORIGIN",
+          "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-lc10_cuda"], "link of _native.so failed")
+    os.replace(tmp, NATIVE)
     return LIB
 
 

@@ -639,10 +639,11 @@ def test_argument_errors():
         with pytest.raises(blk.BlkError) as e:
             b.attn_paged(d, x.q, x.k_pages, x.v_pages, out, bad)
         assert e.value.status == blk.BLK_ERR_WORKSPACE
-    b._device += 1                             # tensors of another GPU than the block's
+    args = b._args                             # tensors of another GPU than the block's
+    b._args = (args[0], args[1] + 1, *args[2:])
     try:
         with pytest.raises(blk.BlkError) as e:
             b.attn_paged(d, x.q, x.k_pages, x.v_pages, out, ws)
         assert e.value.status == S
     finally:
-        b._device -= 1
+        b._args = args
