@@ -144,13 +144,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ int64_t start_cum;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  // what needs nothing of the kernels before
   if (tid == 0) {
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
-  }
-  griddep_wait();
-  griddep_launch();
-  if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 4);
@@ -161,6 +158,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     start_cum = 0;
     abort_s = 0;
   }
+  griddep_wait();
+  griddep_launch();
   // tiles of all sequences (one kv head), and those before this thread's
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
@@ -809,14 +808,21 @@ cudaError_t launch_paged_few(const PagedAttnParams& p, cudaStream_t s, bool pdl)
 
 cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  // The fewer rows there are to merge, the more warps take one (figures at the kernel).
-  const int64_t units = (int64_t)p.a.B * p.a.Hkv;
-  const int64_t cut = p.prefix                           ? (int64_t)p.a.N * p.a.Hq     // rows at most
-                      : p.a.slot_rows > kPagedFewRows ? (int64_t)p.a.nc * p.a.slot_rows
-                      : (units < p.a.nc ? units : p.a.nc) * p.a.max_new * p.a.G;
+  // Rows to merge, at most: with a prefix every row, else those of the units that can be
+  // cut (one begins in a CTA).  The fewer they are, the more warps take one (figures at
+  // the kernel); the grid has no more CTAs than rows, as idle ones still have to come
+  // and go.
+  const PagedAttnParams& a = p.a;
+  const int64_t all = (int64_t)a.N * a.Hq, units = (int64_t)a.B * a.Hkv;
+  int64_t cut = all;
+  if (!p.prefix) {
+    const int64_t most = a.slot_rows > kPagedFewRows
+                             ? (int64_t)a.nc * a.slot_rows
+                             : (units < a.nc ? units : a.nc) * a.max_new * a.G;
+    cut = most < all ? most : all;
+  }
   const int wpr = cut > 16 * num_sms ? 1 : cut > 4 * num_sms ? 2 : 8;
-  const int64_t rows = p.prefix ? (int64_t)p.a.N * p.a.Hq : (int64_t)p.a.nc * p.a.slot_rows;
-  const int64_t per = wpr == 1 ? 16 : 8 / wpr, want = (rows + per - 1) / per;
+  const int64_t per = wpr == 1 ? 16 : 8 / wpr, want = (cut + per - 1) / per;
   const int64_t fit = (int64_t)num_sms * 8;
   cfg.gridDim = dim3((unsigned)(want < fit ? want : fit));
   cfg.blockDim = dim3(256);

@@ -10,29 +10,6 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 
-// Exclusive sum over the block of one value per thread; `total` is the sum.
-__device__ __forceinline__ int64_t block_excl(int64_t v, int64_t* warp_sums, int64_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();   // the sums of an earlier call have been read
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int64_t before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    const int64_t s = warp_sums[w];
-    if (w < warp) before += s;
-    total += s;
-  }
-  return before + x - v;
-}
-
 // Last i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
 __device__ __forceinline__ int last_le(const int* a, int n, int x) {
   int lo = 0, hi = n;
@@ -49,10 +26,13 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
 // beginning behind what the sequences before it took.  Both are sums over the
 // sequences, so every CTA forms them in shared memory by itself (B <= 4096
 // lengths, a few KB) and fills its share of the slots and table entries: one
-// launch, nothing waits on another CTA.  Pages of a row are formed from the
-// lengths and the free list, never read back from the table entries that this
-// launch writes.  Bound by latency: 64 decoding sequences are one CTA and
-// three round trips to L2, 3.9 us in a graph; 200 prompts with 100,000 slots 5.4.
+// launch, nothing waits on another CTA.  One scan gives both sums, packed in 64
+// bits: a sequence whose rows run past N is refused after the scan, but then so is
+// every later one with rows, and what it would have taken moves nobody's pages.
+// Pages of a row are formed from the lengths and the free list, never read back
+// from the table entries that this launch writes.  Bound by latency: 64 decoding
+// sequences are one CTA and three round trips to L2, 3.5 us in a graph (with a scan
+// each and the lengths read in turn 3.9); 200 prompts with 100,000 slots 4.7.
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanParams p) {
   extern __shared__ int sm[];
   int* rs = sm;                  // [B + 1] first row, at most N
@@ -60,51 +40,67 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
   uint8_t* bad = reinterpret_cast<uint8_t*>(base + p.B);   // [B] refused
   __shared__ int64_t warp_sums[kPlanThreads / 32];
   __shared__ int used_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) used_s = 0;
   griddep_wait();
   griddep_launch();
-  const int tid = threadIdx.x;
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   const int64_t cap = p.max_blocks << p.page_lg, mask = ((int64_t)1 << p.page_lg) - 1;
-  auto n_of = [&](int b) -> int64_t { return p.new_lens ? p.new_lens[b] : 1; };
-  if (tid == 0) used_s = 0;
-  int64_t rows = 0, total;
+  struct Len { int64_t n, L; };
+  auto load = [&](int b) { return Len{p.new_lens ? p.new_lens[b] : 1, p.cache_lens[b]}; };
+  const Len first = b0 < b1 ? load(b0) : Len{0, 0};
+  auto len = [&](int b) { return b == b0 ? first : load(b); };
+  auto rows_of = [&](const Len& s) { return s.n < 0 || s.n > p.N ? (int64_t)0 : s.n; };
+  // (rows past N apart)
+  auto fits = [&](const Len& s) {
+    return s.n >= 0 && s.n <= p.N && s.L >= 0 && s.L <= cap && s.L + s.n <= cap;
+  };
+  auto need_of = [&](const Len& s) {
+    return fits(s) ? ((s.L + s.n + mask) >> p.page_lg) - ((s.L + mask) >> p.page_lg) : (int64_t)0;
+  };
+  // rows (at most 4096 x 2^20) in the low 34 bits, pages (at most 4096 x 2^16 + 4096) above
+  constexpr int kPack = 34;
+  int64_t mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const int64_t n = n_of(b);
-    rows += (n < 0 || n > p.N) ? 0 : n;
+    const Len s = len(b);
+    mine += rows_of(s) + (need_of(s) << kPack);
   }
-  int64_t r = block_excl(rows, warp_sums, total);
-  int64_t need_sum = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int64_t n = n_of(b), L = p.cache_lens[b];
-    const bool n_ok = n >= 0 && n <= p.N;
-    const int64_t r1 = r + (n_ok ? n : 0);
-    const bool ok = n_ok && r1 <= p.N && L >= 0 && L <= cap && L + n <= cap;
-    rs[b] = (int)min(r, p.N);
-    bad[b] = !ok;
-    if (blockIdx.x == 0) p.row_start[b] = r;
-    if (ok) need_sum += ((L + n + mask) >> p.page_lg) - ((L + mask) >> p.page_lg);
-    r = r1;
+  int64_t x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  if (tid == 0) {
-    rs[p.B] = (int)min(total, p.N);
-    if (blockIdx.x == 0) p.row_start[p.B] = total;
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  int64_t before = x - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    const int64_t s = warp_sums[w];
+    if (w < warp) before += s;
+    total += s;
   }
-  int64_t need_total;
-  int64_t take = block_excl(need_sum, warp_sums, need_total);
+  constexpr int64_t kRows = ((int64_t)1 << kPack) - 1;
+  int64_t r = before & kRows, take = before >> kPack;
   int top = 0;
   bool any_bad = false;
   for (int b = b0; b < b1; ++b) {
-    const int64_t n = n_of(b), L = p.cache_lens[b];
-    const int64_t need =
-        bad[b] ? 0 : ((L + n + mask) >> p.page_lg) - ((L + mask) >> p.page_lg);
+    const Len s = len(b);
+    const int64_t r1 = r + rows_of(s), need = need_of(s);
+    const bool no = !fits(s) || r1 > p.N || (need > 0 && take + need > p.n_free);
+    rs[b] = (int)min(r, p.N);
     base[b] = (int)min(take, p.n_free);
-    if (need > 0) {
-      if (take + need > p.n_free) bad[b] = 1;
-      else top = (int)(take + need);
-    }
-    any_bad |= bad[b] != 0;
+    bad[b] = no;
+    if (blockIdx.x == 0) p.row_start[b] = r;
+    if (!no && need > 0) top = (int)(take + need);
+    any_bad |= no;
+    r = r1;
     take += need;
+  }
+  if (tid == 0) {
+    rs[p.B] = (int)min(total & kRows, p.N);
+    if (blockIdx.x == 0) p.row_start[p.B] = total & kRows;
   }
   if (top > 0) atomicMax(&used_s, top);
   if (any_bad && blockIdx.x == 0) set_error(p.err, kDevPage);
