@@ -1400,6 +1400,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
     a.tm_k = few_k;
     a.tm_v = few_v;
     paged_few_slots(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
+    a.by_unit = !prefix && b->n_seqs * Hkv <= a.nc;    // (a CTA for each entry merges it)
     BLK_LAUNCH(tm, kKPagedFew, launch_paged_few(a, s, true));
   } else {
     a.nc = h->num_sms;
@@ -1407,7 +1408,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
     BLK_LAUNCH(tm, kKPagedMany, launch_paged_many(m, s, true));
   }
   mg.a = a;
-  mg.own_btok = few ? kPagedFewRows : m.btok;
+  mg.own_btok = few ? 0 : m.btok;
   BLK_LAUNCH(tm, kKPagedMerge, launch_paged_merge(mg, h->num_sms, s));
   return BLK_OK;
 }

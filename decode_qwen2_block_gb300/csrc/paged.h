@@ -85,7 +85,9 @@ struct PagedAttnParams {
   int slot_rows;               // partial rows of one slot
   float* part;                 // [nc][2][slot_rows][D]
   float2* ml;                  // [nc][2][slot_rows] (m, l)
-  PagedPiece* cut;             // [nc]: the unit that begins in CTA i and goes on behind it
+  PagedPiece* cut;             // [nc]: the unit that begins in CTA i and goes on behind it;
+                               //   by_unit: [Hkv][B], of every unit (at most nc of them)
+  int by_unit;
   // shared prefix: own parts are merged with the prefix's, so whole units
   // leave their (O, m, l) by row and head, and every row says where its own
   // part is
@@ -125,7 +127,7 @@ cudaError_t configure_paged_many();
 struct PagedMergeParams {
   PagedAttnParams a;           // the own parts
   int prefix;                  // 1: merge by rows with the prefix's partials
-  int own_btok;                // tokens of a block of 128 partial rows (few rows: all of them)
+  int own_btok;                // tokens of a block of 128 partial rows (0: rows lie close)
   const float* pre_part;       // prefix partials [pre_nc][2][pre_rows][D]
   const float2* pre_ml;
   const float* pre_own;        // prefix parts of units inside one CTA, by row and head

@@ -173,6 +173,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     mine += seq_weight(p, s);
     bad |= s.bad;
     if (b < 128) first_seqs[b] = s;
+    if (p.by_unit && s.n == 0 && blockIdx.x == 0)
+      for (int g = 0; g < p.Hkv; ++g) p.cut[g * p.B + b].c0 = -1;
   }
   if (bad && blockIdx.x == 0) set_error(p.err, kDevPage);
   int64_t inc = mine;
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int cta = blockIdx.x;
   const int64_t t0 = cta < nc ? range_of(T, cta, nc) : T, t1 = cta < nc ? range_of(T, cta + 1, nc) : T;
   if (t0 >= t1) {   // (uniform over the CTA)
-    if (tid == 0) p.cut[cta].c0 = -1;
+    if (tid == 0 && !p.by_unit) p.cut[cta].c0 = -1;
     return;
   }
   const int g0 = small_div(t0, T1);
@@ -223,8 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int it = 0, seg = 0, base32 = -1;
     PagedSeq mys = {};
     bool ok = true;
-    PagedPiece cut;
-    cut.c0 = -1;
+    PagedPiece cut = {-1, 0, 0, 0, 0};
     while (lin < t1 && ok) {
       if (b >= p.B) {        // the next kv head begins again with the first sequence
         b = 0;
@@ -260,13 +261,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int dst = whole ? -1 : (xa == 0 ? 1 : 0);
       if (xa == 0) {
         const int c1 = whole ? cta : (int)((ue * nc - 1) / T);
-        if (!whole) {
-          cut.c0 = cta;
-          cut.c1 = c1;
-          cut.rows = s.n * p.G;
-          cut.r0 = s.r0;
-          cut.g = g;
-        }
+        const PagedPiece now = {whole ? -1 : cta, s.n * p.G, c1, s.r0, g};
+        if (!whole) cut = now;
+        if (p.by_unit && lane == 0) p.cut[g * p.B + b] = now;
         if (p.row_info)
           for (int t = lane; t < s.n; t += 32)
             p.row_info[(int64_t)(s.r0 + t) * p.Hkv + g] =
@@ -322,13 +319,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++b;
       ++seg;
     }
-    if (lane == 0) {
-      volatile PagedPiece& c = p.cut[cta];
-      c.c1 = cut.c1;
-      c.rows = cut.rows;
-      c.r0 = cut.r0;
-      c.g = cut.g;
-      c.c0 = ok ? cut.c0 : -1;
+    if (lane == 0 && !p.by_unit) {
+      if (!ok) cut.c0 = -1;
+      p.cut[cta] = cut;
     }
     const int st = it % S;
     if (ok && it >= S && !mbar_wait_near(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
@@ -585,19 +578,36 @@ __global__ void __launch_bounds__(kThreads, 2)
 // then the pieces, a round trip each.  The attention with one / two / eight warps a
 // row: 96 rows of 16 pieces 14.2 / 10.7 / 10.3 us, 768 rows 48.9 / 48.3 / 49.7, 32000
 // rows of two (39 MB) 80 / 90 / 127.
-template <int D, int kWPR>
+template <int D, int kWPR, bool kByUnit>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedMergeParams q) {
   // a row's lanes: half a warp where rows are many (two rows' pieces in flight per warp)
   constexpr int kLanes = kWPR == 1 ? 16 : 32, kV = D / kLanes;     // columns per lane
   const PagedAttnParams& p = q.a;
   __shared__ float sacc[kWPR > 1 ? 8 : 1][D + 2];
-  __shared__ int cut_row[512], wsum[8];
+  __shared__ int cut_row[kByUnit ? 1 : 512], wsum[8];
   griddep_wait();
   griddep_launch();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = (lane % kLanes) * kV;
-  int64_t items;
-  if (!q.prefix) {
+  // With a prefix the blocks share all rows and heads.  Else they share the rows of the
+  // cut units: where there is an entry for every unit, blockIdx.x is one and the blocks
+  // of a column share its rows; else they share the rows of the CTAs' entries together
+  // (an entry a column left most blocks without work there: 512 tokens 28.4 -> 30.7 us;
+  // finding a row's entry took 64 decoding sequences from 45.9 to 47.5).
+  PagedPiece u = {};
+  int64_t items, b0 = blockIdx.x, nb = gridDim.x;
+  if constexpr (kByUnit) {
+    u = p.cut[blockIdx.x];
+    // (an attention that timed out may have left its entry as it was)
+    const bool cut = u.c0 >= 0 && u.c0 <= u.c1 && u.c1 < p.nc && u.rows > 0 &&
+                     u.rows <= p.slot_rows && u.r0 >= 0 && u.r0 <= p.N - u.rows / p.G &&
+                     u.g >= 0 && u.g < p.Hkv;
+    items = cut ? u.rows : 0;
+    b0 = blockIdx.y;
+    nb = gridDim.y;
+  } else if (q.prefix) {
+    items = (int64_t)p.N * p.Hq;
+  } else {
     // rows of the cut units before each CTA's (two CTAs a thread; nc <= 512)
     int n2[2] = {0, 0};
 #pragma unroll
@@ -626,29 +636,30 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
     cut_row[2 * tid + 1] = x - n2[1];
     __syncthreads();
     items = all;
-  } else {
-    items = (int64_t)p.N * p.Hq;
   }
   constexpr int kRows = 256 / kLanes / kWPR;  // rows of a block at a time
-  for (int64_t item0 = (int64_t)blockIdx.x * kRows; item0 < items;
-       item0 += (int64_t)gridDim.x * kRows) {
+  for (int64_t item0 = b0 * kRows; item0 < items; item0 += nb * kRows) {
     const int64_t item = item0 + tid / kLanes / kWPR;
     bool here = item < items;                 // (a block's warps stay together: barriers below)
     if (kWPR == 1 && !here) break;
     // pieces: own ones in slots of CTAs c0..c1 (or a whole one), then the prefix's
     int c0 = 0, c1 = 0, row = 0, r = 0, hq = 0, pc0 = 0, pc1 = -1, prow = 0;
     bool own_whole = false, pre_whole = false;
-    if (!q.prefix) {
-      int lo = 0, hi = p.nc;
-      while (hi - lo > 1) {          // (an item behind the last takes no piece)
-        const int mid = (lo + hi) >> 1;
-        if (cut_row[mid] <= item) lo = mid; else hi = mid;
+    if (kByUnit || !q.prefix) {
+      int i = (int)item;             // row of the unit
+      if constexpr (!kByUnit) {
+        int lo = 0, hi = p.nc;
+        while (hi - lo > 1) {        // (an item behind the last takes no piece)
+          const int mid = (lo + hi) >> 1;
+          if (cut_row[mid] <= i) lo = mid; else hi = mid;
+        }
+        u = p.cut[lo];
+        i -= cut_row[lo];
       }
-      const PagedPiece u = p.cut[lo];
-      const int tl = ((int)item - cut_row[lo]) / p.G, hh = (int)item - cut_row[lo] - tl * p.G;
+      const int tl = i / p.G, hh = i - tl * p.G;
       c0 = u.c0;
       c1 = u.c1;
-      row = tl / q.own_btok * 128 + tl % q.own_btok * p.G + hh;
+      row = q.own_btok ? tl / q.own_btok * 128 + tl % q.own_btok * p.G + hh : i;
       r = u.r0 + tl;
       hq = u.g * p.G + hh;
     } else {
@@ -678,9 +689,9 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
       prow = tl / q.pre_btok * 128 + tl % q.pre_btok * p.G + hh;
     }
     const int n_own = own_whole ? 1 : c1 - c0 + 1;
-    const int n_all = !here ? 0 : n_own + (q.prefix ? pc1 - pc0 + 1 : 0);
+    const int n_all = !here ? 0 : n_own + (!kByUnit && q.prefix ? pc1 - pc0 + 1 : 0);
     auto piece = [&](int i, const float*& o, float2& ml) {
-      if (i < n_own) {
+      if (kByUnit || i < n_own) {
         const int64_t at = own_whole ? (int64_t)r * p.Hq + hq
                                      : ((int64_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.slot_rows + row;
         o = (own_whole ? p.own : p.part) + at * D;
@@ -809,22 +820,22 @@ cudaError_t launch_paged_few(const PagedAttnParams& p, cudaStream_t s, bool pdl)
 cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   // Rows to merge, at most: with a prefix every row, else those of the units that can be
-  // cut (one begins in a CTA).  The fewer they are, the more warps take one (figures at
-  // the kernel); the grid has no more CTAs than rows, as idle ones still have to come
-  // and go.
+  // cut, each in an entry of its own.  The fewer they are, the more warps take one
+  // (figures at the kernel); the grid has few CTAs that find nothing to do, as those
+  // still have to come and go.
   const PagedAttnParams& a = p.a;
-  const int64_t all = (int64_t)a.N * a.Hq, units = (int64_t)a.B * a.Hkv;
-  int64_t cut = all;
-  if (!p.prefix) {
-    const int64_t most = a.slot_rows > kPagedFewRows
-                             ? (int64_t)a.nc * a.slot_rows
-                             : (units < a.nc ? units : a.nc) * a.max_new * a.G;
-    cut = most < all ? most : all;
-  }
+  const bool few = a.slot_rows <= kPagedFewRows;
+  const int64_t entries = a.by_unit ? (int64_t)a.B * a.Hkv : a.nc, all = (int64_t)a.N * a.Hq;
+  const int64_t rows = few ? a.max_new * a.G : a.slot_rows;          // of a unit
+  const int64_t cut = p.prefix || entries * rows > all ? all : entries * rows;
   const int wpr = cut > 16 * num_sms ? 1 : cut > 4 * num_sms ? 2 : 8;
-  const int64_t per = wpr == 1 ? 16 : 8 / wpr, want = (cut + per - 1) / per;
-  const int64_t fit = (int64_t)num_sms * 8;
-  cfg.gridDim = dim3((unsigned)(want < fit ? want : fit));
+  const int64_t per = wpr == 1 ? 16 : 8 / wpr;
+  if (a.by_unit) {
+    cfg.gridDim = dim3((unsigned)entries, (unsigned)((rows + per - 1) / per));
+  } else {
+    const int64_t want = (cut + per - 1) / per, fit = (int64_t)num_sms * 8;
+    cfg.gridDim = dim3((unsigned)(want < fit ? want : fit));
+  }
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -832,13 +843,21 @@ cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.a.D == 128)
-    return wpr == 1   ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 1>, p)
-           : wpr == 2 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 2>, p)
-                      : cudaLaunchKernelEx(&cfg, paged_merge_kernel<128, 8>, p);
-  return wpr == 1   ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 1>, p)
-         : wpr == 2 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 2>, p)
-                    : cudaLaunchKernelEx(&cfg, paged_merge_kernel<64, 8>, p);
+  const int d = a.D == 128, v = wpr == 1 ? 0 : wpr == 2 ? 1 : 2;
+  if (a.by_unit) {
+    void (*const k[2][3])(PagedMergeParams) = {
+        {paged_merge_kernel<64, 1, true>, paged_merge_kernel<64, 2, true>,
+         paged_merge_kernel<64, 8, true>},
+        {paged_merge_kernel<128, 1, true>, paged_merge_kernel<128, 2, true>,
+         paged_merge_kernel<128, 8, true>}};
+    return cudaLaunchKernelEx(&cfg, k[d][v], p);
+  }
+  void (*const k[2][3])(PagedMergeParams) = {
+      {paged_merge_kernel<64, 1, false>, paged_merge_kernel<64, 2, false>,
+       paged_merge_kernel<64, 8, false>},
+      {paged_merge_kernel<128, 1, false>, paged_merge_kernel<128, 2, false>,
+       paged_merge_kernel<128, 8, false>}};
+  return cudaLaunchKernelEx(&cfg, k[d][v], p);
 }
 
 cudaError_t configure_paged_few() {

@@ -343,6 +343,32 @@ def test_short_pieces_one_after_another_give_the_same_bits(heads, kv, dim, top):
         assert torch.equal(out.view(torch.int16), first.view(torch.int16))
 
 
+@pytest.mark.parametrize("top", [1, 5, 60])
+def test_a_workspace_keeps_nothing_of_the_call_before(top):
+    """The same workspace for batches whose sequences are cut over many CTAs, idle, inside
+    one CTA, refused, more, fewer."""
+    b = block(12, 2, 128)
+    nb = b.attn_paged_workspace_bytes(2000, 400)
+    ws = torch.zeros(nb, dtype=torch.uint8, device="cuda")
+    for seed, (hist, new) in enumerate([
+            ([6000] * 6, [top] * 6), ([6000] * 6, [0, top, 0, 0, 1, 0]),
+            ([3] * 152, [1] * 152), ([700] * 153, [0, 1, 1] * 51), ([9000, 2, 4000], [1, top, 0]),
+            ([9000], [top]), ([0] * 6, [0] * 5 + [1]), ([800] * 4, [1, 1, top, 1])]):
+        x = Batch(12, 2, 128, 64, hist, new, seed=30 + seed, pad_rows=1)
+        bad = [1] if len(hist) == 4 else []
+        d = x.descriptor(b, max_new=max(new + [1]))
+        if bad:
+            x.lens[1] = -1
+        out = torch.full((x.rows, 12, 128), MARK, dtype=torch.float16, device="cuda")
+        b.attn_paged(d, x.q, x.k_pages, x.v_pages, out, ws)
+        if bad:
+            with pytest.raises(blk.BlkError):
+                b.check()
+        else:
+            b.check()
+        check_rows(x, out, skip=bad)
+
+
 @pytest.mark.parametrize("top", [1, 4, 40])
 @pytest.mark.parametrize("prefix", [0, 8192])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
