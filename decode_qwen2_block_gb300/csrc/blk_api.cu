@@ -1343,9 +1343,11 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   a.out = static_cast<__half*>(out); a.out_stride = out_stride;
   a.row_start = b->row_start; a.cache_lens = b->cache_lens;
   a.table = b->block_table; a.prefix_pages = b->prefix_pages;
-  a.max_blocks = b->max_blocks; a.n_pages = b->n_pages; a.window = h->window;
+  a.max_blocks = b->max_blocks; a.n_pages = b->n_pages;
+  a.window = h->window < 0x7fffffff ? (int)h->window : 0;   // (slots are below 2^31)
   a.max_len = b->max_len; a.prefix_len = b->prefix_len;
   a.pre_here = prefix ? 0 : b->prefix_len;
+  a.own_lo = (int)(b->prefix_len - a.pre_here);
   a.B = (int)b->n_seqs; a.N = (int)b->n_rows; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.G = G;
   a.page_lg = page_log2(page); a.max_new = (int)b->max_new;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));

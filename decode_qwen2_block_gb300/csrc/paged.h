@@ -73,12 +73,14 @@ struct PagedAttnParams {
   const int64_t* cache_lens;   // [B]
   const int32_t* table;        // [B][max_blocks]
   const int32_t* prefix_pages; // [prefix_len / page] or null
-  int64_t max_blocks, n_pages, window;
+  int64_t max_blocks, n_pages;
   int64_t max_len;             // slots of the longest sequence, new ones with it; it fits the
                                //   table's rows and 31 bits
   int64_t prefix_len;          // every sequence has at least the shared prefix's slots
   int64_t pre_here;            // slots of it that the own parts take with them (their pages from
                                //   prefix_pages); the others belong to the prefix's own launch
+  int own_lo;                  // the first slot of the own parts: prefix_len - pre_here
+  int window;                  // of the handle; 0: all slots
   int B, N, Hq, Hkv, D, G, page_lg, max_new;
   float scale_log2;
   int nc;                      // CTAs of the kernel

@@ -34,18 +34,24 @@ __device__ __forceinline__ PagedSeq load_seq(const PagedAttnParams& p, int b) {
   return s;
 }
 
-// First slot that the rows from slot `first` on see here (the prefix's slots only
-// where it has no launch of its own).
+// First slot that a row in slot `last` sees, and first slot that the rows from slot
+// `first` on see here (the prefix's slots only where it has no launch of its own).
+__device__ __forceinline__ int paged_window(const PagedAttnParams& p, int last) {
+  return p.window > 0 && last >= p.window ? last - p.window + 1 : 0;
+}
 __device__ __forceinline__ int paged_lo(const PagedAttnParams& p, int first) {
-  const int64_t w = window_lo(p.window, first);
-  const int64_t own = p.prefix_len - p.pre_here;
-  return (int)(w > own ? w : own);
+  return max(paged_window(p, first), p.own_lo);
 }
 
-// T * i / n and x / y of non-negative values, in 32 bits where they fit (a 64-bit
-// division takes some 100 clocks, and every CTA begins with a few).
+// T * i / n, the CTA of n that has tile x of T (the greatest i with T * i / n <= x), and
+// x / y, of non-negative values, in 32 bits where they fit (a 64-bit division takes
+// some 100 clocks or more, and every CTA begins with a few).
 __device__ __forceinline__ int64_t range_of(int64_t T, int i, int n) {
   return T < (1 << 20) ? (int64_t)((uint32_t)((uint32_t)T * (uint32_t)i) / (uint32_t)n) : T * i / n;
+}
+__device__ __forceinline__ int cta_of(int64_t T, int64_t x, int n) {
+  return T < (1 << 20) ? (int)(((uint32_t)(x + 1) * (uint32_t)n - 1) / (uint32_t)T)
+                       : (int)(((x + 1) * n - 1) / T);
 }
 __device__ __forceinline__ int small_div(int64_t x, int64_t y) {
   return ((x | y) >> 31) == 0 ? (int)((uint32_t)x / (uint32_t)y) : (int)(x / y);

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool whole = xa == 0 && xb == nt;
       const int dst = whole ? -1 : (xa == 0 ? 1 : 0);
       if (xa == 0) {
-        const int c1 = whole ? cta : (int)((ue * nc - 1) / T);
+        const int c1 = whole ? cta : cta_of(T, ue - 1, nc);
         const PagedPiece now = {whole ? -1 : cta, s.n * p.G, c1, s.r0, g};
         if (!whole) cut = now;
         if (p.by_unit && lane == 0) p.cut[g * p.B + b] = now;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int h2 = 0; h2 < 2; ++h2) {
           const int row = mt * 16 + grp + 8 * h2;
           last[mt][h2] = L + min(row / p.G, n - 1);
-          low[mt][h2] = (int)window_lo(p.window, last[mt][h2]);
+          low[mt][h2] = paged_window(p, last[mt][h2]);
           m_r[mt][h2] = -INFINITY;
           l_r[mt][h2] = 0.f;
 #pragma unroll

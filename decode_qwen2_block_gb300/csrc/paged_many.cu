@@ -42,7 +42,7 @@ namespace {
 constexpr int kThreads = 384;
 // Registers: a softmax thread holds a row of 128 scores.  The block is launched
 // with 168 a thread (384 x 168 = 64512); warps 0-3 keep 72, the softmax warps take
-// 216 (with the prefix's simpler producer 88 and 208 spill less): 128 x 72 + 256 x
+// 216 (the prefix's variant 88 and 208: 56.2 us against 59.4): 128 x 72 + 256 x
 // 216 = 128 x 88 + 256 x 208 = 64512.  configure_paged_many checks the 168.
 constexpr int kRegsLaunch = 168;
 template <bool kPrefix>
@@ -74,7 +74,7 @@ struct MSmem {
   static constexpr int kRingOff = 2 * kQBlk;
   static constexpr int kInfoOff = kRingOff + kRing * kKV;
   static constexpr int kBarOff = kInfoOff + kInfos * (int)sizeof(ManyInfo);
-  static constexpr int kEnd = kBarOff + (kRing + 2 * kS + 7) * 8 + 16;
+  static constexpr int kEnd = kBarOff + (kRing + 2 * kS + 8) * 8 + 16;
   static constexpr size_t kBytes = (size_t)kEnd + 1024;
   static constexpr uint32_t kSCol = 0, kOCol = 256;
   static_assert(kBarOff % 8 == 0 && kBytes <= 232448, "shared memory");
@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = smem + Sm::kRingOff;
   volatile ManyInfo* infos = reinterpret_cast<volatile ManyInfo*>(smem + Sm::kInfoOff);
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + Sm::kBarOff);
-  uint64_t* q_full = kv_full + R;
-  uint64_t* s_full = q_full + 1;        // [2][kS] S of a block in TMEM, tile j's at j % kS
+  uint64_t* q_full = kv_full + R;       // [2] q of a block
+  uint64_t* s_full = q_full + 2;        // [2][kS] S of a block in TMEM, tile j's at j % kS
   uint64_t* p_full = s_full + 2 * kS;   // [2] P of a block in TMEM (O rescaled)
   uint64_t* o_full = p_full + 2;        // [2] O complete at the end of a piece
   uint64_t* drain = o_full + 2;         // [2]
@@ -211,11 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // what needs nothing of the kernels before: barriers, TMEM, tensor maps
   if (threadIdx.x == 0) {
     for (int s = 0; s < R; ++s) mbar_init(&kv_full[s], 1);
-    mbar_init(q_full, 1);
     for (int k = 0; k < 2 * kS; ++k) mbar_init(&s_full[k], 1);
     for (int k = 0; k < 2; ++k) {
       mbar_init(&p_full[k], 5);      // the softmax warps and the other block's issuer
       mbar_init(&o_full[k], 1);
+      mbar_init(&q_full[k], 1);
     }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
@@ -254,7 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     T1 = (int64_t)q.units * ((p.prefix_len + kTile - 1) / kTile + kHead);
   } else {
     // Every CTA sums the units' tiles itself: units of all sequences first (a run
-    // of sequences per thread), then their tiles (a run of units per thread).
+    // of sequences per thread), then their tiles (a run of units per thread).  (By the
+    // producer warp alone, without barriers: one prompt's chunk 28.0 -> 27.6 us, but 8
+    // prompts 80.4 -> 82.4, a lane having nine units of theirs one after another.)
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     int64_t n = 0, R64;
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = blk * q.btok + rt; // token of the unit
         row_ok = rt < q.btok && t < ntok;
         last = kPrefix ? hi - 1 : first + min(t, ntok - 1);
-        low = kPrefix ? 0 : max(lo, (int)window_lo(p.window, last));
+        low = kPrefix ? 0 : max(lo, paged_window(p, last));
         m = -INFINITY;
         l = 0.f;
       }
@@ -548,7 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       cum = start_cum;
     }
     int64_t lin = t0;
-    int it = 0, seg = 0, qn = 0, item = 0;   // tiles, pieces, q loads, ring items so far
+    int it = 0, seg = 0, item = 0;     // tiles, pieces, ring items so far
+    int qn0 = 0, qn1 = 0;              // q loads of block 0, 1
     bool ok = true;
     PagedPiece cut;
     cut.c0 = -1;
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = lane; t < u.ntok; t += 32)
             p.row_info[(int64_t)(u.r0 + t) * p.Hkv + g] = make_int4(-2, 0, 0, 0);
         } else {
-          const int c1 = whole ? cta : (int)((ue * nc - 1) / T);
+          const int c1 = whole ? cta : cta_of(T, ue - 1, nc);
           if (!whole) {
             cut.c0 = cta;
             cut.c1 = c1;
@@ -664,13 +667,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x == xa) {
           wait_s(it - 1);             // q of the piece before is used up
           if (!ok) break;
-          ++qn;
+          // (a barrier a block: block 0 begins when its q is there)
+          ++qn0;
+          qn1 += two;
           if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * q.btok * p.G * D * 2);
-            for (int blk = 0; blk < (two ? 2 : 1); ++blk)
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk) {
+              if (blk == 1 && !two) break;
+              mbar_arrive_expect_tx(&q_full[blk], q.btok * p.G * D * 2);
               for (int hh = 0; hh < H; ++hh)
                 tma_3d(smem + blk * Sm::kQBlk + hh * 16384, &p.tm_q, hh * 64, g * p.G,
-                       u.r0 + blk * q.btok, q_full);
+                       u.r0 + blk * q.btok, &q_full[blk]);
+            }
           }
         }
         wait_s((item - R + 1) >> 1);
@@ -698,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // copies in flight land before shared memory goes away
-      if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1u, nullptr);
+      if (qn0 > 0) mbar_wait(&q_full[0], (uint32_t)(qn0 - 1) & 1u, nullptr);
+      if (qn1 > 0) mbar_wait(&q_full[1], (uint32_t)(qn1 - 1) & 1u, nullptr);
       for (int j = max(0, item - R); j < item; ++j)
         mbar_wait(&kv_full[j % R], (uint32_t)(j / R) & 1u, nullptr);
     }
@@ -709,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int blk = warp - 1;
       const uint32_t qb = smem_u32(smem) + blk * Sm::kQBlk, ra = smem_u32(ring);
       const uint32_t tS = tmem + Sm::kSCol + blk * 128, tO = tmem + Sm::kOCol + blk * 128;
-      int seg = -1;                    // piece of the tile whose S was issued last
+      int qs = 0;                      // pieces whose q was waited for
       auto landed = [&](int i) {       // ring item i
         return mbar_wait_near(&kv_full[i % R], (uint32_t)(i / R) & 1u, p.err);
       };
@@ -722,9 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t v_hi = (uint32_t)(tc_desc_mnmajor(0) >> 32), rv_lo = (uint32_t)tc_desc_mnmajor(ra);
       auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
       auto start_s = [&](int it, int f, uint32_t kd_lo) -> bool {
-        if (f & 1) {                   // a new piece: its q
-          ++seg;
-          if (!mbar_wait_near(q_full, (uint32_t)seg & 1u, p.err)) return false;
+        if ((f & 1) && (blk == 0 || (f & 8))) {    // a new piece: its q
+          if (!mbar_wait_near(&q_full[blk], (uint32_t)qs & 1u, p.err)) return false;
+          ++qs;
         }
         tc_fence_after();
         if (!(f & 4) && (blk == 0 || (f & 8))) {
