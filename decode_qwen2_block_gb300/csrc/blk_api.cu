@@ -1374,6 +1374,11 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
       return BLK_ERR_CUDA;
   }
   m.btok = paged_btok(G);
+  // entries for all units where the CTAs' entries are as many
+  auto units_each = [&]() -> int {
+    const int64_t each = few ? 1 : (b->max_new + 2 * m.btok - 1) / (2 * m.btok);
+    return !prefix && b->n_seqs * Hkv * each <= a.nc ? (int)each : 0;
+  };
   PagedMergeParams mg = {};
   if (prefix) {
     a.own = reinterpret_cast<float*>(base + lay.own);
@@ -1402,11 +1407,12 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
     a.tm_k = few_k;
     a.tm_v = few_v;
     paged_few_slots(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
-    a.by_unit = !prefix && b->n_seqs * Hkv <= a.nc;    // (a CTA for each entry merges it)
+    a.upb = units_each();
     BLK_LAUNCH(tm, kKPagedFew, launch_paged_few(a, s, true));
   } else {
     a.nc = h->num_sms;
     a.slot_rows = kPagedManyRows;
+    a.upb = units_each();
     BLK_LAUNCH(tm, kKPagedMany, launch_paged_many(m, s, true));
   }
   mg.a = a;

@@ -88,8 +88,8 @@ struct PagedAttnParams {
   float* part;                 // [nc][2][slot_rows][D]
   float2* ml;                  // [nc][2][slot_rows] (m, l)
   PagedPiece* cut;             // [nc]: the unit that begins in CTA i and goes on behind it;
-                               //   by_unit: [Hkv][B], of every unit (at most nc of them)
-  int by_unit;
+                               //   with upb: [Hkv][B][upb], of every unit (at most nc)
+  int upb;                     // units of a sequence at most, if there are entries for all
   // shared prefix: own parts are merged with the prefix's, so whole units
   // leave their (O, m, l) by row and head, and every row says where its own
   // part is
@@ -100,7 +100,7 @@ struct PagedAttnParams {
 };
 
 // Rows of one unit that the few-row kernel takes (16 per MMA row tile): at 30 rows it
-// takes 32 us for what takes the many-row kernel 36, with 64 rows (four row tiles) it
+// takes 29 us for what takes the many-row kernel 35, with 64 rows (four row tiles) it
 // was the slower one.
 constexpr int kPagedFewRows = 32;
 bool paged_few_rows(int G, int64_t max_new);
@@ -120,7 +120,8 @@ struct PagedManyParams {
 inline int paged_btok(int G) { return 128 / G; }
 constexpr int kPagedManyRows = 256;     // partial rows of a slot
 constexpr int kPagedManyTile = 128;     // slots of a tile
-// A unit's begin and end in the line, in tiles (8 prompts: 1 84 us, 3 81, 5 85).
+// A unit's begin and end in the line, in tiles (8 prompts, with 1 / 3 / 5: 84 / 81 / 85
+// us).
 constexpr int kPagedManyHead = 3;
 cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl);
 cudaError_t configure_paged_many();

@@ -26,11 +26,11 @@
 // memory: 0 * NaN would reach O.  Every wait is bounded.
 //
 // Measured with the merge, in a graph: 64 sequences of 1 - 8191 slots, 12 heads on 2
-// kv heads of 128, 48 us (5.3 TB/s of 6.8 that a copy reaches); 16 of 32768 slots, 32
-// heads on 2, 88 us (6.1 TB/s); 32 of 4096 with 4 - 5 tokens each (30 rows) 32 us: there
-// the two row tiles' mma.sync and shared memory take 3200 clocks for two tiles that
-// arrive in 2300; 8 of 1024 10.3 us, all latency.  On the many-row kernel these
-// take 70, 102, 36 and 17 us.
+// kv heads of 128, 46 us (5.5 TB/s of 6.8 that a copy reaches); 16 of 32768 slots, 32
+// heads on 2, 87 us (6.2 TB/s); 32 of 4096 with 4 - 5 tokens each (30 rows) 29 us, 22 of
+// them streaming at 5.1 TB/s; 8 of 1024 8.6 us, all latency: 1.3 us until the CTA knows
+// its range, 1.6 until its first tile is there, 1.5 for it, then the merge.  On the
+// many-row kernel these take 70, 102, 36 and 17 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -43,7 +43,8 @@ namespace {
 constexpr int kTile = 64;            // slots of a tile
 constexpr int kConsumers = 128, kThreads = 160;
 // What a unit's beginning and end (q, the pieces' ends) count for in the line, in
-// tiles; they lie before its first tile.  (30 rows a unit: 0 32.8 us, 1 32.1, 2 32.7.)
+// tiles; they lie before its first tile.  (30 rows a unit, with 0 / 1 / 2: 32.8 / 32.1 /
+// 32.7 us.)
 constexpr int kHead = 1;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     mine += seq_weight(p, s);
     bad |= s.bad;
     if (b < 128) first_seqs[b] = s;
-    if (p.by_unit && s.n == 0 && blockIdx.x == 0)
+    if (p.upb && s.n == 0 && blockIdx.x == 0)
       for (int g = 0; g < p.Hkv; ++g) p.cut[g * p.B + b].c0 = -1;
   }
   if (bad && blockIdx.x == 0) set_error(p.err, kDevPage);
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int cta = blockIdx.x;
   const int64_t t0 = cta < nc ? range_of(T, cta, nc) : T, t1 = cta < nc ? range_of(T, cta + 1, nc) : T;
   if (t0 >= t1) {   // (uniform over the CTA)
-    if (tid == 0 && !p.by_unit) p.cut[cta].c0 = -1;
+    if (tid == 0 && !p.upb) p.cut[cta].c0 = -1;
     return;
   }
   const int g0 = small_div(t0, T1);
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int c1 = whole ? cta : cta_of(T, ue - 1, nc);
         const PagedPiece now = {whole ? -1 : cta, s.n * p.G, c1, s.r0, g};
         if (!whole) cut = now;
-        if (p.by_unit && lane == 0) p.cut[g * p.B + b] = now;
+        if (p.upb && lane == 0) p.cut[g * p.B + b] = now;
         if (p.row_info)
           for (int t = lane; t < s.n; t += 32)
             p.row_info[(int64_t)(s.r0 + t) * p.Hkv + g] =
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++b;
       ++seg;
     }
-    if (lane == 0 && !p.by_unit) {
+    if (lane == 0 && !p.upb) {
       if (!ok) cut.c0 = -1;
       p.cut[cta] = cut;
     }
@@ -576,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // timing): eight where few rows have many pieces (one long sequence alone is cut
 // into 150), one where many rows have a few.  Bound by latency: the pieces' places,
 // then the pieces, a round trip each.  The attention with one / two / eight warps a
-// row: 96 rows of 16 pieces 14.2 / 10.7 / 10.3 us, 768 rows 48.9 / 48.3 / 49.7, 32000
-// rows of two (39 MB) 80 / 90 / 127.
+// row (a row's entry searched for in each): 96 rows of 16 pieces 14.2 / 10.7 / 10.3 us,
+// 768 rows 48.9 / 48.3 / 49.7, 32000 rows of two (39 MB) 80 / 90 / 127.
 template <int D, int kWPR, bool kByUnit>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedMergeParams q) {
   // a row's lanes: half a warp where rows are many (two rows' pieces in flight per warp)
@@ -592,8 +593,9 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   // With a prefix the blocks share all rows and heads.  Else they share the rows of the
   // cut units: where there is an entry for every unit, blockIdx.x is one and the blocks
   // of a column share its rows; else they share the rows of the CTAs' entries together
-  // (an entry a column left most blocks without work there: 512 tokens 28.4 -> 30.7 us;
-  // finding a row's entry took 64 decoding sequences from 45.9 to 47.5).
+  // (a CTA's entry a column left most blocks without work: 512 tokens 28.4 -> 30.7 us;
+  // finding a row's entry took 64 decoding sequences from 45.9 to 47.5, 512 tokens from
+  // 27.0 to 27.8).
   PagedPiece u = {};
   int64_t items, b0 = blockIdx.x, nb = gridDim.x;
   if constexpr (kByUnit) {
@@ -825,12 +827,12 @@ cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStrea
   // still have to come and go.
   const PagedAttnParams& a = p.a;
   const bool few = a.slot_rows <= kPagedFewRows;
-  const int64_t entries = a.by_unit ? (int64_t)a.B * a.Hkv : a.nc, all = (int64_t)a.N * a.Hq;
+  const int64_t entries = a.upb ? (int64_t)a.B * a.Hkv * a.upb : a.nc, all = (int64_t)a.N * a.Hq;
   const int64_t rows = few ? a.max_new * a.G : a.slot_rows;          // of a unit
   const int64_t cut = p.prefix || entries * rows > all ? all : entries * rows;
   const int wpr = cut > 16 * num_sms ? 1 : cut > 4 * num_sms ? 2 : 8;
   const int64_t per = wpr == 1 ? 16 : 8 / wpr;
-  if (a.by_unit) {
+  if (a.upb) {
     cfg.gridDim = dim3((unsigned)entries, (unsigned)((rows + per - 1) / per));
   } else {
     const int64_t want = (cut + per - 1) / per, fit = (int64_t)num_sms * 8;
@@ -844,7 +846,7 @@ cudaError_t launch_paged_merge(const PagedMergeParams& p, int num_sms, cudaStrea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const int d = a.D == 128, v = wpr == 1 ? 0 : wpr == 2 ? 1 : 2;
-  if (a.by_unit) {
+  if (a.upb) {
     void (*const k[2][3])(PagedMergeParams) = {
         {paged_merge_kernel<64, 1, true>, paged_merge_kernel<64, 2, true>,
          paged_merge_kernel<64, 8, true>},

@@ -24,8 +24,8 @@
 // is NaN).  Every wait is bounded.
 //
 // Measured with the merge, in a graph, 12 heads on 2 kv heads of 128: 8 prompts of 700 -
-// 2000 tokens 80 us (645 TFLOP/s; the kernel alone 686), 512 tokens behind 3584 slots
-// 28 us.  A tile takes ~3400 clocks of 2048 for its 32 MMAs: S = Q K^T reads 128 bytes
+// 2000 tokens 80 us (648 TFLOP/s; the kernel alone 690), 512 tokens behind 3584 slots
+// 27 us.  A tile takes ~3400 clocks of 2048 for its 32 MMAs: S = Q K^T reads 128 bytes
 // of shared memory per clock, all there is, while the next tiles' 64 KB arrive.  A
 // unit's begin and end take some 3000 clocks, a launch 6 us before its first tile is
 // there.
@@ -266,6 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       n += (s.n + utok - 1) / utok;
       bad |= s.bad;
       if (few_seqs) seqs[b] = s;
+      if (p.upb && cta == 0)           // entries of units that are not there
+        for (int u = (s.n + utok - 1) / utok; u < p.upb; ++u)
+          for (int g = 0; g < p.Hkv; ++g) p.cut[(g * p.B + b) * p.upb + u].c0 = -1;
     }
     if (bad && cta == 0) set_error(p.err, kDevPage);
     int64_t at = block_excl(n, wsum, R64);
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t t0 = cta < nc ? range_of(T, cta, nc) : T;
   const int64_t t1 = cta < nc ? range_of(T, cta + 1, nc) : T;
   if (t0 >= t1) {
-    if (threadIdx.x == 0 && !kPrefix) p.cut[cta].c0 = -1;
+    if (threadIdx.x == 0 && !kPrefix && !p.upb) p.cut[cta].c0 = -1;
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -553,8 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int it = 0, seg = 0, item = 0;     // tiles, pieces, ring items so far
     int qn0 = 0, qn1 = 0;              // q loads of block 0, 1
     bool ok = true;
-    PagedPiece cut;
-    cut.c0 = -1;
+    if (!kPrefix && !p.upb && lane == 0) p.cut[cta].c0 = -1;   // until a unit is cut here
     auto wait_s = [&](int j) {         // both S of tile j are done (j < 0: nothing to wait for)
       if (j >= 0 &&
           (!mbar_wait_near(&s_full[j % kS], (uint32_t)(j / kS) & 1u, p.err) ||
@@ -618,13 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.row_info[(int64_t)(u.r0 + t) * p.Hkv + g] = make_int4(-2, 0, 0, 0);
         } else {
           const int c1 = whole ? cta : cta_of(T, ue - 1, nc);
-          if (!whole) {
-            cut.c0 = cta;
-            cut.c1 = c1;
-            cut.rows = u.ntok * p.G;
-            cut.r0 = u.r0;
-            cut.g = g;
-          }
+          const PagedPiece now = {whole ? -1 : cta, u.ntok * p.G, c1, u.r0, g};
+          if (lane == 0 && (p.upb || !whole))
+            p.cut[p.upb ? (g * p.B + b) * p.upb + ui - 1 : cta] = now;
           if (p.row_info)
             for (int t = lane; t < u.ntok; t += 32)
               p.row_info[(int64_t)(u.r0 + t) * p.Hkv + g] =
@@ -689,14 +687,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++item;
       }
       ++seg;
-    }
-    if (!kPrefix && lane == 0) {
-      volatile PagedPiece& c = p.cut[cta];
-      c.c1 = cut.c1;
-      c.rows = cut.rows;
-      c.r0 = cut.r0;
-      c.g = cut.g;
-      c.c0 = ok ? cut.c0 : -1;
     }
     if (ok) wait_s((item - R + 1) >> 1);
     if (ok) {

@@ -31,8 +31,8 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
 // every later one with rows, and what it would have taken moves nobody's pages.
 // Pages of a row are formed from the lengths and the free list, never read back
 // from the table entries that this launch writes.  Bound by latency: 64 decoding
-// sequences are one CTA and three round trips to L2, 3.5 us in a graph (with a scan
-// each and the lengths read in turn 3.9); 200 prompts with 100,000 slots 4.7.
+// sequences are one CTA and three round trips to L2, 3.1 - 3.5 us in a graph (with a
+// scan each and the lengths read in turn 3.9); 200 prompts with 100,000 slots 4.6.
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanParams p) {
   extern __shared__ int sm[];
   int* rs = sm;                  // [B + 1] first row, at most N
