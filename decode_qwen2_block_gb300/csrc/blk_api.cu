@@ -1502,8 +1502,9 @@ int run_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b,
     BLK_LAUNCH(tm, kKRmsNorm,
                launch_rmsnorm_rows(x, false, static_cast<const __half*>(w->ln1_g), M, H,
                                    c.rms_eps, xn16, s, first_pdl));
-  // QKV + bias + RoPE; the new K/V go to a buffer [Hkv][M][D] (a cache of M
-  // slots as the projection's epilogue sees it) and from there to their pages
+  // QKV + bias + RoPE.  Of few rows the projection's finisher puts K/V into their pages;
+  // of more they go to a buffer [Hkv][M][D] (a cache of M slots as the projection's
+  // epilogue sees it) and from there to their pages.
   TcGemmParams g = {};
   if (make_tmap_2d(&g.tmA, xn16, M, H, tc_a_box_rows(M)) ||
       make_tmap_2d(&g.tmB[0], w->wq, (int64_t)Hq * D, H, 64) ||
@@ -1523,6 +1524,8 @@ int run_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b,
   g.kc = reinterpret_cast<__half*>(base + lay.k16);
   g.vc = reinterpret_cast<__half*>(base + lay.v16);
   g.max_ctx = M; g.cache_len = 0;
+  g.n_slots = b->n_pages * b->page_size;
+  g.page_lg = page_log2(b->page_size);
   g.err = h->status;
   float* part = reinterpret_cast<float*>(base + lay.part32);
   if (M <= kFrMaxRows) {
@@ -1535,19 +1538,22 @@ int run_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b,
     BLK_LAUNCH(tm, kKGemmQKV, launch_fr_gemm(fq, kFrPart, h->num_sms, s, true));
     g.part = part;
     g.splits = fq.splits;
+    g.slot_map = slot_map;
+    g.kc = static_cast<__half*>(k_pages);
+    g.vc = static_cast<__half*>(v_pages);
     BLK_LAUNCH(tm, kKQkvFinish, launch_qkv_finish(g, s));
   } else {
     BLK_LAUNCH(tm, kKGemmQKV, launch_tc_gemm(g, kTcQKV, h->num_sms, s, true));
+    PageAppendParams pa = {};
+    pa.k = g.kc; pa.v = g.vc;
+    pa.row_stride = D; pa.head_stride = (int64_t)M * D;
+    pa.slot_map = slot_map;
+    pa.k_pages = static_cast<__half*>(k_pages); pa.v_pages = static_cast<__half*>(v_pages);
+    pa.n_slots = g.n_slots;
+    pa.N = M; pa.Hkv = Hkv; pa.D = D; pa.page_lg = g.page_lg;
+    pa.err = h->status;
+    BLK_LAUNCH(tm, kKPageAppend, launch_page_append(pa, h->num_sms, s, true));
   }
-  PageAppendParams pa = {};
-  pa.k = g.kc; pa.v = g.vc;
-  pa.row_stride = D; pa.head_stride = (int64_t)M * D;
-  pa.slot_map = slot_map;
-  pa.k_pages = static_cast<__half*>(k_pages); pa.v_pages = static_cast<__half*>(v_pages);
-  pa.n_slots = b->n_pages * b->page_size;
-  pa.N = M; pa.Hkv = Hkv; pa.D = D; pa.page_lg = page_log2(b->page_size);
-  pa.err = h->status;
-  BLK_LAUNCH(tm, kKPageAppend, launch_page_append(pa, h->num_sms, s, true));
   const int rc = run_attn_paged(h, b, q16, (int64_t)Hq * D, k_pages, v_pages, attn16,
                                 (int64_t)Hq * D, base + lay.attn, s, tm);
   if (rc) return rc;

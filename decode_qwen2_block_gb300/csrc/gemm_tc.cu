@@ -732,7 +732,8 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* __restr
 // Finishes a K-split QKV projection: element (row m, head hd, pair i) of the
 // fused q | k | v output is the sum of the split partials (split order) plus
 // the bias, rotated by RoPE for q and k heads, then stored exactly as the
-// GEMM's own QKV epilogue does (q16; K/V into the cache slot and k_new/v_new).
+// GEMM's own QKV epilogue does (q16; K/V into the cache slot and k_new/v_new), or
+// in a paged step K/V into their pages.
 template <int MAXS>
 __global__ void __launch_bounds__(64) qkv_finish_kernel(const __grid_constant__ TcGemmParams p) {
   griddep_wait();
@@ -786,6 +787,18 @@ __global__ void __launch_bounds__(64) qkv_finish_kernel(const __grid_constant__ 
     const bool is_k = hd < p.Hq + p.Hkv;
     __half* cache = is_k ? p.kc : p.vc;
     __half* nw = is_k ? p.k_new : p.v_new;
+    if (p.slot_map) {
+      const int64_t slot = p.slot_map[m];
+      if (slot >= 0 && slot < p.n_slots) {
+        const int64_t page = slot >> p.page_lg, at = slot - (page << p.page_lg);
+        __half* dst = cache + (((page * p.Hkv + local) << p.page_lg) + at) * D;
+        dst[i] = ha;
+        dst[half + i] = hb;
+      } else if (slot != -1 && i == 0) {
+        set_error(p.err, kDevPage);
+      }
+      continue;
+    }
     int64_t slot = p.cache_len + m;
     if (p.cache_lens) {
       slot = p.cache_lens[m];

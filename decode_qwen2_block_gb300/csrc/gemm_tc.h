@@ -39,6 +39,11 @@ struct TcGemmParams {
   // slot cache_lens[m] of the caches at kc/vc + m * seq_stride
   const int64_t* cache_lens;
   int64_t seq_stride;
+  // paged step (qkv_finish with slot_map != null): kc and vc are pools of n_slots slots
+  // in pages of 2^page_lg, row m's K/V go to slot slot_map[m] (-1: left out)
+  const int64_t* slot_map;
+  int64_t n_slots;
+  int page_lg;
   // other epilogues
   const __half* res16;
   const float* res32;

@@ -157,6 +157,33 @@ def test_step_argument_errors_enqueue_nothing():
     assert all((p == MARK).all() for p in pools)
 
 
+@pytest.mark.parametrize("rows", [4, 150])
+def test_step_reports_a_slot_outside_the_pool_and_writes_nothing_there(rows):
+    """Rows whose K/V go to their pages from the projection (few) and by the append."""
+    s = synth.TINY
+    block = blk.Block(s, 256)
+    wt = blk.Block.weights(wd := {k: to_dev(v) for k, v in synth.block_weights(s, seed=4).items()})
+    whole = [torch.full((13, 2, 16, 64), MARK, dtype=torch.float16, device="cuda") for _ in range(2)]
+    pools = [p[1:12] for p in whole]
+    table = torch.arange(11, dtype=torch.int32, device="cuda")[None]
+    batch = block.paged_batch(_i64([0, rows]), _i64([0]), table, rows, 16, 11, rows, 176)
+    x = to_dev(synth.hidden_input(s, rows, seed=4))
+    out = torch.empty_like(x)
+    ws = torch.empty(block.step_paged_workspace_bytes(rows, 1), dtype=torch.uint8, device="cuda")
+    pos = torch.arange(rows, device="cuda")
+    slots = pos.clone()
+    slots[1], slots[2], slots[3] = 11 * 16, -16, -1
+    block.step_paged(wt, batch, x, pos, slots, *pools, out, ws)
+    torch.cuda.synchronize()
+    with pytest.raises(blk.BlkError) as e:
+        block.check()
+    assert e.value.status == blk.BLK_ERR_PAGE
+    for p in whole:
+        at = (p != MARK).any(-1).any(1).flatten().nonzero().flatten().tolist()     # slots written
+        assert at == [16] + list(range(16 + 4, 16 + rows))
+    assert wd
+
+
 def _layers(s, n, seed):
     return [{k: to_dev(v) for k, v in synth.block_weights(s, layer=l, seed=seed).items()}
             for l in range(n)]
