@@ -1331,7 +1331,7 @@ bool share_prefix(const blk_config& c, const blk_paged_batch* b) {
 
 int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_t q_stride,
                    const void* k_pages, const void* v_pages, void* out, int64_t out_stride,
-                   unsigned char* base, cudaStream_t s, Timer& tm) {
+                   unsigned char* base, cudaStream_t s, Timer& tm, bool early) {
   const blk_config& c = h->cfg;
   const int D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads, G = Hq / Hkv;
   const bool prefix = b->prefix_len > 0 && share_prefix(c, b);
@@ -1408,6 +1408,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
     a.tm_v = few_v;
     paged_few_slots(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
     a.upb = units_each();
+    a.early = early && !prefix;
     BLK_LAUNCH(tm, kKPagedFew, launch_paged_few(a, s, true));
   } else {
     a.nc = h->num_sms;
@@ -1554,8 +1555,9 @@ int run_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b,
     pa.err = h->status;
     BLK_LAUNCH(tm, kKPageAppend, launch_page_append(pa, h->num_sms, s, true));
   }
+  // (two kernels or more lie between the caller's work and the attention: early)
   const int rc = run_attn_paged(h, b, q16, (int64_t)Hq * D, k_pages, v_pages, attn16,
-                                (int64_t)Hq * D, base + lay.attn, s, tm);
+                                (int64_t)Hq * D, base + lay.attn, s, tm, true);
   if (rc) return rc;
   return run_block_tail(h, w, x, attn16, reinterpret_cast<float*>(base + lay.h32),
                         reinterpret_cast<__half*>(base + lay.hn16),
@@ -1637,7 +1639,7 @@ int blk_attn_paged(blk_handle h, const blk_paged_batch* batch, const void* q, in
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Timer tm{h, s};
   return run_attn_paged(h, batch, q, q_stride, k_pages, v_pages, out, out_stride,
-                        static_cast<unsigned char*>(ws), s, tm);
+                        static_cast<unsigned char*>(ws), s, tm, false);
 }
 
 size_t blk_step_paged_workspace_bytes(blk_handle h, int64_t max_rows, int64_t max_seqs,

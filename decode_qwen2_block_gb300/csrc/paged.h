@@ -81,6 +81,9 @@ struct PagedAttnParams {
                                //   prefix_pages); the others belong to the prefix's own launch
   int own_lo;                  // the first slot of the own parts: prefix_len - pre_here
   int window;                  // of the handle; 0: all slots
+  int early;                   // few rows: lengths, tables and the slots of the history are
+                               //   older than the kernel before this one, which writes q
+                               //   and the new slots; nothing else of it is waited for
   int B, N, Hq, Hkv, D, G, page_lg, max_new;
   float scale_log2;
   int nc;                      // CTAs of the kernel

@@ -159,8 +159,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     start_cum = 0;
     abort_s = 0;
   }
-  griddep_wait();
-  griddep_launch();
+  // (early: the producer waits, before q and the new slots)
+  if (!p.early) {
+    griddep_wait();
+    griddep_launch();
+  }
   // tiles of all sequences (one kv head), and those before this thread's
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
@@ -198,6 +201,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int cta = blockIdx.x;
   const int64_t t0 = cta < nc ? range_of(T, cta, nc) : T, t1 = cta < nc ? range_of(T, cta + 1, nc) : T;
   if (t0 >= t1) {   // (uniform over the CTA)
+    if (p.early) {
+      griddep_wait();
+      griddep_launch();
+    }
     if (tid == 0 && !p.upb) p.cut[cta].c0 = -1;
     return;
   }
@@ -225,7 +232,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     int64_t cum = start_cum, lin = t0;
     int it = 0, seg = 0, base32 = -1;
     PagedSeq mys = {};
-    bool ok = true;
+    bool ok = true, waited = !p.early;
+    auto wait_before = [&] {           // for what the kernel before this one writes
+      if (!waited) {
+        griddep_wait();
+        griddep_launch();
+        waited = true;
+      }
+    };
     PagedPiece cut = {-1, 0, 0, 0, 0};
     while (lin < t1 && ok) {
       if (b >= p.B) {        // the next kv head begins again with the first sequence
@@ -302,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           f.dst = dst;
           mbar_arrive_expect_tx(&full[st], __popc(m) * box_bytes + qrows * D * 2);
         }
+        if (slot0 + kTile > s.L) wait_before();
         __syncwarp();
         if (take) {
           const uint32_t to = ring + st * 2 * Sm::kKV + (lane < 16 ? 0 : Sm::kKV) + i * box_bytes;
@@ -310,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           tma_page(to, lane < 16 ? &p.tm_k : &p.tm_v, first & ((1 << p.page_lg) - 1), z,
                    &full[st]);
         }
+        if (qrows > 0) wait_before();
         for (int r = lane; r < qrows; r += 32) {
           const int t = r / p.G, hh = r - t * p.G;
           bulk_g2s(smem + Sm::kQOff + r * Sm::kQStride,
@@ -320,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++b;
       ++seg;
     }
+    wait_before();                     // (a range of heads alone has no tile)
     if (lane == 0 && !p.upb) {
       if (!ok) cut.c0 = -1;
       p.cut[cta] = cut;

@@ -461,7 +461,9 @@ int blk_attn_paged(blk_handle h, const blk_paged_batch* batch, const void* q, in
  * the pages, o_proj, MLP.  x, out: device fp16 [n_rows, hidden] (out must not
  * alias x); pos, slot_map: device int64 [n_rows] as blk_page_plan writes them
  * (positions below the handle's max_ctx); k_pages, v_pages: the layer's pools
- * (host arrays of them for the stack).  Rows that belong to no sequence come out
+ * (host arrays of them for the stack).  The slots of a sequence's history,
+ * [0, cache_lens[b]), are there before the call: a slot that this step writes for
+ * another sequence is not among them.  Rows that belong to no sequence come out
  * undefined.  ws: blk_step_paged_workspace_bytes(h, max_rows, max_seqs,
  * with_prefix) bytes for either call.  Agrees with blk_prefill_kv and blk_decode
  * on each sequence within the tolerance. */

@@ -288,6 +288,33 @@ def test_paged_stack_steps_on_changing_streams():
     assert torch.equal(results[0].view(torch.int16), results[1].view(torch.int16))
 
 
+def test_steps_whose_kernels_overlap_equal_steps_whose_kernels_do_not():
+    """The attention begins under the kernel that writes q and the new slots: the
+    projection's finisher, or of more than 128 rows (every fifth step) the append.  With the
+    per-kernel timing on no two kernels overlap: the same bits."""
+    s, n, B = synth.TINY, 6, 60
+    wd = _layers(s, n, 38)
+    x = to_dev(synth.hidden_input(s, 1800, seed=38))
+    prompts = [(37 * b) % 61 + 1 for b in range(B)]
+    results = []
+    for timed in (False, True):
+        pg = PagedStack(s, wd, 256, 900, 16, B, 1800)
+        pg.block.timing(timed)
+        pg.step(x[:sum(prompts[:20])], prompts[:20])
+        pg.block.timing_collect()
+        pg.step(x[:sum(prompts[20:])], [0] * 20 + prompts[20:])
+        outs = []
+        for step in range(40):
+            new = [1 + (b + step) % 4 if step % 5 == 4 else 1 for b in range(B)]
+            outs.append(pg.step(x[step:step + sum(new)], new))
+            pg.block.timing_collect()
+        pg.block.timing(False)
+        torch.cuda.synchronize()
+        pg.block.check()
+        results.append(torch.cat(outs))
+    assert torch.equal(results[0].view(torch.int16), results[1].view(torch.int16))
+
+
 def test_paged_stack_refuses_what_does_not_fit():
     s = synth.TINY
     pg = PagedStack(s, _layers(s, 1, 34), 64, 5, 16, 2, 100)
