@@ -50,8 +50,8 @@ cudaError_t launch_page_append(const PageAppendParams& p, int num_sms, cudaStrea
 // (a group of rows of one sequence and one kv head) are numbered in one line
 // and CTA i takes tiles [i T / n, (i + 1) T / n).  A unit inside one CTA is
 // finished there; of a cut unit every CTA leaves a partial (its unnormalised
-// O, maximum m in log2 units and sum l, fp32) in one of its two slots: slot 1 of
-// the piece that begins the unit, slot 0 of those that go on.  In the line a unit
+// O and sum l, fp32, both of 2^(score - m) with the m that it took, in log2 units) in one
+// of its two slots: slot 1 of the piece that begins the unit, slot 0 of those that go on.  In the line a unit
 // also has a head before its first tile, for what its begin and end cost.
 struct alignas(8) PagedPiece { // what merging needs of one cut unit
   int c0;                      // first CTA that holds a piece of it (-1: no unit)

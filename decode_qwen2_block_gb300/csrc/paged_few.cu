@@ -16,9 +16,9 @@
 //              first tile as bulk copies into rows padded by 16 bytes.
 //   warps 0-3  16 slots each: S = Q K^T by mma.sync m16n8k16 (the rows are the M
 //              side: at most 32, a tcgen05 MMA's 128 rows would be padding),
-//              the row maxima meet in shared memory, P (fp16, in [0, 1]: the
-//              rounding is at most 2^-11 of a weight) goes there too, and each
-//              warp forms O for its quarter of the columns over all 64 slots.
+//              the row maxima meet in shared memory, P (fp16, see kWeightLog2)
+//              goes there too, and each warp forms O for its quarter of the columns
+//              over all 64 slots.
 //              So a unit's end needs no merge of O between warps, which with
 //              short sequences would cost more than their tiles.
 // Slots of a tile that no row of the unit sees (behind the last, before the
@@ -46,6 +46,12 @@ constexpr int kConsumers = 128, kThreads = 160;
 // tiles; they lie before its first tile.  (30 rows a unit, with 0 / 1 / 2: 32.8 / 32.1 /
 // 32.7 us.)
 constexpr int kHead = 1;
+// Weights are formed 2^14 times their size (O and l carry the factor, it cancels): fp16
+// then holds them to 2^-11 of themselves down to 2^-28 of the greatest and to half of
+// 2^-38 below.  Formed at their size those below 2^-14 would lose bits and those below
+// 2^-25 be lost: e^-15 of one slot's weight is off by 2.6 % in every one of 32,000
+// others.  The greatest, 2^14, leaves a factor 2 of room.
+constexpr float kWeightLog2 = 14.f;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -362,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int bs_lg = p.page_lg < 6 ? p.page_lg : 6;
   const int slab = warp * 16;
   const float sl2 = p.scale_log2;
+  // m_r: what exponents are taken against, the row's maximum (log2 units) less kWeightLog2
   float m_r[MT][2], l_r[MT][2], O[MT][kNT][4];
   int last[MT][2], low[MT][2];
   uint32_t qf[D / 16][MT][4];          // the unit's q: A fragments
@@ -483,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int row = mt * 16 + grp + 8 * h2;
         const float4 m4 = *reinterpret_cast<const float4*>(stat + row * 4);
         const float mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-        const float mn = fmaxf(m_r[mt][h2], mx * sl2);       // log2 units
+        const float mn = fmaxf(m_r[mt][h2], fmaf(mx, sl2, -kWeightLog2));
         corr[mt][h2] = mn == -INFINITY ? 1.f : ex2(m_r[mt][h2] - mn);
         moved |= mn != m_r[mt][h2];
         m_r[mt][h2] = mn;

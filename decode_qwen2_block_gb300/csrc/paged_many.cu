@@ -53,6 +53,10 @@ struct Regs {
 constexpr int kTile = kPagedManyTile;
 constexpr int kInfos = 8;
 constexpr float kRescaleLog2 = 8.f;   // see the softmax
+// Weights are formed 2^7 times their size (O and l carry the factor, it cancels), so that
+// fp16 holds them to 2^-11 of themselves down to 2^-21 of the greatest and to half of
+// 2^-31 below; with kRescaleLog2 they reach 2^15, half of what fp16 holds.
+constexpr float kWeightLog2 = 7.f;
 constexpr int kMinTiles = 2;          // of a CTA: a piece of less is all begin and end
 constexpr int kHead = kPagedManyHead;
 
@@ -428,9 +432,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         a2 = max3(a2, sv[c + 4], sv[c + 5]);
         a3 = max3(a3, sv[c + 6], sv[c + 7]);
       }
-      const float mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sl2;   // log2 units
+      // (log2 units, less kWeightLog2; so is m)
+      const float mx = fmaf(fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)), sl2, -kWeightLog2);
       // A row's reference maximum moves (and O, l are rescaled) only when the
-      // maximum grew by more than 2^8 since: P <= 256 fits fp16, and 1 / l at the
+      // maximum grew by more than 2^8 since: P <= 2^15 fits fp16, and 1 / l at the
       // end makes the choice exact.
       // (Rows of no token hold whatever lay there: they take no part, or the moment
       // of a move, and with it the rounding of P, would differ from call to call.)
