@@ -99,8 +99,18 @@ struct PagedAttnParams {
   float* own;                  // [N][Hq][D]
   float2* own_ml;              // [N][Hq]
   int4* row_info;              // [N][Hkv]: c0 (-1 whole, -2 no part), c1, 0, partial row of head 0
+                               //   (an attention that timed out leaves entries unwritten: the
+                               //   merge takes those that paged_row_part accepts)
   int* err;
 };
+
+// Whether a row_info entry names a row's own part: a whole one, or pieces in the slots of
+// CTAs c0 .. c1 whose G rows lie in a slot.  Anything else (no part, or what lay in the
+// workspace where an attention that timed out wrote no entry) is no part: an address is
+// formed from accepted entries only.
+__host__ __device__ inline bool paged_row_part(int c0, int c1, int row, int nc, int slot_rows, int G) {
+  return c0 == -1 || (c0 >= 0 && c0 <= c1 && c1 < nc && row >= 0 && row <= slot_rows - G);
+}
 
 // Rows of one unit that the few-row kernel takes (16 per MMA row tile): at 30 rows it
 // takes 29 us for what takes the many-row kernel 35, with 64 rows (four row tiles) it

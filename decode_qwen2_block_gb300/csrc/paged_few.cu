@@ -693,7 +693,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
       hq = (int)(item - (int64_t)r * p.Hq);
       const int g = hq / p.G, hh = hq - g * p.G;
       const int4 f = here ? p.row_info[(int64_t)r * p.Hkv + g] : make_int4(-2, 0, 0, 0);
-      here = f.x != -2;                      // else a row behind the batch, or refused
+      // (else a row behind the batch, or refused)
+      here = paged_row_part(f.x, f.y, f.w, p.nc, p.slot_rows, p.G);
       if (kWPR == 1 && !here) continue;
       own_whole = f.x == -1;
       c0 = f.x;
