@@ -208,6 +208,15 @@ class PagedStack:
     def _ints(self, values, dtype):
         return torch.tensor(values, dtype=dtype).to(self.device, non_blocking=True)
 
+    def _follow(self, stream):
+        """The step's stream, behind the last step's.  All that a step makes or writes of the
+        runner's own is on it: the current stream may be another one that nothing orders."""
+        s = torch.cuda.current_stream() if stream is None else stream
+        if s != self._last:
+            s.wait_stream(self._last)
+            self._last = s
+        return s
+
     def _run(self, table, lens, news, x, out, prefix, stream):
         """Plans and runs one step of the sequences of `table`; returns (out, how many of
         free_ids it took)."""
@@ -220,10 +229,7 @@ class PagedStack:
             raise BlkError(BLK_ERR_PAGE, "PagedStack.step: no pages left")
         if n != sum(news) or n > self.max_rows or min(news) < 0:
             raise BlkError(BLK_ERR_SHAPE, "PagedStack.step: rows")
-        s = torch.cuda.current_stream() if stream is None else stream
-        if s != self._last:
-            s.wait_stream(self._last)
-            self._last = s
+        s = self._follow(stream)
         with torch.cuda.stream(s):
             i64 = torch.int64
             lens_d, news_d = self._ints(lens, i64), self._ints(news, i64)
@@ -250,14 +256,14 @@ class PagedStack:
         the page size) before any sequence has tokens; returns the last layer's rows."""
         if any(self.lens) or self.prefix is not None or x.shape[0] % self.page:
             raise BlkError(BLK_ERR_SHAPE, "PagedStack.prefill_prefix")
-        table = torch.full((1, self.max_blocks), -1, dtype=torch.int32, device=self.device)
-        out, need = self._run(table, [0], [x.shape[0]], x, None, None, stream)
+        s = self._follow(stream)
+        with torch.cuda.stream(s):
+            table = torch.full((1, self.max_blocks), -1, dtype=torch.int32, device=self.device)
+            out, need = self._run(table, [0], [x.shape[0]], x, None, None, s)
+            self.prefix = table[0, :need[0]].clone()
+            self.table[:, :need[0]] = self.prefix
         self.prefix_ids = self.free_ids[:need[0]]
         del self.free_ids[:need[0]]
-        s = torch.cuda.current_stream() if stream is None else stream
-        with torch.cuda.stream(s):
-            self.prefix = table[0, :need[0]].contiguous()
-            self.table[:, :need[0]] = self.prefix
         self.lens = [x.shape[0]] * self.max_seqs
         return out
 
