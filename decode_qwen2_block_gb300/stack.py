@@ -200,6 +200,8 @@ class PagedStack:
         if nbytes == 0:
             raise BlkError(BLK_ERR_SHAPE, "PagedStack: max_rows or max_seqs")
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        # with the streams that each is made on or recorded for
+        self._held = [(t, [self._last]) for t in (*sum(self.pools, ()), self.table, self.ws)]
         n = self.n_layers
         self._w_arr = (BlkWeights * n)(*[Block.weights(w) for w in layer_weights])
         self._k_arr = (ctypes.c_void_p * n)(*[k.data_ptr() for k, _ in self.pools])
@@ -217,6 +219,14 @@ class PagedStack:
             self._last = s
         return s
 
+    def _hold(self, s):
+        """The runner's buffers, on a stream other than the one each was made on: their
+        memory is not given away under a step that still runs there."""
+        for t, streams in self._held:
+            if s not in streams:
+                t.record_stream(s)
+                streams.append(s)
+
     def _run(self, table, lens, news, x, out, prefix, stream):
         """Plans and runs one step of the sequences of `table`; returns (out, how many of
         free_ids it took)."""
@@ -230,6 +240,7 @@ class PagedStack:
         if n != sum(news) or n > self.max_rows or min(news) < 0:
             raise BlkError(BLK_ERR_SHAPE, "PagedStack.step: rows")
         s = self._follow(stream)
+        self._hold(s)
         with torch.cuda.stream(s):
             i64 = torch.int64
             lens_d, news_d = self._ints(lens, i64), self._ints(news, i64)
@@ -261,6 +272,7 @@ class PagedStack:
             table = torch.full((1, self.max_blocks), -1, dtype=torch.int32, device=self.device)
             out, need = self._run(table, [0], [x.shape[0]], x, None, None, s)
             self.prefix = table[0, :need[0]].clone()
+            self._held.append((self.prefix, [s]))
             self.table[:, :need[0]] = self.prefix
         self.prefix_ids = self.free_ids[:need[0]]
         del self.free_ids[:need[0]]

@@ -48,6 +48,7 @@ def runner(monkeypatch):
     log = []
     fake = Torch(log)
     monkeypatch.setattr(stack_mod, "torch", fake)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)   # (CUDA tensors' own)
     monkeypatch.setattr(stack_mod, "blk_step_paged_stack",
                         lambda *a: log.append(("layers", fake.now[-1].name)) or blk.BLK_OK)
 
@@ -111,3 +112,27 @@ def test_steps_wait_for_the_step_before_on_another_stream(runner):
         pg.step(torch.zeros(2, 8), [2], stream=s)
     assert [e for e in log if e[0] == "wait"] == [("wait", "a", "current"), ("wait", "b", "a"),
                                                  ("wait", "current", "b")]
+
+
+def test_the_runners_buffers_are_held_for_every_stream_that_steps_use(runner, monkeypatch):
+    """A buffer whose memory the allocator gives to another tensor once the runner is gone,
+    while a step on a stream not its own still runs, is recorded for that stream; each once."""
+    pg, fake, log = runner
+    held = []
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: held.append((t.data_ptr(), s.name)))
+    own = [t.data_ptr() for pair in pg.pools for t in pair] + [pg.table.data_ptr(), pg.ws.data_ptr()]
+    a, b = Stream("a", log), Stream("b", log)
+    pg.step(torch.zeros(2, 8), [2])
+    assert held == []
+    pg.step(torch.zeros(2, 8), [2], stream=a)
+    assert sorted(held) == sorted((p, "a") for p in own)
+    pg.step(torch.zeros(2, 8), [2], stream=a)
+    pg.step(torch.zeros(2, 8), [2])
+    assert len(held) == len(own)
+    pg.free(0)
+    pg.prefill_prefix(torch.zeros(32, 8), stream=b)
+    del held[:]
+    pg.step(torch.zeros(2, 8), [2], stream=a)     # (the prefix is newer than a's first step)
+    pg.step(torch.zeros(2, 8), [2], stream=b)
+    assert held == [(pg.prefix.data_ptr(), "a")]
