@@ -455,6 +455,18 @@ def _current_stream() -> int:
     return _raw_stream()
 
 
+_calls = None
+
+
+def _paged_calls():
+    """The compiled module of the paged calls, loaded with the first of them: a program that
+    makes none needs neither it nor what it was built against."""
+    global _calls
+    import importlib
+    _calls = importlib.import_module(__name__ + "._native")
+    return _calls
+
+
 class Block:
     """One block shape on the current CUDA device.
 
@@ -462,7 +474,7 @@ class Block:
     intermediate, has_qkv_bias, rms_eps, rope_theta."""
 
     def __init__(self, shape, max_ctx: int, chain: bool = False):
-        global torch, _native   # for the methods: this module itself loads without them
+        global torch            # for the methods: this module itself loads without it
         import torch
         self.shape = shape
         self.max_ctx = int(max_ctx)
@@ -470,7 +482,6 @@ class Block:
                              shape.intermediate, shape.rms_eps, shape.rope_theta, self.max_ctx,
                              1 if shape.has_qkv_bias else 0)
         self.handle = blk_create(self.cfg)
-        from . import _native   # (calls the library that blk_create has loaded)
         self._device = torch.cuda.current_device()
         self._args = (self.handle, self._device, shape.n_heads, shape.n_kv_heads, shape.head_dim)
         if chain:
@@ -610,16 +621,17 @@ class Block:
         int32, taken from the front (used[0] of them); block_table: int32 [B,
         max_blocks], the new pages' entries written; row_start int64 [B + 1],
         slot_map and pos int64 [n_rows], used int64 [1]: written."""
-        _native.page_plan(self._args, page_size, cache_lens, new_lens, free_pages, block_table,
-                          row_start, slot_map, pos, used,
-                          None if stream is None else stream.cuda_stream)
+        (_calls or _paged_calls()).page_plan(
+            self._args, page_size, cache_lens, new_lens, free_pages, block_table, row_start,
+            slot_map, pos, used, None if stream is None else stream.cuda_stream)
 
     def page_append(self, k, v, slot_map, k_pages, v_pages, stream=None):
         """Rows of k and v (fp16 [n, n_kv_heads, head_dim], the last dimension
         contiguous, both with the same strides) into the slots of slot_map (int64
         [n]; -1 leaves a row out)."""
-        _native.page_append(self._args, k, v, slot_map, k_pages, v_pages,
-                            None if stream is None else stream.cuda_stream)
+        (_calls or _paged_calls()).page_append(
+            self._args, k, v, slot_map, k_pages, v_pages,
+            None if stream is None else stream.cuda_stream)
 
     def paged_batch(self, row_start, cache_lens, block_table, n_rows: int, page_size: int,
                     n_pages: int, max_new: int, max_len: int, prefix_pages=None) -> BlkPagedBatch:
@@ -649,8 +661,9 @@ class Block:
     def attn_paged(self, batch: BlkPagedBatch, q, k_pages, v_pages, out, ws, stream=None):
         """Attention of the batch's rows: q, out fp16 [n_rows, n_heads, head_dim], heads
         contiguous, rows at any stride."""
-        _native.attn_paged(self._args, batch, q, k_pages, v_pages, out, ws,
-                           None if stream is None else stream.cuda_stream)
+        (_calls or _paged_calls()).attn_paged(
+            self._args, batch, q, k_pages, v_pages, out, ws,
+            None if stream is None else stream.cuda_stream)
 
     def step_paged_workspace_bytes(self, max_rows: int, max_seqs: int, prefix: bool = True) -> int:
         return blk_step_paged_workspace_bytes(self.handle, max_rows, max_seqs, prefix)
