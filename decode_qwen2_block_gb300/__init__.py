@@ -460,11 +460,15 @@ _calls = None
 
 def _paged_calls():
     """The compiled module of the paged calls, loaded with the first of them: a program that
-    makes none needs neither it nor what it was built against."""
+    makes none needs neither it nor what it was built against.  It calls the library that is
+    loaded, whichever that is."""
     global _calls
     import importlib
-    _calls = importlib.import_module(__name__ + "._native")
-    return _calls
+    lib, calls = load(), importlib.import_module(__name__ + "._native")
+    calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (lib.blk_page_plan, lib.blk_page_append, lib.blk_attn_paged)))
+    _calls = calls
+    return calls
 
 
 class Block:

@@ -2,7 +2,7 @@
 
 Each .cu file compiles to an object in parallel, then one shared library is
 linked; beside it the Python module of csrc/binding.cpp, against torch's headers,
-which calls that library.  No CMake, no torch extension machinery.
+which calls the library that the package has loaded.  No CMake, no torch extension machinery.
 """
 from __future__ import annotations
 
@@ -79,9 +79,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     _run([NVCC, *ARCH, "-shared", "-o", tmp, *objs], "link of libblk.so failed")
     os.replace(tmp, LIB)
     tmp = NATIVE + f".tmp{os.getpid()}"
-    _run(["g++", "-shared", "-o", tmp, binding, "-L", HERE, "-l:libblk.so", "-Wl,-rpath,$ORIGIN",
-          "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
-          "-lc10_cuda"], "link of _native.so failed")
+    _run(["g++", "-shared", "-o", tmp, binding, "-L", os.path.join(torch_dir, "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "link of _native.so failed")
     os.replace(tmp, NATIVE)
     return LIB
 

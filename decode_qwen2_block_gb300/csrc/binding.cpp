@@ -3,6 +3,9 @@
 // calls on a few rows; checked in Python, array by array, and passed through
 // ctypes, plan and append took 7.4 us each for kernels of 4 and 2.
 //
+// The library is the one that the package has loaded: bind() takes its functions'
+// addresses, nothing here links to a library of its own.
+//
 // Every function returns None or raises BlkError.  `stream` is None (the current
 // stream of the block's device) or a stream's handle.
 #define PY_SSIZE_T_CLEAN
@@ -16,6 +19,12 @@
 namespace {
 
 struct Refused {};   // a Python exception is set
+
+struct {             // the loaded library's functions
+  decltype(&blk_page_plan) page_plan;
+  decltype(&blk_page_append) page_append;
+  decltype(&blk_attn_paged) attn_paged;
+} lib = {};
 
 [[noreturn]] void refuse(int status, const std::string& what) {
   PyObject* mod = PyImport_ImportModule("decode_qwen2_block_gb300");
@@ -139,6 +148,12 @@ PyObject* call(Py_ssize_t given, Py_ssize_t wanted, const char* what, F f) {
   Py_RETURN_NONE;
 }
 
+void need_library() {
+  if (lib.page_plan) return;
+  PyErr_SetString(PyExc_RuntimeError, "_native: no library is bound");
+  throw Refused();
+}
+
 struct NoGil {       // the library's call may wait for room in the stream's queue
   PyThreadState* s = PyEval_SaveThread();
   ~NoGil() { PyEval_RestoreThread(s); }
@@ -167,8 +182,9 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* tab = table.data_ptr<int32_t>();
     void* s = stream_of(a[10], b.device);
     if (page != (int32_t)page) return (int)BLK_ERR_SHAPE;
+    need_library();
     NoGil g;
-    return blk_page_plan(b.h, (int32_t)page, B, lens, news, free_pages, n_free, tab, blocks, rows,
+    return lib.page_plan(b.h, (int32_t)page, B, lens, news, free_pages, n_free, tab, blocks, rows,
                          start, slots, pos, used, s);
   });
 }
@@ -186,8 +202,9 @@ PyObject* page_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t rs = k.stride(0), hs = k.stride(1);
     const void *kp = k.data_ptr(), *vp = v.data_ptr();
     void *kt = p.k.data_ptr(), *vt = p.v.data_ptr(), *s = stream_of(a[6], b.device);
+    need_library();
     NoGil g;
-    return blk_page_append(b.h, kp, vp, rs, hs, slots, rows, (int32_t)p.page(), p.n_pages(), kt, vt,
+    return lib.page_append(b.h, kp, vp, rs, hs, slots, rows, (int32_t)p.page(), p.n_pages(), kt, vt,
                            s);
   });
 }
@@ -210,13 +227,32 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void *qp = q.data_ptr(), *kp = p.k.data_ptr(), *vp = p.v.data_ptr();
     void *op = o.data_ptr(), *wp = ws.data_ptr(), *s = stream_of(a[7], b.device);
     const size_t bytes = ws.nbytes();
+    need_library();
     NoGil g;
-    return blk_attn_paged(b.h, &d, qp, qs, kp, vp, op, os, wp, bytes, s);
+    return lib.attn_paged(b.h, &d, qp, qs, kp, vp, op, os, wp, bytes, s);
   });
+}
+
+// bind(page_plan, page_append, attn_paged): the functions' addresses.
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* f[3];
+  if (n != 3) return PyErr_Format(PyExc_TypeError, "bind: 3 arguments");
+  for (int i = 0; i < 3; ++i) {
+    f[i] = PyLong_AsVoidPtr(a[i]);
+    if (!f[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null address");
+      return nullptr;
+    }
+  }
+  lib.page_plan = reinterpret_cast<decltype(lib.page_plan)>(f[0]);
+  lib.page_append = reinterpret_cast<decltype(lib.page_append)>(f[1]);
+  lib.attn_paged = reinterpret_cast<decltype(lib.attn_paged)>(f[2]);
+  Py_RETURN_NONE;
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL
 PyMethodDef methods[] = {
+    {"bind", FAST(bind), "(page_plan, page_append, attn_paged): the library's functions"},
     {"page_plan", FAST(page_plan),
      "(block, page_size, cache_lens, new_lens, free_pages, block_table, row_start, slot_map, pos, "
      "used, stream)"},

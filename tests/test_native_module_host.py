@@ -45,3 +45,31 @@ def test_the_module_is_loaded_with_the_first_paged_call(no_gpu, monkeypatch):
             b.page_plan(16, t, None, t, t, t, t, t, t)
         assert e.value.status == blk.BLK_ERR_SHAPE
     assert blk._calls is importlib.import_module(MODULE)
+
+
+def test_the_module_calls_the_library_that_is_loaded(tmp_path):
+    """With a library of another place loaded, the in-tree one (whose kernels and handles are
+    others) does not come in beside it."""
+    import os
+    import shutil
+    import subprocess
+    other = str(tmp_path / "libother.so")
+    shutil.copy(blk.LIB_PATH, other)
+    code = ("import sys, torch, decode_qwen2_block_gb300 as blk; blk.load(sys.argv[1]); blk._paged_calls();"
+            "print(open('/proc/self/maps').read())")
+    root = os.path.dirname(os.path.dirname(blk.LIB_PATH))
+    maps = subprocess.run([sys.executable, "-c", code, other], cwd=root, check=True,
+                          capture_output=True, text=True).stdout
+    assert other in maps and "_native" in maps and "libblk.so" not in maps
+
+
+def test_the_module_refuses_calls_before_it_has_a_library():
+    """(in a process of its own: the module is bound once)"""
+    import os
+    import subprocess
+    code = ("import torch; from decode_qwen2_block_gb300 import _native\n"
+            "try: _native.bind(0, 0, 0)\n"
+            "except ValueError: print('refused')")
+    root = os.path.dirname(os.path.dirname(blk.LIB_PATH))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
