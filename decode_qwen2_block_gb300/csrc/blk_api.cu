@@ -44,6 +44,7 @@ struct blk_handle_s {
   int* status;    // device status word
   uint32_t flags;
   bool decode_ok;  // shape fits the persistent decode kernel
+  bool paged_many; // the many-row paged kernels may be launched (configure_paged_many)
   int64_t window;  // sliding-window attention in slots (0 = full), blk_set_window
   blk::DecodeParams* dec;  // parameter block of the decode launch
   uint64_t* trace;         // optional decode timeline buffer
@@ -858,13 +859,15 @@ int blk_create(const blk_config* cfg, blk_handle* out) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))
     return BLK_ERR_CUDA;
   if (major != 10 || minor != 3) return BLK_ERR_DEVICE;
-  if (configure_kernels() != cudaSuccess) return BLK_ERR_CUDA;
+  bool paged_many = false;
+  if (configure_kernels(&paged_many) != cudaSuccess) return BLK_ERR_CUDA;
 
   blk_handle h = new (std::nothrow) blk_handle_s();
   if (!h) return BLK_ERR_CUDA;
   h->cfg = *cfg;
   h->device = dev;
   h->num_sms = sms;
+  h->paged_many = paged_many;
   {
     // the decode kernel stages at most kDecMaxVec inputs and keeps the
     // residual of at most 152 o_proj rows (8-row units) per CTA (one per SM)
@@ -1273,6 +1276,8 @@ int check_paged(blk_handle h, const blk_paged_batch* b) {
     if (!aligned(b->prefix_pages, 4)) return BLK_ERR_ALIGN;
     if (h->window > 0) return BLK_ERR_SHAPE;
   }
+  if (!h->paged_many && !paged_few_rows(h->cfg.n_heads / h->cfg.n_kv_heads, b->max_new))
+    return BLK_ERR_CUDA;
   return BLK_OK;
 }
 
@@ -1334,7 +1339,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
                    unsigned char* base, cudaStream_t s, Timer& tm, bool early) {
   const blk_config& c = h->cfg;
   const int D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads, G = Hq / Hkv;
-  const bool prefix = b->prefix_len > 0 && share_prefix(c, b);
+  const bool prefix = b->prefix_len > 0 && h->paged_many && share_prefix(c, b);
   const PagedWs lay = paged_ws(c, b->n_rows, prefix, h->num_sms);
   const int64_t page = b->page_size, heads = b->n_pages * Hkv;
   PagedManyParams m = {};
@@ -1775,7 +1780,7 @@ const char* blk_status_str(int status) {
 }  // extern "C"
 
 namespace blk {
-cudaError_t configure_kernels() {
+cudaError_t configure_kernels(bool* paged_many) {
   cudaError_t e = configure_decode_persistent();
   if (e == cudaSuccess) e = configure_tc_gemm_kernels();
   if (e == cudaSuccess) e = configure_fr_gemm_kernels();
@@ -1783,7 +1788,7 @@ cudaError_t configure_kernels() {
   if (e == cudaSuccess) e = configure_lm_head();
   if (e == cudaSuccess) e = configure_decode_attn_batch();
   if (e == cudaSuccess) e = configure_paged_few();
-  if (e == cudaSuccess) e = configure_paged_many();
+  if (e == cudaSuccess) e = configure_paged_many(paged_many);
   return e;
 }
 }  // namespace blk

@@ -117,7 +117,6 @@ cudaError_t launch_embed(const __half* table, int64_t vocab, const int64_t* ids,
                          __half* x, int* err, cudaStream_t s, bool pdl);
 cudaError_t configure_lm_head();
 
-// Sets the per-kernel shared-memory limits (called once per device).
 // Quantized weights formed as fp16: fmt 1 INT8 (q int8 [rows, K], scale
 // fp16 [rows]), fmt 2 int4 (packed uint8 [rows, K / 2], scale fp16 and zero
 // uint8 [rows, K / group]); w fp16 [rows, K].  K a multiple of 16.
@@ -125,6 +124,8 @@ cudaError_t launch_dequant(int fmt, const void* q, const void* scale, const void
                            int64_t rows, int64_t K, int group, __half* w, int num_sms,
                            cudaStream_t s);
 
-cudaError_t configure_kernels();
+// Sets the per-kernel shared-memory limits (called with every handle); paged_many: see
+// configure_paged_many.
+cudaError_t configure_kernels(bool* paged_many);
 
 }  // namespace blk

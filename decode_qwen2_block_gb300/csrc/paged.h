@@ -137,7 +137,9 @@ constexpr int kPagedManyTile = 128;     // slots of a tile
 // us).
 constexpr int kPagedManyHead = 3;
 cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl);
-cudaError_t configure_paged_many();
+// `usable` becomes false, and the kernels must not be launched, where the compiler gave one
+// another register count than its warps share out.
+cudaError_t configure_paged_many(bool* usable);
 
 // Merges cut units (and, with a prefix, every row's own and prefix parts).
 struct PagedMergeParams {

@@ -43,7 +43,9 @@ constexpr int kThreads = 384;
 // Registers: a softmax thread holds a row of 128 scores.  The block is launched
 // with 168 a thread (384 x 168 = 64512); warps 0-3 keep 72, the softmax warps take
 // 216 (the prefix's variant 88 and 208: 56.2 us against 59.4): 128 x 72 + 256 x
-// 216 = 128 x 88 + 256 x 208 = 64512.  configure_paged_many checks the 168.
+// 216 = 128 x 88 + 256 x 208 = 64512.  The launch bounds allow 168 and the compiler takes
+// them all, but nothing forces it: a larger share would wait forever for registers that the
+// block does not have, so configure_paged_many looks at the count.
 constexpr int kRegsLaunch = 168;
 template <bool kPrefix>
 struct Regs {
@@ -801,11 +803,11 @@ cudaError_t launch_many(const PagedManyParams& p, cudaStream_t s, bool pdl) {
 }
 
 template <int D, bool kPrefix>
-cudaError_t configure_one() {
+cudaError_t configure_one(bool* usable) {
   cudaFuncAttributes fa;
   const cudaError_t e = cudaFuncGetAttributes(&fa, paged_many_kernel<D, kPrefix>);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;   // see kRegsLaunch
+  if (fa.numRegs != kRegsLaunch) *usable = false;
   return cudaFuncSetAttribute(paged_many_kernel<D, kPrefix>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MSmem<D>::kBytes);
 }
@@ -821,11 +823,12 @@ cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl
   return cudaErrorInvalidValue;
 }
 
-cudaError_t configure_paged_many() {
-  cudaError_t e = configure_one<128, true>();
-  if (e == cudaSuccess) e = configure_one<128, false>();
-  if (e == cudaSuccess) e = configure_one<64, true>();
-  if (e == cudaSuccess) e = configure_one<64, false>();
+cudaError_t configure_paged_many(bool* usable) {
+  *usable = true;
+  cudaError_t e = configure_one<128, true>(usable);
+  if (e == cudaSuccess) e = configure_one<128, false>(usable);
+  if (e == cudaSuccess) e = configure_one<64, true>(usable);
+  if (e == cudaSuccess) e = configure_one<64, false>(usable);
   return e;
 }
 

@@ -383,9 +383,11 @@ int blk_decode_batch_stack(blk_handle h, const blk_weights* w, int n_layers,
  *
  * Every call below returns BLK_OK, BLK_ERR_NULL, BLK_ERR_ALIGN, BLK_ERR_SHAPE (a
  * size outside its range), BLK_ERR_CACHE_OVERFLOW, BLK_ERR_WORKSPACE or
- * BLK_ERR_CUDA (also: the current device is not the handle's), checks before it
- * enqueues anything, allocates nothing and is asynchronous on `stream`.  Calls
- * in flight at the same time need workspaces of their own. */
+ * BLK_ERR_CUDA (also: the current device is not the handle's, or the call needs the
+ * kernel for many rows and the compiler gave that another register count than it is
+ * launched with), checks before it enqueues anything, allocates nothing and is
+ * asynchronous on `stream`.  Calls in flight at the same time need workspaces of their
+ * own. */
 
 /* Block tables, slot map and positions of a step, on the GPU, from the
  * requests' lengths:
