@@ -60,6 +60,11 @@ const at::Tensor& checked(PyObject* o, const char* what, at::ScalarType type, in
   return t;
 }
 
+// The stride of dimension i; of one of size 1, which steps nowhere and may have any, `plain`.
+int64_t stride_of(const at::Tensor& t, int i, int64_t plain) {
+  return t.size(i) == 1 ? plain : t.stride(i);
+}
+
 const at::Tensor& workspace(PyObject* o, int64_t device) {
   const at::Tensor& t = tensor(o, "ws");
   if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous()) {
@@ -197,9 +202,10 @@ PyObject* page_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t* slots = checked(a[3], "slot_map", at::kLong, b.device, {rows}).data_ptr<int64_t>();
     const at::Tensor& k = checked(a[1], "k", at::kHalf, b.device, {rows, b.kv_heads, b.dim}, false);
     const at::Tensor& v = checked(a[2], "v", at::kHalf, b.device, {rows, b.kv_heads, b.dim}, false);
-    if (k.strides() != v.strides() || k.stride(2) != 1)
+    const int64_t rs = stride_of(k, 0, b.kv_heads * b.dim), hs = stride_of(k, 1, b.dim);
+    if (stride_of(v, 0, b.kv_heads * b.dim) != rs || stride_of(v, 1, b.dim) != hs ||
+        k.stride(2) != 1 || v.stride(2) != 1)
       refuse(BLK_ERR_SHAPE, "page_append: strides");
-    const int64_t rs = k.stride(0), hs = k.stride(1);
     const void *kp = k.data_ptr(), *vp = v.data_ptr();
     void *kt = p.k.data_ptr(), *vt = p.v.data_ptr(), *s = stream_of(a[6], b.device);
     need_library();
@@ -220,10 +226,10 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& q = checked(a[2], "q", at::kHalf, b.device, {d.n_rows, b.heads, b.dim}, false);
     const at::Tensor& o = checked(a[5], "out", at::kHalf, b.device, {d.n_rows, b.heads, b.dim}, false);
     for (const at::Tensor* t : {&q, &o})
-      if (t->stride(1) != b.dim || t->stride(2) != 1)
+      if (stride_of(*t, 1, b.dim) != b.dim || t->stride(2) != 1)
         refuse(BLK_ERR_SHAPE, "attn_paged: a row's heads must be contiguous");
     const at::Tensor& ws = workspace(a[6], b.device);
-    const int64_t qs = q.stride(0), os = o.stride(0);
+    const int64_t width = b.heads * b.dim, qs = stride_of(q, 0, width), os = stride_of(o, 0, width);
     const void *qp = q.data_ptr(), *kp = p.k.data_ptr(), *vp = p.v.data_ptr();
     void *op = o.data_ptr(), *wp = ws.data_ptr(), *s = stream_of(a[7], b.device);
     const size_t bytes = ws.nbytes();
