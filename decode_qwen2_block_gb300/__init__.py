@@ -632,8 +632,7 @@ class Block:
     def page_append(self, k, v, slot_map, k_pages, v_pages, stream=None):
         """Rows of k and v (fp16 [n, n_kv_heads, head_dim], the last dimension
         contiguous, both with the same strides where a dimension is longer than one) into
-        the slots of slot_map (int64
-        [n]; -1 leaves a row out)."""
+        the slots of slot_map (int64 [n]; -1 leaves a row out)."""
         (_calls or _paged_calls()).page_append(
             self._args, k, v, slot_map, k_pages, v_pages,
             None if stream is None else stream.cuda_stream)
