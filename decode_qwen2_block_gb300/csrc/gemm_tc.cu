@@ -736,6 +736,9 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* __restr
 // in a paged step K/V into their pages.
 template <int MAXS>
 __global__ void __launch_bounds__(64) qkv_finish_kernel(const __grid_constant__ TcGemmParams p) {
+  // In this order: the few-row attention of a paged step, launched behind this kernel, reads
+  // what is older than it (lengths, tables, the history's slots) ahead of its own wait, and
+  // those kernels are complete only because this one has waited before it lets it start.
   griddep_wait();
   griddep_launch();
   const int hd = blockIdx.x, m = blockIdx.y;

@@ -83,7 +83,9 @@ struct PagedAttnParams {
   int window;                  // of the handle; 0: all slots
   int early;                   // few rows: lengths, tables and the slots of the history are
                                //   older than the kernel before this one, which writes q
-                               //   and the new slots; nothing else of it is waited for
+                               //   and the new slots; nothing else of it is waited for.
+                               //   That kernel (qkv_finish_kernel, page_append_kernel) waits
+                               //   for its own predecessors before it lets this one start
   int B, N, Hq, Hkv, D, G, page_lg, max_new;
   float scale_log2;
   int nc;                      // CTAs of the kernel

@@ -139,6 +139,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
 // eight items a thread 11.9 / 12.1 / 14.6.
 constexpr int kUnroll = 2;
 __global__ void __launch_bounds__(256) page_append_kernel(const PageAppendParams p) {
+  // In this order: the few-row attention of a paged step, launched behind this kernel, reads
+  // what is older than it (lengths, tables, the history's slots) ahead of its own wait, and
+  // those kernels are complete only because this one has waited before it lets it start.
   griddep_wait();
   griddep_launch();
   const uint32_t cpr = p.D >> 3;                  // 16-byte pieces of a head's row

@@ -41,3 +41,29 @@ def test_a_prefix_on_the_last_stream_while_another_is_current(used_before):
         assert pg.table[:, :2].tolist() == [pg.prefix_ids] * 2
         results.append(torch.cat(outs))
     assert torch.equal(results[0].view(torch.int16), results[1].view(torch.int16))
+
+
+@pytest.mark.parametrize("seqs", [8, 150])
+def test_overlapping_kernels_of_the_full_shape(seqs):
+    """Steps through blocks of 1536 hidden, whose attention begins under the projection's
+    finisher (8 rows) or the append (150): the bits of steps whose kernels do not overlap
+    (with the per-kernel timing on)."""
+    s = synth.QWEN2_1P5B
+    wd = _layers(s, 3, 46)
+    x = to_dev(synth.hidden_input(s, 3000, seed=46))
+    prompts = [(37 * b) % 15 + 1 for b in range(seqs)]
+    prompts[0] = 300
+    results = []
+    for timed in (False, True):
+        pg = PagedStack(s, wd, 512, 700, 16, seqs, 3000)
+        pg.block.timing(timed)
+        pg.step(x[:sum(prompts)], prompts)
+        outs = []
+        for step in range(30):
+            outs.append(pg.step(x[step:step + seqs], [1] * seqs))
+            pg.block.timing_collect()
+        pg.block.timing(False)
+        torch.cuda.synchronize()
+        pg.block.check()
+        results.append(torch.cat(outs))
+    assert torch.equal(results[0].view(torch.int16), results[1].view(torch.int16))
