@@ -136,7 +136,7 @@ inline int paged_btok(int G) { return 128 / G; }
 constexpr int kPagedManyRows = 256;     // partial rows of a slot
 constexpr int kPagedManyTile = 128;     // slots of a tile
 // A unit's begin and end in the line, in tiles (8 prompts, with 1 / 3 / 5: 84 / 81 / 85
-// us).
+// us; they take the time of 1.6, and a piece that the line cuts off takes them again).
 constexpr int kPagedManyHead = 3;
 cudaError_t launch_paged_many(const PagedManyParams& p, cudaStream_t s, bool pdl);
 // `usable` becomes false, and the kernels must not be launched, where the compiler gave one

@@ -397,7 +397,8 @@ int blk_decode_batch_stack(blk_handle h, const blk_weights* w, int n_layers,
  *   block_table  device int32 [n_seqs][max_blocks]: entries [0, ceil(len / page_size))
  *                are read, the entries that the new tokens need are written,
  *                all others stay
- *   row_start    device int64 [n_seqs + 1], written: sums of new_lens
+ *   row_start    device int64 [n_seqs + 1], written: sums of new_lens (one below 0 or
+ *                above n_rows counts as 0: that sequence has no rows)
  *   slot_map     device int64 [n_rows], written: page * page_size + slot in the page
  *   pos          device int64 [n_rows], written: the row's slot number
  *   used         device int64 [1], written: how many of free_pages were taken
@@ -442,9 +443,9 @@ typedef struct {
  *   ws      blk_attn_paged_workspace_bytes(h, max_rows, max_seqs, with_prefix)
  *           bytes or more, for any max_rows >= n_rows and max_seqs >= n_seqs
  * With prefix_len > 0 the first prefix_len slots of every sequence are those of
- * prefix_pages: the block tables' entries for them are not read, and every sequence with rows must hold the
- * whole prefix (cache_lens[b] >= prefix_len; refused otherwise).  A prefix does
- * not go with a sliding window (BLK_ERR_SHAPE).  The result is that of the same
+ * prefix_pages: the block tables' entries for them are not read, and every sequence
+ * with rows must hold the whole prefix (cache_lens[b] >= prefix_len; refused
+ * otherwise).  A prefix does not go with a sliding window (BLK_ERR_SHAPE).  The result is that of the same
  * batch without the prefix, up to the order of sums.
  * Up to 32 rows (max_new x query heads per kv head) per sequence run on the
  * few-row kernel (K/V streamed once, mma.sync), more on the tcgen05 kernel; the
