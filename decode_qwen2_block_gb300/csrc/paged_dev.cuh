@@ -34,6 +34,12 @@ __device__ __forceinline__ PagedSeq load_seq(const PagedAttnParams& p, int b) {
   return s;
 }
 
+// A row's exponents are taken against its maximum x (log2 units) less w, so that weights
+// come out 2^w times their size (w: see the kernels).  Not where x is past 2^22, which fp32
+// holds to half a unit or worse: there a weight is off by a factor of that size, and needs
+// fp16's room for it.
+__device__ __forceinline__ bool weight_plain(float x) { return fabsf(x) >= 4194304.f; }
+
 // First slot that a row in slot `last` sees, and first slot that the rows from slot
 // `first` on see here (the prefix's slots only where it has no launch of its own).
 __device__ __forceinline__ int paged_window(const PagedAttnParams& p, int last) {

@@ -50,7 +50,8 @@ constexpr int kHead = 1;
 // then holds them to 2^-11 of themselves down to 2^-28 of the greatest and to half of
 // 2^-38 below.  Formed at their size those below 2^-14 would lose bits and those below
 // 2^-25 be lost: e^-15 of one slot's weight is off by 2.6 % in every one of 32,000
-// others.  The greatest, 2^14, leaves a factor 2 of room.
+// others.  The greatest, 2^14, leaves a factor 2 of room
+// (see weight_plain for scores that need more).
 constexpr float kWeightLog2 = 14.f;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     named_sync(1, kConsumers);
     if (*(volatile int*)&abort_s) return;       // (set before a warp's arrival, see above)
-    float corr[MT][2];
+    float corr[MT][2], m_new[MT][2];
     bool moved = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -490,9 +491,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int row = mt * 16 + grp + 8 * h2;
         const float4 m4 = *reinterpret_cast<const float4*>(stat + row * 4);
         const float mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-        const float mn = fmaxf(m_r[mt][h2], fmaf(mx, sl2, -kWeightLog2));
+        m_new[mt][h2] = fmaxf(m_r[mt][h2], fmaf(mx, sl2, -kWeightLog2));
+        moved |= m_new[mt][h2] != m_r[mt][h2];
+      }
+    if (moved) {                        // (seldom, after a unit's first tiles)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2)
+          if (m_new[mt][h2] != m_r[mt][h2] && weight_plain(m_new[mt][h2]))
+            m_new[mt][h2] += kWeightLog2;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        const float mn = m_new[mt][h2];
         corr[mt][h2] = mn == -INFINITY ? 1.f : ex2(m_r[mt][h2] - mn);
-        moved |= mn != m_r[mt][h2];
         m_r[mt][h2] = mn;
         const float nref = mn == -INFINITY ? 0.f : -mn;      // 2^-inf = 0
         float sum = 0.f;

@@ -58,7 +58,8 @@ constexpr int kInfos = 8;
 constexpr float kRescaleLog2 = 8.f;   // see the softmax
 // Weights are formed 2^7 times their size (O and l carry the factor, it cancels), so that
 // fp16 holds them to 2^-11 of themselves down to 2^-21 of the greatest and to half of
-// 2^-31 below; with kRescaleLog2 they reach 2^15, half of what fp16 holds.
+// 2^-31 below; with kRescaleLog2 they reach 2^15, half of what fp16 holds (see weight_plain
+// for scores that need more room).
 constexpr float kWeightLog2 = 7.f;
 constexpr int kMinTiles = 2;          // of a CTA: a piece of less is all begin and end
 constexpr int kHead = kPagedManyHead;
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // workspace's parts are with respect to one another by 256)
     const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.out_stride % 16 == 0;
     const bool wide_part = reinterpret_cast<uintptr_t>(p.part) % 32 == 0;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, most = kRescaleLog2;
     int seg = 0, last = 0, low = 0;              // slots that the row sees: [low, last]
     bool row_ok = false;                         // the row is a token's
     bool ok = true;
@@ -439,13 +440,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mx = fmaf(fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)), sl2, -kWeightLog2);
       // A row's reference maximum moves (and O, l are rescaled) only when the
       // maximum grew by more than 2^8 since: P <= 2^15 fits fp16, and 1 / l at the
-      // end makes the choice exact.
+      // end makes the choice exact.  (most: kRescaleLog2, counted from m as it stands.)
       // (Rows of no token hold whatever lay there: they take no part, or the moment
       // of a move, and with it the rounding of P, would differ from call to call.)
-      const bool need = row_ok && ((m == -INFINITY) ? (mx != -INFINITY) : (mx - m > kRescaleLog2));
+      const bool need = row_ok && ((m == -INFINITY) ? (mx != -INFINITY) : (mx - m > most));
       const bool move = __any_sync(0xffffffffu, need);
       if (move) {
-        const float mn = fmaxf(m, mx);
+        float mn = fmaxf(m, mx);
+        if (mn != m && weight_plain(mn)) mn += kWeightLog2;
+        most = weight_plain(mn) ? kRescaleLog2 - kWeightLog2 : kRescaleLog2;
         const float alpha = (m == -INFINITY || mn == m) ? 1.f : ex2(m - mn);
         m = mn;
         l *= alpha;

@@ -90,3 +90,54 @@ def test_shared_prefix(top, at, nats):
     assert n == 1
     check_weights(x, out, K_MANY)
 
+
+
+@pytest.mark.parametrize("top", [1, 60])
+@pytest.mark.parametrize("prefix", [0, 8192])
+def test_a_slot_far_above_all_others_is_the_result(top, prefix):
+    """Scores of 10^7 and more, whose fp32 values are whole numbers apart: weights stay in
+    fp16's range, and the row is that slot's V (its weight and the result rounded once each,
+    U16 of |V|; its exponential and their quotient in fp32).  The slot is another one, and of another
+    score, in every sequence and kv head."""
+    hist = [prefix + 200 + 37 * (i % 5) for i in range(60)]
+    x = Batch(12, 2, 128, 64, hist, [top] + [1] * 59, seed=44, prefix=prefix)
+    x.k_pages[~x.k_pages.isnan()] = 0
+    x.q[..., 0] = 30000
+    want = torch.empty_like(x.q)
+    r0 = 0
+    for b, (have, more) in enumerate(zip(x.hist, x.new)):
+        for g in range(2):
+            at = prefix + 3 * b + g
+            pg = int(x.table[b, at // 64])
+            x.k_pages[pg, g, at % 64, 0] = 8000 + 199 * b + 64 * g
+            want[r0:r0 + more, g * 6:g * 6 + 6] = x.v_pages[pg, g, at % 64]
+        r0 += more
+    out, b = run_attention(x)
+    b.check()
+    off = (out.double() - want.double()).abs()
+    assert (off <= (2 * U16 + 2.0 ** -13) * want.double().abs() + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("step", [60, 94, 200, -94])
+@pytest.mark.parametrize("top,prefix", [(1, 0), (60, 0), (1, 8192)])
+def test_large_scores_that_rise_from_tile_to_tile(top, prefix, step):
+    """Scores of 3 10^7 that grow or fall by some e-folds from one 128 slots to the next: their
+    weights are rough (fp32 holds such scores to 2), but a row stays between the least and
+    the greatest of V, weights and their sum being of the same exponentials (each weight,
+    and the result, rounded once)."""
+    hist = [prefix + 900 + 37 * (i % 5) for i in range(60)]
+    x = Batch(12, 2, 128, 128, hist, [top] + [1] * 59, seed=45, prefix=prefix)
+    seen = ~x.k_pages.isnan()
+    x.k_pages[seen] = 0
+    x.v_pages[seen] = 1 + x.v_pages[seen].abs().clamp(max=1)
+    x.q[..., 0], x.q[..., 1] = 30000, 1
+    for b, (have, more) in enumerate(zip(x.hist, x.new)):
+        for j in range(-(-(have + more) // 128)):
+            pg = int(x.table[b, j])
+            x.k_pages[pg, :, :, 0] = torch.where(seen[pg, :, :, 0], 12000, x.k_pages[pg, :, :, 0])
+            x.k_pages[pg, :, :, 1] = torch.where(seen[pg, :, :, 1], 94 * 100 + step * (j - 60),
+                                                 x.k_pages[pg, :, :, 1])
+    out, b = run_attention(x)
+    b.check()
+    got = out[:x.n].double()
+    assert got.min().item() >= 1 - 2 * U16 - 2.0 ** -13 and got.max().item() <= 2 + 4 * U16 + 2.0 ** -12
