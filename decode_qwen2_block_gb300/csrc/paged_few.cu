@@ -369,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int bs_lg = p.page_lg < 6 ? p.page_lg : 6;
   const int slab = warp * 16;
   const float sl2 = p.scale_log2;
-  // m_r: what exponents are taken against, the row's maximum (log2 units) less kWeightLog2
-  float m_r[MT][2], l_r[MT][2], O[MT][kNT][4];
+  // top: the row's maximum (log2 units) less kWeightLog2; m_r: what exponents are taken
+  // against, the same but where weight_plain
+  float top[MT][2], m_r[MT][2], l_r[MT][2], O[MT][kNT][4];
   int last[MT][2], low[MT][2];
   uint32_t qf[D / 16][MT][4];          // the unit's q: A fragments
   // A K or V tile is boxes [D / 64][bs slots][128 B] with the 128-byte swizzle:
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int row = mt * 16 + grp + 8 * h2;
           last[mt][h2] = L + min(row / p.G, n - 1);
           low[mt][h2] = paged_window(p, last[mt][h2]);
-          m_r[mt][h2] = -INFINITY;
+          top[mt][h2] = m_r[mt][h2] = -INFINITY;
           l_r[mt][h2] = 0.f;
 #pragma unroll
           for (int i = 0; i < kNT; ++i) O[mt][i][2 * h2] = O[mt][i][2 * h2 + 1] = 0.f;
@@ -491,16 +492,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int row = mt * 16 + grp + 8 * h2;
         const float4 m4 = *reinterpret_cast<const float4*>(stat + row * 4);
         const float mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-        m_new[mt][h2] = fmaxf(m_r[mt][h2], fmaf(mx, sl2, -kWeightLog2));
-        moved |= m_new[mt][h2] != m_r[mt][h2];
+        const float t = fmaxf(top[mt][h2], fmaf(mx, sl2, -kWeightLog2));
+        moved |= t != top[mt][h2];
+        top[mt][h2] = t;
+        m_new[mt][h2] = m_r[mt][h2];
       }
     if (moved) {                        // (seldom, after a unit's first tiles)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int h2 = 0; h2 < 2; ++h2)
-          if (m_new[mt][h2] != m_r[mt][h2] && weight_plain(m_new[mt][h2]))
-            m_new[mt][h2] += kWeightLog2;
+          m_new[mt][h2] = weight_plain(top[mt][h2]) ? top[mt][h2] + kWeightLog2 : top[mt][h2];
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)

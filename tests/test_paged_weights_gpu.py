@@ -119,10 +119,11 @@ def test_a_slot_far_above_all_others_is_the_result(top, prefix):
 
 
 @pytest.mark.parametrize("step", [60, 94, 200, -94])
+@pytest.mark.parametrize("k0", [12000, 18000, 25000])
 @pytest.mark.parametrize("top,prefix", [(1, 0), (60, 0), (1, 8192)])
-def test_large_scores_that_rise_from_tile_to_tile(top, prefix, step):
-    """Scores of 3 10^7 that grow or fall by some e-folds from one 128 slots to the next: their
-    weights are rough (fp32 holds such scores to 2), but a row stays between the least and
+def test_large_scores_that_rise_from_tile_to_tile(top, prefix, k0, step):
+    """Scores of 3 - 7 10^7 that grow or fall by some e-folds from one 128 slots to the next:
+    their weights are rough (fp32 holds such scores to 2 - 8), but a row stays between the least and
     the greatest of V, weights and their sum being of the same exponentials (each weight,
     and the result, rounded once)."""
     hist = [prefix + 900 + 37 * (i % 5) for i in range(60)]
@@ -134,7 +135,7 @@ def test_large_scores_that_rise_from_tile_to_tile(top, prefix, step):
     for b, (have, more) in enumerate(zip(x.hist, x.new)):
         for j in range(-(-(have + more) // 128)):
             pg = int(x.table[b, j])
-            x.k_pages[pg, :, :, 0] = torch.where(seen[pg, :, :, 0], 12000, x.k_pages[pg, :, :, 0])
+            x.k_pages[pg, :, :, 0] = torch.where(seen[pg, :, :, 0], k0, x.k_pages[pg, :, :, 0])
             x.k_pages[pg, :, :, 1] = torch.where(seen[pg, :, :, 1], 94 * 100 + step * (j - 60),
                                                  x.k_pages[pg, :, :, 1])
     out, b = run_attention(x)
