@@ -46,8 +46,10 @@ EXPORTED = ("blk_create", "blk_destroy", "blk_set_flags", "blk_workspace_bytes",
             "blk_decode_q", "blk_decode_stack_q", "blk_set_window", "blk_set_rope_yarn",
             "blk_prefill_stack_workspace_bytes", "blk_prefill_stack", "blk_page_plan",
             "blk_page_append", "blk_attn_paged_workspace_bytes", "blk_attn_paged",
-            "blk_step_paged_workspace_bytes", "blk_step_paged", "blk_step_paged_stack")
-BLK_N_KERNELS = 24
+            "blk_step_paged_workspace_bytes", "blk_step_paged", "blk_step_paged_stack",
+            "blk_page_append_kv8", "blk_page_read_kv8", "blk_attn_paged_kv8", "blk_step_paged_kv8",
+            "blk_step_paged_stack_kv8")
+BLK_N_KERNELS = 32
 
 WEIGHT_FIELDS = ("ln1_g", "wq", "wk", "wv", "bq", "bk", "bv", "wo", "ln2_g", "w_gate", "w_up",
                  "w_down")
@@ -94,6 +96,11 @@ class BlkPagedBatch(ctypes.Structure):
                 [("max_blocks", ctypes.c_int64), ("n_pages", ctypes.c_int64),
                  ("prefix_pages", ctypes.c_void_p), ("prefix_len", ctypes.c_int64),
                  ("page_size", ctypes.c_int32)])
+
+
+class BlkKv8Pool(ctypes.Structure):
+    """A layer's 8-bit K/V pages (blk_kv8_pool): codes and scales."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
 
 
 class BlkError(RuntimeError):
@@ -216,6 +223,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                          ctypes.POINTER(vp), ctypes.POINTER(vp), vp, vp, vp, vp, vp,
                                          ctypes.c_size_t, vp]
     lib.blk_step_paged_stack.restype = i32
+    kp = ctypes.POINTER(BlkKv8Pool)
+    lib.blk_page_append_kv8.argtypes = [vp, vp, vp, i64, i64, vp, i64, ctypes.c_int32, i64, kp, vp]
+    lib.blk_page_append_kv8.restype = i32
+    lib.blk_page_read_kv8.argtypes = [vp, vp, i64, ctypes.c_int32, i64, kp, vp, vp, i64, i64, vp]
+    lib.blk_page_read_kv8.restype = i32
+    lib.blk_attn_paged_kv8.argtypes = [vp, bt, vp, i64, kp, vp, i64, vp, ctypes.c_size_t, vp]
+    lib.blk_attn_paged_kv8.restype = i32
+    lib.blk_step_paged_kv8.argtypes = [vp, ctypes.POINTER(BlkWeights), bt, vp, vp, vp, kp, vp, vp,
+                                       ctypes.c_size_t, vp]
+    lib.blk_step_paged_kv8.restype = i32
+    lib.blk_step_paged_stack_kv8.argtypes = [vp, ctypes.POINTER(BlkWeights), i32, bt, kp, vp, vp, vp,
+                                             vp, vp, ctypes.c_size_t, vp]
+    lib.blk_step_paged_stack_kv8.restype = i32
     _lib = lib
     return lib
 
@@ -410,6 +430,37 @@ def blk_step_paged_stack(handle, w_array, n_layers, batch: BlkPagedBatch, k_page
                                        slot_map, out, ws, ws_bytes, stream)
 
 
+def blk_page_append_kv8(handle, k, v, row_stride, head_stride, slot_map, n_rows, page_size, n_pages,
+                        pool: BlkKv8Pool, stream) -> int:
+    return load().blk_page_append_kv8(handle, k, v, row_stride, head_stride, slot_map, n_rows,
+                                      page_size, n_pages, pool, stream)
+
+
+def blk_page_read_kv8(handle, slot_map, n_rows, page_size, n_pages, pool: BlkKv8Pool, k, v,
+                      row_stride, head_stride, stream) -> int:
+    return load().blk_page_read_kv8(handle, slot_map, n_rows, page_size, n_pages, pool, k, v,
+                                    row_stride, head_stride, stream)
+
+
+def blk_attn_paged_kv8(handle, batch: BlkPagedBatch, q, q_stride, pool: BlkKv8Pool, out, out_stride,
+                       ws, ws_bytes, stream) -> int:
+    return load().blk_attn_paged_kv8(handle, batch, q, q_stride, pool, out, out_stride, ws, ws_bytes,
+                                     stream)
+
+
+def blk_step_paged_kv8(handle, w: BlkWeights, batch: BlkPagedBatch, x, pos, slot_map,
+                       pool: BlkKv8Pool, out, ws, ws_bytes, stream) -> int:
+    return load().blk_step_paged_kv8(handle, w, batch, x, pos, slot_map, pool, out, ws, ws_bytes,
+                                     stream)
+
+
+def blk_step_paged_stack_kv8(handle, w_array, n_layers, batch: BlkPagedBatch, pools, x, pos,
+                             slot_map, out, ws, ws_bytes, stream) -> int:
+    """w_array: (BlkWeights * n); pools: (BlkKv8Pool * n)."""
+    return load().blk_step_paged_stack_kv8(handle, w_array, n_layers, batch, pools, x, pos, slot_map,
+                                           out, ws, ws_bytes, stream)
+
+
 def blk_check(handle, stream) -> int:
     return load().blk_check(handle, stream)
 
@@ -466,7 +517,8 @@ def _paged_calls():
     import importlib
     lib, calls = load(), importlib.import_module(__name__ + "._native")
     calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                 for f in (lib.blk_page_plan, lib.blk_page_append, lib.blk_attn_paged)))
+                 for f in (lib.blk_page_plan, lib.blk_page_append, lib.blk_attn_paged,
+                           lib.blk_page_append_kv8, lib.blk_page_read_kv8, lib.blk_attn_paged_kv8)))
     _calls = calls
     return calls
 
@@ -687,6 +739,50 @@ class Block:
                             out.data_ptr(), ws.data_ptr(), ws.nbytes, self._stream(stream))
         if rc != BLK_OK:
             raise BlkError(rc, "blk_step_paged")
+
+    # ---- the paged cache in 8 bits: codes uint8 [n_pages, n_kv_heads, page_size, head_dim]
+    # and scales float8_e5m2 [n_pages, n_kv_heads, page_size, head_dim / 32], K and V each
+
+    def page_append_kv8(self, k, v, slot_map, k_pages, v_pages, k_scales, v_scales, stream=None):
+        """page_append into 8-bit pages: rows of k and v (fp16) are quantised into their
+        slots, block by block of 32 columns."""
+        (_calls or _paged_calls()).page_append_kv8(
+            self._args, k, v, slot_map, k_pages, v_pages, k_scales, v_scales,
+            None if stream is None else stream.cuda_stream)
+
+    def page_read_kv8(self, slot_map, k_pages, v_pages, k_scales, v_scales, k, v, stream=None):
+        """What the slots of slot_map (int64 [n]; -1 leaves a row as it was) stand for, into
+        the rows of k and v (fp16 [n, n_kv_heads, head_dim], strides as for page_append, no
+        rows over each other)."""
+        (_calls or _paged_calls()).page_read_kv8(
+            self._args, slot_map, k_pages, v_pages, k_scales, v_scales, k, v,
+            None if stream is None else stream.cuda_stream)
+
+    def attn_paged_kv8(self, batch: BlkPagedBatch, q, k_pages, v_pages, k_scales, v_scales, out, ws,
+                       stream=None):
+        """attn_paged over 8-bit pages; the workspace is the same."""
+        (_calls or _paged_calls()).attn_paged_kv8(
+            self._args, batch, q, k_pages, v_pages, k_scales, v_scales, out, ws,
+            None if stream is None else stream.cuda_stream)
+
+    def step_paged_kv8(self, w: BlkWeights, batch: BlkPagedBatch, x, pos, slot_map, k_pages, v_pages,
+                       k_scales, v_scales, out, ws, stream=None):
+        """step_paged over 8-bit pages; the workspace is the same."""
+        shape = (batch.n_pages, self.cfg.n_kv_heads, batch.page_size, self.cfg.head_dim)
+        for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            self._tensor(t, torch.uint8, what, shape)
+        for t, what in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            self._tensor(t, torch.float8_e5m2, what, (*shape[:3], shape[3] // 32))
+        self._paged_rows(batch, x, pos, slot_map, out)
+        if ws.get_device() != self._device or not ws.is_contiguous():
+            raise BlkError(BLK_ERR_WORKSPACE, f"workspace {tuple(ws.shape)} on {ws.device}")
+        pool = BlkKv8Pool(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                          v_scales.data_ptr())
+        rc = blk_step_paged_kv8(self.handle, w, batch, x.data_ptr(), pos.data_ptr(),
+                                slot_map.data_ptr(), pool, out.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                self._stream(stream))
+        if rc != BLK_OK:
+            raise BlkError(rc, "blk_step_paged_kv8")
 
     def _paged_rows(self, batch, x, pos, slot_map, out):
         for t, what in ((x, "x"), (out, "out")):

@@ -24,6 +24,9 @@ struct {             // the loaded library's functions
   decltype(&blk_page_plan) page_plan;
   decltype(&blk_page_append) page_append;
   decltype(&blk_attn_paged) attn_paged;
+  decltype(&blk_page_append_kv8) page_append_kv8;
+  decltype(&blk_page_read_kv8) page_read_kv8;
+  decltype(&blk_attn_paged_kv8) attn_paged_kv8;
 } lib = {};
 
 [[noreturn]] void refuse(int status, const std::string& what) {
@@ -121,6 +124,46 @@ struct Pools {
   int64_t page() const { return k.size(2); }
 };
 
+// The codes and scales of an 8-bit cache: a[0 .. 3] are k_pages, v_pages, k_scales, v_scales.
+struct Pools8 {
+  blk_kv8_pool pool;
+  int64_t n_pages, page;
+  Pools8(const BlockArgs& b, PyObject* const* a) {
+    const at::Tensor& k = tensor(a[0], "k_pages");
+    const auto shape = k.sizes();
+    if (shape.size() != 4 || shape[1] != b.kv_heads || shape[3] != b.dim) {
+      std::ostringstream s;
+      s << "k_pages: " << shape;
+      refuse(BLK_ERR_SHAPE, s.str());
+    }
+    n_pages = shape[0];
+    page = shape[2];
+    const int64_t scales[4] = {n_pages, b.kv_heads, page, b.dim / 32};
+    pool.k = checked(a[0], "k_pages", at::kByte, b.device, shape).data_ptr();
+    pool.v = checked(a[1], "v_pages", at::kByte, b.device, shape).data_ptr();
+    pool.k_scale = checked(a[2], "k_scales", at::kFloat8_e5m2, b.device, scales).data_ptr();
+    pool.v_scale = checked(a[3], "v_scales", at::kFloat8_e5m2, b.device, scales).data_ptr();
+  }
+};
+
+// Rows of K and V [rows, kv_heads, dim] in fp16 with the same strides, the last dimension
+// contiguous.
+struct Rows {
+  void *k, *v;
+  int64_t row_stride, head_stride;
+  Rows(const BlockArgs& b, int64_t rows, PyObject* ko, PyObject* vo, const char* what) {
+    const at::Tensor& kt = checked(ko, "k", at::kHalf, b.device, {rows, b.kv_heads, b.dim}, false);
+    const at::Tensor& vt = checked(vo, "v", at::kHalf, b.device, {rows, b.kv_heads, b.dim}, false);
+    row_stride = stride_of(kt, 0, b.kv_heads * b.dim);
+    head_stride = stride_of(kt, 1, b.dim);
+    if (stride_of(vt, 0, b.kv_heads * b.dim) != row_stride ||
+        stride_of(vt, 1, b.dim) != head_stride || kt.stride(2) != 1 || vt.stride(2) != 1)
+      refuse(BLK_ERR_SHAPE, std::string(what) + ": strides");
+    k = kt.data_ptr();
+    v = vt.data_ptr();
+  }
+};
+
 // A ctypes structure's bytes.
 struct Batch {
   Py_buffer view;
@@ -153,8 +196,9 @@ PyObject* call(Py_ssize_t given, Py_ssize_t wanted, const char* what, F f) {
   Py_RETURN_NONE;
 }
 
-void need_library() {
-  if (lib.page_plan) return;
+template <typename F>
+void need_library(F f) {
+  if (f) return;
   PyErr_SetString(PyExc_RuntimeError, "_native: no library is bound");
   throw Refused();
 }
@@ -187,7 +231,7 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* tab = table.data_ptr<int32_t>();
     void* s = stream_of(a[10], b.device);
     if (page != (int32_t)page) return (int)BLK_ERR_SHAPE;
-    need_library();
+    need_library(lib.page_plan);
     NoGil g;
     return lib.page_plan(b.h, (int32_t)page, B, lens, news, free_pages, n_free, tab, blocks, rows,
                          start, slots, pos, used, s);
@@ -208,7 +252,7 @@ PyObject* page_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse(BLK_ERR_SHAPE, "page_append: strides");
     const void *kp = k.data_ptr(), *vp = v.data_ptr();
     void *kt = p.k.data_ptr(), *vt = p.v.data_ptr(), *s = stream_of(a[6], b.device);
-    need_library();
+    need_library(lib.page_append);
     NoGil g;
     return lib.page_append(b.h, kp, vp, rs, hs, slots, rows, (int32_t)p.page(), p.n_pages(), kt, vt,
                            s);
@@ -233,17 +277,72 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void *qp = q.data_ptr(), *kp = p.k.data_ptr(), *vp = p.v.data_ptr();
     void *op = o.data_ptr(), *wp = ws.data_ptr(), *s = stream_of(a[7], b.device);
     const size_t bytes = ws.nbytes();
-    need_library();
+    need_library(lib.attn_paged);
     NoGil g;
     return lib.attn_paged(b.h, &d, qp, qs, kp, vp, op, os, wp, bytes, s);
   });
 }
 
-// bind(page_plan, page_append, attn_paged): the functions' addresses.
+PyObject* page_append_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 9, "blk_page_append_kv8", [&] {
+    const BlockArgs b(a[0]);
+    const Pools8 p(b, a + 4);
+    const int64_t rows = tensor(a[3], "slot_map").numel();
+    const int64_t* slots = checked(a[3], "slot_map", at::kLong, b.device, {rows}).data_ptr<int64_t>();
+    const Rows r(b, rows, a[1], a[2], "page_append_kv8");
+    void* s = stream_of(a[8], b.device);
+    need_library(lib.page_append_kv8);
+    NoGil g;
+    return lib.page_append_kv8(b.h, r.k, r.v, r.row_stride, r.head_stride, slots, rows,
+                               (int32_t)p.page, p.n_pages, &p.pool, s);
+  });
+}
+
+PyObject* page_read_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 9, "blk_page_read_kv8", [&] {
+    const BlockArgs b(a[0]);
+    const Pools8 p(b, a + 2);
+    const int64_t rows = tensor(a[1], "slot_map").numel();
+    const int64_t* slots = checked(a[1], "slot_map", at::kLong, b.device, {rows}).data_ptr<int64_t>();
+    const Rows r(b, rows, a[6], a[7], "page_read_kv8");
+    void* s = stream_of(a[8], b.device);
+    need_library(lib.page_read_kv8);
+    NoGil g;
+    return lib.page_read_kv8(b.h, slots, rows, (int32_t)p.page, p.n_pages, &p.pool, r.k, r.v,
+                             r.row_stride, r.head_stride, s);
+  });
+}
+
+PyObject* attn_paged_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 10, "blk_attn_paged_kv8", [&] {
+    const BlockArgs b(a[0]);
+    const Batch batch(a[1]);
+    const blk_paged_batch& d = batch.get();
+    const Pools8 p(b, a + 3);
+    if (p.n_pages != d.n_pages || p.page != d.page_size)
+      refuse(BLK_ERR_SHAPE, "the pools are not those of the batch");
+    const at::Tensor& q = checked(a[2], "q", at::kHalf, b.device, {d.n_rows, b.heads, b.dim}, false);
+    const at::Tensor& o = checked(a[7], "out", at::kHalf, b.device, {d.n_rows, b.heads, b.dim}, false);
+    for (const at::Tensor* t : {&q, &o})
+      if (stride_of(*t, 1, b.dim) != b.dim || t->stride(2) != 1)
+        refuse(BLK_ERR_SHAPE, "attn_paged_kv8: a row's heads must be contiguous");
+    const at::Tensor& ws = workspace(a[8], b.device);
+    const int64_t width = b.heads * b.dim, qs = stride_of(q, 0, width), os = stride_of(o, 0, width);
+    const void* qp = q.data_ptr();
+    void *op = o.data_ptr(), *wp = ws.data_ptr(), *s = stream_of(a[9], b.device);
+    const size_t bytes = ws.nbytes();
+    need_library(lib.attn_paged_kv8);
+    NoGil g;
+    return lib.attn_paged_kv8(b.h, &d, qp, qs, &p.pool, op, os, wp, bytes, s);
+  });
+}
+
+// bind(page_plan, page_append, attn_paged[, page_append_kv8, page_read_kv8, attn_paged_kv8]):
+// the functions' addresses.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* f[3];
-  if (n != 3) return PyErr_Format(PyExc_TypeError, "bind: 3 arguments");
-  for (int i = 0; i < 3; ++i) {
+  void* f[6] = {};
+  if (n != 3 && n != 6) return PyErr_Format(PyExc_TypeError, "bind: 3 or 6 arguments");
+  for (int i = 0; i < n; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (!f[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null address");
@@ -253,17 +352,28 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   lib.page_plan = reinterpret_cast<decltype(lib.page_plan)>(f[0]);
   lib.page_append = reinterpret_cast<decltype(lib.page_append)>(f[1]);
   lib.attn_paged = reinterpret_cast<decltype(lib.attn_paged)>(f[2]);
+  lib.page_append_kv8 = reinterpret_cast<decltype(lib.page_append_kv8)>(f[3]);
+  lib.page_read_kv8 = reinterpret_cast<decltype(lib.page_read_kv8)>(f[4]);
+  lib.attn_paged_kv8 = reinterpret_cast<decltype(lib.attn_paged_kv8)>(f[5]);
   Py_RETURN_NONE;
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL
 PyMethodDef methods[] = {
-    {"bind", FAST(bind), "(page_plan, page_append, attn_paged): the library's functions"},
+    {"bind", FAST(bind),
+     "(page_plan, page_append, attn_paged[, page_append_kv8, page_read_kv8, attn_paged_kv8]): the "
+     "library's functions"},
     {"page_plan", FAST(page_plan),
      "(block, page_size, cache_lens, new_lens, free_pages, block_table, row_start, slot_map, pos, "
      "used, stream)"},
     {"page_append", FAST(page_append), "(block, k, v, slot_map, k_pages, v_pages, stream)"},
     {"attn_paged", FAST(attn_paged), "(block, batch, q, k_pages, v_pages, out, ws, stream)"},
+    {"page_append_kv8", FAST(page_append_kv8),
+     "(block, k, v, slot_map, k_pages, v_pages, k_scales, v_scales, stream)"},
+    {"page_read_kv8", FAST(page_read_kv8),
+     "(block, slot_map, k_pages, v_pages, k_scales, v_scales, k, v, stream)"},
+    {"attn_paged_kv8", FAST(attn_paged_kv8),
+     "(block, batch, q, k_pages, v_pages, k_scales, v_scales, out, ws, stream)"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The paged calls from torch tensors.", -1,
                       methods};

@@ -14,6 +14,7 @@
 #include "gemm_fr.h"
 #include "gemm_tc.h"
 #include "kernels.h"
+#include "kv8.h"
 #include "paged.h"
 
 using namespace blk;
@@ -25,7 +26,8 @@ enum KernelId {
   kKRmsNorm = 0, kKGemmQKV, kKSplitReduce, kKAttnPrefill, kKGemmO, kKGemmGateUp,
   kKGemmDown, kKDecodeStep, kKAttnMerge, kKLmHead, kKArgmax, kKEmbed, kKDecodeAttnBatch,
   kKQkvFinish, kKDequant, kKReduceNorm, kKPagePlan, kKPageAppend, kKPagedFew, kKPagedMany,
-  kKPagedPrefix, kKPagedMerge, kKCount
+  kKPagedPrefix, kKPagedMerge, kKPageAppend8, kKPageRead8, kKPagedFew8, kKPagedMany8,
+  kKPagedPrefix8, kKCount
 };
 static_assert(kKCount <= BLK_N_KERNELS, "kernel id table");
 const char* const kKernelNames[BLK_N_KERNELS] = {
@@ -33,7 +35,8 @@ const char* const kKernelNames[BLK_N_KERNELS] = {
     "gemm_gateup", "gemm_down", "decode_persistent", "attn_merge", "lm_head", "argmax_reduce",
     "embed", "decode_attn_batch", "qkv_finish", "dequant_weights", "splitk_reduce_norm",
     "page_plan", "page_append", "attn_paged_few", "attn_paged_many", "attn_paged_prefix",
-    "attn_paged_merge"};
+    "attn_paged_merge", "page_append_kv8", "page_read_kv8", "attn_paged_few_kv8",
+    "attn_paged_many_kv8", "attn_paged_prefix_kv8"};
 }  // namespace
 
 struct blk_handle_s {
@@ -1281,6 +1284,26 @@ int check_paged(blk_handle h, const blk_paged_batch* b) {
   return BLK_OK;
 }
 
+// A layer's K/V pages: fp16 pools, or the codes and scales of 8-bit ones (ks != null).
+struct Pool {
+  void *k, *v, *ks, *vs;
+};
+Pool pool_f16(const void* k, const void* v) {
+  return {const_cast<void*>(k), const_cast<void*>(v), nullptr, nullptr};
+}
+Pool pool_kv8(const blk_kv8_pool* p) { return {p->k, p->v, p->k_scale, p->v_scale}; }
+Kv8Pools kv8_of(const Pool& p) {
+  return {static_cast<uint8_t*>(p.k), static_cast<uint8_t*>(p.v), static_cast<uint8_t*>(p.ks),
+          static_cast<uint8_t*>(p.vs)};
+}
+// Null and unaligned pointers of an 8-bit pool.
+int check_kv8(const blk_kv8_pool* p) {
+  if (!p || !p->k || !p->v || !p->k_scale || !p->v_scale) return BLK_ERR_NULL;
+  for (const void* ptr : {p->k, p->v, p->k_scale, p->v_scale})
+    if (!aligned(ptr, 16)) return BLK_ERR_ALIGN;
+  return BLK_OK;
+}
+
 // Attention workspace: partials and (m, l) of the own parts, the cut units;
 // with a prefix also its partials and the
 // whole units' parts by row and head.
@@ -1334,9 +1357,26 @@ bool share_prefix(const blk_config& c, const blk_paged_batch* b) {
   return with_own > alone;
 }
 
+// The arguments of the 8-bit append and read (k and v are rows of fp16).
+int check_rows_kv8(blk_handle h, const void* k, const void* v, int64_t row_stride,
+                   int64_t head_stride, const int64_t* slot_map, int64_t n_rows,
+                   int32_t page_size, int64_t n_pages, const blk_kv8_pool* pool) {
+  if (!h || !k || !v || !slot_map) return BLK_ERR_NULL;
+  int rc = check_kv8(pool);
+  if (rc) return rc;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 8) || row_stride % 8 ||
+      head_stride % 8)
+    return BLK_ERR_ALIGN;
+  rc = check_pool(h, page_size, n_pages);
+  if (rc) return rc;
+  if (n_rows < 1 || n_rows > kMaxPagedRows || row_stride < 0 || head_stride < 0)
+    return BLK_ERR_SHAPE;
+  return on_device(h) ? BLK_OK : BLK_ERR_CUDA;
+}
+
 int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_t q_stride,
-                   const void* k_pages, const void* v_pages, void* out, int64_t out_stride,
-                   unsigned char* base, cudaStream_t s, Timer& tm, bool early) {
+                   const Pool& pool, void* out, int64_t out_stride, unsigned char* base,
+                   cudaStream_t s, Timer& tm, bool early) {
   const blk_config& c = h->cfg;
   const int D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads, G = Hq / Hkv;
   const bool prefix = b->prefix_len > 0 && h->paged_many && share_prefix(c, b);
@@ -1360,6 +1400,12 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   a.ml = reinterpret_cast<float2*>(base + lay.ml);
   a.cut = reinterpret_cast<PagedPiece*>(base + lay.cut);
   a.err = h->status;
+  if (pool.ks) {
+    Kv8AttnParams p8 = {a, kv8_of(pool)};
+    BLK_LAUNCH(tm, kKPagedFew8, launch_kv8_attn(p8, s, true));
+    return BLK_OK;
+  }
+  const void *k_pages = pool.k, *v_pages = pool.v;
   const bool few = paged_few_rows(G, b->max_new);
   CUtensorMap few_k, few_v;
   if (few) {
@@ -1493,9 +1539,8 @@ int check_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* 
 // One layer of a paged step (arguments checked).  x_normed and next_ln1 as in
 // run_decode_batch.
 int run_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b, const void* x,
-                   const int64_t* pos, const int64_t* slot_map, void* k_pages, void* v_pages,
-                   void* out, unsigned char* base, cudaStream_t s, bool x_normed,
-                   const __half* next_ln1) {
+                   const int64_t* pos, const int64_t* slot_map, const Pool& pool, void* out,
+                   unsigned char* base, cudaStream_t s, bool x_normed, const __half* next_ln1) {
   const blk_config& c = h->cfg;
   const StepPagedWs lay = step_paged_ws(c, b->n_rows, b->prefix_len > 0, h->num_sms);
   __half* xn16 = reinterpret_cast<__half*>(base + lay.xn16);
@@ -1544,30 +1589,63 @@ int run_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b,
     BLK_LAUNCH(tm, kKGemmQKV, launch_fr_gemm(fq, kFrPart, h->num_sms, s, true));
     g.part = part;
     g.splits = fq.splits;
-    g.slot_map = slot_map;
-    g.kc = static_cast<__half*>(k_pages);
-    g.vc = static_cast<__half*>(v_pages);
+    if (!pool.ks) {
+      g.slot_map = slot_map;
+      g.kc = static_cast<__half*>(pool.k);
+      g.vc = static_cast<__half*>(pool.v);
+    }
     BLK_LAUNCH(tm, kKQkvFinish, launch_qkv_finish(g, s));
   } else {
     BLK_LAUNCH(tm, kKGemmQKV, launch_tc_gemm(g, kTcQKV, h->num_sms, s, true));
+  }
+  if (pool.ks) {
+    Kv8AppendParams pa = {};
+    pa.k = g.kc; pa.v = g.vc;
+    pa.row_stride = D; pa.head_stride = (int64_t)M * D;
+    pa.slot_map = slot_map;
+    pa.to = kv8_of(pool);
+    pa.n_slots = g.n_slots;
+    pa.N = M; pa.Hkv = Hkv; pa.D = D; pa.page_lg = g.page_lg;
+    pa.err = h->status;
+    BLK_LAUNCH(tm, kKPageAppend8, launch_kv8_append(pa, h->num_sms, s, true));
+  } else if (M > kFrMaxRows) {
     PageAppendParams pa = {};
     pa.k = g.kc; pa.v = g.vc;
     pa.row_stride = D; pa.head_stride = (int64_t)M * D;
     pa.slot_map = slot_map;
-    pa.k_pages = static_cast<__half*>(k_pages); pa.v_pages = static_cast<__half*>(v_pages);
+    pa.k_pages = static_cast<__half*>(pool.k); pa.v_pages = static_cast<__half*>(pool.v);
     pa.n_slots = g.n_slots;
     pa.N = M; pa.Hkv = Hkv; pa.D = D; pa.page_lg = g.page_lg;
     pa.err = h->status;
     BLK_LAUNCH(tm, kKPageAppend, launch_page_append(pa, h->num_sms, s, true));
   }
   // (two kernels or more lie between the caller's work and the attention: early)
-  const int rc = run_attn_paged(h, b, q16, (int64_t)Hq * D, k_pages, v_pages, attn16,
-                                (int64_t)Hq * D, base + lay.attn, s, tm, true);
+  const int rc = run_attn_paged(h, b, q16, (int64_t)Hq * D, pool, attn16, (int64_t)Hq * D,
+                                base + lay.attn, s, tm, true);
   if (rc) return rc;
   return run_block_tail(h, w, x, attn16, reinterpret_cast<float*>(base + lay.h32),
                         reinterpret_cast<__half*>(base + lay.hn16),
                         reinterpret_cast<__half*>(base + lay.act16), part, step_splits(M), true,
                         true, out, M, s, tm, next_ln1, xn16);
+}
+
+// The layers of a paged step (arguments checked); pool_of(l): a layer's pages.
+template <typename PoolOf>
+int run_step_paged_stack(blk_handle h, const blk_weights* w, int n_layers,
+                         const blk_paged_batch* batch, PoolOf pool_of, const void* x,
+                         const int64_t* pos, const int64_t* slot_map, void* out,
+                         unsigned char* base, cudaStream_t s) {
+  const StepPagedWs lay = step_paged_ws(h->cfg, batch->n_rows, batch->prefix_len > 0, h->num_sms);
+  for (int l = 0; l < n_layers; ++l) {
+    const void* in = l == 0 ? x : base + lay.act[(l - 1) % 2];
+    void* to = l == n_layers - 1 ? out : base + lay.act[l % 2];
+    const __half* next_ln1 =
+        l + 1 < n_layers ? static_cast<const __half*>(w[l + 1].ln1_g) : nullptr;
+    const int rc = run_step_paged(h, &w[l], batch, in, pos, slot_map, pool_of(l), to, base, s, l > 0,
+                                  next_ln1);
+    if (rc) return rc;
+  }
+  return BLK_OK;
 }
 
 }  // namespace
@@ -1643,7 +1721,67 @@ int blk_attn_paged(blk_handle h, const blk_paged_batch* batch, const void* q, in
   if (!on_device(h)) return BLK_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Timer tm{h, s};
-  return run_attn_paged(h, batch, q, q_stride, k_pages, v_pages, out, out_stride,
+  return run_attn_paged(h, batch, q, q_stride, pool_f16(k_pages, v_pages), out, out_stride,
+                        static_cast<unsigned char*>(ws), s, tm, false);
+}
+
+int blk_page_append_kv8(blk_handle h, const void* k, const void* v, int64_t row_stride,
+                        int64_t head_stride, const int64_t* slot_map, int64_t n_rows,
+                        int32_t page_size, int64_t n_pages, const blk_kv8_pool* pool,
+                        void* stream) {
+  int rc = check_rows_kv8(h, k, v, row_stride, head_stride, slot_map, n_rows, page_size, n_pages,
+                          pool);
+  if (rc) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Kv8AppendParams p = {};
+  p.k = static_cast<const __half*>(k); p.v = static_cast<const __half*>(v);
+  p.row_stride = row_stride; p.head_stride = head_stride; p.slot_map = slot_map;
+  p.to = kv8_of(pool_kv8(pool));
+  p.n_slots = n_pages * page_size;
+  p.N = (int)n_rows; p.Hkv = h->cfg.n_kv_heads; p.D = h->cfg.head_dim;
+  p.page_lg = page_log2(page_size); p.err = h->status;
+  Timer tm{h, s};
+  BLK_LAUNCH(tm, kKPageAppend8, launch_kv8_append(p, h->num_sms, s, true));
+  return BLK_OK;
+}
+
+int blk_page_read_kv8(blk_handle h, const int64_t* slot_map, int64_t n_rows, int32_t page_size,
+                      int64_t n_pages, const blk_kv8_pool* pool, void* k, void* v,
+                      int64_t row_stride, int64_t head_stride, void* stream) {
+  int rc = check_rows_kv8(h, k, v, row_stride, head_stride, slot_map, n_rows, page_size, n_pages,
+                          pool);
+  if (rc) return rc;
+  // rows over each other would be written by several threads at once
+  const int64_t D = h->cfg.head_dim, H = h->cfg.n_kv_heads, rs = row_stride, hs = head_stride;
+  const bool one_row = n_rows == 1, one_head = H == 1;
+  if ((!one_row && rs < D) || (!one_head && hs < D) ||
+      (!one_row && !one_head && rs < (H - 1) * hs + D && hs < (n_rows - 1) * rs + D))
+    return BLK_ERR_SHAPE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Kv8ReadParams p = {};
+  p.k = static_cast<__half*>(k); p.v = static_cast<__half*>(v);
+  p.row_stride = row_stride; p.head_stride = head_stride; p.slot_map = slot_map;
+  p.from = kv8_of(pool_kv8(pool));
+  p.n_slots = n_pages * page_size;
+  p.N = (int)n_rows; p.Hkv = h->cfg.n_kv_heads; p.D = h->cfg.head_dim;
+  p.page_lg = page_log2(page_size); p.err = h->status;
+  Timer tm{h, s};
+  BLK_LAUNCH(tm, kKPageRead8, launch_kv8_read(p, h->num_sms, s, true));
+  return BLK_OK;
+}
+
+int blk_attn_paged_kv8(blk_handle h, const blk_paged_batch* batch, const void* q, int64_t q_stride,
+                       const blk_kv8_pool* pool, void* out, int64_t out_stride, void* ws,
+                       size_t ws_bytes, void* stream) {
+  int rc = check_kv8(pool);
+  if (!h || !batch) rc = BLK_ERR_NULL;
+  if (rc) return rc;
+  rc = check_attn_paged(h, batch, q, q_stride, pool->k, pool->v, out, out_stride, ws, ws_bytes);
+  if (rc) return rc;
+  if (!on_device(h)) return BLK_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timer tm{h, s};
+  return run_attn_paged(h, batch, q, q_stride, pool_kv8(pool), out, out_stride,
                         static_cast<unsigned char*>(ws), s, tm, false);
 }
 
@@ -1665,9 +1803,16 @@ int blk_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* ba
                                   ws_bytes);
   if (rc) return rc;
   if (!on_device(h)) return BLK_ERR_CUDA;
-  return run_step_paged(h, w, batch, x, pos, slot_map, k_pages, v_pages, out,
+  return run_step_paged(h, w, batch, x, pos, slot_map, pool_f16(k_pages, v_pages), out,
                         static_cast<unsigned char*>(ws), static_cast<cudaStream_t>(stream), false,
                         nullptr);
+}
+
+int blk_step_paged_kv8(blk_handle h, const blk_weights* w, const blk_paged_batch* batch,
+                       const void* x, const int64_t* pos, const int64_t* slot_map,
+                       const blk_kv8_pool* pool, void* out, void* ws, size_t ws_bytes,
+                       void* stream) {
+  return blk_step_paged_stack_kv8(h, w, 1, batch, pool, x, pos, slot_map, out, ws, ws_bytes, stream);
 }
 
 int blk_step_paged_stack(blk_handle h, const blk_weights* w, int n_layers,
@@ -1684,18 +1829,29 @@ int blk_step_paged_stack(blk_handle h, const blk_weights* w, int n_layers,
     if (rc) return rc;
   }
   if (!on_device(h)) return BLK_ERR_CUDA;
-  const StepPagedWs lay = step_paged_ws(h->cfg, batch->n_rows, batch->prefix_len > 0, h->num_sms);
-  unsigned char* base = static_cast<unsigned char*>(ws);
+  return run_step_paged_stack(h, w, n_layers, batch,
+                              [&](int l) { return pool_f16(k_pages[l], v_pages[l]); }, x, pos,
+                              slot_map, out, static_cast<unsigned char*>(ws),
+                              static_cast<cudaStream_t>(stream));
+}
+
+int blk_step_paged_stack_kv8(blk_handle h, const blk_weights* w, int n_layers,
+                             const blk_paged_batch* batch, const blk_kv8_pool* pools,
+                             const void* x, const int64_t* pos, const int64_t* slot_map,
+                             void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!h || !w || !batch || !pools || !ws) return BLK_ERR_NULL;
+  if (n_layers < 1) return BLK_ERR_SHAPE;
   for (int l = 0; l < n_layers; ++l) {
-    const void* in = l == 0 ? x : base + lay.act[(l - 1) % 2];
-    void* to = l == n_layers - 1 ? out : base + lay.act[l % 2];
-    const __half* next_ln1 =
-        l + 1 < n_layers ? static_cast<const __half*>(w[l + 1].ln1_g) : nullptr;
-    const int rc = run_step_paged(h, &w[l], batch, in, pos, slot_map, k_pages[l], v_pages[l], to,
-                                  base, static_cast<cudaStream_t>(stream), l > 0, next_ln1);
+    int rc = check_kv8(&pools[l]);
+    if (rc) return rc;
+    rc = check_step_paged(h, &w[l], batch, x, pos, slot_map, pools[l].k, pools[l].v, out, ws,
+                          ws_bytes);
     if (rc) return rc;
   }
-  return BLK_OK;
+  if (!on_device(h)) return BLK_ERR_CUDA;
+  return run_step_paged_stack(h, w, n_layers, batch, [&](int l) { return pool_kv8(&pools[l]); }, x,
+                              pos, slot_map, out, static_cast<unsigned char*>(ws),
+                              static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,57 @@
+// A paged K/V cache in 8 bits: parameter blocks and launchers.
+//
+// A row (slot, kv head) of D values is D / 32 blocks of 32 columns.  A block whose
+// greatest magnitude is a has the scale
+//   s = the least E5M2 number with 127 s / 64 >= a,
+// codes c = rint(64 x / s) (ties to even; |c| <= 127), kept as c + 128 in a byte, and
+// stands for c s / 64.  An E5M2 number is the upper byte of an fp16 number.  c has 7 bits
+// and s 3, and their product's last bit is worth 2^-22 or more: the value is an fp16
+// number, so reading a block back, and the attention's use of it, round nothing.
+// A block with an infinity or a NaN has the scale NaN: all of it reads as NaN.
+//
+// Pools: codes K and V each [n_pages][Hkv][page][D] bytes, scales [n_pages][Hkv][page][D / 32].
+#pragma once
+
+#include "paged.h"
+
+namespace blk {
+
+constexpr int kKv8Block = 32;       // columns of a scale
+
+struct Kv8Pools {
+  uint8_t *k, *v;              // codes
+  uint8_t *ks, *vs;            // scales
+};
+
+struct Kv8AppendParams {
+  const __half* k;             // row r, head h at r * row_stride + h * head_stride
+  const __half* v;
+  int64_t row_stride, head_stride;
+  const int64_t* slot_map;     // [N]
+  Kv8Pools to;
+  int64_t n_slots;             // n_pages * page
+  int N, Hkv, D, page_lg;
+  int* err;
+};
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, int num_sms, cudaStream_t s, bool pdl);
+
+struct Kv8ReadParams {
+  __half* k;                   // row r, head h at r * row_stride + h * head_stride
+  __half* v;
+  int64_t row_stride, head_stride;
+  const int64_t* slot_map;     // [N]
+  Kv8Pools from;
+  int64_t n_slots;
+  int N, Hkv, D, page_lg;
+  int* err;
+};
+cudaError_t launch_kv8_read(const Kv8ReadParams& p, int num_sms, cudaStream_t s, bool pdl);
+
+// Attention over such pools (the batch and all else as in PagedAttnParams).
+struct Kv8AttnParams {
+  PagedAttnParams a;
+  Kv8Pools from;
+};
+cudaError_t launch_kv8_attn(const Kv8AttnParams& p, cudaStream_t s, bool pdl);
+
+}  // namespace blk

@@ -295,7 +295,7 @@ int blk_wait_probe(blk_handle h, const void* flag, uint64_t limit_ns, void* stre
  * timed and blk_timing_collect returns BLK_ERR_WORKSPACE).  blk_timing_read
  * returns the totals of kernel id `kernel` (0 <= kernel < BLK_N_KERNELS) and
  * its name; BLK_ERR_SHAPE for an unknown id. */
-#define BLK_N_KERNELS 24
+#define BLK_N_KERNELS 32
 int blk_timing(blk_handle h, int on);
 int blk_timing_collect(blk_handle h, void* stream);
 int blk_timing_read(blk_handle h, int kernel, double* total_ms,
@@ -480,6 +480,59 @@ int blk_step_paged_stack(blk_handle h, const blk_weights* w, int n_layers,
                          void* const* v_pages, const void* x, const int64_t* pos,
                          const int64_t* slot_map, void* out, void* ws, size_t ws_bytes,
                          void* stream);
+
+/* ---- paged K/V cache in 8 bits ------------------------------------------------
+ * The same cache in about half the bytes: a row (slot, kv head) of head_dim values
+ * is held in blocks of 32 columns.  A block whose greatest magnitude is a has
+ *   a scale s, the least E5M2 number with 127 s / 64 >= a (one byte, the upper byte
+ *             of an fp16 number; 0 where a is 0), and
+ *   codes     c = rint(64 x / s), ties to even, each kept as c + 128 in a byte,
+ * and stands for c s / 64: fp16 numbers, at most s / 128 from x.  Reading them back
+ * and attending to them rounds nothing more.  A block with an infinity or NaN reads
+ * as NaN throughout.
+ * Pools are device arrays: codes [n_pages][n_kv_heads][page_size][head_dim] bytes and
+ * scales [n_pages][n_kv_heads][page_size][head_dim / 32] bytes, 16-byte aligned, for K
+ * and for V.  Pages, tables, plans and batches are those of the paged cache above, and
+ * so are the return codes and what becomes of a sequence or page that does not fit. */
+typedef struct {
+  void *k, *v;                  /* codes                                               */
+  void *k_scale, *v_scale;      /* scales                                              */
+} blk_kv8_pool;
+
+/* Quantises n_rows (1 .. 2^20) rows of K and V into their slots: k, v, their strides
+ * and slot_map as for blk_page_append.  Of rows with equal slots the slot may come to
+ * hold one's codes with another's scales. */
+int blk_page_append_kv8(blk_handle h, const void* k, const void* v, int64_t row_stride,
+                        int64_t head_stride, const int64_t* slot_map, int64_t n_rows,
+                        int32_t page_size, int64_t n_pages, const blk_kv8_pool* pool,
+                        void* stream);
+
+/* The other way: row r of k and v (device fp16, row r and head h at r * row_stride +
+ * h * head_stride elements, both multiples of 8, no two rows over each other:
+ * BLK_ERR_SHAPE) becomes
+ * what slot slot_map[r] stands for.  A row of slot -1 stays as it was; another slot
+ * outside the pool leaves its row too and is reported. */
+int blk_page_read_kv8(blk_handle h, const int64_t* slot_map, int64_t n_rows, int32_t page_size,
+                      int64_t n_pages, const blk_kv8_pool* pool, void* k, void* v,
+                      int64_t row_stride, int64_t head_stride, void* stream);
+
+/* blk_attn_paged over such pools, with the same workspace: the result is that of an
+ * fp16 cache that holds what blk_page_read_kv8 gives, up to the order of sums. */
+int blk_attn_paged_kv8(blk_handle h, const blk_paged_batch* batch, const void* q, int64_t q_stride,
+                       const blk_kv8_pool* pool, void* out, int64_t out_stride, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* blk_step_paged and blk_step_paged_stack over such pools (one per layer), with the same
+ * workspaces: the new K/V are quantised into their slots, and the step's own rows attend
+ * to what the slots then hold. */
+int blk_step_paged_kv8(blk_handle h, const blk_weights* w, const blk_paged_batch* batch,
+                       const void* x, const int64_t* pos, const int64_t* slot_map,
+                       const blk_kv8_pool* pool, void* out, void* ws, size_t ws_bytes,
+                       void* stream);
+int blk_step_paged_stack_kv8(blk_handle h, const blk_weights* w, int n_layers,
+                             const blk_paged_batch* batch, const blk_kv8_pool* pools,
+                             const void* x, const int64_t* pos, const int64_t* slot_map,
+                             void* out, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- around the block stack: embedding in, next token out ----------------
  * The inference flow of the MLIR-compilation page (§2.3 "LLM inference
