@@ -1400,15 +1400,20 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   a.ml = reinterpret_cast<float2*>(base + lay.ml);
   a.cut = reinterpret_cast<PagedPiece*>(base + lay.cut);
   a.err = h->status;
-  if (pool.ks) {
-    Kv8AttnParams p8 = {a, kv8_of(pool)};
-    BLK_LAUNCH(tm, kKPagedFew8, launch_kv8_attn(p8, s, true));
-    return BLK_OK;
-  }
   const void *k_pages = pool.k, *v_pages = pool.v;
   const bool few = paged_few_rows(G, b->max_new);
+  if (pool.ks && (!few || prefix)) {
+    Kv8AttnParams p8 = {a, kv8_of(pool)};
+    BLK_LAUNCH(tm, kKPagedMany8, launch_kv8_attn(p8, s, true));
+    return BLK_OK;
+  }
   CUtensorMap few_k, few_v;
-  if (few) {
+  if (few && pool.ks) {
+    const int rows = (int)(page < 64 ? page : 64);
+    if (make_tmap_codes8(&few_k, k_pages, D, page, heads, rows) ||
+        make_tmap_codes8(&few_v, v_pages, D, page, heads, rows))
+      return BLK_ERR_CUDA;
+  } else if (few) {
     // a page's slots (at most 64 of them) and all of D in one box
     const int64_t kd[4] = {64, page, D / 64, heads}, ks[3] = {(int64_t)D * 2, 128, page * D * 2};
     const int kb[4] = {64, (int)(page < 64 ? page : 64), D / 64, 1};
@@ -1460,7 +1465,12 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
     paged_few_slots(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
     a.upb = units_each();
     a.early = early && !prefix;
-    BLK_LAUNCH(tm, kKPagedFew, launch_paged_few(a, s, true));
+    if (pool.ks) {
+      const PagedFew8Params f8 = {a, kv8_of(pool).ks, kv8_of(pool).vs};
+      BLK_LAUNCH(tm, kKPagedFew8, launch_paged_few_kv8(f8, s, true));
+    } else {
+      BLK_LAUNCH(tm, kKPagedFew, launch_paged_few(a, s, true));
+    }
   } else {
     a.nc = h->num_sms;
     a.slot_rows = kPagedManyRows;
@@ -1944,6 +1954,7 @@ cudaError_t configure_kernels(bool* paged_many) {
   if (e == cudaSuccess) e = configure_lm_head();
   if (e == cudaSuccess) e = configure_decode_attn_batch();
   if (e == cudaSuccess) e = configure_paged_few();
+  if (e == cudaSuccess) e = configure_paged_few_kv8();
   if (e == cudaSuccess) e = configure_paged_many(paged_many);
   return e;
 }

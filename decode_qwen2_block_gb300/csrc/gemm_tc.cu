@@ -944,6 +944,20 @@ int make_tmap_4d(CUtensorMap* map, const void* base, const int64_t* dims,
   return r == CUDA_SUCCESS ? 0 : -1;
 }
 
+int make_tmap_codes8(CUtensorMap* map, const void* base, int D, int64_t page, int64_t heads,
+                     int rows) {
+  const EncodeTiledFn encode = encode_tiled();
+  if (!encode) return -1;
+  cuuint64_t d[3] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)heads};
+  cuuint64_t st[2] = {(cuuint64_t)D, (cuuint64_t)(page * D)};
+  cuuint32_t bx[3] = {(cuuint32_t)D, (cuuint32_t)rows, 1}, es[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), d, st, bx,
+                            es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -1;
+}
+
 int make_tmap_rows8(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int cbs,
                     int* is3d) {
   const EncodeTiledFn encode = encode_tiled();

@@ -65,6 +65,10 @@ struct TcGemmParams {
 // are never stored, so they need not be loaded).
 inline int tc_a_box_rows(int64_t M) { return M >= 128 ? 128 : (int)((M + 7) & ~int64_t(7)); }
 
+// The codes of an 8-bit paged cache [heads][page][D] in boxes of all columns of `rows`
+// slots, swizzled by 128 bytes, of D = 64 by 64; zeros behind the pool.
+int make_tmap_codes8(CUtensorMap* map, const void* base, int D, int64_t page, int64_t heads, int rows);
+
 // 2-D tensor map over a row-major [rows, K] fp16 matrix, box 64 x box_rows,
 // 128-byte swizzle, zero fill out of bounds.  Returns 0 on success.
 int make_tmap_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t K,

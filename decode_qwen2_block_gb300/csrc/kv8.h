@@ -54,4 +54,12 @@ struct Kv8AttnParams {
 };
 cudaError_t launch_kv8_attn(const Kv8AttnParams& p, cudaStream_t s, bool pdl);
 
+// Few rows (paged_few_rows): as launch_paged_few, the merge of cut units behind it.
+struct PagedFew8Params {
+  PagedAttnParams a;           // tm_k, tm_v: codes, boxes of all columns of one page's slots (at most 64)
+  const uint8_t *ks, *vs;      // scales
+};
+cudaError_t launch_paged_few_kv8(const PagedFew8Params& p, cudaStream_t s, bool pdl);
+cudaError_t configure_paged_few_kv8();
+
 }  // namespace blk
