@@ -6,20 +6,22 @@
 //   out[r, h] = softmax(q[r, h] . K / sqrt(D)) V  over the slots row r sees
 //
 // Bound by memory and by issue: D + D / 32 bytes a row of K or V, and for each pair of
-// codes a byte permute, a subtraction and a product before mma.sync can take them.
+// codes a byte permute and a fused multiply-add before mma.sync can take them.
 //   warp 4     producer: codes and scales, page by page (at most 64 slots), by TMA.
-//   warps 0-3  16 slots each of every 64-slot tile: S = Q K^T, the warp's own running
-//              maximum and sum, O = P V of all columns.  Nothing is exchanged between
-//              warps until the unit ends (the weights' fragments are the scores' own), so
-//              a warp waits for no other while tiles come.
+//   warps 0-3  16 slots each of every 64-slot tile: S' = K Q' (the slots are the M side, so
+//              that rows come in eights), the warp's own running maximum and sum, O' = V' P'
+//              of all columns.  Nothing is exchanged between warps until the unit ends,
+//              so a warp waits for no other while tiles come.
 // A lane's codes are wide loads because the MMA's inner index may run over the columns in
 // any order if q's does too: lane (grp, tig) takes 16-byte pieces tig (and tig + 4) of its
 // slot's row, whose j-th four codes are inner indexes 2 tig, 2 tig + 1, 2 tig + 8,
 // 2 tig + 9 of product j.  For V the inner index is the slot and the lane's four are
 // words of four columns each; two permutes a pair of words bring equal columns together.
-// Slots are dealt to the scores' columns so that neither read meets bank conflicts.
+// Slots are dealt to the scores' rows so that neither read meets bank conflicts.
 // A slot that no row sees has its V scale taken as 0, so its codes count for nothing.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv8.cuh"
@@ -31,7 +33,12 @@ namespace {
 constexpr int kTile = 64;            // slots of a tile
 constexpr int kWarps = 4, kConsumers = 32 * kWarps, kThreads = kConsumers + 32;
 constexpr int kHead = 1;             // a unit's begin and end in the line, in tiles
-constexpr float kWeightLog2 = 14.f;  // weights are formed 2^14 times their size (see paged_few.cu)
+// Weights are formed 2^10 times their size (O and l carry the factor, it cancels), and a
+// row's reference maximum follows only when a score passes it by 2^5: weights reach 2^15,
+// half of what fp16 holds (see weight_plain for scores that need more room), and keep 11
+// bits down to 2^-24 of the greatest.  Following every rise, as the fp16 caches' kernel does
+// with 2^14, rescales O for nearly every tile while a piece has few.
+constexpr float kWeightLog2 = 10.f, kRescaleLog2 = 5.f;
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -77,8 +84,34 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error 2^-22; 
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ __half2 unit_of_bits(uint32_t h) {   // s / 64 of two fp16 s
-  return __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(1.f / 64.f));
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {    // an 8 x 8 matrix of fp16
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Two codes' factors, from the fp16 bits of their two scales.  1024 + code times s / 64 less
+// 18 s is (code - 128) s / 64, exact as one fused operation while 18 s is an fp16 number: up to
+// s = 3584.  Larger scales (kBig) subtract first.
+template <bool kBig>
+struct Unit {
+  __half2 mul, add;
+  __device__ __forceinline__ explicit Unit(uint32_t bits) {
+    const __half2 s = *reinterpret_cast<const __half2*>(&bits);
+    mul = __hmul2(s, __float2half2_rn(1.f / 64.f));
+    add = kBig ? __float2half2_rn(-1152.f) : __hmul2(s, __float2half2_rn(-18.f));
+  }
+  // the codes that `sel` places, from w
+  __device__ __forceinline__ uint32_t operator()(uint32_t w, uint32_t sel) const {
+    const uint32_t b = __byte_perm(w, 0x64646464u, sel);
+    const __half2 x = *reinterpret_cast<const __half2*>(&b);
+    const __half2 y = kBig ? __hmul2(__hadd2(x, add), mul) : __hfma2(x, mul, add);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+};
+// Whether one of four scale bytes is above 3584's, 0x6b (NaN's is).
+__device__ __forceinline__ uint32_t big_scales(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x14141414u) & 0x80808080u;
 }
 
 struct TileInfo {      // what the consumers need of a tile
@@ -90,21 +123,23 @@ struct TileInfo {      // what the consumers need of a tile
   int dst;             // -1 the whole unit, else the partial slot
 };
 
-template <int D, int MT>
+template <int D, int NT>
 struct FSmem {
   static constexpr int NB = D / kKv8Block;
   static constexpr int kKV = kTile * D;                         // K or V codes of a tile
   static constexpr int kSc = kTile * NB;                        // their scales
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kQStride = D * 2 + 16;                   // bytes (conflict-free reads)
-  static constexpr int kQBytes = 16 * MT * kQStride;
-  static constexpr int kQBufs = MT;                             // two row tiles re-read q for every tile
-  static constexpr int kXBytes = 3 * NB * 16 * 32 * 4;          // a unit's end: O on its way
+  static constexpr int kQBytes = 8 * NT * kQStride;
+  static constexpr bool kQRegs = NT == 1;                       // else q is re-read for every tile
+  static constexpr int kQBufs = kQRegs ? 1 : 2;
+  static constexpr int kXTiles = NT < 2 ? 1 : 2;                // row tiles that go out at a time
+  static constexpr int kXBytes = kXTiles * 3 * NB * 8 * 32 * 4; // a unit's end: O on its way
   static constexpr int kScOff = kStages * 2 * kKV;
   static constexpr int kQOff = kScOff + kStages * 2 * kSc;
   static constexpr int kXOff = kQOff + kQBufs * kQBytes;
-  static constexpr int kStatOff = kXOff + kXBytes;              // [16 MT][4 warps] maxima, then sums
-  static constexpr int kInfoOff = kStatOff + 2 * 4 * 16 * MT * 4;
+  static constexpr int kStatOff = kXOff + kXBytes;              // [8 NT][4 warps] maxima, then sums
+  static constexpr int kInfoOff = kStatOff + 2 * 4 * 8 * NT * 4;
   static constexpr int kBarOff = (kInfoOff + kStages * (int)sizeof(TileInfo) + 15) / 16 * 16;
   static constexpr int kEnd = kBarOff + (2 * kStages + kQBufs) * 8 + 64;
   static constexpr size_t kBytes = (size_t)kEnd + 1024;         // the ring is 1024-aligned
@@ -119,10 +154,10 @@ __device__ __forceinline__ int seq_weight(const PagedAttnParams& p, const PagedS
   return s.n == 0 ? 0 : seq_tiles(p, s) + kHead;
 }
 
-template <int D, int MT>
+template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_few_kv8_kernel(const __grid_constant__ PagedFew8Params q8) {
-  using Sm = FSmem<D, MT>;
+  using Sm = FSmem<D, NT>;
   constexpr int S = Sm::kStages, NB = Sm::NB;
   const PagedAttnParams& p = q8.a;
   extern __shared__ uint8_t smem_raw[];
@@ -131,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t ring = smem_u32(smem), sring = smem_u32(smem + Sm::kScOff),
                  qbase = smem_u32(smem + Sm::kQOff), xbase = smem_u32(smem + Sm::kXOff);
   float* stat_m = reinterpret_cast<float*>(smem + Sm::kStatOff);
-  float* stat_l = stat_m + 4 * 16 * MT;
+  float* stat_l = stat_m + 4 * 8 * NT;
   volatile TileInfo* infos = reinterpret_cast<volatile TileInfo*>(smem + Sm::kInfoOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Sm::kBarOff);
   uint64_t* empty = full + S;
@@ -360,14 +395,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int grp = lane >> 2, tig = lane & 3;
   const int slab = warp * 16;
   const float sl2 = p.scale_log2;
-  // The slot (of 8) behind column c of a score tile.  With rows of 128 bytes and the
-  // 128-byte swizzle rows 0 - 3 and 4 - 7 have a piece in different halves, so columns
+  // The slot (of 8) behind row c of a score tile.  With rows of 128 bytes and the
+  // 128-byte swizzle rows 0 - 3 and 4 - 7 have a piece in different halves, so rows
   // 2 i, 2 i + 1 are slots i, i + 4; rows of 64 bytes alternate by themselves.
   auto slot_of = [](int c) { return D == 128 ? (c >> 1) | ((c & 1) << 2) : c; };
   auto row_sw = [](int r) { return D == 128 ? r & 7 : (r >> 1) & 3; };
-  const int kr = slab + slot_of(grp);                 // + 8 t: K row of the lane's column
+  const int kr = slab + slot_of(grp);                 // the lane's K slots: kr, kr + 8
   const uint32_t k_off = kr * D + ((tig ^ row_sw(kr)) << 4);      // (^ 64: piece tig + 4)
-  const int se = slab + slot_of(2 * tig), so = slab + slot_of(2 * tig + 1);   // V rows, + 8 p
+  const int se = slab + slot_of(2 * tig), so = slab + slot_of(2 * tig + 1);   // V's, and + 8
   // lanes of odd tig read the odd slot first: their rows' pieces then lie elsewhere
   const int r_a = tig & 1 ? so : se, r_b = tig & 1 ? se : so;
   const uint32_t va_off = r_a * D + ((((grp >> 2) ^ row_sw(r_a))) << 4) + (grp & 3) * 4;
@@ -376,17 +411,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   // a K piece's block of 32 columns, as a permute that doubles its scale's byte to fp16
   const uint32_t kb = tig >> 1, sel_k0 = kb << 12 | 4 << 8 | kb << 4 | 4, sel_k1 = sel_k0 + 0x2020;
   const uint32_t q_lane = qbase + grp * Sm::kQStride + tig * 32;
-  // top: the row's maximum (log2 units) less kWeightLog2; m_r: what exponents are taken
-  // against, the same but where weight_plain
-  float top[MT][2], m_r[MT][2], l_r[MT][2], O[MT][NB * 4][4];
-  int last[MT][2], low[MT][2];
-  uint32_t qf[MT == 1 ? D / 16 : 1][4];               // the unit's q, if there is room for it
-  // q's A fragments of products 2 x, 2 x + 1 (x < D / 32) of row tile mt
-  auto load_q = [&](uint32_t qb, int mt, int x, uint32_t* a, uint32_t* b) {
-    const uint32_t at = qb + mt * 16 * Sm::kQStride + (x >> 1) * 128 + (x & 1) * 16;
-    const uint4 u = lds128(at), w = lds128(at + 8 * Sm::kQStride);
-    a[0] = u.x; a[1] = w.x; a[2] = u.y; a[3] = w.y;
-    b[0] = u.z; b[1] = w.z; b[2] = u.w; b[3] = w.w;
+  // The lane's rows: 8 nt + 2 tig + e.  m_r: what their exponents are taken against (log2
+  // units, less kWeightLog2 but where weight_plain), lim: where that has to follow.
+  float m_r[NT][2], lim[NT][2], l_r[NT][2], O[NT][NB * 2][4];
+  int last[NT][2], low[NT][2];
+  uint32_t qf[Sm::kQRegs ? D / 16 : 1][2];
+  // q's fragments of products 2 x, 2 x + 1 (x < D / 32) of row tile nt
+  auto load_q = [&](uint32_t qb, int nt, int x, uint32_t* a, uint32_t* b) {
+    const uint4 u = lds128(qb + nt * 8 * Sm::kQStride + (x >> 1) * 128 + (x & 1) * 16);
+    a[0] = u.x; a[1] = u.y;
+    b[0] = u.z; b[1] = u.w;
   };
   int seg = 0;
   for (int it = 0;; ++it) {
@@ -409,18 +443,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (flags & 1) {
       const int L = infos[st].L;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const int row = mt * 16 + grp + 8 * h2;
-          last[mt][h2] = L + min(row / p.G, n - 1);
-          low[mt][h2] = paged_window(p, last[mt][h2]);
-          top[mt][h2] = m_r[mt][h2] = -INFINITY;
-          l_r[mt][h2] = 0.f;
-#pragma unroll
-          for (int i = 0; i < NB * 4; ++i) O[mt][i][2 * h2] = O[mt][i][2 * h2 + 1] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          last[nt][e] = L + min((nt * 8 + 2 * tig + e) / p.G, n - 1);
+          low[nt][e] = paged_window(p, last[nt][e]);
+          m_r[nt][e] = lim[nt][e] = -INFINITY;
+          l_r[nt][e] = 0.f;
         }
-      if constexpr (MT == 1) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < NB * 2; ++i) O[nt][i][0] = O[nt][i][1] = O[nt][i][2] = O[nt][i][3] = 0.f;
+      if constexpr (Sm::kQRegs) {
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) load_q(qb, 0, x, qf[2 * x], qf[2 * x + 1]);
         __syncwarp();
@@ -431,106 +466,108 @@ __global__ void __launch_bounds__(kThreads, 2)
       // every row sees every slot of this warp's 16: n - 1 slots from the end are
       // behind the first row, windows begin at most n - 1 slots behind vlo
       const bool clear = slab + 16 <= vhi - (n - 1) && slab >= (p.window > 0 ? vlo + (n - 1) : vlo);
-      float sc[MT][2][4];
+      // (one row tile: two sums, so that products follow one another half as far)
+      constexpr int kSums = NT == 1 ? 2 : 1;
+      float sc[NT][kSums][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) sc[mt][t][0] = sc[mt][t][1] = sc[mt][t][2] = sc[mt][t][3] = 0.f;
-      const uint32_t w0 = lds_scales<NB>(ks + kr * NB), w1 = lds_scales<NB>(ks + (kr + 8) * NB);
+        for (int k = 0; k < kSums; ++k) sc[nt][k][0] = sc[nt][k][1] = sc[nt][k][2] = sc[nt][k][3] = 0.f;
+      {
+        const uint32_t w0 = lds_scales<NB>(ks + kr * NB), w1 = lds_scales<NB>(ks + (kr + 8) * NB);
+        auto scores = [&](auto big) {
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        const uint4 c0 = lds128(kt + (k_off ^ (h << 6))), c1 = lds128(kt + (k_off ^ (h << 6)) + 8 * D);
-        const uint32_t cw[2][4] = {{c0.x, c0.y, c0.z, c0.w}, {c1.x, c1.y, c1.z, c1.w}};
-        const uint32_t sel = h ? sel_k1 : sel_k0;
-        const __half2 u[2] = {unit_of_bits(__byte_perm(w0, 0, sel)), unit_of_bits(__byte_perm(w1, 0, sel))};
+          for (int h = 0; h < D / 64; ++h) {
+            const uint4 c0 = lds128(kt + (k_off ^ (h << 6))), c1 = lds128(kt + (k_off ^ (h << 6)) + 8 * D);
+            const uint32_t cw[2][4] = {{c0.x, c0.y, c0.z, c0.w}, {c1.x, c1.y, c1.z, c1.w}};
+            const uint32_t sel = h ? sel_k1 : sel_k0;
+            const Unit<decltype(big)::value> u0(__byte_perm(w0, 0, sel)), u1(__byte_perm(w1, 0, sel));
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t qa[MT][2][4];
-          if constexpr (MT > 1) {
+            for (int x = 0; x < 2; ++x) {
+              uint32_t qv[NT][2][2];
+              if constexpr (!Sm::kQRegs) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) load_q(qb, mt, 2 * h + x, qa[mt][0], qa[mt][1]);
-          }
+                for (int nt = 0; nt < NT; ++nt) load_q(qb, nt, 2 * h + x, qv[nt][0], qv[nt][1]);
+              }
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t a[4] = {u0(cw[0][2 * x + y], 0x4140), u1(cw[1][2 * x + y], 0x4140),
+                                       u0(cw[0][2 * x + y], 0x4342), u1(cw[1][2 * x + y], 0x4342)};
+                if constexpr (Sm::kQRegs) {
+                  const uint32_t* b = qf[4 * h + 2 * x + y];
+                  mma16816(sc[0][y % kSums], a, b[0], b[1]);
+                } else {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const uint32_t b0 = kv8_pair(cw[t][2 * x + y], 0x4140, u[t]);
-              const uint32_t b1 = kv8_pair(cw[t][2 * x + y], 0x4342, u[t]);
-              if constexpr (MT == 1) {
-                mma16816(sc[0][t], qf[4 * h + 2 * x + y], b0, b1);
-              } else {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma16816(sc[mt][t], qa[mt][y], b0, b1);
+                  for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt][0], a, qv[nt][y][0], qv[nt][y][1]);
+                }
               }
             }
-        }
+          }
+        };
+        if (__any_sync(0xffffffffu, (big_scales(w0) | big_scales(w1)) != 0)) scores(std::true_type());
+        else scores(std::false_type());
+      }
+      if constexpr (kSums == 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[0][0][k] += sc[0][1][k];
       }
       if (!clear) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int k = 0; k < 4; ++k) {
+            const int c = kr + 8 * (k >> 1), slot = slot0 + c;
+            if (!(c >= vlo && slot <= last[nt][k & 1] && slot >= low[nt][k & 1])) sc[nt][0][k] = -INFINITY;
+          }
+      }
+      bool need = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int c = (e & 1 ? so : se) + 8 * t, slot = slot0 + c;
-              const bool seen = c >= vlo && slot <= last[mt][e >> 1] && slot >= low[mt][e >> 1];
-              if (!seen) sc[mt][t][e] = -INFINITY;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          need |= fmaf(fmaxf(sc[nt][0][e], sc[nt][0][2 + e]), sl2, -kWeightLog2) > lim[nt][e];
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(sc[nt][0][e], sc[nt][0][2 + e]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            const float t = fmaf(x, sl2, -kWeightLog2);
+            if (t > lim[nt][e]) {         // (alike in the row's lanes)
+              const bool plain = weight_plain(t);
+              const float mn = plain ? t + kWeightLog2 : t, f = ex2(m_r[nt][e] - mn);
+              m_r[nt][e] = mn;
+              lim[nt][e] = mn + (plain ? kRescaleLog2 - kWeightLog2 : kRescaleLog2);
+              l_r[nt][e] *= f;
+#pragma unroll
+              for (int i = 0; i < NB * 2; ++i) {
+                O[nt][i][e] *= f;
+                O[nt][i][2 + e] *= f;
+              }
             }
-      }
-      float corr[MT][2], mx[MT][2];
-      bool moved = false;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          float x = fmaxf(fmaxf(sc[mt][0][2 * h2], sc[mt][0][2 * h2 + 1]),
-                          fmaxf(sc[mt][1][2 * h2], sc[mt][1][2 * h2 + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          mx[mt][h2] = fmaxf(top[mt][h2], fmaf(x, sl2, -kWeightLog2));
-          moved |= mx[mt][h2] != top[mt][h2];
-        }
-      if (__any_sync(0xffffffffu, moved)) {       // (seldom, after a unit's first tiles)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-            const float t = mx[mt][h2], mn = t == top[mt][h2] ? m_r[mt][h2]
-                                             : weight_plain(t) ? t + kWeightLog2 : t;
-            corr[mt][h2] = mn == -INFINITY ? 1.f : ex2(m_r[mt][h2] - mn);
-            top[mt][h2] = t;
-            m_r[mt][h2] = mn;
-            l_r[mt][h2] *= corr[mt][h2];
-          }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < NB * 4; ++i) {
-            O[mt][i][0] *= corr[mt][0];
-            O[mt][i][1] *= corr[mt][0];
-            O[mt][i][2] *= corr[mt][1];
-            O[mt][i][3] *= corr[mt][1];
           }
       }
-      uint32_t pa[MT][4];
+      uint32_t pb[NT][2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const float nref = m_r[mt][h2] == -INFINITY ? 0.f : -m_r[mt][h2];      // 2^-inf = 0
-          float sum = 0.f;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float e0 = ex2(fmaf(sc[mt][t][2 * h2], sl2, nref));
-            const float e1 = ex2(fmaf(sc[mt][t][2 * h2 + 1], sl2, nref));
-            sum += e0 + e1;
-            const __half2 ph = __floats2half2_rn(e0, e1);
-            pa[mt][2 * t + h2] = *reinterpret_cast<const uint32_t*>(&ph);
-          }
-          l_r[mt][h2] += sum;
+        for (int k = 0; k < 4; ++k) {
+          const float m = m_r[nt][k & 1];
+          w[k] = ex2(fmaf(sc[nt][0][k], sl2, m == -INFINITY ? 0.f : -m));      // 2^-inf = 0
         }
-      // O += P V
-      uint32_t sw[2][2];               // scales of the even and odd slot, + 8 p
+        l_r[nt][0] += w[0] + w[2];
+        l_r[nt][1] += w[1] + w[3];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const __half2 h = __floats2half2_rn(w[2 * t], w[2 * t + 1]);
+          pb[nt][t] = transposed(*reinterpret_cast<const uint32_t*>(&h));
+        }
+      }
+      // O' += V' P'
+      uint32_t sw[2][2], any_big = 0;      // scales of the even and the odd slot, + 8 x
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         sw[x][0] = lds_scales<NB>(vs + (se + 8 * x) * NB);
@@ -539,28 +576,33 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (se + 8 * x < vlo || se + 8 * x >= vhi) sw[x][0] = 0;
           if (so + 8 * x < vlo || so + 8 * x >= vhi) sw[x][1] = 0;
         }
+        any_big |= big_scales(sw[x][0]) | big_scales(sw[x][1]);
       }
+      auto values = [&](auto big) {
 #pragma unroll
-      for (int g = 0; g < NB; ++g) {
-        uint32_t lo2[2], hi2[2];
-        __half2 u[2];
+        for (int g = 0; g < NB; ++g) {
+          uint32_t lo2[2], hi2[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t a = lds32(vt + (va_off ^ (g << 5)) + x * 8 * D);
-          const uint32_t b = lds32(vt + (vb_off ^ (g << 5)) + x * 8 * D);
-          lo2[x] = __byte_perm(a, b, sel_lo);      // columns 0, 1: even and odd slot's codes
-          hi2[x] = __byte_perm(a, b, sel_hi);      // columns 2, 3
-          u[x] = unit_of_bits(__byte_perm(sw[x][0], sw[x][1], (4 + g) << 12 | g << 4) & 0xff00ff00u);
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t a = lds32(vt + (va_off ^ (g << 5)) + x * 8 * D);
+            const uint32_t b = lds32(vt + (vb_off ^ (g << 5)) + x * 8 * D);
+            lo2[x] = __byte_perm(a, b, sel_lo);      // columns 0, 1: even and odd slot's codes
+            hi2[x] = __byte_perm(a, b, sel_hi);      // columns 2, 3
+          }
+          const uint32_t sel = (4 + g) << 12 | g << 4;
+          const Unit<decltype(big)::value> u0(__byte_perm(sw[0][0], sw[0][1], sel) & 0xff00ff00u),
+              u1(__byte_perm(sw[1][0], sw[1][1], sel) & 0xff00ff00u);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {              // columns 2 j, 2 j + 1
+            const uint32_t v0 = j ? hi2[0] : lo2[0], v1 = j ? hi2[1] : lo2[1];
+            const uint32_t a[4] = {u0(v0, 0x4140), u0(v0, 0x4342), u1(v1, 0x4140), u1(v1, 0x4342)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(O[nt][g * 2 + j], a, pb[nt][0], pb[nt][1]);
+          }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t sel = j & 1 ? 0x4342 : 0x4140;
-          const uint32_t b0 = kv8_pair(j < 2 ? lo2[0] : hi2[0], sel, u[0]);
-          const uint32_t b1 = kv8_pair(j < 2 ? lo2[1] : hi2[1], sel, u[1]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma16816(O[mt][g * 4 + j], pa[mt], b0, b1);
-        }
-      }
+      };
+      if (__any_sync(0xffffffffu, any_big != 0)) values(std::true_type());
+      else values(std::false_type());
     }
     if (flags & 2) {
       // The piece's end: the warps' maxima meet, each brings its sums to the greatest,
@@ -568,108 +610,100 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int rows = n * p.G, r0 = infos[st].r0, g = infos[st].g, dst = infos[st].dst;
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
-      if (MT > 1 && lane == 0) mbar_arrive(&q_empty[seg % Sm::kQBufs]);
+      if (!Sm::kQRegs && lane == 0) mbar_arrive(&q_empty[seg % Sm::kQBufs]);
       ++seg;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2)
-          if (tig == 0) stat_m[(mt * 16 + grp + 8 * h2) * 4 + warp] = m_r[mt][h2];
+        for (int e = 0; e < 2; ++e)
+          if (grp == 0) stat_m[(nt * 8 + 2 * tig + e) * 4 + warp] = m_r[nt][e];
       named_sync(1, kConsumers);
       if (*(volatile int*)&abort_s) return;       // (set before a warp's arrival, see above)
-      float M[MT][2];
+      float M[NT][2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const int row = mt * 16 + grp + 8 * h2;
+        for (int e = 0; e < 2; ++e) {
+          const int row = nt * 8 + 2 * tig + e;
           const float4 m4 = *reinterpret_cast<const float4*>(stat_m + row * 4);
-          M[mt][h2] = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-          const float f = m_r[mt][h2] == -INFINITY ? 0.f : ex2(m_r[mt][h2] - M[mt][h2]);
-          float l = l_r[mt][h2] * f;
-          l += __shfl_xor_sync(0xffffffffu, l, 1);
-          l += __shfl_xor_sync(0xffffffffu, l, 2);
-          if (tig == 0) stat_l[row * 4 + warp] = l;
+          M[nt][e] = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+          const float f = m_r[nt][e] == -INFINITY ? 0.f : ex2(m_r[nt][e] - M[nt][e]);
+          float l = l_r[nt][e] * f;
 #pragma unroll
-          for (int i = 0; i < NB * 4; ++i) {
-            O[mt][i][2 * h2] *= f;
-            O[mt][i][2 * h2 + 1] *= f;
+          for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+          if (grp == 0) stat_l[row * 4 + warp] = l;
+#pragma unroll
+          for (int i = 0; i < NB * 2; ++i) {
+            O[nt][i][e] *= f;
+            O[nt][i][2 + e] *= f;
           }
         }
+      constexpr int X = Sm::kXTiles;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (mt > 0) named_sync(1, kConsumers);    // the first row tile's O is read
-        // a lane's O of a column block: columns 8 tig .. + 7 of rows grp and grp + 8
+      for (int nt0 = 0; nt0 < NT; nt0 += X) {
+        if (nt0 > 0) named_sync(1, kConsumers);    // the row tiles before are read
+        // a lane's O of a column block: columns 4 grp .. + 3 of rows 2 tig and 2 tig + 1
+        auto place = [&](int d, int s, int k, int e) {      // of warp s for warp d
+          const int row = 2 * tig + e;
+          return xbase + ((d * 3 + (s < d ? s : s - 1)) * X + k) * 1024 + row * 128 + ((grp ^ (tig << 1)) << 4);
+        };
 #pragma unroll
         for (int d = 0; d < NB; ++d)
           if (d != warp) {
-            const uint32_t to = xbase + (d * 3 + (warp < d ? warp : warp - 1)) * 2048;
 #pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2)
+            for (int k = 0; k < X && nt0 + k < NT; ++k)
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int row = grp + 8 * h2;
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 to + row * 128 + (((2 * tig + x) ^ (row & 7)) << 4)),
-                             "f"(O[mt][d * 4][2 * h2 + x]), "f"(O[mt][d * 4 + 1][2 * h2 + x]),
-                             "f"(O[mt][d * 4 + 2][2 * h2 + x]), "f"(O[mt][d * 4 + 3][2 * h2 + x])
+              for (int e = 0; e < 2; ++e) {
+                const float (*o)[4] = &O[nt0 + k][d * 2];
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(place(d, warp, k, e)),
+                             "f"(o[0][e]), "f"(o[0][2 + e]), "f"(o[1][e]), "f"(o[1][2 + e])
                              : "memory");
               }
           }
         named_sync(1, kConsumers);
         if (warp >= NB) continue;
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const int row = grp + 8 * h2, urow = mt * 16 + row;
-          float v[8];
+        for (int k = 0; k < X && nt0 + k < NT; ++k)
 #pragma unroll
-          for (int s = 0; s < kWarps; ++s)
+          for (int e = 0; e < 2; ++e) {
+            const int nt = nt0 + k, row = nt * 8 + 2 * tig + e;
+            float v[4] = {};
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int s = 0; s < kWarps; ++s) {
               float4 f;
               if (s == warp) {
 #pragma unroll
                 for (int d = 0; d < NB; ++d)
                   if (d == warp)
-                    f = make_float4(O[mt][d * 4][2 * h2 + x], O[mt][d * 4 + 1][2 * h2 + x],
-                                    O[mt][d * 4 + 2][2 * h2 + x], O[mt][d * 4 + 3][2 * h2 + x]);
+                    f = make_float4(O[nt][d * 2][e], O[nt][d * 2][2 + e], O[nt][d * 2 + 1][e],
+                                    O[nt][d * 2 + 1][2 + e]);
               } else {
-                const uint32_t from = xbase + (warp * 3 + (s < warp ? s : s - 1)) * 2048;
-                const uint4 w = lds128(from + row * 128 + (((2 * tig + x) ^ (row & 7)) << 4));
+                const uint4 w = lds128(place(warp, s, k, e));
                 f = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
                                 __uint_as_float(w.w));
               }
-              if (s == 0) {
-                v[4 * x] = f.x; v[4 * x + 1] = f.y; v[4 * x + 2] = f.z; v[4 * x + 3] = f.w;
-              } else {
-                v[4 * x] += f.x; v[4 * x + 1] += f.y; v[4 * x + 2] += f.z; v[4 * x + 3] += f.w;
-              }
+              v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
             }
-          if (urow >= rows) continue;
-          const float4 l4 = *reinterpret_cast<const float4*>(stat_l + urow * 4);
-          const float l = (l4.x + l4.y) + (l4.z + l4.w);
-          const int t = urow / p.G, hq = g * p.G + (urow - t * p.G);
-          const int col = warp * 32 + 8 * tig;
-          if (dst < 0 && !p.own) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __half2 h = __floats2half2_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
-              w[k] = *reinterpret_cast<const uint32_t*>(&h);
+            if (row >= rows) continue;
+            const float4 l4 = *reinterpret_cast<const float4*>(stat_l + row * 4);
+            const float l = (l4.x + l4.y) + (l4.z + l4.w);
+            const int t = row / p.G, hq = g * p.G + (row - t * p.G);
+            const int col = warp * 32 + 4 * grp;
+            if (dst < 0 && !p.own) {
+              const float inv = l > 0.f ? 1.f / l : 0.f;
+              const __half2 h0 = __floats2half2_rn(v[0] * inv, v[1] * inv);
+              const __half2 h1 = __floats2half2_rn(v[2] * inv, v[3] * inv);
+              *reinterpret_cast<uint2*>(p.out + (int64_t)(r0 + t) * p.out_stride + (int64_t)hq * D + col) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+            } else {
+              const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
+                                         : ((int64_t)cta * 2 + dst) * p.slot_rows + row;
+              *reinterpret_cast<float4*>((dst < 0 ? p.own : p.part) + at * D + col) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+              if (warp == 0 && grp == 0)
+                (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(M[nt][e], l);
             }
-            *reinterpret_cast<uint4*>(p.out + (int64_t)(r0 + t) * p.out_stride + (int64_t)hq * D + col) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          } else {
-            const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
-                                       : ((int64_t)cta * 2 + dst) * p.slot_rows + urow;
-            float4* o = reinterpret_cast<float4*>((dst < 0 ? p.own : p.part) + at * D + col);
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
-            if (warp == 0 && tig == 0)
-              (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(M[mt][h2], l);
           }
-        }
       }
       continue;
     }
@@ -678,43 +712,46 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <int D, int MT>
+template <int D, int NT>
 cudaError_t launch_few(const PagedFew8Params& p, cudaStream_t s, bool pdl) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.a.nc);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = FSmem<D, MT>::kBytes;
+  cfg.dynamicSmemBytes = FSmem<D, NT>::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_few_kv8_kernel<D, MT>, p);
+  return cudaLaunchKernelEx(&cfg, paged_few_kv8_kernel<D, NT>, p);
 }
 
-template <int D, int MT>
+template <int D, int NT>
 cudaError_t configure_one() {
-  return cudaFuncSetAttribute(paged_few_kv8_kernel<D, MT>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FSmem<D, MT>::kBytes);
+  return cudaFuncSetAttribute(paged_few_kv8_kernel<D, NT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FSmem<D, NT>::kBytes);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_few_kv8(const PagedFew8Params& p, cudaStream_t s, bool pdl) {
   if (p.a.max_new * p.a.G > p.a.slot_rows || p.a.nc < 1 || p.a.nc > 512) return cudaErrorInvalidValue;
-  const int mt = p.a.slot_rows / 16;
-  if (p.a.D == 128) return mt == 1 ? launch_few<128, 1>(p, s, pdl) : launch_few<128, 2>(p, s, pdl);
-  if (p.a.D == 64) return mt == 1 ? launch_few<64, 1>(p, s, pdl) : launch_few<64, 2>(p, s, pdl);
-  return cudaErrorInvalidValue;
+  const int tiles = (int)((p.a.max_new * p.a.G + 7) / 8) - 1;      // of eight rows
+  using F = cudaError_t (*)(const PagedFew8Params&, cudaStream_t, bool);
+  constexpr F f[2][4] = {{launch_few<64, 1>, launch_few<64, 2>, launch_few<64, 3>, launch_few<64, 4>},
+                         {launch_few<128, 1>, launch_few<128, 2>, launch_few<128, 3>, launch_few<128, 4>}};
+  if ((p.a.D != 64 && p.a.D != 128) || tiles < 0 || tiles > 3) return cudaErrorInvalidValue;
+  return f[p.a.D == 128][tiles](p, s, pdl);
 }
 
 cudaError_t configure_paged_few_kv8() {
-  cudaError_t e = configure_one<128, 1>();
-  if (e == cudaSuccess) e = configure_one<128, 2>();
-  if (e == cudaSuccess) e = configure_one<64, 1>();
-  if (e == cudaSuccess) e = configure_one<64, 2>();
-  return e;
+  for (auto f : {configure_one<64, 1>, configure_one<64, 2>, configure_one<64, 3>, configure_one<64, 4>,
+                 configure_one<128, 1>, configure_one<128, 2>, configure_one<128, 3>, configure_one<128, 4>}) {
+    const cudaError_t e = f();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace blk
