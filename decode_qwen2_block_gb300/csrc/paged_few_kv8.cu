@@ -12,12 +12,12 @@
 //              that rows come in eights), the warp's own running maximum and sum, O' = V' P'
 //              of all columns.  Nothing is exchanged between warps until the unit ends,
 //              so a warp waits for no other while tiles come.
-// A lane's codes are wide loads because the MMA's inner index may run over the columns in
+// A lane's K codes are wide loads because the MMA's inner index may run over the columns in
 // any order if q's does too: lane (grp, tig) takes 16-byte pieces tig (and tig + 4) of its
 // slot's row, whose j-th four codes are inner indexes 2 tig, 2 tig + 1, 2 tig + 8,
-// 2 tig + 9 of product j.  For V the inner index is the slot and the lane's four are
-// words of four columns each; two permutes a pair of words bring equal columns together.
-// Slots are dealt to the scores' rows so that neither read meets bank conflicts.
+// 2 tig + 9 of product j.  V's codes come transposed (ldmatrix of 16 x 16 bytes): four slots
+// of a column a word.  Slots are dealt to the scores' rows so that neither read meets bank
+// conflicts.
 // A slot that no row sees has its V scale taken as 0, so its codes count for nothing.
 #include <math.h>
 
@@ -55,18 +55,23 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-// The scales of a slot: D / 32 bytes.
-template <int NB>
-__device__ __forceinline__ uint32_t lds_scales(uint32_t addr) {
-  if constexpr (NB == 4) return lds32(addr);
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
   return v;
+}
+// Two matrices of 16 x 16 bytes, transposed: lanes 0 - 15 point to the first one's rows, 16 -
+// 31 to the second's; lane (grp, tig) gets rows 4 tig .. + 3 of columns grp, 8 + grp of each.
+__device__ __forceinline__ void ldsm_bytes_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 // Codes of a page: (0, y, z), all columns of some slots.
 __device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, int y, int z,
@@ -90,28 +95,27 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {    // an 8 x 8 matr
   return d;
 }
 
-// Two codes' factors, from the fp16 bits of their two scales.  1024 + code times s / 64 less
-// 18 s is (code - 128) s / 64, exact as one fused operation while 18 s is an fp16 number: up to
-// s = 3584.  Larger scales (kBig) subtract first.
+// Two codes' factors, from the fp16 bits of their two scales.  A code u in the low bits of
+// 0x4c00 is 16 + u / 64; times s less 18 s that is (u - 128) s / 64, exact as one fused
+// operation while 18 s is an fp16 number: up to s = 3584.  Larger scales (kBig) subtract first.
 template <bool kBig>
 struct Unit {
   __half2 mul, add;
   __device__ __forceinline__ explicit Unit(uint32_t bits) {
-    const __half2 s = *reinterpret_cast<const __half2*>(&bits);
-    mul = __hmul2(s, __float2half2_rn(1.f / 64.f));
-    add = kBig ? __float2half2_rn(-1152.f) : __hmul2(s, __float2half2_rn(-18.f));
+    mul = *reinterpret_cast<const __half2*>(&bits);
+    add = kBig ? __float2half2_rn(-18.f) : __hmul2(mul, __float2half2_rn(-18.f));
   }
   // the codes that `sel` places, from w
   __device__ __forceinline__ uint32_t operator()(uint32_t w, uint32_t sel) const {
-    const uint32_t b = __byte_perm(w, 0x64646464u, sel);
+    const uint32_t b = __byte_perm(w, 0x4c4c4c4cu, sel);
     const __half2 x = *reinterpret_cast<const __half2*>(&b);
     const __half2 y = kBig ? __hmul2(__hadd2(x, add), mul) : __hfma2(x, mul, add);
     return *reinterpret_cast<const uint32_t*>(&y);
   }
 };
 // Whether one of four scale bytes is above 3584's, 0x6b (NaN's is).
-__device__ __forceinline__ uint32_t big_scales(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x14141414u) & 0x80808080u;
+__device__ __forceinline__ uint32_t big_scales(uint32_t w) {      // (bit 7 of a byte says so)
+  return (w & 0x7f7f7f7fu) + 0x14141414u;
 }
 
 struct TileInfo {      // what the consumers need of a tile
@@ -133,8 +137,8 @@ struct FSmem {
   static constexpr int kQBytes = 8 * NT * kQStride;
   static constexpr bool kQRegs = NT == 1;                       // else q is re-read for every tile
   static constexpr int kQBufs = kQRegs ? 1 : 2;
-  static constexpr int kXTiles = NT < 2 ? 1 : 2;                // row tiles that go out at a time
-  static constexpr int kXBytes = kXTiles * 3 * NB * 8 * 32 * 4; // a unit's end: O on its way
+  static constexpr int kXTiles = NT == 2 ? 2 : 1;               // row tiles that go out at a time
+  static constexpr int kXBytes = kXTiles * kWarps * NB * 1024;  // a unit's end: O on its way
   static constexpr int kScOff = kStages * 2 * kKV;
   static constexpr int kQOff = kScOff + kStages * 2 * kSc;
   static constexpr int kXOff = kQOff + kQBufs * kQBytes;
@@ -395,25 +399,33 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int grp = lane >> 2, tig = lane & 3;
   const int slab = warp * 16;
   const float sl2 = p.scale_log2;
-  // The slot (of 8) behind row c of a score tile.  With rows of 128 bytes and the
-  // 128-byte swizzle rows 0 - 3 and 4 - 7 have a piece in different halves, so rows
-  // 2 i, 2 i + 1 are slots i, i + 4; rows of 64 bytes alternate by themselves.
-  auto slot_of = [](int c) { return D == 128 ? (c >> 1) | ((c & 1) << 2) : c; };
-  auto row_sw = [](int r) { return D == 128 ? r & 7 : (r >> 1) & 3; };
-  const int kr = slab + slot_of(grp);                 // the lane's K slots: kr, kr + 8
-  const uint32_t k_off = kr * D + ((tig ^ row_sw(kr)) << 4);      // (^ 64: piece tig + 4)
-  const int se = slab + slot_of(2 * tig), so = slab + slot_of(2 * tig + 1);   // V's, and + 8
-  // lanes of odd tig read the odd slot first: their rows' pieces then lie elsewhere
-  const int r_a = tig & 1 ? so : se, r_b = tig & 1 ? se : so;
-  const uint32_t va_off = r_a * D + ((((grp >> 2) ^ row_sw(r_a))) << 4) + (grp & 3) * 4;
-  const uint32_t vb_off = r_b * D + ((((grp >> 2) ^ row_sw(r_b))) << 4) + (grp & 3) * 4;
-  const uint32_t sel_lo = tig & 1 ? 0x1504 : 0x5140, sel_hi = tig & 1 ? 0x3726 : 0x7362;
+  // The slot (of 16) behind row c of score tile t.  Equal pieces of rows 2 i, 2 i + 1 of a
+  // tile lie in different halves of the banks (K's loads: the swizzle parts rows 0 - 3 from
+  // 4 - 7 where a row has 128 bytes, even from odd ones where it has 64), and rows 4 i ..
+  // 4 i + 3 of both tiles are eight rows of different places (V's).
+  auto slot_of = [](int t, int c) {
+    return D == 128 ? 8 * (c >> 2) + 2 * ((c >> 1) & 1) + 4 * (c & 1) + t
+                    : 8 * (c >> 2) + 4 * ((c >> 1) & 1) + (c & 1) + 2 * t;
+  };
+  auto piece_at = [](int r, int c) {                  // piece c of row r of a tile's codes
+    return r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+  };
+  constexpr int kT1 = D == 128 ? 1 : 2;               // from tile 0's slot to tile 1's
+  const int kr = slab + slot_of(0, grp);              // the lane's K slots: kr, kr + kT1
+  const uint32_t k_off0 = piece_at(kr, tig), k_off1 = piece_at(kr + kT1, tig);   // (^ 64: piece tig + 4)
+  // V: inner indexes 2 tig, 2 tig + 1 of tile 0 are slots ve, ve + vo; of tile 1 kT1 further.
+  // The matrix row that the lane points to, and which of a pair of pieces.
+  const int ve = slab + slot_of(0, 2 * tig);
+  constexpr int vo = D == 128 ? 4 : 1;
+  const int vr = slab + slot_of((lane >> 1) & 1, 2 * ((lane >> 2) & 3) + (lane & 1));
+  const uint32_t v_off = piece_at(vr, lane >> 4);     // (^ 32 g: pieces 2 g, 2 g + 1)
   // a K piece's block of 32 columns, as a permute that doubles its scale's byte to fp16
   const uint32_t kb = tig >> 1, sel_k0 = kb << 12 | 4 << 8 | kb << 4 | 4, sel_k1 = sel_k0 + 0x2020;
   const uint32_t q_lane = qbase + grp * Sm::kQStride + tig * 32;
-  // The lane's rows: 8 nt + 2 tig + e.  m_r: what their exponents are taken against (log2
-  // units, less kWeightLog2 but where weight_plain), lim: where that has to follow.
-  float m_r[NT][2], lim[NT][2], l_r[NT][2], O[NT][NB * 2][4];
+  // The lane's rows: 8 nt + 2 tig + e.  nref: less what their exponents are taken against (log2
+  // units, less kWeightLog2 but where weight_plain), lim: where that has to follow (-inf:
+  // nothing seen yet).  O: columns 16 i + grp and + 8 of either row.
+  float nref[NT][2], lim[NT][2], l_r[NT][2], O[NT][NB * 2][4];
   int last[NT][2], low[NT][2];
   uint32_t qf[Sm::kQRegs ? D / 16 : 1][2];
   // q's fragments of products 2 x, 2 x + 1 (x < D / 32) of row tile nt
@@ -448,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int e = 0; e < 2; ++e) {
           last[nt][e] = L + min((nt * 8 + 2 * tig + e) / p.G, n - 1);
           low[nt][e] = paged_window(p, last[nt][e]);
-          m_r[nt][e] = lim[nt][e] = -INFINITY;
-          l_r[nt][e] = 0.f;
+          nref[nt][e] = l_r[nt][e] = 0.f;
+          lim[nt][e] = -INFINITY;
         }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -473,40 +485,64 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < kSums; ++k) sc[nt][k][0] = sc[nt][k][1] = sc[nt][k][2] = sc[nt][k][3] = 0.f;
-      {
-        const uint32_t w0 = lds_scales<NB>(ks + kr * NB), w1 = lds_scales<NB>(ks + (kr + 8) * NB);
-        auto scores = [&](auto big) {
+      // the scales: K's of the lane's two slots, V's of its four (sw[tile][even, odd])
+      uint32_t kw[2], sw[2][2];
+      if constexpr (D == 128) {
+        const uint2 k2 = lds64(ks + kr * NB), e2 = lds64(vs + ve * NB), o2 = lds64(vs + (ve + vo) * NB);
+        kw[0] = k2.x; kw[1] = k2.y;
+        sw[0][0] = e2.x; sw[1][0] = e2.y;
+        sw[0][1] = o2.x; sw[1][1] = o2.y;
+      } else {
+        const uint2 v4 = lds64(vs + ve * NB);         // (one behind the other)
+        kw[0] = lds16(ks + kr * NB);
+        kw[1] = lds16(ks + (kr + kT1) * NB);
+        sw[0][0] = v4.x & 0xffffu; sw[0][1] = v4.x >> 16;
+        sw[1][0] = v4.y & 0xffffu; sw[1][1] = v4.y >> 16;
+      }
+      if (slab < vlo || slab + 16 > vhi) {
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            const uint4 c0 = lds128(kt + (k_off ^ (h << 6))), c1 = lds128(kt + (k_off ^ (h << 6)) + 8 * D);
-            const uint32_t cw[2][4] = {{c0.x, c0.y, c0.z, c0.w}, {c1.x, c1.y, c1.z, c1.w}};
-            const uint32_t sel = h ? sel_k1 : sel_k0;
-            const Unit<decltype(big)::value> u0(__byte_perm(w0, 0, sel)), u1(__byte_perm(w1, 0, sel));
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t qv[NT][2][2];
-              if constexpr (!Sm::kQRegs) {
+          for (int o = 0; o < 2; ++o) {
+            const int c = ve + t * kT1 + o * vo;
+            if (c < vlo || c >= vhi) sw[t][o] = 0;
+          }
+      }
+      const bool any_big =
+          __any_sync(0xffffffffu, ((big_scales(kw[0]) | big_scales(kw[1]) | big_scales(sw[0][0]) |
+                                    big_scales(sw[0][1]) | big_scales(sw[1][0]) | big_scales(sw[1][1])) &
+                                   0x80808080u) != 0);
+      auto scores = [&](auto big) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) load_q(qb, nt, 2 * h + x, qv[nt][0], qv[nt][1]);
-              }
+        for (int h = 0; h < D / 64; ++h) {
+          const uint4 c0 = lds128(kt + (k_off0 ^ (h << 6))), c1 = lds128(kt + (k_off1 ^ (h << 6)));
+          const uint32_t cw[2][4] = {{c0.x, c0.y, c0.z, c0.w}, {c1.x, c1.y, c1.z, c1.w}};
+          const uint32_t sel = h ? sel_k1 : sel_k0;
+          const Unit<decltype(big)::value> u0(__byte_perm(kw[0], 0, sel)), u1(__byte_perm(kw[1], 0, sel));
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t a[4] = {u0(cw[0][2 * x + y], 0x4140), u1(cw[1][2 * x + y], 0x4140),
-                                       u0(cw[0][2 * x + y], 0x4342), u1(cw[1][2 * x + y], 0x4342)};
-                if constexpr (Sm::kQRegs) {
-                  const uint32_t* b = qf[4 * h + 2 * x + y];
-                  mma16816(sc[0][y % kSums], a, b[0], b[1]);
-                } else {
+          for (int x = 0; x < 2; ++x) {
+            [[maybe_unused]] uint32_t qv[Sm::kQRegs ? 1 : NT][2][2];
+            if constexpr (!Sm::kQRegs) {
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt][0], a, qv[nt][y][0], qv[nt][y][1]);
-                }
+              for (int nt = 0; nt < NT; ++nt) load_q(qb, nt, 2 * h + x, qv[nt][0], qv[nt][1]);
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t a[4] = {u0(cw[0][2 * x + y], 0x4140), u1(cw[1][2 * x + y], 0x4140),
+                                     u0(cw[0][2 * x + y], 0x4342), u1(cw[1][2 * x + y], 0x4342)};
+              if constexpr (Sm::kQRegs) {
+                const uint32_t* b = qf[4 * h + 2 * x + y];
+                mma16816(sc[0][y % kSums], a, b[0], b[1]);
+              } else {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt][0], a, qv[nt][y][0], qv[nt][y][1]);
               }
             }
           }
-        };
-        if (__any_sync(0xffffffffu, (big_scales(w0) | big_scales(w1)) != 0)) scores(std::true_type());
-        else scores(std::false_type());
-      }
+        }
+      };
+      if (any_big) scores(std::true_type());
+      else scores(std::false_type());
       if constexpr (kSums == 2) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) sc[0][0][k] += sc[0][1][k];
@@ -516,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int c = kr + 8 * (k >> 1), slot = slot0 + c;
+            const int c = kr + kT1 * (k >> 1), slot = slot0 + c;
             if (!(c >= vlo && slot <= last[nt][k & 1] && slot >= low[nt][k & 1])) sc[nt][0][k] = -INFINITY;
           }
       }
@@ -537,8 +573,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float t = fmaf(x, sl2, -kWeightLog2);
             if (t > lim[nt][e]) {         // (alike in the row's lanes)
               const bool plain = weight_plain(t);
-              const float mn = plain ? t + kWeightLog2 : t, f = ex2(m_r[nt][e] - mn);
-              m_r[nt][e] = mn;
+              const float mn = plain ? t + kWeightLog2 : t;
+              const float f = lim[nt][e] == -INFINITY ? 0.f : ex2(-nref[nt][e] - mn);
+              nref[nt][e] = -mn;
               lim[nt][e] = mn + (plain ? kRescaleLog2 - kWeightLog2 : kRescaleLog2);
               l_r[nt][e] *= f;
 #pragma unroll
@@ -554,10 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int nt = 0; nt < NT; ++nt) {
         float w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float m = m_r[nt][k & 1];
-          w[k] = ex2(fmaf(sc[nt][0][k], sl2, m == -INFINITY ? 0.f : -m));      // 2^-inf = 0
-        }
+        for (int k = 0; k < 4; ++k) w[k] = ex2(fmaf(sc[nt][0][k], sl2, nref[nt][k & 1]));   // 2^-inf = 0
         l_r[nt][0] += w[0] + w[2];
         l_r[nt][1] += w[1] + w[3];
 #pragma unroll
@@ -567,41 +601,24 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       // O' += V' P'
-      uint32_t sw[2][2], any_big = 0;      // scales of the even and the odd slot, + 8 x
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        sw[x][0] = lds_scales<NB>(vs + (se + 8 * x) * NB);
-        sw[x][1] = lds_scales<NB>(vs + (so + 8 * x) * NB);
-        if (slab < vlo || slab + 16 > vhi) {
-          if (se + 8 * x < vlo || se + 8 * x >= vhi) sw[x][0] = 0;
-          if (so + 8 * x < vlo || so + 8 * x >= vhi) sw[x][1] = 0;
-        }
-        any_big |= big_scales(sw[x][0]) | big_scales(sw[x][1]);
-      }
       auto values = [&](auto big) {
 #pragma unroll
         for (int g = 0; g < NB; ++g) {
-          uint32_t lo2[2], hi2[2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t a = lds32(vt + (va_off ^ (g << 5)) + x * 8 * D);
-            const uint32_t b = lds32(vt + (vb_off ^ (g << 5)) + x * 8 * D);
-            lo2[x] = __byte_perm(a, b, sel_lo);      // columns 0, 1: even and odd slot's codes
-            hi2[x] = __byte_perm(a, b, sel_hi);      // columns 2, 3
-          }
+          uint32_t v[4];
+          ldsm_bytes_t(vt + (v_off ^ (g << 5)), v);
           const uint32_t sel = (4 + g) << 12 | g << 4;
           const Unit<decltype(big)::value> u0(__byte_perm(sw[0][0], sw[0][1], sel) & 0xff00ff00u),
               u1(__byte_perm(sw[1][0], sw[1][1], sel) & 0xff00ff00u);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {              // columns 2 j, 2 j + 1
-            const uint32_t v0 = j ? hi2[0] : lo2[0], v1 = j ? hi2[1] : lo2[1];
-            const uint32_t a[4] = {u0(v0, 0x4140), u0(v0, 0x4342), u1(v1, 0x4140), u1(v1, 0x4342)};
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a[4] = {u0(v[2 * j], 0x4140), u0(v[2 * j + 1], 0x4140), u1(v[2 * j], 0x4342),
+                                   u1(v[2 * j + 1], 0x4342)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816(O[nt][g * 2 + j], a, pb[nt][0], pb[nt][1]);
           }
         }
       };
-      if (__any_sync(0xffffffffu, any_big != 0)) values(std::true_type());
+      if (any_big) values(std::true_type());
       else values(std::false_type());
     }
     if (flags & 2) {
@@ -612,22 +629,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) mbar_arrive(&empty[st]);
       if (!Sm::kQRegs && lane == 0) mbar_arrive(&q_empty[seg % Sm::kQBufs]);
       ++seg;
+      float m_r[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e) {
+          m_r[nt][e] = lim[nt][e] == -INFINITY ? -INFINITY : -nref[nt][e];
           if (grp == 0) stat_m[(nt * 8 + 2 * tig + e) * 4 + warp] = m_r[nt][e];
+        }
       named_sync(1, kConsumers);
       if (*(volatile int*)&abort_s) return;       // (set before a warp's arrival, see above)
-      float M[NT][2];
+      auto max_of = [&](int row) {
+        const float4 m4 = *reinterpret_cast<const float4*>(stat_m + row * 4);
+        return fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+      };
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = nt * 8 + 2 * tig + e;
-          const float4 m4 = *reinterpret_cast<const float4*>(stat_m + row * 4);
-          M[nt][e] = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-          const float f = m_r[nt][e] == -INFINITY ? 0.f : ex2(m_r[nt][e] - M[nt][e]);
+          const float f = m_r[nt][e] == -INFINITY ? 0.f : ex2(m_r[nt][e] - max_of(row));
           float l = l_r[nt][e] * f;
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -638,72 +659,69 @@ __global__ void __launch_bounds__(kThreads, 2)
             O[nt][i][2 + e] *= f;
           }
         }
+      // O's way: [block of 32 columns][warp][row of the tile][32 columns], eight columns
+      // moved by the row's pair and four by its parity (no bank conflicts on either side)
       constexpr int X = Sm::kXTiles;
 #pragma unroll
       for (int nt0 = 0; nt0 < NT; nt0 += X) {
         if (nt0 > 0) named_sync(1, kConsumers);    // the row tiles before are read
-        // a lane's O of a column block: columns 4 grp .. + 3 of rows 2 tig and 2 tig + 1
-        auto place = [&](int d, int s, int k, int e) {      // of warp s for warp d
-          const int row = 2 * tig + e;
-          return xbase + ((d * 3 + (s < d ? s : s - 1)) * X + k) * 1024 + row * 128 + ((grp ^ (tig << 1)) << 4);
-        };
 #pragma unroll
-        for (int d = 0; d < NB; ++d)
-          if (d != warp) {
+        for (int k = 0; k < X; ++k)
 #pragma unroll
-            for (int k = 0; k < X && nt0 + k < NT; ++k)
+          for (int d = 0; d < NB; ++d)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float (*o)[4] = &O[nt0 + k][d * 2];
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(place(d, warp, k, e)),
-                             "f"(o[0][e]), "f"(o[0][2 + e]), "f"(o[1][e]), "f"(o[1][2 + e])
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)          // column 8 x + grp of block d
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                                 xbase + ((d * kWarps + warp) * X + k) * 1024 + (2 * tig + e) * 128 +
+                                 ((x ^ tig) << 5) + ((grp ^ (4 * e)) << 2)),
+                             "f"(O[nt0 + k][d * 2 + (x >> 1)][2 * (x & 1) + e])
                              : "memory");
-              }
-          }
         named_sync(1, kConsumers);
         if (warp >= NB) continue;
 #pragma unroll
-        for (int k = 0; k < X && nt0 + k < NT; ++k)
+        for (int k = 0; k < X; ++k) {
+          // row lane / 4, columns 8 (lane % 4) .. + 7
+          const int r8 = lane >> 2, row = (nt0 + k) * 8 + r8;
+          const uint32_t from = xbase + (warp * kWarps * X + k) * 1024 + r8 * 128 +
+                                (((lane & 3) ^ (r8 >> 1)) << 5);
+          float v[8] = {};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int nt = nt0 + k, row = nt * 8 + 2 * tig + e;
-            float v[4] = {};
+          for (int s = 0; s < kWarps; ++s)
 #pragma unroll
-            for (int s = 0; s < kWarps; ++s) {
-              float4 f;
-              if (s == warp) {
-#pragma unroll
-                for (int d = 0; d < NB; ++d)
-                  if (d == warp)
-                    f = make_float4(O[nt][d * 2][e], O[nt][d * 2][2 + e], O[nt][d * 2 + 1][e],
-                                    O[nt][d * 2 + 1][2 + e]);
-              } else {
-                const uint4 w = lds128(place(warp, s, k, e));
-                f = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
-                                __uint_as_float(w.w));
-              }
-              v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+            for (int x = 0; x < 2; ++x) {
+              const uint4 w = lds128(from + s * X * 1024 + ((x ^ (r8 & 1)) << 4));
+              v[4 * x] += __uint_as_float(w.x);
+              v[4 * x + 1] += __uint_as_float(w.y);
+              v[4 * x + 2] += __uint_as_float(w.z);
+              v[4 * x + 3] += __uint_as_float(w.w);
             }
-            if (row >= rows) continue;
-            const float4 l4 = *reinterpret_cast<const float4*>(stat_l + row * 4);
-            const float l = (l4.x + l4.y) + (l4.z + l4.w);
-            const int t = row / p.G, hq = g * p.G + (row - t * p.G);
-            const int col = warp * 32 + 4 * grp;
-            if (dst < 0 && !p.own) {
-              const float inv = l > 0.f ? 1.f / l : 0.f;
-              const __half2 h0 = __floats2half2_rn(v[0] * inv, v[1] * inv);
-              const __half2 h1 = __floats2half2_rn(v[2] * inv, v[3] * inv);
-              *reinterpret_cast<uint2*>(p.out + (int64_t)(r0 + t) * p.out_stride + (int64_t)hq * D + col) =
-                  make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-            } else {
-              const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
-                                         : ((int64_t)cta * 2 + dst) * p.slot_rows + row;
-              *reinterpret_cast<float4*>((dst < 0 ? p.own : p.part) + at * D + col) =
-                  make_float4(v[0], v[1], v[2], v[3]);
-              if (warp == 0 && grp == 0)
-                (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(M[nt][e], l);
+          if (row >= rows) continue;
+          const float4 l4 = *reinterpret_cast<const float4*>(stat_l + row * 4);
+          const float l = (l4.x + l4.y) + (l4.z + l4.w);
+          const int t = row / p.G, hq = g * p.G + (row - t * p.G);
+          const int col = warp * 32 + 8 * (lane & 3);
+          if (dst < 0 && !p.own) {
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            uint32_t w[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const __half2 h = __floats2half2_rn(v[2 * c] * inv, v[2 * c + 1] * inv);
+              w[c] = *reinterpret_cast<const uint32_t*>(&h);
             }
+            *reinterpret_cast<uint4*>(p.out + (int64_t)(r0 + t) * p.out_stride + (int64_t)hq * D + col) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+            const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
+                                       : ((int64_t)cta * 2 + dst) * p.slot_rows + row;
+            float4* o = reinterpret_cast<float4*>((dst < 0 ? p.own : p.part) + at * D + col);
+            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+            if (warp == 0 && (lane & 3) == 0)
+              (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(max_of(row), l);
           }
+        }
       }
       continue;
     }
