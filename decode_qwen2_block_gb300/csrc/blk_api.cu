@@ -1319,7 +1319,7 @@ PagedWs paged_ws(const blk_config& c, int64_t N, bool prefix, int num_sms) {
   size_t o = 0;
   w.part = o; o = align_up(o + rows * D * 4);
   w.ml = o; o = align_up(o + rows * 8);
-  w.cut = o; o = align_up(o + (size_t)2 * num_sms * sizeof(PagedPiece));
+  w.cut = o; o = align_up(o + (size_t)3 * num_sms * sizeof(PagedPiece));
   w.own = w.own_ml = w.info = w.ppart = w.pml = w.pown = w.pown_ml = o;
   if (prefix) {
     w.own = o; o = align_up(o + (size_t)N * Hq * D * 4);
@@ -1462,7 +1462,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   if (few) {
     a.tm_k = few_k;
     a.tm_v = few_v;
-    paged_few_slots(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
+    (pool.ks ? paged_few_kv8_slots : paged_few_slots)(h->num_sms, G, b->max_new, &a.nc, &a.slot_rows);
     a.upb = units_each();
     a.early = early && !prefix;
     if (pool.ks) {

@@ -59,6 +59,7 @@ struct PagedFew8Params {
   PagedAttnParams a;           // tm_k, tm_v: codes, boxes of all columns of one page's slots (at most 64)
   const uint8_t *ks, *vs;      // scales
 };
+void paged_few_kv8_slots(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows);
 cudaError_t launch_paged_few_kv8(const PagedFew8Params& p, cudaStream_t s, bool pdl);
 cudaError_t configure_paged_few_kv8();
 

@@ -132,22 +132,25 @@ struct FSmem {
   static constexpr int NB = D / kKv8Block;
   static constexpr int kKV = kTile * D;                         // K or V codes of a tile
   static constexpr int kSc = kTile * NB;                        // their scales
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  // More warps than two CTAs' hide more of a slab's chain of loads, products and exponentials:
+  // three, while O's registers leave room (65536 / 16 warps).
+  static constexpr int kCtas = NT <= 2 ? 3 : 2;
   static constexpr int kQStride = D * 2 + 16;                   // bytes (conflict-free reads)
   static constexpr int kQBytes = 8 * NT * kQStride;
   static constexpr bool kQRegs = NT == 1;                       // else q is re-read for every tile
   static constexpr int kQBufs = kQRegs ? 1 : 2;
-  static constexpr int kXTiles = NT == 2 ? 2 : 1;               // row tiles that go out at a time
-  static constexpr int kXBytes = kXTiles * kWarps * NB * 1024;  // a unit's end: O on its way
+  static constexpr int kStage = 2 * (kKV + kSc);
+  static constexpr int kStages =
+      (233472 / kCtas - 1024 - 2304 - 1024 - 1024 - kQBufs * kQBytes) / kStage;
   static constexpr int kScOff = kStages * 2 * kKV;
   static constexpr int kQOff = kScOff + kStages * 2 * kSc;
-  static constexpr int kXOff = kQOff + kQBufs * kQBytes;
-  static constexpr int kStatOff = kXOff + kXBytes;              // [8 NT][4 warps] maxima, then sums
+  static constexpr int kStatOff = kQOff + kQBufs * kQBytes;     // [8 NT][4 warps] maxima, then sums
   static constexpr int kInfoOff = kStatOff + 2 * 4 * 8 * NT * 4;
   static constexpr int kBarOff = (kInfoOff + kStages * (int)sizeof(TileInfo) + 15) / 16 * 16;
   static constexpr int kEnd = kBarOff + (2 * kStages + kQBufs) * 8 + 64;
   static constexpr size_t kBytes = (size_t)kEnd + 1024;         // the ring is 1024-aligned
-  static_assert(kBytes + 3072 <= 233472 / 2, "two CTAs per SM");   // (1 KB the system's, statics)
+  static_assert(kStages >= 3 && kWarps * NB * 1024 <= 2 * kKV, "O goes through a tile's place");
+  static_assert(kBytes + 3328 <= 233472 / kCtas, "shared memory");   // (1 KB the system's, statics)
 };
 
 __device__ __forceinline__ int seq_tiles(const PagedAttnParams& p, const PagedSeq& s) {
@@ -159,7 +162,7 @@ __device__ __forceinline__ int seq_weight(const PagedAttnParams& p, const PagedS
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
     paged_few_kv8_kernel(const __grid_constant__ PagedFew8Params q8) {
   using Sm = FSmem<D, NT>;
   constexpr int S = Sm::kStages, NB = Sm::NB;
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_u32(smem), sring = smem_u32(smem + Sm::kScOff),
-                 qbase = smem_u32(smem + Sm::kQOff), xbase = smem_u32(smem + Sm::kXOff);
+                 qbase = smem_u32(smem + Sm::kQOff);
   float* stat_m = reinterpret_cast<float*>(smem + Sm::kStatOff);
   float* stat_l = stat_m + 4 * 8 * NT;
   volatile TileInfo* infos = reinterpret_cast<volatile TileInfo*>(smem + Sm::kInfoOff);
@@ -273,6 +276,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         waited = true;
       }
     };
+    // Page ids come 32 table entries at a time, a lane each, the next 32 and the next
+    // sequence's first ahead of their use: a tile is a few hundred clocks of work, as long
+    // as one of these loads takes.
+    auto entries = [&](int b, int lo, int hi, int base) -> int {
+      const int e = base + lane;
+      if (b >= p.B || e < lo >> p.page_lg || e > (hi - 1) >> p.page_lg) return -1;
+      return (e < (int)(p.pre_here >> p.page_lg) ? p.prefix_pages : p.table + (int64_t)b * p.max_blocks)[e];
+    };
+    int ids = -1, ids_next = -1, ids_seq = -1, seq_ahead = -1;      // the last: whose ids_seq are
     PagedPiece cut = {-1, 0, 0, 0, 0};
     while (lin < t1 && ok) {
       if (b >= p.B) {        // the next kv head begins again with the first sequence
@@ -318,15 +330,31 @@ __global__ void __launch_bounds__(kThreads, 2)
                 make_int4(whole ? -1 : cta, c1, 0, t * p.G);
       }
       const int lo = paged_lo(p, s.L), hi = s.L + s.n, j0 = lo / kTile;
-      const int32_t* row = p.table + (int64_t)b * p.max_blocks;
+      int base = (((j0 + xa) * kTile) >> p.page_lg) & ~31;
+      ids = seq_ahead == b && xa == 0 ? ids_seq : entries(b, lo, hi, base);
+      ids_next = entries(b, lo, hi, base + 32);
+      seq_ahead = -1;
+      if (((b + 1) & ~31) == base32) {       // (its lengths are here)
+        const int n2 = __shfl_sync(0xffffffffu, mys.n, (b + 1) & 31);
+        const int L2 = __shfl_sync(0xffffffffu, mys.L, (b + 1) & 31);
+        if (n2 > 0 && lin < t1) {
+          const int lo2 = paged_lo(p, L2);
+          ids_seq = entries(b + 1, lo2, L2 + n2, ((lo2 / kTile * kTile) >> p.page_lg) & ~31);
+          seq_ahead = b + 1;
+        }
+      }
       for (int x = xa; x < xb; ++x, ++it) {
         const int st = it % S;
         const int slot0 = (j0 + x) * kTile;
         // box i of the tile: slots slot0 + i * bs ..; lanes 0-15 take K, 16-31 V
         const int i = lane & 15, first = slot0 + (i << bs_lg);
         const bool take = i < boxes && first < hi && first + bs > lo;
-        int64_t page = -1;
-        if (take) page = (first < p.pre_here ? p.prefix_pages : row)[first >> p.page_lg];
+        if ((slot0 >> p.page_lg) - base >= 32) {
+          base += 32;
+          ids = ids_next;
+          ids_next = entries(b, lo, hi, base + 32);
+        }
+        const int page = __shfl_sync(0xffffffffu, ids, (first >> p.page_lg) & 31);
         const bool in = page >= 0 && page < p.n_pages;
         if (take && !in) set_error(p.err, kDevPage);
         if (it >= S && !mbar_wait_near(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
@@ -355,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (take) {
           const int v = lane >> 4, y = first & ((1 << p.page_lg) - 1);
           // a bad page reads as zeros: the coordinate lies behind the pool
-          const int z = in ? (int)(page * p.Hkv + g) : (int)(p.n_pages * p.Hkv);
+          const int z = in ? (int)((int64_t)page * p.Hkv + g) : (int)(p.n_pages * p.Hkv);
           tma_codes(ring + (st * 2 + v) * Sm::kKV + (i << bs_lg) * D, v ? &p.tm_v : &p.tm_k, y, z,
                     &full[st]);
           // (not by a tensor map: a box of those would have to lie at 128 bytes here)
@@ -541,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       };
-      if (any_big) scores(std::true_type());
+      if (__builtin_expect(any_big, 0)) scores(std::true_type());
       else scores(std::false_type());
       if constexpr (kSums == 2) {
 #pragma unroll
@@ -618,15 +646,16 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       };
-      if (any_big) values(std::true_type());
+      if (__builtin_expect(any_big, 0)) values(std::true_type());
       else values(std::false_type());
     }
     if (flags & 2) {
       // The piece's end: the warps' maxima meet, each brings its sums to the greatest,
-      // and warp w < D / 32 adds all warps' O of column block w.
+      // and warp w < D / 32 adds all warps' O of column block w.  O goes through the place
+      // of the last tile's codes, which all warps have read behind the first barrier.
       const int rows = n * p.G, r0 = infos[st].r0, g = infos[st].g, dst = infos[st].dst;
+      const uint32_t xbase = kt;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
       if (!Sm::kQRegs && lane == 0) mbar_arrive(&q_empty[seg % Sm::kQBufs]);
       ++seg;
       float m_r[NT][2];
@@ -661,69 +690,65 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       // O's way: [block of 32 columns][warp][row of the tile][32 columns], eight columns
       // moved by the row's pair and four by its parity (no bank conflicts on either side)
-      constexpr int X = Sm::kXTiles;
 #pragma unroll
-      for (int nt0 = 0; nt0 < NT; nt0 += X) {
-        if (nt0 > 0) named_sync(1, kConsumers);    // the row tiles before are read
+      for (int nt = 0; nt < NT; ++nt) {
+        __syncwarp();
+        if (nt > 0) named_sync(1, kConsumers);     // the row tile before is read
 #pragma unroll
-        for (int k = 0; k < X; ++k)
+        for (int d = 0; d < NB; ++d)
 #pragma unroll
-          for (int d = 0; d < NB; ++d)
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)          // column 8 x + grp of block d
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(
-                                 xbase + ((d * kWarps + warp) * X + k) * 1024 + (2 * tig + e) * 128 +
-                                 ((x ^ tig) << 5) + ((grp ^ (4 * e)) << 2)),
-                             "f"(O[nt0 + k][d * 2 + (x >> 1)][2 * (x & 1) + e])
-                             : "memory");
+            for (int x = 0; x < 4; ++x)            // column 8 x + grp of block d
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                               xbase + (d * kWarps + warp) * 1024 + (2 * tig + e) * 128 +
+                               ((x ^ tig) << 5) + ((grp ^ (4 * e)) << 2)),
+                           "f"(O[nt][d * 2 + (x >> 1)][2 * (x & 1) + e])
+                           : "memory");
         named_sync(1, kConsumers);
-        if (warp >= NB) continue;
-#pragma unroll
-        for (int k = 0; k < X; ++k) {
+        if (warp < NB) {
           // row lane / 4, columns 8 (lane % 4) .. + 7
-          const int r8 = lane >> 2, row = (nt0 + k) * 8 + r8;
-          const uint32_t from = xbase + (warp * kWarps * X + k) * 1024 + r8 * 128 +
-                                (((lane & 3) ^ (r8 >> 1)) << 5);
+          const int r8 = lane >> 2, row = nt * 8 + r8;
+          const uint32_t from = xbase + warp * kWarps * 1024 + r8 * 128 + (((lane & 3) ^ (r8 >> 1)) << 5);
           float v[8] = {};
 #pragma unroll
           for (int s = 0; s < kWarps; ++s)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint4 w = lds128(from + s * X * 1024 + ((x ^ (r8 & 1)) << 4));
+              const uint4 w = lds128(from + s * 1024 + ((x ^ (r8 & 1)) << 4));
               v[4 * x] += __uint_as_float(w.x);
               v[4 * x + 1] += __uint_as_float(w.y);
               v[4 * x + 2] += __uint_as_float(w.z);
               v[4 * x + 3] += __uint_as_float(w.w);
             }
-          if (row >= rows) continue;
-          const float4 l4 = *reinterpret_cast<const float4*>(stat_l + row * 4);
-          const float l = (l4.x + l4.y) + (l4.z + l4.w);
-          const int t = row / p.G, hq = g * p.G + (row - t * p.G);
-          const int col = warp * 32 + 8 * (lane & 3);
-          if (dst < 0 && !p.own) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            uint32_t w[4];
+          if (row < rows) {
+            const float4 l4 = *reinterpret_cast<const float4*>(stat_l + row * 4);
+            const float l = (l4.x + l4.y) + (l4.z + l4.w);
+            const int t = row / p.G, hq = g * p.G + (row - t * p.G);
+            const int col = warp * 32 + 8 * (lane & 3);
+            if (dst < 0 && !p.own) {
+              const float inv = l > 0.f ? 1.f / l : 0.f;
+              uint32_t w[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const __half2 h = __floats2half2_rn(v[2 * c] * inv, v[2 * c + 1] * inv);
-              w[c] = *reinterpret_cast<const uint32_t*>(&h);
+              for (int c = 0; c < 4; ++c) {
+                const __half2 h = __floats2half2_rn(v[2 * c] * inv, v[2 * c + 1] * inv);
+                w[c] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *reinterpret_cast<uint4*>(p.out + (int64_t)(r0 + t) * p.out_stride + (int64_t)hq * D + col) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+              const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
+                                         : ((int64_t)cta * 2 + dst) * p.slot_rows + row;
+              float4* o = reinterpret_cast<float4*>((dst < 0 ? p.own : p.part) + at * D + col);
+              o[0] = make_float4(v[0], v[1], v[2], v[3]);
+              o[1] = make_float4(v[4], v[5], v[6], v[7]);
+              if (warp == 0 && (lane & 3) == 0)
+                (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(max_of(row), l);
             }
-            *reinterpret_cast<uint4*>(p.out + (int64_t)(r0 + t) * p.out_stride + (int64_t)hq * D + col) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          } else {
-            const int64_t at = dst < 0 ? (int64_t)(r0 + t) * p.Hq + hq
-                                       : ((int64_t)cta * 2 + dst) * p.slot_rows + row;
-            float4* o = reinterpret_cast<float4*>((dst < 0 ? p.own : p.part) + at * D + col);
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
-            if (warp == 0 && (lane & 3) == 0)
-              (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(max_of(row), l);
           }
         }
       }
-      continue;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next copy there
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
@@ -752,6 +777,11 @@ cudaError_t configure_one() {
 }
 
 }  // namespace
+
+void paged_few_kv8_slots(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows) {
+  *nc = (max_new * G <= 16 ? 3 : 2) * num_sms;      // FSmem::kCtas
+  *slot_rows = max_new * G <= 16 ? 16 : 32;
+}
 
 cudaError_t launch_paged_few_kv8(const PagedFew8Params& p, cudaStream_t s, bool pdl) {
   if (p.a.max_new * p.a.G > p.a.slot_rows || p.a.nc < 1 || p.a.nc > 512) return cudaErrorInvalidValue;
