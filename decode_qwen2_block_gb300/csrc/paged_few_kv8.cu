@@ -82,8 +82,12 @@ __device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-// The scales of a page that is not there (a box's, at most).
-__device__ const uint4 kZeroScales[kTile * 4 / 16] = {};
+// 16 bytes by this lane, or zeros; and this lane's arrival on `bar` when they are there.
+__device__ __forceinline__ void copy16_arrive(uint32_t dst, const void* src, bool there, uint64_t* bar) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error 2^-22; 2^-inf = 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -132,6 +136,7 @@ struct FSmem {
   static constexpr int NB = D / kKv8Block;
   static constexpr int kKV = kTile * D;                         // K or V codes of a tile
   static constexpr int kSc = kTile * NB;                        // their scales
+  static constexpr int kScLanes = 2 * kSc / 16;                 // lanes that copy 16 bytes of those
   // More warps than two CTAs' hide more of a slab's chain of loads, products and exponentials:
   // three, while O's registers leave room (65536 / 16 warps).
   static constexpr int kCtas = NT <= 2 ? 3 : 2;
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + Sm::kScLanes);
       mbar_init(&empty[s], kWarps);
     }
     for (int s = 0; s < Sm::kQBufs; ++s) mbar_init(&q_empty[s], kWarps);
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
     // -------------------------------------------------------------- producer
     const int bs_lg = p.page_lg < 6 ? p.page_lg : 6, bs = 1 << bs_lg;   // slots of a box
     const int boxes = kTile >> bs_lg;
-    const uint32_t box_bytes = (uint32_t)bs * (D + NB);
+    const uint32_t box_bytes = (uint32_t)bs * D;
     int b = start_b, g = g0;
     int64_t cum = start_cum, lin = t0;
     int it = 0, seg = 0, base32 = -1;
@@ -386,10 +391,17 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
           const int z = in ? (int)((int64_t)page * p.Hkv + g) : (int)(p.n_pages * p.Hkv);
           tma_codes(ring + (st * 2 + v) * Sm::kKV + (i << bs_lg) * D, v ? &p.tm_v : &p.tm_k, y, z,
                     &full[st]);
-          // (not by a tensor map: a box of those would have to lie at 128 bytes here)
-          const uint8_t* sc = (v ? q8.vs : q8.ks) + (((int64_t)z << p.page_lg) + y) * NB;
-          bulk_g2s(smem + Sm::kScOff + (st * 2 + v) * Sm::kSc + (i << bs_lg) * NB,
-                   in ? sc : reinterpret_cast<const uint8_t*>(kZeroScales), bs * NB, &full[st]);
+        }
+        // the scales: 16 bytes a lane whatever the page (a copy of each page's own costs as
+        // much as one of its codes: 96 sequences over pages of 16 took 69 us, over pages of 64 58)
+        const int sv = lane / (Sm::kScLanes / 2), at = lane % (Sm::kScLanes / 2) * (16 / NB);
+        const int slot = slot0 + at;
+        const int spage = __shfl_sync(0xffffffffu, ids, (slot >> p.page_lg) & 31);
+        if (lane < Sm::kScLanes) {
+          const bool there = slot < hi && slot + 16 / NB > lo && spage >= 0 && spage < p.n_pages;
+          const int64_t row = (((int64_t)spage * p.Hkv + g) << p.page_lg) + (slot & ((1 << p.page_lg) - 1));
+          copy16_arrive(sring + (st * 2 + sv) * Sm::kSc + at * NB, (sv ? q8.vs : q8.ks) + (there ? row * NB : 0),
+                        there, &full[st]);
         }
         if (qrows > 0) wait_before();
         for (int r = lane; r < qrows; r += 32) {
@@ -411,10 +423,10 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
     if (ok && it >= S && !mbar_wait_near(&empty[st], (uint32_t)(it / S - 1) & 1u, p.err)) ok = false;
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
-      if (lane == 0) {
-        infos[st].flags = 4;
-        mbar_arrive(&full[st]);
-      }
+      if (lane == 0) infos[st].flags = 4;
+      __syncwarp();
+      if (lane <= Sm::kScLanes) mbar_arrive(&full[st]);
+      if (Sm::kScLanes == 32 && lane == 0) mbar_arrive(&full[st]);
     } else {
       // copies in flight land before shared memory goes away
       for (int k = max(0, it - S); k < it; ++k)
