@@ -1409,7 +1409,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   }
   CUtensorMap few_k, few_v;
   if (few && pool.ks) {
-    const int rows = (int)(page < 64 ? page : 64);
+    const int rows = (int)(page < kv8_few_tile(D) ? page : kv8_few_tile(D));
     if (make_tmap_codes8(&few_k, k_pages, D, page, heads, rows) ||
         make_tmap_codes8(&few_v, v_pages, D, page, heads, rows))
       return BLK_ERR_CUDA;

@@ -55,8 +55,10 @@ struct Kv8AttnParams {
 cudaError_t launch_kv8_attn(const Kv8AttnParams& p, cudaStream_t s, bool pdl);
 
 // Few rows (paged_few_rows): as launch_paged_few, the merge of cut units behind it.
+constexpr int kv8_few_tile(int D) { return D == 128 ? 64 : 128; }     // slots of a tile
 struct PagedFew8Params {
-  PagedAttnParams a;           // tm_k, tm_v: codes, boxes of all columns of one page's slots (at most 64)
+  PagedAttnParams a;           // tm_k, tm_v: codes, boxes of all columns of a page's slots, a
+                               //   tile's at most
   const uint8_t *ks, *vs;      // scales
 };
 void paged_few_kv8_slots(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows);

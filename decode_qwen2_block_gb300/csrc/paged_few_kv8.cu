@@ -7,8 +7,9 @@
 //
 // Bound by memory and by issue: D + D / 32 bytes a row of K or V, and for each pair of
 // codes a byte permute and a fused multiply-add before mma.sync can take them.
-//   warp 4     producer: codes and scales, page by page (at most 64 slots), by TMA.
-//   warps 0-3  16 slots each of every 64-slot tile: S' = K Q' (the slots are the M side, so
+//   warp 4     producer: codes page by page by TMA, scales by 16-byte copies.
+//   warps 0-3  16 slots each of every 64-slot tile (32 of 128 slots where a row has 64 columns
+//              and half the work): S' = K Q' (the slots are the M side, so
 //              that rows come in eights), the warp's own running maximum and sum, O' = V' P'
 //              of all columns.  Nothing is exchanged between warps until the unit ends,
 //              so a warp waits for no other while tiles come.
@@ -30,7 +31,6 @@
 namespace blk {
 namespace {
 
-constexpr int kTile = 64;            // slots of a tile
 constexpr int kWarps = 4, kConsumers = 32 * kWarps, kThreads = kConsumers + 32;
 constexpr int kHead = 1;             // a unit's begin and end in the line, in tiles
 // Weights are formed 2^10 times their size (O and l carry the factor, it cancels), and a
@@ -134,9 +134,11 @@ struct TileInfo {      // what the consumers need of a tile
 template <int D, int NT>
 struct FSmem {
   static constexpr int NB = D / kKv8Block;
+  static constexpr int kTile = kv8_few_tile(D);                 // slots of a tile
+  static constexpr int NS = kTile / (16 * kWarps);              // groups of 16 that a warp takes
   static constexpr int kKV = kTile * D;                         // K or V codes of a tile
   static constexpr int kSc = kTile * NB;                        // their scales
-  static constexpr int kScLanes = 2 * kSc / 16;                 // lanes that copy 16 bytes of those
+  static_assert(2 * kSc == 32 * 16, "16 bytes of K's and V's a lane");
   // More warps than two CTAs' hide more of a slab's chain of loads, products and exponentials:
   // three, while O's registers leave room (65536 / 16 warps).
   static constexpr int kCtas = NT <= 2 ? 3 : 2;
@@ -158,19 +160,21 @@ struct FSmem {
   static_assert(kBytes + 3328 <= 233472 / kCtas, "shared memory");   // (1 KB the system's, statics)
 };
 
+template <int kTile>
 __device__ __forceinline__ int seq_tiles(const PagedAttnParams& p, const PagedSeq& s) {
   if (s.n == 0) return 0;
   return (s.L + s.n + kTile - 1) / kTile - paged_lo(p, s.L) / kTile;
 }
+template <int kTile>
 __device__ __forceinline__ int seq_weight(const PagedAttnParams& p, const PagedSeq& s) {
-  return s.n == 0 ? 0 : seq_tiles(p, s) + kHead;
+  return s.n == 0 ? 0 : seq_tiles<kTile>(p, s) + kHead;
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
     paged_few_kv8_kernel(const __grid_constant__ PagedFew8Params q8) {
   using Sm = FSmem<D, NT>;
-  constexpr int S = Sm::kStages, NB = Sm::NB;
+  constexpr int S = Sm::kStages, NB = Sm::NB, NS = Sm::NS, kTile = Sm::kTile;
   const PagedAttnParams& p = q8.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1 + Sm::kScLanes);
+      mbar_init(&full[s], 1 + 32);      // the boxes and q, and each lane's scales
       mbar_init(&empty[s], kWarps);
     }
     for (int s = 0; s < Sm::kQBufs; ++s) mbar_init(&q_empty[s], kWarps);
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
     const PagedSeq s = load_seq(p, b);
-    mine += seq_weight(p, s);
+    mine += seq_weight<kTile>(p, s);
     bad |= s.bad;
     if (b < 128) first_seqs[b] = s;
     if (p.upb && s.n == 0 && blockIdx.x == 0)
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
     int64_t cum = before;
     int b = b0;
     for (; b + 1 < b1; ++b) {
-      const int wt = seq_weight(p, load_seq(p, b));
+      const int wt = seq_weight<kTile>(p, load_seq(p, b));
       if (x0 < cum + wt) break;
       cum += wt;
     }
@@ -266,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
 
   if (warp == kWarps) {
     // -------------------------------------------------------------- producer
-    const int bs_lg = p.page_lg < 6 ? p.page_lg : 6, bs = 1 << bs_lg;   // slots of a box
+    constexpr int kBoxLg = kTile == 64 ? 6 : 7;
+    const int bs_lg = p.page_lg < kBoxLg ? p.page_lg : kBoxLg, bs = 1 << bs_lg;   // slots of a box
     const int boxes = kTile >> bs_lg;
     const uint32_t box_bytes = (uint32_t)bs * D;
     int b = start_b, g = g0;
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
       s.r0 = __shfl_sync(0xffffffffu, mys.r0, b & 31);
       s.n = __shfl_sync(0xffffffffu, mys.n, b & 31);
       s.L = __shfl_sync(0xffffffffu, mys.L, b & 31);
-      const int nt = seq_tiles(p, s);
+      const int nt = seq_tiles<kTile>(p, s);
       if (nt == 0) {
         ++b;
         continue;
@@ -394,15 +399,13 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
         }
         // the scales: 16 bytes a lane whatever the page (a copy of each page's own costs as
         // much as one of its codes: 96 sequences over pages of 16 took 69 us, over pages of 64 58)
-        const int sv = lane / (Sm::kScLanes / 2), at = lane % (Sm::kScLanes / 2) * (16 / NB);
+        const int sv = lane >> 4, at = (lane & 15) * (16 / NB);
         const int slot = slot0 + at;
         const int spage = __shfl_sync(0xffffffffu, ids, (slot >> p.page_lg) & 31);
-        if (lane < Sm::kScLanes) {
-          const bool there = slot < hi && slot + 16 / NB > lo && spage >= 0 && spage < p.n_pages;
-          const int64_t row = (((int64_t)spage * p.Hkv + g) << p.page_lg) + (slot & ((1 << p.page_lg) - 1));
-          copy16_arrive(sring + (st * 2 + sv) * Sm::kSc + at * NB, (sv ? q8.vs : q8.ks) + (there ? row * NB : 0),
-                        there, &full[st]);
-        }
+        const bool there = slot < hi && slot + 16 / NB > lo && spage >= 0 && spage < p.n_pages;
+        const int64_t row = (((int64_t)spage * p.Hkv + g) << p.page_lg) + (slot & ((1 << p.page_lg) - 1));
+        copy16_arrive(sring + (st * 2 + sv) * Sm::kSc + at * NB, (sv ? q8.vs : q8.ks) + (there ? row * NB : 0),
+                      there, &full[st]);
         if (qrows > 0) wait_before();
         for (int r = lane; r < qrows; r += 32) {
           const int t = r / p.G, hh = r - t * p.G;
@@ -425,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
     if (ok) {
       if (lane == 0) infos[st].flags = 4;
       __syncwarp();
-      if (lane <= Sm::kScLanes) mbar_arrive(&full[st]);
-      if (Sm::kScLanes == 32 && lane == 0) mbar_arrive(&full[st]);
+      mbar_arrive(&full[st]);
+      if (lane == 0) mbar_arrive(&full[st]);
     } else {
       // copies in flight land before shared memory goes away
       for (int k = max(0, it - S); k < it; ++k)
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
 
   // ---------------------------------------------------------------- consumers
   const int grp = lane >> 2, tig = lane & 3;
-  const int slab = warp * 16;
+  const int slab = warp * 16 * NS;                    // the warp's slots of a tile
   const float sl2 = p.scale_log2;
   // The slot (of 16) behind row c of score tile t.  Equal pieces of rows 2 i, 2 i + 1 of a
   // tile lie in different halves of the banks (K's loads: the swizzle parts rows 0 - 3 from
@@ -514,51 +517,60 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
         if (lane == 0) mbar_arrive(&q_empty[0]);       // q's place is free
       }
     }
-    if (slab < vhi && slab + 16 > vlo) {
-      // every row sees every slot of this warp's 16: n - 1 slots from the end are
-      // behind the first row, windows begin at most n - 1 slots behind vlo
-      const bool clear = slab + 16 <= vhi - (n - 1) && slab >= (p.window > 0 ? vlo + (n - 1) : vlo);
+    if (slab < vhi && slab + 16 * NS > vlo) {
+      // every row sees every slot of this warp's: n - 1 slots from the end are behind the
+      // first row, windows begin at most n - 1 slots behind vlo
+      const bool clear = slab + 16 * NS <= vhi - (n - 1) && slab >= (p.window > 0 ? vlo + (n - 1) : vlo);
+      // the scales: K's of the lane's two slots, V's of its four ([tile][even, odd])
+      uint32_t kw[NS][2], sw[NS][2][2], large = 0;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if constexpr (D == 128) {
+          const uint2 k2 = lds64(ks + (kr + 16 * s) * NB), e2 = lds64(vs + (ve + 16 * s) * NB),
+                      o2 = lds64(vs + (ve + vo + 16 * s) * NB);
+          kw[s][0] = k2.x; kw[s][1] = k2.y;
+          sw[s][0][0] = e2.x; sw[s][1][0] = e2.y;
+          sw[s][0][1] = o2.x; sw[s][1][1] = o2.y;
+        } else {
+          const uint2 v4 = lds64(vs + (ve + 16 * s) * NB);     // (one behind the other)
+          kw[s][0] = lds16(ks + (kr + 16 * s) * NB);
+          kw[s][1] = lds16(ks + (kr + kT1 + 16 * s) * NB);
+          sw[s][0][0] = v4.x & 0xffffu; sw[s][0][1] = v4.x >> 16;
+          sw[s][1][0] = v4.y & 0xffffu; sw[s][1][1] = v4.y >> 16;
+        }
+        if (slab < vlo || slab + 16 * NS > vhi) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const int c = ve + 16 * s + t * kT1 + o * vo;
+              if (c < vlo || c >= vhi) sw[s][t][o] = 0;
+            }
+        }
+        large |= big_scales(kw[s][0]) | big_scales(kw[s][1]) | big_scales(sw[s][0][0]) |
+                 big_scales(sw[s][0][1]) | big_scales(sw[s][1][0]) | big_scales(sw[s][1][1]);
+      }
+      const bool any_big = __any_sync(0xffffffffu, (large & 0x80808080u) != 0);
       // (one row tile: two sums, so that products follow one another half as far)
       constexpr int kSums = NT == 1 ? 2 : 1;
-      float sc[NT][kSums][4];
+      float sc[NS][NT][kSums][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int k = 0; k < kSums; ++k) sc[nt][k][0] = sc[nt][k][1] = sc[nt][k][2] = sc[nt][k][3] = 0.f;
-      // the scales: K's of the lane's two slots, V's of its four (sw[tile][even, odd])
-      uint32_t kw[2], sw[2][2];
-      if constexpr (D == 128) {
-        const uint2 k2 = lds64(ks + kr * NB), e2 = lds64(vs + ve * NB), o2 = lds64(vs + (ve + vo) * NB);
-        kw[0] = k2.x; kw[1] = k2.y;
-        sw[0][0] = e2.x; sw[1][0] = e2.y;
-        sw[0][1] = o2.x; sw[1][1] = o2.y;
-      } else {
-        const uint2 v4 = lds64(vs + ve * NB);         // (one behind the other)
-        kw[0] = lds16(ks + kr * NB);
-        kw[1] = lds16(ks + (kr + kT1) * NB);
-        sw[0][0] = v4.x & 0xffffu; sw[0][1] = v4.x >> 16;
-        sw[1][0] = v4.y & 0xffffu; sw[1][1] = v4.y >> 16;
-      }
-      if (slab < vlo || slab + 16 > vhi) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const int c = ve + t * kT1 + o * vo;
-            if (c < vlo || c >= vhi) sw[t][o] = 0;
-          }
-      }
-      const bool any_big =
-          __any_sync(0xffffffffu, ((big_scales(kw[0]) | big_scales(kw[1]) | big_scales(sw[0][0]) |
-                                    big_scales(sw[0][1]) | big_scales(sw[1][0]) | big_scales(sw[1][1])) &
-                                   0x80808080u) != 0);
+          for (int k = 0; k < kSums; ++k)
+            sc[s][nt][k][0] = sc[s][nt][k][1] = sc[s][nt][k][2] = sc[s][nt][k][3] = 0.f;
       auto scores = [&](auto big) {
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-          const uint4 c0 = lds128(kt + (k_off0 ^ (h << 6))), c1 = lds128(kt + (k_off1 ^ (h << 6)));
-          const uint32_t cw[2][4] = {{c0.x, c0.y, c0.z, c0.w}, {c1.x, c1.y, c1.z, c1.w}};
+          uint4 c[NS][2];
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            c[s][0] = lds128(kt + (k_off0 ^ (h << 6)) + s * 16 * D);
+            c[s][1] = lds128(kt + (k_off1 ^ (h << 6)) + s * 16 * D);
+          }
           const uint32_t sel = h ? sel_k1 : sel_k0;
-          const Unit<decltype(big)::value> u0(__byte_perm(kw[0], 0, sel)), u1(__byte_perm(kw[1], 0, sel));
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             [[maybe_unused]] uint32_t qv[Sm::kQRegs ? 1 : NT][2][2];
@@ -567,15 +579,21 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
               for (int nt = 0; nt < NT; ++nt) load_q(qb, nt, 2 * h + x, qv[nt][0], qv[nt][1]);
             }
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t a[4] = {u0(cw[0][2 * x + y], 0x4140), u1(cw[1][2 * x + y], 0x4140),
-                                     u0(cw[0][2 * x + y], 0x4342), u1(cw[1][2 * x + y], 0x4342)};
-              if constexpr (Sm::kQRegs) {
-                const uint32_t* b = qf[4 * h + 2 * x + y];
-                mma16816(sc[0][y % kSums], a, b[0], b[1]);
-              } else {
+            for (int s = 0; s < NS; ++s) {
+              const Unit<decltype(big)::value> u0(__byte_perm(kw[s][0], 0, sel)),
+                  u1(__byte_perm(kw[s][1], 0, sel));
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt][0], a, qv[nt][y][0], qv[nt][y][1]);
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t w0 = x ? (y ? c[s][0].w : c[s][0].z) : (y ? c[s][0].y : c[s][0].x);
+                const uint32_t w1 = x ? (y ? c[s][1].w : c[s][1].z) : (y ? c[s][1].y : c[s][1].x);
+                const uint32_t a[4] = {u0(w0, 0x4140), u1(w1, 0x4140), u0(w0, 0x4342), u1(w1, 0x4342)};
+                if constexpr (Sm::kQRegs) {
+                  const uint32_t* b = qf[4 * h + 2 * x + y];
+                  mma16816(sc[s][0][y % kSums], a, b[0], b[1]);
+                } else {
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma16816(sc[s][nt][0], a, qv[nt][y][0], qv[nt][y][1]);
+                }
               }
             }
           }
@@ -583,31 +601,41 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
       };
       if (__builtin_expect(any_big, 0)) scores(std::true_type());
       else scores(std::false_type());
-      if constexpr (kSums == 2) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[0][0][k] += sc[0][1][k];
-      }
-      if (!clear) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int c = kr + kT1 * (k >> 1), slot = slot0 + c;
-            if (!(c >= vlo && slot <= last[nt][k & 1] && slot >= low[nt][k & 1])) sc[nt][0][k] = -INFINITY;
-          }
-      }
       bool need = false;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if constexpr (kSums == 2) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[s][0][0][k] += sc[s][0][1][k];
+        }
+        if (!clear) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int c = kr + 16 * s + kT1 * (k >> 1), slot = slot0 + c;
+              if (!(c >= vlo && slot <= last[nt][k & 1] && slot >= low[nt][k & 1]))
+                sc[s][nt][0][k] = -INFINITY;
+            }
+        }
+      }
+      float top[NT][2];                   // of the lane's slots
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          need |= fmaf(fmaxf(sc[nt][0][e], sc[nt][0][2 + e]), sl2, -kWeightLog2) > lim[nt][e];
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(sc[0][nt][0][e], sc[0][nt][0][2 + e]);
+#pragma unroll
+          for (int s = 1; s < NS; ++s) x = fmaxf(x, fmaxf(sc[s][nt][0][e], sc[s][nt][0][2 + e]));
+          top[nt][e] = x;
+          need |= fmaf(x, sl2, -kWeightLog2) > lim[nt][e];
+        }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(sc[nt][0][e], sc[nt][0][2 + e]);
+            float x = top[nt][e];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
             const float t = fmaf(x, sl2, -kWeightLog2);
@@ -626,37 +654,41 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
             }
           }
       }
-      uint32_t pb[NT][2];
+      uint32_t pb[NS][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+      for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = ex2(fmaf(sc[nt][0][k], sl2, nref[nt][k & 1]));   // 2^-inf = 0
-        l_r[nt][0] += w[0] + w[2];
-        l_r[nt][1] += w[1] + w[3];
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const __half2 h = __floats2half2_rn(w[2 * t], w[2 * t + 1]);
-          pb[nt][t] = transposed(*reinterpret_cast<const uint32_t*>(&h));
+          for (int k = 0; k < 4; ++k) w[k] = ex2(fmaf(sc[s][nt][0][k], sl2, nref[nt][k & 1]));   // 2^-inf = 0
+          l_r[nt][0] += w[0] + w[2];
+          l_r[nt][1] += w[1] + w[3];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const __half2 h = __floats2half2_rn(w[2 * t], w[2 * t + 1]);
+            pb[s][nt][t] = transposed(*reinterpret_cast<const uint32_t*>(&h));
+          }
         }
-      }
       // O' += V' P'
       auto values = [&](auto big) {
 #pragma unroll
-        for (int g = 0; g < NB; ++g) {
-          uint32_t v[4];
-          ldsm_bytes_t(vt + (v_off ^ (g << 5)), v);
-          const uint32_t sel = (4 + g) << 12 | g << 4;
-          const Unit<decltype(big)::value> u0(__byte_perm(sw[0][0], sw[0][1], sel) & 0xff00ff00u),
-              u1(__byte_perm(sw[1][0], sw[1][1], sel) & 0xff00ff00u);
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t a[4] = {u0(v[2 * j], 0x4140), u0(v[2 * j + 1], 0x4140), u1(v[2 * j], 0x4342),
-                                   u1(v[2 * j + 1], 0x4342)};
+          for (int g = 0; g < NB; ++g) {
+            uint32_t v[4];
+            ldsm_bytes_t(vt + (v_off ^ (g << 5)) + s * 16 * D, v);
+            const uint32_t sel = (4 + g) << 12 | g << 4;
+            const Unit<decltype(big)::value> u0(__byte_perm(sw[s][0][0], sw[s][0][1], sel) & 0xff00ff00u),
+                u1(__byte_perm(sw[s][1][0], sw[s][1][1], sel) & 0xff00ff00u);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(O[nt][g * 2 + j], a, pb[nt][0], pb[nt][1]);
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t a[4] = {u0(v[2 * j], 0x4140), u0(v[2 * j + 1], 0x4140), u1(v[2 * j], 0x4342),
+                                     u1(v[2 * j + 1], 0x4342)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(O[nt][g * 2 + j], a, pb[s][nt][0], pb[s][nt][1]);
+            }
           }
-        }
       };
       if (__builtin_expect(any_big, 0)) values(std::true_type());
       else values(std::false_type());
