@@ -48,6 +48,7 @@ struct blk_handle_s {
   uint32_t flags;
   bool decode_ok;  // shape fits the persistent decode kernel
   bool paged_many; // the many-row paged kernels may be launched (configure_paged_many)
+  bool paged_many8; // those over 8-bit pools
   int64_t window;  // sliding-window attention in slots (0 = full), blk_set_window
   blk::DecodeParams* dec;  // parameter block of the decode launch
   uint64_t* trace;         // optional decode timeline buffer
@@ -862,8 +863,8 @@ int blk_create(const blk_config* cfg, blk_handle* out) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))
     return BLK_ERR_CUDA;
   if (major != 10 || minor != 3) return BLK_ERR_DEVICE;
-  bool paged_many = false;
-  if (configure_kernels(&paged_many) != cudaSuccess) return BLK_ERR_CUDA;
+  bool paged_many = false, paged_many8 = false;
+  if (configure_kernels(&paged_many, &paged_many8) != cudaSuccess) return BLK_ERR_CUDA;
 
   blk_handle h = new (std::nothrow) blk_handle_s();
   if (!h) return BLK_ERR_CUDA;
@@ -871,6 +872,7 @@ int blk_create(const blk_config* cfg, blk_handle* out) {
   h->device = dev;
   h->num_sms = sms;
   h->paged_many = paged_many;
+  h->paged_many8 = paged_many8;
   {
     // the decode kernel stages at most kDecMaxVec inputs and keeps the
     // residual of at most 152 o_proj rows (8-row units) per CTA (one per SM)
@@ -1260,7 +1262,7 @@ int check_pool(blk_handle h, int64_t page_size, int64_t n_pages) {
   return BLK_OK;
 }
 
-int check_paged(blk_handle h, const blk_paged_batch* b) {
+int check_paged(blk_handle h, const blk_paged_batch* b, bool kv8 = false) {
   if (!h || !b) return BLK_ERR_NULL;
   if (!b->row_start || !b->cache_lens || !b->block_table) return BLK_ERR_NULL;
   if (!aligned(b->row_start, 8) || !aligned(b->cache_lens, 8) || !aligned(b->block_table, 4))
@@ -1279,7 +1281,8 @@ int check_paged(blk_handle h, const blk_paged_batch* b) {
     if (!aligned(b->prefix_pages, 4)) return BLK_ERR_ALIGN;
     if (h->window > 0) return BLK_ERR_SHAPE;
   }
-  if (!h->paged_many && !paged_few_rows(h->cfg.n_heads / h->cfg.n_kv_heads, b->max_new))
+  if (!(kv8 ? h->paged_many8 : h->paged_many) &&
+      !paged_few_rows(h->cfg.n_heads / h->cfg.n_kv_heads, b->max_new))
     return BLK_ERR_CUDA;
   return BLK_OK;
 }
@@ -1379,7 +1382,8 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
                    cudaStream_t s, Timer& tm, bool early) {
   const blk_config& c = h->cfg;
   const int D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads, G = Hq / Hkv;
-  const bool prefix = b->prefix_len > 0 && h->paged_many && share_prefix(c, b);
+  const bool many = pool.ks ? h->paged_many8 : h->paged_many;
+  const bool prefix = b->prefix_len > 0 && many && share_prefix(c, b);
   const PagedWs lay = paged_ws(c, b->n_rows, prefix, h->num_sms);
   const int64_t page = b->page_size, heads = b->n_pages * Hkv;
   PagedManyParams m = {};
@@ -1402,11 +1406,6 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   a.err = h->status;
   const void *k_pages = pool.k, *v_pages = pool.v;
   const bool few = paged_few_rows(G, b->max_new);
-  if (pool.ks && (!few || prefix)) {
-    Kv8AttnParams p8 = {a, kv8_of(pool)};
-    BLK_LAUNCH(tm, kKPagedMany8, launch_kv8_attn(p8, s, true));
-    return BLK_OK;
-  }
   CUtensorMap few_k, few_v;
   if (few && pool.ks) {
     const int rows = (int)(page < kv8_few_tile(D) ? page : kv8_few_tile(D));
@@ -1425,9 +1424,11 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
     const int kb[3] = {64, (int)page, 1};
     const int64_t qd[3] = {D, Hq, b->n_rows}, qs[2] = {(int64_t)D * 2, q_stride * 2};
     const int qb[3] = {64, G, paged_btok(G)};
-    if (make_tmap_3d(&a.tm_k, k_pages, kd, ks, kb) || make_tmap_3d(&a.tm_v, v_pages, kd, ks, kb) ||
-        make_tmap_3d(&a.tm_q, q, qd, qs, qb))
+    if (pool.ks ? make_tmap_codes8(&a.tm_k, k_pages, D, page, heads, (int)page) ||
+                      make_tmap_codes8(&a.tm_v, v_pages, D, page, heads, (int)page)
+                : make_tmap_3d(&a.tm_k, k_pages, kd, ks, kb) || make_tmap_3d(&a.tm_v, v_pages, kd, ks, kb))
       return BLK_ERR_CUDA;
+    if (make_tmap_3d(&a.tm_q, q, qd, qs, qb)) return BLK_ERR_CUDA;
   }
   m.btok = paged_btok(G);
   // entries for all units where the CTAs' entries are as many
@@ -1451,7 +1452,10 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
     const int64_t tiles = (b->prefix_len + kPagedManyTile - 1) / kPagedManyTile;
     const int64_t T = (int64_t)Hkv * pm.units * tiles;
     pm.a.nc = (int)(T < h->num_sms ? T : h->num_sms);
-    BLK_LAUNCH(tm, kKPagedPrefix, launch_paged_many(pm, s, true));
+    if (pool.ks)
+      BLK_LAUNCH(tm, kKPagedPrefix8, launch_paged_many_kv8({pm, kv8_of(pool).ks, kv8_of(pool).vs}, s, true));
+    else
+      BLK_LAUNCH(tm, kKPagedPrefix, launch_paged_many(pm, s, true));
     mg.prefix = 1;
     mg.pre_part = pm.a.part; mg.pre_ml = pm.a.ml;
     mg.pre_own = pm.a.own; mg.pre_own_ml = pm.a.own_ml;
@@ -1475,7 +1479,10 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
     a.nc = h->num_sms;
     a.slot_rows = kPagedManyRows;
     a.upb = units_each();
-    BLK_LAUNCH(tm, kKPagedMany, launch_paged_many(m, s, true));
+    if (pool.ks)
+      BLK_LAUNCH(tm, kKPagedMany8, launch_paged_many_kv8({m, kv8_of(pool).ks, kv8_of(pool).vs}, s, true));
+    else
+      BLK_LAUNCH(tm, kKPagedMany, launch_paged_many(m, s, true));
   }
   mg.a = a;
   mg.own_btok = few ? 0 : m.btok;
@@ -1485,8 +1492,8 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
 
 int check_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_t q_stride,
                      const void* k_pages, const void* v_pages, const void* out,
-                     int64_t out_stride, const void* ws, size_t ws_bytes) {
-  const int rc = check_paged(h, b);
+                     int64_t out_stride, const void* ws, size_t ws_bytes, bool kv8 = false) {
+  const int rc = check_paged(h, b, kv8);
   if (rc) return rc;
   if (!q || !k_pages || !v_pages || !out || !ws) return BLK_ERR_NULL;
   for (const void* ptr : {q, k_pages, v_pages, out, ws})
@@ -1532,8 +1539,9 @@ StepPagedWs step_paged_ws(const blk_config& c, int64_t N, bool prefix, int num_s
 
 int check_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b, const void* x,
                      const int64_t* pos, const int64_t* slot_map, const void* k_pages,
-                     const void* v_pages, const void* out, const void* ws, size_t ws_bytes) {
-  int rc = check_paged(h, b);
+                     const void* v_pages, const void* out, const void* ws, size_t ws_bytes,
+                     bool kv8 = false) {
+  int rc = check_paged(h, b, kv8);
   if (rc) return rc;
   rc = check_weights(h->cfg, w);
   if (rc) return rc;
@@ -1786,7 +1794,7 @@ int blk_attn_paged_kv8(blk_handle h, const blk_paged_batch* batch, const void* q
   int rc = check_kv8(pool);
   if (!h || !batch) rc = BLK_ERR_NULL;
   if (rc) return rc;
-  rc = check_attn_paged(h, batch, q, q_stride, pool->k, pool->v, out, out_stride, ws, ws_bytes);
+  rc = check_attn_paged(h, batch, q, q_stride, pool->k, pool->v, out, out_stride, ws, ws_bytes, true);
   if (rc) return rc;
   if (!on_device(h)) return BLK_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1855,7 +1863,7 @@ int blk_step_paged_stack_kv8(blk_handle h, const blk_weights* w, int n_layers,
     int rc = check_kv8(&pools[l]);
     if (rc) return rc;
     rc = check_step_paged(h, &w[l], batch, x, pos, slot_map, pools[l].k, pools[l].v, out, ws,
-                          ws_bytes);
+                          ws_bytes, true);
     if (rc) return rc;
   }
   if (!on_device(h)) return BLK_ERR_CUDA;
@@ -1946,7 +1954,7 @@ const char* blk_status_str(int status) {
 }  // extern "C"
 
 namespace blk {
-cudaError_t configure_kernels(bool* paged_many) {
+cudaError_t configure_kernels(bool* paged_many, bool* paged_many8) {
   cudaError_t e = configure_decode_persistent();
   if (e == cudaSuccess) e = configure_tc_gemm_kernels();
   if (e == cudaSuccess) e = configure_fr_gemm_kernels();
@@ -1956,6 +1964,7 @@ cudaError_t configure_kernels(bool* paged_many) {
   if (e == cudaSuccess) e = configure_paged_few();
   if (e == cudaSuccess) e = configure_paged_few_kv8();
   if (e == cudaSuccess) e = configure_paged_many(paged_many);
+  if (e == cudaSuccess) e = configure_paged_many_kv8(paged_many8);
   return e;
 }
 }  // namespace blk

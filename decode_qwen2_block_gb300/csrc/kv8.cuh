@@ -57,4 +57,57 @@ __device__ __forceinline__ uint32_t kv8_pair(uint32_t w, uint32_t sel, __half2 u
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// Two codes' factors, from the fp16 bits of their two scales.  A code u in the low bits of
+// 0x4c00 is 16 + u / 64; times s less 18 s that is (u - 128) s / 64, exact as one fused
+// operation while 18 s is an fp16 number: up to s = 3584.  Larger scales (kBig) subtract first.
+template <bool kBig>
+struct Kv8Unit {
+  __half2 mul, add;
+  __device__ __forceinline__ explicit Kv8Unit(uint32_t bits) {
+    mul = *reinterpret_cast<const __half2*>(&bits);
+    add = kBig ? __float2half2_rn(-18.f) : __hmul2(mul, __float2half2_rn(-18.f));
+  }
+  // the codes that `sel` places, from w
+  __device__ __forceinline__ uint32_t operator()(uint32_t w, uint32_t sel) const {
+    const uint32_t b = __byte_perm(w, 0x4c4c4c4cu, sel);
+    const __half2 x = *reinterpret_cast<const __half2*>(&b);
+    const __half2 y = kBig ? __hmul2(__hadd2(x, add), mul) : __hfma2(x, mul, add);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+};
+// Whether one of four scale bytes is above 3584's, 0x6b (NaN's is).
+__device__ __forceinline__ uint32_t kv8_big_scales(uint32_t w) {      // (bit 7 of a byte says so)
+  return (w & 0x7f7f7f7fu) + 0x14141414u;
+}
+
+// Codes of a page: (0, y, z), all columns of some slots.
+__device__ __forceinline__ void kv8_tma_codes(uint32_t dst, const CUtensorMap* map, int y, int z,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// 16 bytes by this lane, or zeros; and this lane's arrival on `bar` when they are there.
+__device__ __forceinline__ void kv8_copy16_arrive(uint32_t dst, const void* src, bool there, uint64_t* bar) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The scales of a slot in shared memory: D / 32 bytes.
+template <int NB>
+__device__ __forceinline__ uint32_t kv8_lds_scales(uint32_t addr) {
+  uint32_t v;
+  if constexpr (NB == 4) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  } else {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr) : "memory");
+    v = h;
+  }
+  return v;
+}
+
 }  // namespace blk

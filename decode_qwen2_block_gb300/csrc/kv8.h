@@ -47,13 +47,7 @@ struct Kv8ReadParams {
 };
 cudaError_t launch_kv8_read(const Kv8ReadParams& p, int num_sms, cudaStream_t s, bool pdl);
 
-// Attention over such pools (the batch and all else as in PagedAttnParams).
-struct Kv8AttnParams {
-  PagedAttnParams a;
-  Kv8Pools from;
-};
-cudaError_t launch_kv8_attn(const Kv8AttnParams& p, cudaStream_t s, bool pdl);
-
+// Attention over such pools: the kernels of paged.h over codes and scales.
 // Few rows (paged_few_rows): as launch_paged_few, the merge of cut units behind it.
 constexpr int kv8_few_tile(int D) { return D == 128 ? 64 : 128; }     // slots of a tile
 struct PagedFew8Params {
@@ -64,5 +58,13 @@ struct PagedFew8Params {
 void paged_few_kv8_slots(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows);
 cudaError_t launch_paged_few_kv8(const PagedFew8Params& p, cudaStream_t s, bool pdl);
 cudaError_t configure_paged_few_kv8();
+
+
+// Many rows: as launch_paged_many (tm_k, tm_v: codes, boxes of all columns of one page).
+struct PagedMany8Params : PagedManyParams {
+  const uint8_t *ks, *vs;      // scales
+};
+cudaError_t launch_paged_many_kv8(const PagedMany8Params& p, cudaStream_t s, bool pdl);
+cudaError_t configure_paged_many_kv8(bool* usable);
 
 }  // namespace blk

@@ -73,21 +73,6 @@ __device__ __forceinline__ void ldsm_bytes_t(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
-// Codes of a page: (0, y, z), all columns of some slots.
-__device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, int y, int z,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-// 16 bytes by this lane, or zeros; and this lane's arrival on `bar` when they are there.
-__device__ __forceinline__ void copy16_arrive(uint32_t dst, const void* src, bool there, uint64_t* bar) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
-               : "memory");
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error 2^-22; 2^-inf = 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -97,29 +82,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {    // an 8 x 8 matr
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-
-// Two codes' factors, from the fp16 bits of their two scales.  A code u in the low bits of
-// 0x4c00 is 16 + u / 64; times s less 18 s that is (u - 128) s / 64, exact as one fused
-// operation while 18 s is an fp16 number: up to s = 3584.  Larger scales (kBig) subtract first.
-template <bool kBig>
-struct Unit {
-  __half2 mul, add;
-  __device__ __forceinline__ explicit Unit(uint32_t bits) {
-    mul = *reinterpret_cast<const __half2*>(&bits);
-    add = kBig ? __float2half2_rn(-18.f) : __hmul2(mul, __float2half2_rn(-18.f));
-  }
-  // the codes that `sel` places, from w
-  __device__ __forceinline__ uint32_t operator()(uint32_t w, uint32_t sel) const {
-    const uint32_t b = __byte_perm(w, 0x4c4c4c4cu, sel);
-    const __half2 x = *reinterpret_cast<const __half2*>(&b);
-    const __half2 y = kBig ? __hmul2(__hadd2(x, add), mul) : __hfma2(x, mul, add);
-    return *reinterpret_cast<const uint32_t*>(&y);
-  }
-};
-// Whether one of four scale bytes is above 3584's, 0x6b (NaN's is).
-__device__ __forceinline__ uint32_t big_scales(uint32_t w) {      // (bit 7 of a byte says so)
-  return (w & 0x7f7f7f7fu) + 0x14141414u;
 }
 
 struct TileInfo {      // what the consumers need of a tile
@@ -394,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
           const int v = lane >> 4, y = first & ((1 << p.page_lg) - 1);
           // a bad page reads as zeros: the coordinate lies behind the pool
           const int z = in ? (int)((int64_t)page * p.Hkv + g) : (int)(p.n_pages * p.Hkv);
-          tma_codes(ring + (st * 2 + v) * Sm::kKV + (i << bs_lg) * D, v ? &p.tm_v : &p.tm_k, y, z,
+          kv8_tma_codes(ring + (st * 2 + v) * Sm::kKV + (i << bs_lg) * D, v ? &p.tm_v : &p.tm_k, y, z,
                     &full[st]);
         }
         // the scales: 16 bytes a lane whatever the page (a copy of each page's own costs as
@@ -404,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
         const int spage = __shfl_sync(0xffffffffu, ids, (slot >> p.page_lg) & 31);
         const bool there = slot < hi && slot + 16 / NB > lo && spage >= 0 && spage < p.n_pages;
         const int64_t row = (((int64_t)spage * p.Hkv + g) << p.page_lg) + (slot & ((1 << p.page_lg) - 1));
-        copy16_arrive(sring + (st * 2 + sv) * Sm::kSc + at * NB, (sv ? q8.vs : q8.ks) + (there ? row * NB : 0),
+        kv8_copy16_arrive(sring + (st * 2 + sv) * Sm::kSc + at * NB, (sv ? q8.vs : q8.ks) + (there ? row * NB : 0),
                       there, &full[st]);
         if (qrows > 0) wait_before();
         for (int r = lane; r < qrows; r += 32) {
@@ -547,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
               if (c < vlo || c >= vhi) sw[s][t][o] = 0;
             }
         }
-        large |= big_scales(kw[s][0]) | big_scales(kw[s][1]) | big_scales(sw[s][0][0]) |
-                 big_scales(sw[s][0][1]) | big_scales(sw[s][1][0]) | big_scales(sw[s][1][1]);
+        large |= kv8_big_scales(kw[s][0]) | kv8_big_scales(kw[s][1]) | kv8_big_scales(sw[s][0][0]) |
+                 kv8_big_scales(sw[s][0][1]) | kv8_big_scales(sw[s][1][0]) | kv8_big_scales(sw[s][1][1]);
       }
       const bool any_big = __any_sync(0xffffffffu, (large & 0x80808080u) != 0);
       // (one row tile: two sums, so that products follow one another half as far)
@@ -580,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
             }
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-              const Unit<decltype(big)::value> u0(__byte_perm(kw[s][0], 0, sel)),
+              const Kv8Unit<decltype(big)::value> u0(__byte_perm(kw[s][0], 0, sel)),
                   u1(__byte_perm(kw[s][1], 0, sel));
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
@@ -679,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
             uint32_t v[4];
             ldsm_bytes_t(vt + (v_off ^ (g << 5)) + s * 16 * D, v);
             const uint32_t sel = (4 + g) << 12 | g << 4;
-            const Unit<decltype(big)::value> u0(__byte_perm(sw[s][0][0], sw[s][0][1], sel) & 0xff00ff00u),
+            const Kv8Unit<decltype(big)::value> u0(__byte_perm(sw[s][0][0], sw[s][0][1], sel) & 0xff00ff00u),
                 u1(__byte_perm(sw[s][1][0], sw[s][1][1], sel) & 0xff00ff00u);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {

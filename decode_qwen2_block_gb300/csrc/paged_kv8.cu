@@ -1,11 +1,8 @@
-// A paged K/V cache in 8 bits: rows quantised into their slots, slots read back as rows,
-// and attention over them (the form of the cache: kv8.h).
-#include <math.h>
-
+// A paged K/V cache in 8 bits: rows quantised into their slots, and slots read back as rows
+// (the form of the cache: kv8.h).
 #include "common.cuh"
 #include "kv8.cuh"
 #include "kv8.h"
-#include "paged_dev.cuh"
 
 namespace blk {
 namespace {
@@ -114,79 +111,6 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8ReadParams 
   }
 }
 
-// out[r, h] = softmax(q[r, h] . K / sqrt(D)) V over the slots that row r sees: a warp a
-// (row, head), a lane D / 32 columns, a slot at a time with the running maximum and sum.
-template <int D>
-__global__ void __launch_bounds__(kThreads) kv8_attn_kernel(const __grid_constant__ Kv8AttnParams p) {
-  griddep_wait();
-  griddep_launch();
-  constexpr int C = D / 32;
-  const PagedAttnParams& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < a.B; b += kThreads)
-      if (load_seq(a, b).bad) set_error(a.err, kDevPage);
-  for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-       i < (int64_t)a.N * a.Hq; i += warps) {
-    const int r = (int)(i / a.Hq), h = (int)(i - (int64_t)r * a.Hq), g = h / a.G;
-    int b = 0, t = -1, L = 0;
-    for (; b < a.B; ++b) {
-      const PagedSeq s = load_seq(a, b);
-      if (s.n > 0 && r >= s.r0 && r < s.r0 + s.n) {
-        t = r - s.r0;
-        L = s.L;
-        break;
-      }
-    }
-    if (t < 0) continue;
-    const int last = L + t, low = paged_window(a, last);
-    float q[C], o[C], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int k = 0; k < C; ++k) {
-      q[k] = __half2float(a.q[(int64_t)r * a.q_stride + (int64_t)h * D + lane * C + k]);
-      o[k] = 0.f;
-    }
-    // 64 slots at a time, whose sums then join the others: one by one, 32,000 weights of
-    // e^-15 added to a sum of 1 would each be off by a sixth
-    for (int s0 = low; s0 <= last; s0 += 64) {
-      float mc = -INFINITY, lc = 0.f, oc[C];
-#pragma unroll
-      for (int k = 0; k < C; ++k) oc[k] = 0.f;
-      for (int s = s0; s < s0 + 64 && s <= last; ++s) {
-        const int32_t* row = s < a.prefix_len ? a.prefix_pages : a.table + (int64_t)b * a.max_blocks;
-        const int64_t page = row[s >> a.page_lg];
-        const bool in = page >= 0 && page < a.n_pages;
-        if (!in && lane == 0) set_error(a.err, kDevPage);
-        const int64_t at = in ? ((page * a.Hkv + g) << a.page_lg) + (s & ((1 << a.page_lg) - 1)) : 0;
-        const float uk = in ? __low2float(kv8_unit(p.from.ks[at * C + lane * C / 32])) : 0.f;
-        const float uv = in ? __low2float(kv8_unit(p.from.vs[at * C + lane * C / 32])) : 0.f;
-        float x = 0.f;
-#pragma unroll
-        for (int k = 0; k < C; ++k) x = fmaf(q[k], (p.from.k[at * D + lane * C + k] - 128) * uk, x);
-        x = warp_sum(x) * a.scale_log2;
-        const float mn = fmaxf(mc, x);
-        const float f = mc == -INFINITY ? 0.f : exp2f(mc - mn);
-        const float w = mn == -INFINITY && x == x ? 0.f : exp2f(x - mn);
-        lc = lc * f + w;
-#pragma unroll
-        for (int k = 0; k < C; ++k) oc[k] = oc[k] * f + w * ((p.from.v[at * D + lane * C + k] - 128) * uv);
-        mc = mn;
-      }
-      const float mn = fmaxf(m, mc);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = mc == -INFINITY ? 1.f : exp2f(mc - mn);
-      l = l * f + lc * w;
-#pragma unroll
-      for (int k = 0; k < C; ++k) o[k] = o[k] * f + oc[k] * w;
-      m = mn;
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-#pragma unroll
-    for (int k = 0; k < C; ++k)
-      a.out[(int64_t)r * a.out_stride + (int64_t)h * D + lane * C + k] = __float2half_rn(o[k] * inv);
-  }
-}
-
 template <typename K, typename P>
 cudaError_t launch(K kernel, int grid, cudaStream_t s, bool pdl, const P& p) {
   cudaLaunchConfig_t cfg = {};
@@ -218,13 +142,6 @@ cudaError_t launch_kv8_read(const Kv8ReadParams& p, int num_sms, cudaStream_t s,
   const int64_t total = (int64_t)p.N * p.Hkv * (p.D / 16);
   if (total >= (int64_t)1 << 32 || p.D % kKv8Block) return cudaErrorInvalidValue;
   return launch(kv8_read_kernel, row_grid(total, (int64_t)num_sms * 16), s, pdl, p);
-}
-
-cudaError_t launch_kv8_attn(const Kv8AttnParams& p, cudaStream_t s, bool pdl) {
-  const int grid = row_grid((int64_t)p.a.N * p.a.Hq * 32, 4096);
-  if (p.a.D == 128) return launch(kv8_attn_kernel<128>, grid, s, pdl, p);
-  if (p.a.D == 64) return launch(kv8_attn_kernel<64>, grid, s, pdl, p);
-  return cudaErrorInvalidValue;
 }
 
 }  // namespace blk
