@@ -60,11 +60,11 @@ constexpr int kThreadsOf = k8 ? 512 : 384;
 // k8: 128 a thread at the launch, kConv for the warps that convert.
 template <bool k8>
 constexpr int kRegsLaunch = k8 ? 128 : 168;
-template <bool kPrefix, bool k8>
+template <int D, bool kPrefix, bool k8>
 struct Regs {
-  static constexpr int kFew = k8 ? 56 : kPrefix ? 88 : 72;
-  static constexpr int kMany = k8 ? 200 : kPrefix ? 208 : 216;
-  static constexpr int kConv = k8 ? 56 : 0;
+  static constexpr int kFew = k8 ? (D == 128 ? 56 : 40) : kPrefix ? 88 : 72;
+  static constexpr int kMany = k8 ? (D == 128 ? 200 : 216) : kPrefix ? 208 : 216;
+  static constexpr int kConv = k8 ? (D == 128 ? 56 : 40) : 0;
   static_assert(128 * (kFew + kConv) + 256 * kMany <= kThreadsOf<k8> * kRegsLaunch<k8>, "register split");
 };
 constexpr int kTile = kPagedManyTile;
@@ -223,7 +223,7 @@ template <int D, bool kPrefix, bool k8>
 __global__ void __launch_bounds__(kThreadsOf<k8>, 1)
     paged_many_kernel(const __grid_constant__ ManyParams<k8> q) {
   using Sm = MSmem<D, k8>;
-  using R3 = Regs<kPrefix, k8>;
+  using R3 = Regs<D, kPrefix, k8>;
   constexpr int kThreads = kThreadsOf<k8>;
   // Ring item 2 j is K of tile j, item 2 j + 1 its V.  The commit behind a block's S of
   // tile j says that everything it issued up to there is done: with both blocks'
@@ -814,11 +814,17 @@ __global__ void __launch_bounds__(kThreadsOf<k8>, 1)
           f.dst = dst;
         }
         copy(&p.tm_k, scales_of(0));
+        if constexpr (k8) {            // (V first: it needs no wait for the piece before)
+          wait_item();
+          if (!ok) break;
+          copy(&p.tm_v, scales_of(1));
+        }
         if (x == xa) {
           // q of the piece before is used up
-          if constexpr (k8) ok = ok && (seg == 0 || mbar_wait_near(q_free, (uint32_t)(seg - 1) & 1u, p.err));
-          else wait_s(it - 1);
-          ok = __all_sync(0xffffffffu, ok);
+          if constexpr (k8)
+            ok = __all_sync(0xffffffffu, seg == 0 || mbar_wait_near(q_free, (uint32_t)(seg - 1) & 1u, p.err));
+          else
+            wait_s(it - 1);
           if (!ok) break;
           // (a barrier a block: block 0 begins when its q is there)
           ++qn0;
@@ -834,9 +840,11 @@ __global__ void __launch_bounds__(kThreadsOf<k8>, 1)
             }
           }
         }
-        wait_item();
-        if (!ok) break;
-        copy(&p.tm_v, scales_of(1));
+        if constexpr (!k8) {
+          wait_item();
+          if (!ok) break;
+          copy(&p.tm_v, scales_of(1));
+        }
       }
       ++seg;
     }
