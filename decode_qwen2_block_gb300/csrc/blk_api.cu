@@ -48,7 +48,8 @@ struct blk_handle_s {
   uint32_t flags;
   bool decode_ok;  // shape fits the persistent decode kernel
   bool paged_many; // the many-row paged kernels may be launched (configure_paged_many)
-  bool paged_many8; // those over 8-bit pools
+  bool paged_many8; // those over 8-bit pools, and
+  bool paged_wide8; // the few-row kernels over such pools for more than 16 rows
   int64_t window;  // sliding-window attention in slots (0 = full), blk_set_window
   blk::DecodeParams* dec;  // parameter block of the decode launch
   uint64_t* trace;         // optional decode timeline buffer
@@ -863,8 +864,8 @@ int blk_create(const blk_config* cfg, blk_handle* out) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))
     return BLK_ERR_CUDA;
   if (major != 10 || minor != 3) return BLK_ERR_DEVICE;
-  bool paged_many = false, paged_many8 = false;
-  if (configure_kernels(&paged_many, &paged_many8) != cudaSuccess) return BLK_ERR_CUDA;
+  bool paged_many = false, paged_many8 = false, paged_wide8 = false;
+  if (configure_kernels(&paged_many, &paged_many8, &paged_wide8) != cudaSuccess) return BLK_ERR_CUDA;
 
   blk_handle h = new (std::nothrow) blk_handle_s();
   if (!h) return BLK_ERR_CUDA;
@@ -873,6 +874,7 @@ int blk_create(const blk_config* cfg, blk_handle* out) {
   h->num_sms = sms;
   h->paged_many = paged_many;
   h->paged_many8 = paged_many8;
+  h->paged_wide8 = paged_wide8;
   {
     // the decode kernel stages at most kDecMaxVec inputs and keeps the
     // residual of at most 152 o_proj rows (8-row units) per CTA (one per SM)
@@ -1281,8 +1283,9 @@ int check_paged(blk_handle h, const blk_paged_batch* b, bool kv8 = false) {
     if (!aligned(b->prefix_pages, 4)) return BLK_ERR_ALIGN;
     if (h->window > 0) return BLK_ERR_SHAPE;
   }
-  if (!(kv8 ? h->paged_many8 : h->paged_many) &&
-      !paged_few_rows(h->cfg.n_heads / h->cfg.n_kv_heads, b->max_new))
+  const int G = h->cfg.n_heads / h->cfg.n_kv_heads;
+  if (!paged_few_rows(G, b->max_new) ? !(kv8 ? h->paged_many8 : h->paged_many)
+                                     : kv8 && kv8_few_wide(G, b->max_new) && !h->paged_wide8)
     return BLK_ERR_CUDA;
   return BLK_OK;
 }
@@ -1408,7 +1411,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   const bool few = paged_few_rows(G, b->max_new);
   CUtensorMap few_k, few_v;
   if (few && pool.ks) {
-    const int rows = (int)(page < kv8_few_tile(D) ? page : kv8_few_tile(D));
+    const int tile = kv8_few_tile(D, kv8_few_wide(G, b->max_new)), rows = (int)(page < tile ? page : tile);
     if (make_tmap_codes8(&few_k, k_pages, D, page, heads, rows) ||
         make_tmap_codes8(&few_v, v_pages, D, page, heads, rows))
       return BLK_ERR_CUDA;
@@ -1954,7 +1957,7 @@ const char* blk_status_str(int status) {
 }  // extern "C"
 
 namespace blk {
-cudaError_t configure_kernels(bool* paged_many, bool* paged_many8) {
+cudaError_t configure_kernels(bool* paged_many, bool* paged_many8, bool* paged_wide8) {
   cudaError_t e = configure_decode_persistent();
   if (e == cudaSuccess) e = configure_tc_gemm_kernels();
   if (e == cudaSuccess) e = configure_fr_gemm_kernels();
@@ -1962,7 +1965,7 @@ cudaError_t configure_kernels(bool* paged_many, bool* paged_many8) {
   if (e == cudaSuccess) e = configure_lm_head();
   if (e == cudaSuccess) e = configure_decode_attn_batch();
   if (e == cudaSuccess) e = configure_paged_few();
-  if (e == cudaSuccess) e = configure_paged_few_kv8();
+  if (e == cudaSuccess) e = configure_paged_few_kv8(paged_wide8);
   if (e == cudaSuccess) e = configure_paged_many(paged_many);
   if (e == cudaSuccess) e = configure_paged_many_kv8(paged_many8);
   return e;

@@ -126,6 +126,6 @@ cudaError_t launch_dequant(int fmt, const void* q, const void* scale, const void
 
 // Sets the per-kernel shared-memory limits (called with every handle); paged_many: see
 // configure_paged_many.
-cudaError_t configure_kernels(bool* paged_many, bool* paged_many8);
+cudaError_t configure_kernels(bool* paged_many, bool* paged_many8, bool* paged_wide8);
 
 }  // namespace blk

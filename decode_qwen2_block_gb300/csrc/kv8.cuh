@@ -89,10 +89,12 @@ __device__ __forceinline__ void kv8_tma_codes(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-// 16 bytes by this lane, or zeros; and this lane's arrival on `bar` when they are there.
-__device__ __forceinline__ void kv8_copy16_arrive(uint32_t dst, const void* src, bool there, uint64_t* bar) {
+// 16 bytes by this lane, or zeros; and its arrival on `bar` when all such copies are there.
+__device__ __forceinline__ void kv8_copy16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
                : "memory");
+}
+__device__ __forceinline__ void kv8_copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 

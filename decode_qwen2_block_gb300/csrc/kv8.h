@@ -49,7 +49,11 @@ cudaError_t launch_kv8_read(const Kv8ReadParams& p, int num_sms, cudaStream_t s,
 
 // Attention over such pools: the kernels of paged.h over codes and scales.
 // Few rows (paged_few_rows): as launch_paged_few, the merge of cut units behind it.
-constexpr int kv8_few_tile(int D) { return D == 128 ? 64 : 128; }     // slots of a tile
+// Up to 8 kKv8NarrowTiles rows and more run on different shapes of the kernel; kv8_few_tile:
+// slots of a tile.
+constexpr int kKv8NarrowTiles = 2;
+inline bool kv8_few_wide(int G, int64_t max_new) { return max_new * G > 8 * kKv8NarrowTiles; }
+constexpr int kv8_few_tile(int D, bool wide) { return (D == 128 ? 64 : 128) << wide; }
 struct PagedFew8Params {
   PagedAttnParams a;           // tm_k, tm_v: codes, boxes of all columns of a page's slots, a
                                //   tile's at most
@@ -57,7 +61,9 @@ struct PagedFew8Params {
 };
 void paged_few_kv8_slots(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows);
 cudaError_t launch_paged_few_kv8(const PagedFew8Params& p, cudaStream_t s, bool pdl);
-cudaError_t configure_paged_few_kv8();
+// `wide` becomes false, and the shape for more rows must not be launched, where the compiler
+// gave it another register count than its warps share out.
+cudaError_t configure_paged_few_kv8(bool* wide);
 
 
 // Many rows: as launch_paged_many (tm_k, tm_v: codes, boxes of all columns of one page).

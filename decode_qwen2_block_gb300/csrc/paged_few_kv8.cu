@@ -31,7 +31,6 @@
 namespace blk {
 namespace {
 
-constexpr int kWarps = 4, kConsumers = 32 * kWarps, kThreads = kConsumers + 32;
 constexpr int kHead = 1;             // a unit's begin and end in the line, in tiles
 // Weights are formed 2^10 times their size (O and l carry the factor, it cancels), and a
 // row's reference maximum follows only when a score passes it by 2^5: weights reach 2^15,
@@ -96,30 +95,35 @@ struct TileInfo {      // what the consumers need of a tile
 template <int D, int NT>
 struct FSmem {
   static constexpr int NB = D / kKv8Block;
-  static constexpr int kTile = kv8_few_tile(D);                 // slots of a tile
+  // Up to 16 rows: four warps that take slots, and one; three CTAs an SM, as more warps hide more
+  // of a slab's chain of loads, products and exponentials, while O's registers leave room
+  // (65536 / 16 warps).  More rows: O alone is up to 128 registers, so eight warps with 216 each
+  // and the producer's group with 72 (216 * 256 + 72 * 128 = 168 * 384).
+  static constexpr bool kWide = NT > kKv8NarrowTiles;
+  static constexpr int kCtas = kWide ? 1 : 3;
+  static constexpr int kWarps = kWide ? 8 : 4, kConsumers = 32 * kWarps;
+  static constexpr int kThreads = kConsumers + (kWide ? 128 : 32);
+  static constexpr int kTile = kv8_few_tile(D, kWide);          // slots of a tile
   static constexpr int NS = kTile / (16 * kWarps);              // groups of 16 that a warp takes
   static constexpr int kKV = kTile * D;                         // K or V codes of a tile
   static constexpr int kSc = kTile * NB;                        // their scales
-  static_assert(2 * kSc == 32 * 16, "16 bytes of K's and V's a lane");
-  // More warps than two CTAs' hide more of a slab's chain of loads, products and exponentials:
-  // three, while O's registers leave room (65536 / 16 warps).
-  static constexpr int kCtas = NT <= 2 ? 3 : 2;
+  static constexpr int kScCopies = 2 * kSc / 512;               // 16 bytes of those a lane
   static constexpr int kQStride = D * 2 + 16;                   // bytes (conflict-free reads)
   static constexpr int kQBytes = 8 * NT * kQStride;
   static constexpr bool kQRegs = NT == 1;                       // else q is re-read for every tile
   static constexpr int kQBufs = kQRegs ? 1 : 2;
   static constexpr int kStage = 2 * (kKV + kSc);
   static constexpr int kStages =
-      (233472 / kCtas - 1024 - 2304 - 1024 - 1024 - kQBufs * kQBytes) / kStage;
+      (233472 / kCtas - 1024 - 2304 - 1024 - 1024 - (kWide ? 2048 : 0) - kQBufs * kQBytes) / kStage;
   static constexpr int kScOff = kStages * 2 * kKV;
   static constexpr int kQOff = kScOff + kStages * 2 * kSc;
-  static constexpr int kStatOff = kQOff + kQBufs * kQBytes;     // [8 NT][4 warps] maxima, then sums
-  static constexpr int kInfoOff = kStatOff + 2 * 4 * 8 * NT * 4;
+  static constexpr int kStatOff = kQOff + kQBufs * kQBytes;     // [8 NT][warps] maxima, sums, [8 NT] tops
+  static constexpr int kInfoOff = kStatOff + (2 * kWarps + 1) * 8 * NT * 4;
   static constexpr int kBarOff = (kInfoOff + kStages * (int)sizeof(TileInfo) + 15) / 16 * 16;
   static constexpr int kEnd = kBarOff + (2 * kStages + kQBufs) * 8 + 64;
   static constexpr size_t kBytes = (size_t)kEnd + 1024;         // the ring is 1024-aligned
   static_assert(kStages >= 3 && kWarps * NB * 1024 <= 2 * kKV, "O goes through a tile's place");
-  static_assert(kBytes + 3328 <= 233472 / kCtas, "shared memory");   // (1 KB the system's, statics)
+  static_assert(kBytes + 3328 <= 233472 / kCtas && kBytes <= 230000, "shared memory");   // (1 KB the system's, statics)
 };
 
 template <int kTile>
@@ -133,10 +137,11 @@ __device__ __forceinline__ int seq_weight(const PagedAttnParams& p, const PagedS
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
+__global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
     paged_few_kv8_kernel(const __grid_constant__ PagedFew8Params q8) {
   using Sm = FSmem<D, NT>;
   constexpr int S = Sm::kStages, NB = Sm::NB, NS = Sm::NS, kTile = Sm::kTile;
+  constexpr int kWarps = Sm::kWarps, kConsumers = Sm::kConsumers, kThreads = Sm::kThreads;
   const PagedAttnParams& p = q8.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -144,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
   const uint32_t ring = smem_u32(smem), sring = smem_u32(smem + Sm::kScOff),
                  qbase = smem_u32(smem + Sm::kQOff);
   float* stat_m = reinterpret_cast<float*>(smem + Sm::kStatOff);
-  float* stat_l = stat_m + 4 * 8 * NT;
+  float* stat_l = stat_m + kWarps * 8 * NT;
+  float* stat_top = stat_l + kWarps * 8 * NT;
   volatile TileInfo* infos = reinterpret_cast<volatile TileInfo*>(smem + Sm::kInfoOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Sm::kBarOff);
   uint64_t* empty = full + S;
@@ -230,9 +236,13 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
   }
   __syncthreads();
 
-  if (warp == kWarps) {
+  if (warp >= kWarps) {
+    if constexpr (Sm::kWide) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      if (warp > kWarps) return;
+    }
     // -------------------------------------------------------------- producer
-    constexpr int kBoxLg = kTile == 64 ? 6 : 7;
+    constexpr int kBoxLg = kTile == 64 ? 6 : 7;      // (a page has 128 slots at most)
     const int bs_lg = p.page_lg < kBoxLg ? p.page_lg : kBoxLg, bs = 1 << bs_lg;   // slots of a box
     const int boxes = kTile >> bs_lg;
     const uint32_t box_bytes = (uint32_t)bs * D;
@@ -359,15 +369,19 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
           kv8_tma_codes(ring + (st * 2 + v) * Sm::kKV + (i << bs_lg) * D, v ? &p.tm_v : &p.tm_k, y, z,
                     &full[st]);
         }
-        // the scales: 16 bytes a lane whatever the page (a copy of each page's own costs as
+        // the scales: 16 bytes a lane and copy whatever the page (a copy of each page's own costs as
         // much as one of its codes: 96 sequences over pages of 16 took 69 us, over pages of 64 58)
-        const int sv = lane >> 4, at = (lane & 15) * (16 / NB);
-        const int slot = slot0 + at;
-        const int spage = __shfl_sync(0xffffffffu, ids, (slot >> p.page_lg) & 31);
-        const bool there = slot < hi && slot + 16 / NB > lo && spage >= 0 && spage < p.n_pages;
-        const int64_t row = (((int64_t)spage * p.Hkv + g) << p.page_lg) + (slot & ((1 << p.page_lg) - 1));
-        kv8_copy16_arrive(sring + (st * 2 + sv) * Sm::kSc + at * NB, (sv ? q8.vs : q8.ks) + (there ? row * NB : 0),
-                      there, &full[st]);
+#pragma unroll
+        for (int c = 0; c < Sm::kScCopies; ++c) {
+          const int piece = c * 32 + lane, sv = piece / (Sm::kSc / 16);
+          const int at = piece % (Sm::kSc / 16) * (16 / NB), slot = slot0 + at;      // at: of the tile
+          const int spage = __shfl_sync(0xffffffffu, ids, (slot >> p.page_lg) & 31);
+          const bool there = slot < hi && slot + 16 / NB > lo && spage >= 0 && spage < p.n_pages;
+          const int64_t row = (((int64_t)spage * p.Hkv + g) << p.page_lg) + (slot & ((1 << p.page_lg) - 1));
+          kv8_copy16(sring + (st * 2 + sv) * Sm::kSc + at * NB, (sv ? q8.vs : q8.ks) + (there ? row * NB : 0),
+                     there);
+        }
+        kv8_copies_arrive(&full[st]);
         if (qrows > 0) wait_before();
         for (int r = lane; r < qrows; r += 32) {
           const int t = r / p.G, hh = r - t * p.G;
@@ -401,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
   }
 
   // ---------------------------------------------------------------- consumers
+  if constexpr (Sm::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
   const int grp = lane >> 2, tig = lane & 3;
   const int slab = warp * 16 * NS;                    // the warp's slots of a tile
   const float sl2 = p.scale_log2;
@@ -670,24 +685,31 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           m_r[nt][e] = lim[nt][e] == -INFINITY ? -INFINITY : -nref[nt][e];
-          if (grp == 0) stat_m[(nt * 8 + 2 * tig + e) * 4 + warp] = m_r[nt][e];
+          if (grp == 0) stat_m[(nt * 8 + 2 * tig + e) * kWarps + warp] = m_r[nt][e];
         }
       named_sync(1, kConsumers);
       if (*(volatile int*)&abort_s) return;       // (set before a warp's arrival, see above)
       auto max_of = [&](int row) {
-        const float4 m4 = *reinterpret_cast<const float4*>(stat_m + row * 4);
-        return fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; w += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(stat_m + row * kWarps + w);
+          m = fmaxf(m, fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)));
+        }
+        return m;
       };
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = nt * 8 + 2 * tig + e;
-          const float f = m_r[nt][e] == -INFINITY ? 0.f : ex2(m_r[nt][e] - max_of(row));
+          // (stat_m is read here alone: a warp that has written its O may be at the next piece's)
+          const float M = max_of(row), f = m_r[nt][e] == -INFINITY ? 0.f : ex2(m_r[nt][e] - M);
+          if (warp == 0 && grp == 0) stat_top[row] = M;
           float l = l_r[nt][e] * f;
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-          if (grp == 0) stat_l[row * 4 + warp] = l;
+          if (grp == 0) stat_l[row * kWarps + warp] = l;
 #pragma unroll
           for (int i = 0; i < NB * 2; ++i) {
             O[nt][i][e] *= f;
@@ -728,8 +750,12 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
               v[4 * x + 3] += __uint_as_float(w.w);
             }
           if (row < rows) {
-            const float4 l4 = *reinterpret_cast<const float4*>(stat_l + row * 4);
-            const float l = (l4.x + l4.y) + (l4.z + l4.w);
+            float l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; w += 4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(stat_l + row * kWarps + w);
+              l += (l4.x + l4.y) + (l4.z + l4.w);
+            }
             const int t = row / p.G, hq = g * p.G + (row - t * p.G);
             const int col = warp * 32 + 8 * (lane & 3);
             if (dst < 0 && !p.own) {
@@ -749,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, FSmem<D, NT>::kCtas)
               o[0] = make_float4(v[0], v[1], v[2], v[3]);
               o[1] = make_float4(v[4], v[5], v[6], v[7]);
               if (warp == 0 && (lane & 3) == 0)
-                (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(max_of(row), l);
+                (dst < 0 ? p.own_ml : p.ml)[at] = make_float2(stat_top[row], l);
             }
           }
         }
@@ -765,7 +791,7 @@ template <int D, int NT>
 cudaError_t launch_few(const PagedFew8Params& p, cudaStream_t s, bool pdl) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.a.nc);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(FSmem<D, NT>::kThreads);
   cfg.dynamicSmemBytes = FSmem<D, NT>::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -777,7 +803,13 @@ cudaError_t launch_few(const PagedFew8Params& p, cudaStream_t s, bool pdl) {
 }
 
 template <int D, int NT>
-cudaError_t configure_one() {
+cudaError_t configure_one(bool* wide) {
+  if (FSmem<D, NT>::kWide) {           // their warps share out the registers that the block is launched with
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, paged_few_kv8_kernel<D, NT>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != 168) *wide = false;
+  }
   return cudaFuncSetAttribute(paged_few_kv8_kernel<D, NT>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FSmem<D, NT>::kBytes);
 }
@@ -785,7 +817,7 @@ cudaError_t configure_one() {
 }  // namespace
 
 void paged_few_kv8_slots(int num_sms, int G, int64_t max_new, int* nc, int* slot_rows) {
-  *nc = (max_new * G <= 16 ? 3 : 2) * num_sms;      // FSmem::kCtas
+  *nc = (kv8_few_wide(G, max_new) ? 1 : 3) * num_sms;      // FSmem::kCtas
   *slot_rows = max_new * G <= 16 ? 16 : 32;
 }
 
@@ -799,10 +831,11 @@ cudaError_t launch_paged_few_kv8(const PagedFew8Params& p, cudaStream_t s, bool 
   return f[p.a.D == 128][tiles](p, s, pdl);
 }
 
-cudaError_t configure_paged_few_kv8() {
+cudaError_t configure_paged_few_kv8(bool* wide) {
+  *wide = true;
   for (auto f : {configure_one<64, 1>, configure_one<64, 2>, configure_one<64, 3>, configure_one<64, 4>,
                  configure_one<128, 1>, configure_one<128, 2>, configure_one<128, 3>, configure_one<128, 4>}) {
-    const cudaError_t e = f();
+    const cudaError_t e = f(wide);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -788,10 +788,8 @@ __global__ void __launch_bounds__(kThreadsOf<k8>, 1)
             if (take)
               kv8_tma_codes(smem_u32(smem + Sm::kCOff) + c * Sm::kCodes + (i << ps_lg) * D, map, 0, z, &c_full[c]);
             if (sslot < kTile)
-              kv8_copy16_arrive(smem_u32(smem + Sm::kScOff) + c * Sm::kScales + lane * 16,
-                                scales + srow, sthere, &c_full[c]);
-            else
-              mbar_arrive(&c_full[c]);
+              kv8_copy16(smem_u32(smem + Sm::kScOff) + c * Sm::kScales + lane * 16, scales + srow, sthere);
+            kv8_copies_arrive(&c_full[c]);
           } else {
             if (lane == 0) mbar_arrive_expect_tx(&kv_full[item % R], bytes);
             __syncwarp();

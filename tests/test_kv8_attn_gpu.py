@@ -166,6 +166,22 @@ def test_short_pieces_one_after_another_give_the_same_bits(heads, kv, dim, top):
         assert torch.equal(out.view(torch.int16), first.view(torch.int16))
 
 
+@pytest.mark.parametrize("heads,kv,dim,top", [(12, 2, 128, 1), (12, 2, 128, 2), (12, 2, 128, 4),
+                                              (4, 2, 64, 1), (32, 8, 64, 3), (16, 1, 64, 2)])
+@pytest.mark.parametrize("prefix", [0, 8192])
+def test_pieces_of_which_most_warps_see_nothing(heads, kv, dim, top, prefix):
+    """Sequences of a few slots and of some hundred in turn, cut and whole: warps that find
+    nothing in a piece are far ahead in the next while the others end it."""
+    hist = [prefix + 3, prefix + 500] * 45
+    x = batch8(heads, kv, dim, 64, hist, [top] * 90, seed=25, prefix=prefix)
+    first, b = run8(x)
+    b.check()
+    check_rows(x, first)
+    for _ in range(10):
+        out, _ = run8(x)
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16))
+
+
 @pytest.mark.parametrize("top", [1, 5, 60])
 def test_a_workspace_keeps_nothing_of_the_call_before(top):
     b = block(12, 2, 128)
