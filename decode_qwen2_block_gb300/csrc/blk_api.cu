@@ -1610,16 +1610,16 @@ int run_step_paged(blk_handle h, const blk_weights* w, const blk_paged_batch* b,
     BLK_LAUNCH(tm, kKGemmQKV, launch_fr_gemm(fq, kFrPart, h->num_sms, s, true));
     g.part = part;
     g.splits = fq.splits;
-    if (!pool.ks) {
-      g.slot_map = slot_map;
-      g.kc = static_cast<__half*>(pool.k);
-      g.vc = static_cast<__half*>(pool.v);
-    }
+    g.slot_map = slot_map;
+    g.kc = static_cast<__half*>(pool.k);
+    g.vc = static_cast<__half*>(pool.v);
+    g.ks = static_cast<uint8_t*>(pool.ks);
+    g.vs = static_cast<uint8_t*>(pool.vs);
     BLK_LAUNCH(tm, kKQkvFinish, launch_qkv_finish(g, s));
   } else {
     BLK_LAUNCH(tm, kKGemmQKV, launch_tc_gemm(g, kTcQKV, h->num_sms, s, true));
   }
-  if (pool.ks) {
+  if (M > kFrMaxRows && pool.ks) {
     Kv8AppendParams pa = {};
     pa.k = g.kc; pa.v = g.vc;
     pa.row_stride = D; pa.head_stride = (int64_t)M * D;

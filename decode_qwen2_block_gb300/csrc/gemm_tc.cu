@@ -48,6 +48,7 @@
 
 #include "common.cuh"
 #include "gemm_tc.h"
+#include "kv8.cuh"
 
 namespace blk {
 
@@ -792,7 +793,22 @@ __global__ void __launch_bounds__(64) qkv_finish_kernel(const __grid_constant__ 
     __half* nw = is_k ? p.k_new : p.v_new;
     if (p.slot_map) {
       const int64_t slot = p.slot_map[m];
-      if (slot >= 0 && slot < p.n_slots) {
+      if (slot >= 0 && slot < p.n_slots && p.ks) {
+        // 8 bits: a warp has columns i of one block of 32 and half + i of another
+        const int64_t page = slot >> p.page_lg, at = slot - (page << p.page_lg);
+        const int64_t row = ((page * p.Hkv + local) << p.page_lg) + at;
+        uint8_t* codes = reinterpret_cast<uint8_t*>(cache) + row * D;
+        uint8_t* scales = (is_k ? p.ks : p.vs) + row * (D / kKv8Block);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const __half x = h ? hb : ha;
+          const int col = h * half + i;
+          const uint32_t amax = __reduce_max_sync(0xffffffffu, __half_as_ushort(x) & 0x7fffu);
+          const uint32_t scale = kv8_scale(amax);
+          codes[col] = (uint8_t)kv8_code(__half2float(x), kv8_inverse(scale));
+          if ((threadIdx.x & 31) == 0) scales[col / kKv8Block] = (uint8_t)scale;
+        }
+      } else if (slot >= 0 && slot < p.n_slots) {
         const int64_t page = slot >> p.page_lg, at = slot - (page << p.page_lg);
         __half* dst = cache + (((page * p.Hkv + local) << p.page_lg) + at) * D;
         dst[i] = ha;

@@ -44,6 +44,9 @@ struct TcGemmParams {
   const int64_t* slot_map;
   int64_t n_slots;
   int page_lg;
+  // with scale pools (ks != null) kc and vc are pools of codes: the cache in 8 bits (kv8.h)
+  uint8_t* ks;
+  uint8_t* vs;
   // other epilogues
   const __half* res16;
   const float* res32;

@@ -84,7 +84,7 @@ struct PagedAttnParams {
   int early;                   // few rows: lengths, tables and the slots of the history are
                                //   older than the kernel before this one, which writes q
                                //   and the new slots; nothing else of it is waited for.
-                               //   That kernel (qkv_finish_kernel, page_append_kernel) waits
+                               //   That kernel (qkv_finish_kernel, page_append_kernel, kv8_append_kernel) waits
                                //   for its own predecessors before it lets this one start
   int B, N, Hq, Hkv, D, G, page_lg, max_new;
   float scale_log2;

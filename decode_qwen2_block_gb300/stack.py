@@ -13,10 +13,11 @@ import ctypes
 
 import torch
 
-from . import (BLK_ERR_CACHE_OVERFLOW, BLK_ERR_PAGE, BLK_ERR_SHAPE, BLK_OK, BlkError, Block,
-               BlkQWeights, BlkWeights, blk_decode_batch_stack,
+from . import (BLK_ERR_CACHE_OVERFLOW, BLK_ERR_PAGE, BLK_ERR_SHAPE, BLK_OK, BlkError, BlkKv8Pool,
+               Block, BlkQWeights, BlkWeights, blk_decode_batch_stack,
                blk_decode_batch_stack_workspace_bytes, blk_decode_stack, blk_decode_stack_q,
-               blk_prefill_stack, blk_prefill_stack_workspace_bytes, blk_step_paged_stack)
+               blk_prefill_stack, blk_prefill_stack_workspace_bytes, blk_step_paged_stack,
+               blk_step_paged_stack_kv8)
 
 
 class LayerStack:
@@ -174,10 +175,13 @@ class PagedStack:
     ``prefill_prefix`` computes a prefix that every sequence then begins with:
     its pages are held once, and a step reads its keys once for the whole batch
     where that pays.  The host knows the lengths it asked for, so no step waits
-    for the GPU.  Steps follow one another whatever streams they are given."""
+    for the GPU.  Steps follow one another whatever streams they are given.
+
+    With ``kv8`` the pages hold K and V in 8 bits (codes and scales, see include/blk.h):
+    about twice the slots in the same memory."""
 
     def __init__(self, shape, layer_weights, max_ctx: int, n_pages: int, page_size: int,
-                 max_seqs: int, max_rows: int, device="cuda"):
+                 max_seqs: int, max_rows: int, device="cuda", kv8: bool = False):
         self.shape = shape
         self.n_layers = len(layer_weights)
         self.block = Block(shape, max_ctx, chain=True)
@@ -186,8 +190,14 @@ class PagedStack:
         self.max_seqs, self.max_rows, self.device = max_seqs, max_rows, device
         pool = (n_pages, shape.n_kv_heads, page_size, shape.head_dim)
         self._last = torch.cuda.current_stream()  # the buffers' stream, then the last step's
-        self.pools = [(torch.zeros(pool, dtype=torch.float16, device=device),
-                       torch.zeros(pool, dtype=torch.float16, device=device))
+        self.kv8 = kv8
+        if kv8:                                  # codes of K, of V, their scales
+            scales = (*pool[:3], shape.head_dim // 32)
+            kinds = ((pool, torch.uint8), (pool, torch.uint8), (scales, torch.float8_e5m2),
+                     (scales, torch.float8_e5m2))
+        else:
+            kinds = ((pool, torch.float16), (pool, torch.float16))
+        self.pools = [tuple(torch.zeros(s, dtype=t, device=device) for s, t in kinds)
                       for _ in range(self.n_layers)]
         self.max_blocks = -(-max_ctx // page_size)
         self.table = torch.full((max_seqs, self.max_blocks), -1, dtype=torch.int32, device=device)
@@ -204,8 +214,12 @@ class PagedStack:
         self._held = [(t, [self._last]) for t in (*sum(self.pools, ()), self.table, self.ws)]
         n = self.n_layers
         self._w_arr = (BlkWeights * n)(*[Block.weights(w) for w in layer_weights])
-        self._k_arr = (ctypes.c_void_p * n)(*[k.data_ptr() for k, _ in self.pools])
-        self._v_arr = (ctypes.c_void_p * n)(*[v.data_ptr() for _, v in self.pools])
+        if kv8:
+            self._pool_arr = (BlkKv8Pool * n)(*[BlkKv8Pool(*[t.data_ptr() for t in p])
+                                                for p in self.pools])
+        else:
+            self._k_arr = (ctypes.c_void_p * n)(*[k.data_ptr() for k, _ in self.pools])
+            self._v_arr = (ctypes.c_void_p * n)(*[v.data_ptr() for _, v in self.pools])
 
     def _ints(self, values, dtype):
         return torch.tensor(values, dtype=dtype).to(self.device, non_blocking=True)
@@ -254,12 +268,16 @@ class PagedStack:
                 start, lens_d, table, n, self.page, self.n_pages, max(news),
                 max(have + more for have, more in zip(lens, news)), prefix_pages=prefix)
             self.block._paged_rows(batch, x, pos, slots, out)
-            rc = blk_step_paged_stack(self.block.handle, self._w_arr, self.n_layers, batch,
-                                      self._k_arr, self._v_arr, x.data_ptr(), pos.data_ptr(),
-                                      slots.data_ptr(), out.data_ptr(), self.ws.data_ptr(),
-                                      self.ws.numel(), s.cuda_stream)
+            args = (x.data_ptr(), pos.data_ptr(), slots.data_ptr(), out.data_ptr(),
+                    self.ws.data_ptr(), self.ws.numel(), s.cuda_stream)
+            if self.kv8:
+                rc = blk_step_paged_stack_kv8(self.block.handle, self._w_arr, self.n_layers, batch,
+                                              self._pool_arr, *args)
+            else:
+                rc = blk_step_paged_stack(self.block.handle, self._w_arr, self.n_layers, batch,
+                                          self._k_arr, self._v_arr, *args)
         if rc != BLK_OK:
-            raise BlkError(rc, "blk_step_paged_stack")
+            raise BlkError(rc, "blk_step_paged_stack" + ("_kv8" if self.kv8 else ""))
         return out, need
 
     def prefill_prefix(self, x, stream=None):
@@ -293,6 +311,42 @@ class PagedStack:
             del self.free_ids[:k]
             self.lens[b] += new_lens[b]
         return out
+
+    def read(self, b: int, caches=None, stream=None):
+        """Sequence b's K and V of every layer as contiguous caches hold them: a list of
+        (k, v), fp16 [n_kv_heads, slots, head_dim] (the cache in 8 bits as what it stands for).
+        caches: such pairs to fill from slot 0 on (e.g. LayerStack's), with at least as
+        many slots as the sequence; made to its length when None."""
+        n, page = self.lens[b], self.page
+        if caches is not None and len(caches) != self.n_layers:
+            raise BlkError(BLK_ERR_SHAPE, "PagedStack.read: caches")
+        s = self._follow(stream)
+        self._hold(s)
+        Hkv, D = self.shape.n_kv_heads, self.shape.head_dim
+        with torch.cuda.stream(s):
+            if caches is None:
+                caches = [tuple(torch.empty((Hkv, n, D), dtype=torch.float16, device=self.device)
+                                for _ in range(2)) for _ in range(self.n_layers)]
+            for t in (t for pair in caches for t in pair):
+                if (t.dtype is not torch.float16 or t.dim() != 3 or t.shape[0] != Hkv or
+                        t.shape[1] < n or t.shape[2] != D):
+                    raise BlkError(BLK_ERR_SHAPE, f"PagedStack.read: {tuple(t.shape)} {t.dtype}")
+            if n == 0:
+                return caches
+            most = 1 << 20                           # rows of one call
+            for i in range(0, n, most):
+                j = min(n, i + most)
+                slot = torch.arange(i, j, device=self.device)
+                pages = self.table[b][slot // page].long()
+                slots = pages * page + slot % page
+                for pool, (k, v) in zip(self.pools, caches):
+                    if self.kv8:
+                        self.block.page_read_kv8(slots, *pool, k[:, i:j].transpose(0, 1),
+                                                 v[:, i:j].transpose(0, 1), stream=s)
+                        continue
+                    for p, t in zip(pool, (k, v)):
+                        t[:, i:j] = p[pages, :, slot % page].transpose(0, 1)
+        return caches
 
     def free(self, b: int):
         """Gives sequence b's own pages back; it begins anew behind the prefix."""
