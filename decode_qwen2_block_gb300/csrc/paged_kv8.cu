@@ -79,7 +79,21 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendPar
   }
 }
 
-// Slot slot_map[r] to row r of K and V in fp16.  A thread takes 16 columns of K and of V.
+// 32 bytes; `wide`: dst is 32-byte aligned (else 16).
+__device__ __forceinline__ void store32(__half* dst, const uint32_t* v, bool wide) {
+  if (!wide) {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Slot slot_map[r] to row r of K and V in fp16.  A thread takes 16 columns of K and of V and
+// writes whole 32-byte sectors of them; bound by memory, kUnroll items in flight per thread.
+constexpr int kUnroll = 2;
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8ReadParams p) {
   griddep_wait();
   griddep_launch();
@@ -87,27 +101,54 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8ReadParams 
   const int64_t total = (int64_t)p.N * per_row;
   const int64_t step = (int64_t)gridDim.x * kThreads;
   const int64_t mask = ((int64_t)1 << p.page_lg) - 1;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += step) {
-    const uint32_t r = (uint32_t)i / per_row, e = (uint32_t)i - r * per_row;
-    const uint32_t h = e / cpr, c = e - h * cpr;
-    const int64_t slot = p.slot_map[r];
-    if (slot < 0 || slot >= p.n_slots) {
-      if (slot != -1 && e == 0) set_error(p.err, kDevPage);
-      continue;
-    }
-    const int64_t at = (((slot >> p.page_lg) * p.Hkv + h) << p.page_lg) + (slot & mask);
-    const int64_t sat = at * (p.D / kKv8Block) + (c >> 1);
-    const int64_t dst = (int64_t)r * p.row_stride + h * p.head_stride + c * 16;
+  const bool wide = (reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) % 32 == 0 &&
+                    (p.row_stride | p.head_stride) % 16 == 0;
+  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += step * kUnroll) {
+    int64_t at[kUnroll], dst[kUnroll];
+    uint32_t c[kUnroll];
+    uint4 w[kUnroll][2];
+    uint32_t sc[kUnroll][2];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint4 w = *reinterpret_cast<const uint4*>((kv ? p.from.v : p.from.k) + at * p.D + c * 16);
-      const __half2 u = kv8_unit((kv ? p.from.vs : p.from.ks)[sat]);
-      uint4* o = reinterpret_cast<uint4*>((kv ? p.v : p.k) + dst);
-      o[0] = make_uint4(kv8_pair(w.x, 0x4140, u), kv8_pair(w.x, 0x4342, u),
-                        kv8_pair(w.y, 0x4140, u), kv8_pair(w.y, 0x4342, u));
-      o[1] = make_uint4(kv8_pair(w.z, 0x4140, u), kv8_pair(w.z, 0x4342, u),
-                        kv8_pair(w.w, 0x4140, u), kv8_pair(w.w, 0x4342, u));
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t i = i0 + u * step;
+      at[u] = -1;
+      if (i < total) {
+        const uint32_t r = (uint32_t)i / per_row, e = (uint32_t)i - r * per_row;
+        const uint32_t h = e / cpr;
+        c[u] = e - h * cpr;
+        const int64_t slot = p.slot_map[r];
+        dst[u] = (int64_t)r * p.row_stride + h * p.head_stride + c[u] * 16;
+        if (slot >= 0 && slot < p.n_slots)
+          at[u] = (((slot >> p.page_lg) * p.Hkv + h) << p.page_lg) + (slot & mask);
+        else if (slot != -1 && e == 0)
+          set_error(p.err, kDevPage);
+      }
     }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (at[u] >= 0) {
+        const int64_t s = at[u] * (p.D / kKv8Block) + (c[u] >> 1), k = at[u] * p.D + c[u] * 16;
+        w[u][0] = __ldcs(reinterpret_cast<const uint4*>(p.from.k + k));
+        w[u][1] = __ldcs(reinterpret_cast<const uint4*>(p.from.v + k));
+        sc[u][0] = p.from.ks[s];
+        sc[u][1] = p.from.vs[s];
+      }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (at[u] >= 0) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const __half2 unit = kv8_unit(sc[u][kv]);
+          const uint32_t x[4] = {w[u][kv].x, w[u][kv].y, w[u][kv].z, w[u][kv].w};
+          uint32_t y[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[2 * k] = kv8_pair(x[k], 0x4140, unit);
+            y[2 * k + 1] = kv8_pair(x[k], 0x4342, unit);
+          }
+          store32((kv ? p.v : p.k) + dst[u], y, wide);
+        }
+      }
   }
 }
 
