@@ -1350,16 +1350,32 @@ PagedWs paged_ws(const blk_config& c, int64_t N, bool prefix, int num_sms) {
 // tokens, 8 - 64 sequences, prefixes of 1024 - 16384) the rule took the slower side of
 // six, by 5 % at most.  For instance 12 / 2 heads, one new token: 8 sequences behind
 // 1024 slots 10.9 us with their own against 17.4, 64 behind 8192 64 against 32.
-bool share_prefix(const blk_config& c, const blk_paged_batch* b) {
+// Over 8-bit pools (kv8): 17 for the launch and the merge's start (22 behind many rows; codes
+// become fp16 before the first product), 0.0145 a tile (0.0113 of 64 columns; nine tenths where
+// a sequence's rows fill one block of the two), the few-row kernel 430 / 310 / 245 tiles (8 / 16
+// / 32 rows; of 64 columns 1.8 times as many).  Of 20 batches measured both ways (3 head
+// layouts, 1 / 4 / 60 new tokens, 8 and 64 sequences, prefixes of 1024 - 16384) it takes the
+// slower side of three, by 8 % at most.
+bool share_prefix(const blk_config& c, const blk_paged_batch* b, bool kv8) {
   const int G = c.n_heads / c.n_kv_heads;
   const int64_t utok = 2 * paged_btok(G), tiles = (b->prefix_len + kPagedManyTile - 1) / kPagedManyTile;
+  const double rows_us = (double)b->n_rows * c.n_heads * c.head_dim * 12 / 3e6;
+  const int64_t units = (b->n_rows + utok - 1) / utok, own_units = (b->max_new + utok - 1) / utok;
+  if (kv8) {
+    const double unit = (c.head_dim == 128 ? 0.0145 : 0.0113) * c.n_kv_heads * tiles;
+    const int64_t rows = b->max_new * G;
+    const double passes = (rows <= 8 ? 430.0 : rows <= 16 ? 310.0 : 245.0) * (c.head_dim == 128 ? 1.0 : 1.8);
+    const bool few = paged_few_rows(G, b->max_new);
+    const double with_own = few ? b->n_seqs * c.n_kv_heads * tiles * 2 / passes
+                                : unit * b->n_seqs * (b->max_new <= utok / 2 ? 0.9 : (double)own_units);
+    return with_own > (few ? 17 : 22) + unit * units + rows_us;
+  }
   const double tile = 0.0125 * c.n_kv_heads * tiles;     // a unit of every kv head
-  const double alone = 10 + tile * ((b->n_rows + utok - 1) / utok) +
-                       (double)b->n_rows * c.n_heads * c.head_dim * 12 / 3e6;
+  const double alone = 10 + tile * units + rows_us;
   const double with_own =
       paged_few_rows(G, b->max_new)
           ? b->n_seqs * c.n_kv_heads * tiles * 2 / (b->max_new * G <= 16 ? 300.0 : 200.0)
-          : tile * b->n_seqs * ((b->max_new + utok - 1) / utok);
+          : tile * b->n_seqs * own_units;
   return with_own > alone;
 }
 
@@ -1386,7 +1402,7 @@ int run_attn_paged(blk_handle h, const blk_paged_batch* b, const void* q, int64_
   const blk_config& c = h->cfg;
   const int D = c.head_dim, Hq = c.n_heads, Hkv = c.n_kv_heads, G = Hq / Hkv;
   const bool many = pool.ks ? h->paged_many8 : h->paged_many;
-  const bool prefix = b->prefix_len > 0 && many && share_prefix(c, b);
+  const bool prefix = b->prefix_len > 0 && many && share_prefix(c, b, pool.ks != nullptr);
   const PagedWs lay = paged_ws(c, b->n_rows, prefix, h->num_sms);
   const int64_t page = b->page_size, heads = b->n_pages * Hkv;
   PagedManyParams m = {};
