@@ -63,8 +63,8 @@ constexpr int kRegsLaunch = k8 ? 128 : 168;
 template <int D, bool kPrefix, bool k8>
 struct Regs {
   static constexpr int kFew = k8 ? (D == 128 ? 56 : 40) : kPrefix ? 88 : 72;
-  static constexpr int kMany = k8 ? (D == 128 ? 200 : 216) : kPrefix ? 208 : 216;
-  static constexpr int kConv = k8 ? (D == 128 ? 56 : 40) : 0;
+  static constexpr int kMany = k8 ? (D == 128 ? 208 : 216) : kPrefix ? 208 : 216;
+  static constexpr int kConv = k8 ? 40 : 0;
   static_assert(128 * (kFew + kConv) + 256 * kMany <= kThreadsOf<k8> * kRegsLaunch<k8>, "register split");
 };
 constexpr int kTile = kPagedManyTile;
@@ -253,11 +253,11 @@ __global__ void __launch_bounds__(kThreadsOf<k8>, 1)
 
   // what needs nothing of the kernels before: barriers, TMEM, tensor maps
   if (threadIdx.x == 0) {
-    for (int s = 0; s < R; ++s) mbar_init(&kv_full[s], k8 ? 4 : 1);
+    for (int s = 0; s < R; ++s) mbar_init(&kv_full[s], k8 ? 2 : 1);
     if constexpr (k8) {
       for (int s = 0; s < C; ++s) {
         mbar_init(&c_full[s], 1 + 32);      // the copies of codes, and each lane's scales
-        mbar_init(&c_empty[s], 4);
+        mbar_init(&c_empty[s], 2);
       }
       mbar_init(q_free, 2);
     }
@@ -412,58 +412,52 @@ __global__ void __launch_bounds__(kThreadsOf<k8>, 1)
     if constexpr (k8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R3::kConv));
       // ------------------------------------------------------------- converters
-      // A thread a slot: its codes and scales to fp16 in the place and order that a tile of
-      // an fp16 cache would have, zeros where no row of the unit sees the slot.
-      const int r = threadIdx.x - 384;
-      const uint32_t row_c = smem_u32(smem + Sm::kCOff) + r * D, row_s = smem_u32(smem + Sm::kScOff) + r * Sm::NB;
-      const uint32_t row_h = smem_u32(ring) + r * 128;
-      const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
-      bool seen = false;
-      for (int i = 0;; ++i) {            // ring item i: K (even) or V of tile i / 2
+      // Two warps make K tiles fp16 and two V tiles, 32 slots and 64 columns at a time: a lane's
+      // codes and scales to the place and order that a tile of an fp16 cache would have, zeros
+      // where no row of the unit sees the slot.  (All four warps on one tile after another: the
+      // waits around each follow one another, 2.20 us a tile of 128 columns against 2.15.)
+      const int own = (warp - 12) >> 1, r0 = (warp & 1) * 64 + lane;
+      for (int i = own;; i += 2) {       // ring item i: K (even) or V of tile i / 2
         if (!__all_sync(0xffffffffu, mbar_wait_near(&c_full[i % C], (uint32_t)(i / C) & 1u, p.err))) break;
-        int flags = 0;
-        if (!(i & 1)) {
-          const int4 f = lds128(smem_u32(const_cast<ManyInfo*>(&infos[(i >> 1) % kInfos])));
-          flags = f.x;
-          seen = f.y + r >= f.z && f.y + r < f.w;
-        }
-        uint4 c[D / 16];
-        uint32_t w = 0;
-        if (!(flags & 4)) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const int4 v = lds128(row_c + (i % C) * Sm::kCodes + ((k ^ sw) << 4));
-            c[k] = make_uint4(v.x, v.y, v.z, v.w);
-          }
-          w = kv8_lds_scales<Sm::NB>(row_s + (i % C) * Sm::kScales);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c_empty[i % C]);
+        const int4 f = lds128(smem_u32(const_cast<ManyInfo*>(&infos[(i >> 1) % kInfos])));
+        const bool end = (f.x & 4) != 0;
+        if (end && own == 1) break;
         if (!s_done((i - R + 1) >> 1)) break;        // what lay in the item's place is used up
-        if (!(flags & 4)) {
-          if (!seen) w = 0;
-          auto convert = [&](auto big) {
+        if (!end) {
+#pragma unroll 1
+          for (int part = 0; part < D / 32; ++part) {          // rows r0 / r0 + 32, columns 0 - 63 / 64 - 127
+            const int r = r0 + (part & 1) * 32, half = part >> 1;
+            const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
+            const uint32_t from = smem_u32(smem + Sm::kCOff) + (i % C) * Sm::kCodes + r * D;
+            const uint32_t to = smem_u32(ring) + (i % R) * Sm::kKV + half * 16384 + r * 128;
+            uint4 c[4];
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
+            for (int k = 0; k < 4; ++k) {
+              const int4 v = lds128(from + (((half * 4 + k) ^ sw) << 4));
+              c[k] = make_uint4(v.x, v.y, v.z, v.w);
+            }
+            uint32_t w = kv8_lds_scales<Sm::NB>(smem_u32(smem + Sm::kScOff) + (i % C) * Sm::kScales + r * Sm::NB);
+            w = f.y + r >= f.z && f.y + r < f.w ? w >> (half * 16) : 0;
+            if (part == D / 32 - 1) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&c_empty[i % C]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
               const uint32_t b = k >> 1;        // the block's scale, doubled to fp16
-              const Kv8Unit<decltype(big)::value> u(__byte_perm(w, 0, b << 12 | 4 << 8 | b << 4 | 4));
-              const uint32_t to = row_h + (i % R) * Sm::kKV + (k >> 2) * 16384;
-              const int s = (2 * k) & 7;
-              sts128(to + ((s ^ (r & 7)) << 4), u(c[k].x, 0x4140), u(c[k].x, 0x4342), u(c[k].y, 0x4140),
-                     u(c[k].y, 0x4342));
-              sts128(to + (((s + 1) ^ (r & 7)) << 4), u(c[k].z, 0x4140), u(c[k].z, 0x4342),
+              // (any scale's form: what these warps compute is not what they take their time for)
+              const Kv8Unit<true> u(__byte_perm(w, 0, b << 12 | 4 << 8 | b << 4 | 4));
+              sts128(to + (((2 * k) ^ (r & 7)) << 4), u(c[k].x, 0x4140), u(c[k].x, 0x4342),
+                     u(c[k].y, 0x4140), u(c[k].y, 0x4342));
+              sts128(to + (((2 * k + 1) ^ (r & 7)) << 4), u(c[k].z, 0x4140), u(c[k].z, 0x4342),
                      u(c[k].w, 0x4140), u(c[k].w, 0x4342));
             }
-          };
-          if (__builtin_expect(__any_sync(0xffffffffu, (kv8_big_scales(w) & 0x80808080u) != 0), 0))
-            convert(std::true_type());
-          else
-            convert(std::false_type());
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&kv_full[i % R]);
-        if (flags & 4) break;
+        if (end) break;
       }
     }
   } else if (warp >= 4) {
@@ -850,9 +844,19 @@ __global__ void __launch_bounds__(kThreadsOf<k8>, 1)
     if (ok) {
       if (lane == 0) infos[it % kInfos].flags = 4;
       __syncwarp();
-      if (k8) mbar_arrive(&c_full[item % (k8 ? C : 1)]);
-      if (lane == 0) mbar_arrive(k8 ? &c_full[item % (k8 ? C : 1)] : &kv_full[item % R]);
-    } else {
+      if constexpr (k8) {              // (to K's warps and to V's)
+        for (int k = 0; k < 2; ++k) {
+          wait_item();
+          if (!ok) break;
+          mbar_arrive(&c_full[item % C]);
+          if (lane == 0) mbar_arrive(&c_full[item % C]);
+          ++item;
+        }
+      } else {
+        if (lane == 0) mbar_arrive(&kv_full[item % R]);
+      }
+    }
+    if (!ok) {
       // copies in flight land before shared memory goes away
       if (qn0 > 0) mbar_wait(&q_full[0], (uint32_t)(qn0 - 1) & 1u, nullptr);
       if (qn1 > 0) mbar_wait(&q_full[1], (uint32_t)(qn1 - 1) & 1u, nullptr);
