@@ -20,6 +20,12 @@
 // of a column a word.  Slots are dealt to the scores' rows so that neither read meets bank
 // conflicts.
 // A slot that no row sees has its V scale taken as 0, so its codes count for nothing.
+//
+// Measured with the merge, in a graph: 96 ragged sequences (291 MB, 6 heads a kv head) 62 us
+// over pages of 16 and 56 over pages of 64 (5.2 TB/s), 8 of 131072 slots 90 us (6.1 TB/s) and
+// with 16 heads a kv head 111, 24 of 6000 slots 30, 37, 45 and 60 us for 8, 16, 24 and 32 rows.
+// A cold pass over the first spends 56 us here at 67 % of the memory's peak and 50 % of the
+// issue slots: a warp waits for its own chain of loads, products and exponentials.
 #include <math.h>
 
 #include <type_traits>
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
                     &full[st]);
         }
         // the scales: 16 bytes a lane and copy whatever the page (a copy of each page's own costs as
-        // much as one of its codes: 96 sequences over pages of 16 took 69 us, over pages of 64 58)
+        // much as one of its codes: 96 sequences over pages of 16 took 69 us with those, 62 so)
 #pragma unroll
         for (int c = 0; c < Sm::kScCopies; ++c) {
           const int piece = c * 32 + lane, sv = piece / (Sm::kSc / 16);
@@ -527,7 +533,12 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
         large |= kv8_big_scales(kw[s][0]) | kv8_big_scales(kw[s][1]) | kv8_big_scales(sw[s][0][0]) |
                  kv8_big_scales(sw[s][0][1]) | kv8_big_scales(sw[s][1][0]) | kv8_big_scales(sw[s][1][1]);
       }
-      const bool any_big = __any_sync(0xffffffffu, (large & 0x80808080u) != 0);
+      // One row tile asks whether a scale is large and keeps the values' shorter form for when
+      // none is (half the conversion's arithmetic).  More row tiles have enough products to
+      // hide the longer one behind, and no register for the question: 16 heads a kv head,
+      // 8 x 131072 slots 118 -> 111 us without it, 24 sequences of 24 rows 48.5 -> 45.5;
+      // one row tile without it 62 -> 64 (96 ragged sequences).
+      const bool any_big = NT > 1 || __any_sync(0xffffffffu, (large & 0x80808080u) != 0);
       // (one row tile: two sums, so that products follow one another half as far)
       constexpr int kSums = NT == 1 ? 2 : 1;
       float sc[NS][NT][kSums][4];
@@ -576,7 +587,8 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
           }
         }
       };
-      if (__builtin_expect(any_big, 0)) scores(std::true_type());
+      if constexpr (NT > 1) scores(std::true_type());
+      else if (__builtin_expect(any_big, 0)) scores(std::true_type());
       else scores(std::false_type());
       bool need = false;
 #pragma unroll
@@ -667,7 +679,8 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
             }
           }
       };
-      if (__builtin_expect(any_big, 0)) values(std::true_type());
+      if constexpr (NT > 1) values(std::true_type());
+      else if (__builtin_expect(any_big, 0)) values(std::true_type());
       else values(std::false_type());
     }
     if (flags & 2) {

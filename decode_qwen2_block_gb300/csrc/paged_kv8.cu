@@ -30,7 +30,9 @@ __device__ __forceinline__ uint32_t max_bits16(const uint4& a, const uint4& b) {
 }
 
 // Quantises row r's K and V (Hkv heads of D) into slot slot_map[r].  A thread takes 16
-// columns of K and of V, two neighbours a block of 32.
+// columns of K and of V, two neighbours a block of 32, so a block's maximum is one exchange
+// and a row's codes leave in 16-byte pieces.  Bound by memory, two bytes read and one
+// written a value: 32761 rows of 2 heads of 128 9.8 us, 51 MB (5.2 TB/s).
 __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendParams p) {
   // (in this order: see page_append_kernel)
   griddep_wait();
@@ -92,7 +94,8 @@ __device__ __forceinline__ void store32(__half* dst, const uint32_t* v, bool wid
 }
 
 // Slot slot_map[r] to row r of K and V in fp16.  A thread takes 16 columns of K and of V and
-// writes whole 32-byte sectors of them; bound by memory, kUnroll items in flight per thread.
+// writes whole 32-byte sectors of them; bound by memory, kUnroll items in flight per thread
+// (one: 120007 rows 33.3 us; two: 31.8, 5.9 TB/s).
 constexpr int kUnroll = 2;
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8ReadParams p) {
   griddep_wait();

@@ -33,6 +33,10 @@
 // memory per clock, all there is, while the next tiles' 64 KB arrive), a unit's begin and
 // end 2.6 us (5400 clocks, 1.6 tiles), all else of the call, with the merge that finds
 // nothing cut, 10.6 us.
+// k8, the same way: a tile 2.07 us (64 columns 1.69, fp16 1.53): the conversion reads 32 KB and
+// writes 64 KB of shared memory beside the MMAs' own reads; leaving either out would
+// save 0.2 - 0.3 us, its arithmetic nothing.  The softmax warps as converters, in their waits:
+// 2.89; codes from memory into the converters' registers, no ring of them: 2.60.
 #pragma once
 
 #include <math.h>
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreadsOf<k8>, 1)
       // Two warps make K tiles fp16 and two V tiles, 32 slots and 64 columns at a time: a lane's
       // codes and scales to the place and order that a tile of an fp16 cache would have, zeros
       // where no row of the unit sees the slot.  (All four warps on one tile after another: the
-      // waits around each follow one another, 2.20 us a tile of 128 columns against 2.15.)
+      // waits around each follow one another, 2.20 us a tile of 128 columns against 2.07.)
       const int own = (warp - 12) >> 1, r0 = (warp & 1) * 64 + lane;
       for (int i = own;; i += 2) {       // ring item i: K (even) or V of tile i / 2
         if (!__all_sync(0xffffffffu, mbar_wait_near(&c_full[i % C], (uint32_t)(i / C) & 1u, p.err))) break;
