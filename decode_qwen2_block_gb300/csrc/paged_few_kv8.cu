@@ -23,7 +23,7 @@
 //
 // Measured with the merge, in a graph: 96 ragged sequences (291 MB, 6 heads a kv head) 62 us
 // over pages of 16 and 56 over pages of 64 (5.2 TB/s), 8 of 131072 slots 90 us (6.1 TB/s) and
-// with 16 heads a kv head 111, 24 of 6000 slots 30, 37, 45 and 60 us for 8, 16, 24 and 32 rows.
+// with 16 heads a kv head 112, 24 of 6000 slots 30, 37, 47 and 56 us for 8, 16, 24 and 32 rows.
 // A cold pass over the first spends 56 us here at 67 % of the memory's peak and 50 % of the
 // issue slots: a warp waits for its own chain of loads, products and exponentials.
 #include <math.h>
@@ -43,7 +43,7 @@ constexpr int kHead = 1;             // a unit's begin and end in the line, in t
 // half of what fp16 holds (see weight_plain for scores that need more room), and keep 11
 // bits down to 2^-24 of the greatest.  Following every rise, as the fp16 caches' kernel does
 // with 2^14, rescales O for nearly every tile while a piece has few.
-constexpr float kWeightLog2 = 10.f, kRescaleLog2 = 5.f;
+constexpr float kWeightLog2 = 10.f, kRescaleLog2 = 5.f, kUnseen = 1e38f;   // (scores stay below 2^37)
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -449,10 +449,12 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
   const uint32_t kb = tig >> 1, sel_k0 = kb << 12 | 4 << 8 | kb << 4 | 4, sel_k1 = sel_k0 + 0x2020;
   const uint32_t q_lane = qbase + grp * Sm::kQStride + tig * 32;
   // The lane's rows: 8 nt + 2 tig + e.  nref: less what their exponents are taken against (log2
-  // units, less kWeightLog2 but where weight_plain), lim: where that has to follow (-inf:
-  // nothing seen yet).  O: columns 16 i + grp and + 8 of either row.
-  float nref[NT][2], lim[NT][2], l_r[NT][2], O[NT][NB * 2][4];
-  int last[NT][2], low[NT][2];
+  // units, less kWeightLog2 but where weight_plain; kUnseen: nothing seen yet).  most: the
+  // exponent at which that follows, of all the lane's rows the least.  O: columns 16 i + grp
+  // and + 8 of either row.  (Registers bound 32 rows: with each row's limit and slots in them
+  // 24 x 6000 slots took 59.9 us, so 55.7, though 24 rows 45.8 and so 46.9.)
+  float nref[NT][2], most = 0.f, l_r[NT][2], O[NT][NB * 2][4];
+  uint32_t toks[(NT + 1) / 2] = {};     // the rows' tokens (of at most 32), a byte each; 0x80: no row
   uint32_t qf[Sm::kQRegs ? D / 16 : 1][2];
   // q's fragments of products 2 x, 2 x + 1 (x < D / 32) of row tile nt
   auto load_q = [&](uint32_t qb, int nt, int x, uint32_t* a, uint32_t* b) {
@@ -479,16 +481,18 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
     const uint32_t ks = sring + st * 2 * Sm::kSc, vs = ks + Sm::kSc;
     const uint32_t qb = q_lane + (seg % Sm::kQBufs) * Sm::kQBytes;
     if (flags & 1) {
-      const int L = infos[st].L;
+#pragma unroll
+      for (int w = 0; w < (NT + 1) / 2; ++w) toks[w] = 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          last[nt][e] = L + min((nt * 8 + 2 * tig + e) / p.G, n - 1);
-          low[nt][e] = paged_window(p, last[nt][e]);
-          nref[nt][e] = l_r[nt][e] = 0.f;
-          lim[nt][e] = -INFINITY;
+          const int t = (nt * 8 + 2 * tig + e) / p.G;
+          toks[nt >> 1] |= (uint32_t)(t < n ? t : 0x80) << ((nt & 1) * 16 + e * 8);
+          nref[nt][e] = kUnseen;
+          l_r[nt][e] = 0.f;
         }
+      most = kWeightLog2 + kRescaleLog2;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -536,7 +540,7 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
       // One row tile asks whether a scale is large and keeps the values' shorter form for when
       // none is (half the conversion's arithmetic).  More row tiles have enough products to
       // hide the longer one behind, and no register for the question: 16 heads a kv head,
-      // 8 x 131072 slots 118 -> 111 us without it, 24 sequences of 24 rows 48.5 -> 45.5;
+      // 8 x 131072 slots 118 -> 111 us without it, 24 sequences of 24 rows 48.5 -> 46;
       // one row tile without it 62 -> 64 (96 ragged sequences).
       const bool any_big = NT > 1 || __any_sync(0xffffffffu, (large & 0x80808080u) != 0);
       // (one row tile: two sums, so that products follow one another half as far)
@@ -598,13 +602,18 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
           for (int k = 0; k < 4; ++k) sc[s][0][0][k] += sc[s][0][1][k];
         }
         if (!clear) {
+          const int L = infos[st].L;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int c = kr + 16 * s + kT1 * (k >> 1), slot = slot0 + c;
-              if (!(c >= vlo && slot <= last[nt][k & 1] && slot >= low[nt][k & 1]))
-                sc[s][nt][0][k] = -INFINITY;
+            for (int e = 0; e < 2; ++e) {
+              const int last = L + (int)(toks[nt >> 1] >> ((nt & 1) * 16 + e * 8) & 0x7f);
+              const int low = paged_window(p, last);
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const int c = kr + 16 * s + kT1 * t, slot = slot0 + c;
+                if (!(c >= vlo && slot <= last && slot >= low)) sc[s][nt][0][2 * t + e] = -INFINITY;
+              }
             }
         }
       }
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
 #pragma unroll
           for (int s = 1; s < NS; ++s) x = fmaxf(x, fmaxf(sc[s][nt][0][e], sc[s][nt][0][2 + e]));
           top[nt][e] = x;
-          need |= fmaf(x, sl2, -kWeightLog2) > lim[nt][e];
+          need |= fmaf(x, sl2, nref[nt][e]) > most;
         }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -627,13 +636,14 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
             float x = top[nt][e];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            const float t = fmaf(x, sl2, -kWeightLog2);
-            if (t > lim[nt][e]) {         // (alike in the row's lanes)
+            if (fmaf(x, sl2, nref[nt][e]) > most) {       // (alike in the row's lanes)
+              const float t = fmaf(x, sl2, -kWeightLog2);
               const bool plain = weight_plain(t);
               const float mn = plain ? t + kWeightLog2 : t;
-              const float f = lim[nt][e] == -INFINITY ? 0.f : ex2(-nref[nt][e] - mn);
+              const float f = ex2(-nref[nt][e] - mn);     // (nothing seen: 0)
               nref[nt][e] = -mn;
-              lim[nt][e] = mn + (plain ? kRescaleLog2 - kWeightLog2 : kRescaleLog2);
+              // (places of no row hold whatever lay there: the bits of others do not depend on it)
+              if (plain && !(toks[nt >> 1] >> ((nt & 1) * 16 + e * 8) & 0x80)) most = kRescaleLog2;
               l_r[nt][e] *= f;
 #pragma unroll
               for (int i = 0; i < NB * 2; ++i) {
@@ -697,7 +707,7 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          m_r[nt][e] = lim[nt][e] == -INFINITY ? -INFINITY : -nref[nt][e];
+          m_r[nt][e] = nref[nt][e] == kUnseen ? -INFINITY : -nref[nt][e];
           if (grp == 0) stat_m[(nt * 8 + 2 * tig + e) * kWarps + warp] = m_r[nt][e];
         }
       named_sync(1, kConsumers);
