@@ -601,3 +601,47 @@ def test_argument_errors():
         b.attn_paged_kv8(d, x.q, *p, out, ws.cpu())
     assert e.value.status == blk.BLK_ERR_WORKSPACE
     assert NAN_SCALE == 0x7f
+
+
+@pytest.mark.parametrize("heads,kv,dim,top", [(12, 2, 128, 1), (12, 2, 128, 2), (12, 2, 128, 4),
+                                              (8, 2, 128, 8), (8, 8, 64, 7), (16, 4, 64, 3),
+                                              (16, 4, 64, 6), (16, 4, 64, 8), (16, 4, 64, 30)])
+@pytest.mark.parametrize("k_gain,v_gain", [(9000.0, 9000.0), (9000.0, 1e-6), (1e-4, 9000.0)])
+def test_large_scales_at_every_number_of_rows(heads, kv, dim, top, k_gain, v_gain):
+    """Scales above 3584 in K, in V and in both, for 1 - 4 tiles of rows and for many."""
+    x = Batch(heads, kv, dim, 64, [300, 70, 1000], [top, 1, top], seed=48)
+    for pool, gain in ((x.k_pages, k_gain), (x.v_pages, v_gain)):
+        pool.copy_((pool.double() * gain).clamp(-65504, 65504))
+    x.q.copy_(x.q.double() / k_gain)         # (the scores' size is the one that the bound is for)
+    x = in_8_bits(x)
+    out, b = run8(x)
+    b.check()
+    check_rows(x, out)
+
+
+@pytest.mark.parametrize("heads,kv,dim,top", [(12, 2, 128, 2), (12, 2, 128, 4), (16, 4, 64, 3),
+                                              (16, 4, 64, 6), (16, 4, 64, 8)])
+def test_rows_of_large_and_small_scores_beside_one_another(heads, kv, dim, top):
+    """Heads whose scores pass 2^22 in the same tiles of rows as heads whose scores do not: the
+    former take the V of the slot that is far above all others, the latter keep to their bound."""
+    x = Batch(heads, kv, dim, 64, [500, 90, 1200], [top, 1, top], seed=49)
+    x.k_pages[..., 0].copy_(torch.where(x.k_pages[..., 0].isnan(), x.k_pages[..., 0], 0))
+    big = torch.arange(heads, device="cuda") % 3 == 1
+    at = [(0, 1, 5), (1, 0, 60), (2, 10, 17)]           # (sequence, page of its table, slot of it)
+    x.q[..., 0] = 0
+    for b_, blk_, s in at:
+        x.k_pages[int(x.table[b_, blk_]), :, s, :] = 0
+        x.k_pages[int(x.table[b_, blk_]), :, s, 0] = 16000
+    x = in_8_bits(x)
+    want, bound = x.reference()
+    x.q[:, big, 0] = 30000
+    out, b = run8(x)
+    b.check()
+    off = (out.double() - want).abs()
+    assert (off <= bound)[:, ~big].all()
+    r0 = 0
+    for (b_, blk_, s), n in zip(at, x.new):
+        v = x.v_pages[int(x.table[b_, blk_]), :, s].double().repeat_interleave(heads // kv, 0)[big]
+        got = out[r0:r0 + n, big].double()
+        assert ((got - v).abs() <= (2 * U16 + 2.0 ** -13) * v.abs() + 2.0 ** -25).all()
+        r0 += n
