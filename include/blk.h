@@ -517,7 +517,10 @@ int blk_page_read_kv8(blk_handle h, const int64_t* slot_map, int64_t n_rows, int
                       int64_t row_stride, int64_t head_stride, void* stream);
 
 /* blk_attn_paged over such pools, with the same workspace: the result is that of an
- * fp16 cache that holds what blk_page_read_kv8 gives, up to the order of sums. */
+ * fp16 cache that holds what blk_page_read_kv8 gives, up to the order of sums.  Scores
+ * q . k / sqrt(head_dim) past 9e7 in magnitude, which fp32 holds to steps of 8 and more,
+ * leave fp16 no room for their weights (blk_attn_paged's neither): such rows may come out
+ * as NaN or infinities. */
 int blk_attn_paged_kv8(blk_handle h, const blk_paged_batch* batch, const void* q, int64_t q_stride,
                        const blk_kv8_pool* pool, void* out, int64_t out_stride, void* ws,
                        size_t ws_bytes, void* stream);
