@@ -639,7 +639,9 @@ __global__ void __launch_bounds__(FSmem<D, NT>::kThreads, FSmem<D, NT>::kCtas)
             if (fmaf(x, sl2, nref[nt][e]) > most) {       // (alike in the row's lanes)
               const float t = fmaf(x, sl2, -kWeightLog2);
               const bool plain = weight_plain(t);
-              const float mn = plain ? t + kWeightLog2 : t;
+              // Never below where it stands: the limit may be another row's, and a reference
+              // that fell with a row's scores would let O and l grow without end.
+              const float mn = fmaxf(plain ? t + kWeightLog2 : t, -nref[nt][e]);
               const float f = ex2(-nref[nt][e] - mn);     // (nothing seen: 0)
               nref[nt][e] = -mn;
               // (places of no row hold whatever lay there: the bits of others do not depend on it)
