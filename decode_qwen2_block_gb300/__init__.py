@@ -753,7 +753,7 @@ class Block:
     def page_read_kv8(self, slot_map, k_pages, v_pages, k_scales, v_scales, k, v, stream=None):
         """What the slots of slot_map (int64 [n]; -1 leaves a row as it was) stand for, into
         the rows of k and v (fp16 [n, n_kv_heads, head_dim], strides as for page_append, no
-        rows over each other)."""
+        rows over each other, K's and V's neither)."""
         (_calls or _paged_calls()).page_read_kv8(
             self._args, slot_map, k_pages, v_pages, k_scales, v_scales, k, v,
             None if stream is None else stream.cuda_stream)

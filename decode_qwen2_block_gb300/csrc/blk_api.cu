@@ -1788,11 +1788,9 @@ int blk_page_read_kv8(blk_handle h, const int64_t* slot_map, int64_t n_rows, int
   int rc = check_rows_kv8(h, k, v, row_stride, head_stride, slot_map, n_rows, page_size, n_pages,
                           pool);
   if (rc) return rc;
-  // rows over each other would be written by several threads at once
-  const int64_t D = h->cfg.head_dim, H = h->cfg.n_kv_heads, rs = row_stride, hs = head_stride;
-  const bool one_row = n_rows == 1, one_head = H == 1;
-  if ((!one_row && rs < D) || (!one_head && hs < D) ||
-      (!one_row && !one_head && rs < (H - 1) * hs + D && hs < (n_rows - 1) * rs + D))
+  const int64_t D = h->cfg.head_dim, H = h->cfg.n_kv_heads;
+  const int64_t apart = (reinterpret_cast<intptr_t>(v) - reinterpret_cast<intptr_t>(k)) / 2;
+  if (kv8_rows_meet(n_rows, H, row_stride, head_stride, D, apart))
     return BLK_ERR_SHAPE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Kv8ReadParams p = {};

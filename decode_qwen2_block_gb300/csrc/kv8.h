@@ -45,6 +45,32 @@ struct Kv8ReadParams {
   int N, Hkv, D, page_lg;
   int* err;
 };
+
+// Whether rows that the read writes lie over each other, and several threads would write one
+// place: rows of D values at r * row_stride + h * head_stride (r < n, h < H), and the same `apart`
+// elements further (V's from K's).  Heads may lie within rows or rows within heads; the span of
+// what lies within fits the stride of the other.
+inline bool kv8_rows_meet(int64_t n, int64_t H, int64_t row_stride, int64_t head_stride, int64_t D,
+                          int64_t apart) {
+  int64_t a = head_stride, na = H, b = row_stride, nb = n;          // within, around
+  if (n > 1 && (H == 1 || row_stride < (H - 1) * head_stride + D)) {
+    a = row_stride, na = n;
+    b = head_stride, nb = H;
+  }
+  if ((na > 1 && a < D) || (nb > 1 && b < (na > 1 ? (na - 1) * a : 0) + D)) return true;
+  // a row of one over a row of the other: |apart - i a - j b| < D for some |i| < na, |j| < nb,
+  // and with |i a| + D <= b only the two j around apart / b can give that
+  const int64_t d = apart < 0 ? -apart : apart;
+  const int64_t j0 = nb > 1 ? d / b : 0;
+  for (int64_t j = j0; j < nb && j <= j0 + 1; ++j) {
+    const int64_t rest = d - (nb > 1 ? j * b : 0), at = rest < 0 ? -rest : rest;
+    const int64_t i = na > 1 ? at / a : 0, left = at - (na > 1 ? i * a : 0);
+    if (i < na && left < D) return true;
+    if (na > 1 && i + 1 < na && a - left < D) return true;
+  }
+  return false;
+}
+
 cudaError_t launch_kv8_read(const Kv8ReadParams& p, int num_sms, cudaStream_t s, bool pdl);
 
 // Attention over such pools: the kernels of paged.h over codes and scales.

@@ -508,10 +508,9 @@ int blk_page_append_kv8(blk_handle h, const void* k, const void* v, int64_t row_
                         void* stream);
 
 /* The other way: row r of k and v (device fp16, row r and head h at r * row_stride +
- * h * head_stride elements, both multiples of 8, no two rows over each other:
- * BLK_ERR_SHAPE) becomes
- * what slot slot_map[r] stands for.  A row of slot -1 stays as it was; another slot
- * outside the pool leaves its row too and is reported. */
+ * h * head_stride elements, both multiples of 8, no two rows over each other, of k, of v
+ * or of both: BLK_ERR_SHAPE) becomes what slot slot_map[r] stands for.  A row of slot -1
+ * stays as it was; another slot outside the pool leaves its row too and is reported. */
 int blk_page_read_kv8(blk_handle h, const int64_t* slot_map, int64_t n_rows, int32_t page_size,
                       int64_t n_pages, const blk_kv8_pool* pool, void* k, void* v,
                       int64_t row_stride, int64_t head_stride, void* stream);
