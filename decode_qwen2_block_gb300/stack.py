@@ -316,7 +316,9 @@ class PagedStack:
         """Sequence b's K and V of every layer as contiguous caches hold them: a list of
         (k, v), fp16 [n_kv_heads, slots, head_dim] (the cache in 8 bits as what it stands for).
         caches: such pairs to fill from slot 0 on (e.g. LayerStack's), with at least as
-        many slots as the sequence; made to its length when None."""
+        many slots as the sequence; made to its length when None.  Over 8-bit pages k and v
+        of a pair have the same strides, the last one 1; others are refused before any
+        cache is written."""
         n, page = self.lens[b], self.page
         if caches is not None and len(caches) != self.n_layers:
             raise BlkError(BLK_ERR_SHAPE, "PagedStack.read: caches")
@@ -333,6 +335,10 @@ class PagedStack:
                     raise BlkError(BLK_ERR_SHAPE, f"PagedStack.read: {tuple(t.shape)} {t.dtype}")
             if n == 0:
                 return caches
+            for k, v in caches if self.kv8 else ():
+                if (k.stride(2) != 1 or v.stride(2) != 1 or (Hkv > 1 and k.stride(0) != v.stride(0)) or
+                        (n > 1 and k.stride(1) != v.stride(1))):
+                    raise BlkError(BLK_ERR_SHAPE, f"PagedStack.read: strides {k.stride()}, {v.stride()}")
             most = 1 << 20                           # rows of one call
             for i in range(0, n, most):
                 j = min(n, i + most)
