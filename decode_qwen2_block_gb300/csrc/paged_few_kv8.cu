@@ -22,8 +22,8 @@
 // A slot that no row sees has its V scale taken as 0, so its codes count for nothing.
 //
 // Measured with the merge, in a graph: 96 ragged sequences (291 MB, 6 heads a kv head) 62 us
-// over pages of 16 and 56 over pages of 64 (5.2 TB/s), 8 of 131072 slots 90 us (6.1 TB/s) and
-// with 16 heads a kv head 112, 24 of 6000 slots 30, 37, 47 and 56 us for 8, 16, 24 and 32 rows.
+// over pages of 16 and 59 over pages of 64 (5.0 TB/s), 8 of 131072 slots 90 us (6.1 TB/s) and
+// with 16 heads a kv head 112, 24 of 5000 slots 30, 37, 45 and 55 us for 8, 16, 24 and 32 rows.
 // A cold pass over the first spends 56 us here at 67 % of the memory's peak and 50 % of the
 // issue slots: a warp waits for its own chain of loads, products and exponentials.
 #include <math.h>
@@ -38,11 +38,12 @@ namespace blk {
 namespace {
 
 constexpr int kHead = 1;             // a unit's begin and end in the line, in tiles
-// Weights are formed 2^10 times their size (O and l carry the factor, it cancels), and a
-// row's reference maximum follows only when a score passes it by 2^5: weights reach 2^15,
+// Weights are rounded to fp16, mma.sync's type for the second product (l sums them before
+// that, in fp32).  They are formed 2^10 times their size (O and l carry the factor, it
+// cancels), and a row's reference maximum follows only when a score passes it by 2^5: weights reach 2^15,
 // half of what fp16 holds (see weight_plain for scores that need more room), and keep 11
 // bits down to 2^-24 of the greatest.  Following every rise, as the fp16 caches' kernel does
-// with 2^14, rescales O for nearly every tile while a piece has few.
+// with 2^14 (11 bits down to 2^-28), rescales O for nearly every tile while a piece has few.
 constexpr float kWeightLog2 = 10.f, kRescaleLog2 = 5.f, kUnseen = 1e38f;   // (scores stay below 2^37)
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {

@@ -515,8 +515,11 @@ int blk_page_read_kv8(blk_handle h, const int64_t* slot_map, int64_t n_rows, int
                       int64_t n_pages, const blk_kv8_pool* pool, void* k, void* v,
                       int64_t row_stride, int64_t head_stride, void* stream);
 
-/* blk_attn_paged over such pools, with the same workspace: the result is that of an
- * fp16 cache that holds what blk_page_read_kv8 gives, up to the order of sums.  Scores
+/* blk_attn_paged over such pools, with the same workspace: the attention of an fp16
+ * cache that holds what blk_page_read_kv8 gives, up to the order of sums and the rounding
+ * of small softmax weights.  Few rows: a weight has fp16's 11 bits down to 2^-24 of the
+ * row's greatest, fewer below that and none from 2^-35 on (blk_attn_paged 2^-28 and 2^-39);
+ * many rows as blk_attn_paged.  Scores
  * q . k / sqrt(head_dim) past 9e7 in magnitude, which fp32 holds to steps of 8 and more,
  * leave fp16 no room for their weights (blk_attn_paged's neither): such rows may come out
  * as NaN or infinities. */
